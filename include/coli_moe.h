@@ -477,6 +477,135 @@ int coli_moe_test_cache_policy(int32_t n_experts, int32_t n_slots, int32_t reser
                                const int32_t *pins, int32_t n_pins, const int32_t *calls, const int32_t *call_len,
                                int32_t n_calls, int32_t *miss_out, int32_t *slot_out);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the layer: the residual addition with the root-mean-square
+ * norm that makes the layer's (post-norm) input, dense matrix products with
+ * their epilogue, and the balance loss of the router's choices with its
+ * gradient.  No handle: arguments come in one struct per call, every pointer
+ * in it is DEVICE memory of the current device, and a call only enqueues
+ * kernels on `stream` (it neither allocates nor copies, so it may be
+ * captured into a graph).  Strides count elements between rows; elements of
+ * a row are contiguous.  Pointers must be aligned to their element size.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element types of these operators. */
+#define COLI_MOE_F32 0
+#define COLI_MOE_BF16 1
+#define COLI_MOE_F16 2
+#define COLI_MOE_INT8 3
+#define COLI_MOE_E4M3 4 /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448, no infinities (OCP) */
+
+/*
+ * Residual addition and root-mean-square norm of `rows` rows:
+ *   s = x + residual                     (float32, rounded once to residual_type and
+ *                                         stored in residual_out; without a residual s = x)
+ *   y = (s * r) * weight, r = 1 / sqrt(mean(s^2) + eps)
+ * The norm is of the stored (rounded) s, so a later reader of the residual
+ * stream sees the numbers that were normed.  The mean is summed in float64
+ * and r rounded once to float32, so the result does not depend on how the
+ * kernel splits a row.  The output is y rounded to out_type, or 8-bit codes
+ * with one float32 scale per `group` columns (the last group of a row may be
+ * shorter), Q = 127 (int8) or 448 (e4m3):
+ *   scales[row][g] = max|y| / Q over the group (float32 division),
+ *   out = round(y / scale), to the nearest, ties to even, |out| <= Q;
+ * a group of zeros has scale 0 and codes 0.  Inputs must be finite; a row
+ * that holds Inf or NaN gets an unspecified output, other rows are not
+ * affected.
+ */
+typedef struct {
+  int32_t rows;           /* >= 0; 0 checks the arguments and enqueues nothing */
+  int32_t hidden;         /* 1..32768 */
+  int32_t x_type;         /* F32, BF16 or F16 */
+  int32_t residual_type;  /* F32, BF16 or F16 (of residual and residual_out) */
+  int32_t weight_type;    /* F32, BF16 or F16 */
+  int32_t out_type;       /* any type */
+  int32_t group;          /* 8-bit out: columns per scale, 64 or 128; 0 = the whole row.  Else 0 */
+  float eps;              /* >= 0 */
+  const void *x;
+  int64_t x_stride;
+  const void *residual;   /* NULL: none */
+  int64_t residual_stride;
+  void *residual_out;     /* may be `residual` itself; NULL exactly when residual is */
+  int64_t residual_out_stride;
+  const void *weight;     /* [hidden]; NULL: ones */
+  void *out;              /* no overlap with an input, except out == x with equal type and stride */
+  int64_t out_stride;
+  float *scales;          /* 8-bit out: [rows][1 or ceil(hidden / group)] */
+  int64_t scales_stride;
+} coli_moe_rmsnorm_t;
+
+/* Errors: -4 NULL or misaligned pointer, unsupported type, dimension or
+ * stride; -3 HIP launch error. */
+int coli_moe_rmsnorm(const coli_moe_rmsnorm_t *a, void *stream);
+
+/*
+ * Balance of the router's choices over each of n_seqs sequences (token rows
+ * seq_offsets[s] .. seq_offsets[s+1]-1).  With the valid tokens t of a
+ * sequence (mask[t] != 0), V their number, n_e the kept assignments among
+ * idx[t][0..top_k) that name expert e, N = sum_e n_e, and each token's shares
+ *   p_te = sigma(z_te) / sum_j sigma(z_tj)     (COLI_MOE_SCORES_SIGMOID, the layer's scores)
+ *   p_te = exp(z_te) / sum_j exp(z_tj)         (COLI_MOE_SCORES_SOFTMAX)
+ * of its logits z:
+ *   loss_s   = alpha * sum_e (E n_e / N) * (1/V) sum_t p_te    (alpha when balanced)
+ *   coef_se  = (alpha / V) * (E n_e / N - 1)
+ * coli_moe_balance writes loss [n_seqs], counts n_e [n_seqs][E] and coef
+ * [n_seqs][E]; coli_moe_balance_grad takes coef and the upstream gradient
+ * dloss [n_seqs] (NULL: ones) and writes the gradient with respect to the
+ * logits, the choices (and so n_e) held constant, d_te =
+ *   dloss_s * p_te * (coef_se - sum_j coef_sj p_tj)                                   softmax
+ *   dloss_s * s_te (1 - s_te) / sum_j s_tj * (coef_se - sum_j coef_sj p_tj)           sigmoid
+ * (subtracting alpha / V from every coef_se leaves it unchanged, since a
+ * token's shares sum to 1, and avoids a difference of nearly equal numbers).
+ *
+ * Slots of idx that are negative (dropped by the routing limits) or not
+ * below E count for no expert.  A sequence with no valid token or no kept
+ * assignment has loss 0 and coef 0.  A logit of -Inf is an expert out of the
+ * token's reach (share 0); a token whose logits are all -Inf has shares and
+ * gradient 0.  Masked tokens' logits are never looked at and their gradient
+ * is 0; gradient rows of tokens in no sequence (before the first or behind
+ * the last) are left as they were.  Offsets outside [0, tokens] are clamped;
+ * offsets that decrease give unspecified results within the output arrays.
+ * Sums over tokens: float32 within a workgroup, then float64, in a fixed
+ * order, so the same call gives the same bits.
+ */
+#define COLI_MOE_SCORES_SIGMOID 0
+#define COLI_MOE_SCORES_SOFTMAX 1
+typedef struct {
+  int32_t tokens;             /* rows of logits, idx and mask; >= 0 */
+  int32_t n_experts;          /* 1..512 */
+  int32_t top_k;              /* 1..32, <= n_experts */
+  int32_t n_seqs;             /* 1..65536 */
+  int32_t scores;             /* COLI_MOE_SCORES_* */
+  float alpha;
+  const float *logits;
+  int64_t logits_stride;
+  const int32_t *idx;         /* [tokens][top_k], contiguous; the gradient does not read it */
+  const int32_t *seq_offsets; /* [n_seqs + 1], ascending; NULL: one sequence of all tokens (n_seqs 1) */
+  const uint8_t *mask;        /* [tokens]; NULL: every token is valid */
+} coli_moe_balance_t;
+
+/* Bytes of DEVICE workspace of coli_moe_balance (per-workgroup sums), 0 for
+ * sizes out of range.  It holds nothing between calls; calls whose work may
+ * overlap need one each. */
+size_t coli_moe_balance_workspace_bytes(int32_t tokens, int32_t n_experts, int32_t n_seqs);
+
+/* Errors: -4 NULL or misaligned pointer (workspace: 16 bytes), size out of
+ * range; -2 top_k or n_experts out of range; -1 workspace too small; -3 HIP
+ * launch error.  tokens == 0 writes the empty sequences' loss, counts and
+ * coef. */
+int coli_moe_balance(const coli_moe_balance_t *a, float *loss, int32_t *counts, float *coef, void *workspace,
+                     size_t workspace_bytes, void *stream);
+int coli_moe_balance_grad(const coli_moe_balance_t *a, const float *coef, const float *dloss, float *dlogits,
+                          int64_t dlogits_stride, void *stream);
+
+/* Copy the router logits of the handle's last forward (T tokens) into the
+ * caller's DEVICE buffer [T][n_experts], enqueued on `stream`: with the idx
+ * of coli_moe_last_routing, what coli_moe_balance takes.  (The read probes
+ * overwrite them.)  Returns the T of the last forward (>= 0), -4 or -3. */
+int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream);
+
 /* Static description of an error code. */
 const char *coli_moe_error_string(int32_t code);
 

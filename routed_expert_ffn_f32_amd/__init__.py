@@ -69,6 +69,32 @@ class coli_moe_cache_stats_t(ctypes.Structure):
         return {n: int(getattr(self, n)) for n, _ in self._fields_}
 
 
+# Element types and score kinds of the operators around the layer.
+COLI_MOE_F32 = 0
+COLI_MOE_BF16 = 1
+COLI_MOE_F16 = 2
+COLI_MOE_INT8 = 3
+COLI_MOE_E4M3 = 4
+COLI_MOE_SCORES_SIGMOID = 0
+COLI_MOE_SCORES_SOFTMAX = 1
+
+
+class coli_moe_rmsnorm_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "hidden", "x_type", "residual_type", "weight_type", "out_type",
+                                              "group")] + \
+               [("eps", ctypes.c_float), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("residual_out", ctypes.c_void_p), ("residual_out_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("scales_stride", ctypes.c_int64)]
+
+
+class coli_moe_balance_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "n_experts", "top_k", "n_seqs", "scores")] + \
+               [("alpha", ctypes.c_float), ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+                ("idx", ctypes.c_void_p), ("seq_offsets", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -151,6 +177,17 @@ def load_library():
         L.coli_moe_usage_read.restype = ctypes.c_int
         L.coli_moe_test_cache_policy.argtypes = [i32, i32, i32, ctypes.c_float, i32, vp, i32, vp, vp, i32, vp, vp]
         L.coli_moe_test_cache_policy.restype = ctypes.c_int
+        L.coli_moe_rmsnorm.argtypes = [ctypes.POINTER(coli_moe_rmsnorm_t), vp]
+        L.coli_moe_rmsnorm.restype = ctypes.c_int
+        bp = ctypes.POINTER(coli_moe_balance_t)
+        L.coli_moe_balance_workspace_bytes.argtypes = [i32, i32, i32]
+        L.coli_moe_balance_workspace_bytes.restype = sz
+        L.coli_moe_balance.argtypes = [bp, vp, vp, vp, vp, sz, vp]
+        L.coli_moe_balance.restype = ctypes.c_int
+        L.coli_moe_balance_grad.argtypes = [bp, vp, vp, vp, ctypes.c_int64, vp]
+        L.coli_moe_balance_grad.restype = ctypes.c_int
+        L.coli_moe_last_logits.argtypes = [vp, vp, vp]
+        L.coli_moe_last_logits.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -364,6 +401,220 @@ def coli_moe_test_cache_policy(n_experts, n_slots, reserve, decay, repin_every, 
     return rc, [int(miss[i]) for i in range(len(calls))], [int(v) for v in slots]
 
 
+def coli_moe_rmsnorm(args: coli_moe_rmsnorm_t, stream: int = 0) -> int:
+    return _check(load_library().coli_moe_rmsnorm(args, stream), "coli_moe_rmsnorm")
+
+
+def coli_moe_balance_workspace_bytes(tokens: int, n_experts: int, n_seqs: int) -> int:
+    return int(load_library().coli_moe_balance_workspace_bytes(int(tokens), int(n_experts), int(n_seqs)))
+
+
+def coli_moe_balance(args: coli_moe_balance_t, loss: int, counts: int, coef: int, workspace: int,
+                     workspace_bytes: int, stream: int = 0) -> int:
+    return _check(load_library().coli_moe_balance(args, loss, counts, coef, workspace, workspace_bytes, stream),
+                  "coli_moe_balance")
+
+
+def coli_moe_balance_grad(args: coli_moe_balance_t, coef: int, dloss, dlogits: int, dlogits_stride: int,
+                          stream: int = 0) -> int:
+    return _check(load_library().coli_moe_balance_grad(args, coef, dloss, dlogits, dlogits_stride, stream),
+                  "coli_moe_balance_grad")
+
+
+def coli_moe_last_logits(handle, logits: int, stream: int = 0) -> int:
+    return _check(load_library().coli_moe_last_logits(handle, logits, stream), "coli_moe_last_logits")
+
+
+# ---------------------------------------------------------------------------
+# The operators around the layer on torch device tensors.  Work is enqueued on
+# the current stream of the tensors' device; results are allocated there
+# unless given.  Tensors of other devices, shapes or types than described
+# raise ValueError; sizes and alignments that the library refuses raise
+# ColiMoeError.
+# ---------------------------------------------------------------------------
+
+_DTYPES: dict = {}  # torch dtype -> COLI_MOE_* element type
+
+
+def _dtype_code(dtype, what: str, bytes_too: bool = False) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: COLI_MOE_F32, torch.bfloat16: COLI_MOE_BF16, torch.float16: COLI_MOE_F16,
+                        torch.int8: COLI_MOE_INT8, torch.float8_e4m3fn: COLI_MOE_E4M3})
+    code = _DTYPES.get(dtype)
+    if code is None or (code > COLI_MOE_F16 and not bytes_too):
+        raise ValueError(f"{what}: unsupported type {dtype}")
+    return code
+
+
+def _matrix(t, what: str, device, rows=None, cols=None, dtype=None):
+    """Checks a 2-D device tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows, got shape {tuple(t.shape)}, "
+                         f"strides {tuple(t.stride())}")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
+    _on(t, what, device, dtype)
+    return t
+
+
+def _vector(t, what: str, device, n: int, dtype=None):
+    """Checks a contiguous 1-D device tensor of n elements."""
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous elements, got shape {tuple(t.shape)}, "
+                         f"strides {tuple(t.stride())}")
+    _on(t, what, device, dtype)
+    return t
+
+
+def _on(t, what: str, device, dtype):
+    if t.device != device or t.device.type != "cuda":
+        raise ValueError(f"{what}: expected a tensor on {device if device.type == 'cuda' else 'the GPU'}, got one on "
+                         f"{t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+
+
+def _enqueue(call, device):
+    """call(stream) with `device` current."""
+    import torch
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        return call(stream)
+    with torch.cuda.device(device):
+        return call(stream)
+
+
+def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None, out=None, scales=None,
+             out_dtype=None, group: int = 0):
+    """Root-mean-square norm of the rows of x [rows, hidden] (float32, bf16 or
+    f16), of x + residual if a residual is given; the sum is stored in
+    residual_out (default: in the residual itself).
+
+    Returns the normed rows in out_dtype (default: x's type), or for int8 and
+    float8_e4m3fn the pair (codes, scales) with scales [rows, 1], or
+    [rows, ceil(hidden / group)] for a group of 64 or 128 columns.
+    coli_moe_rmsnorm in include/coli_moe.h gives the formulas."""
+    import torch
+    dev = x.device
+    _matrix(x, "x", dev)
+    rows, hidden = x.shape
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    xt, ot = _dtype_code(x.dtype, "x"), _dtype_code(out_dtype, "out", True)
+    if out is None:
+        out = torch.empty((rows, hidden), dtype=out_dtype, device=dev)
+    else:
+        _matrix(out, "out", dev, rows, hidden, out_dtype)
+    rt = wt = 0
+    if residual is not None:
+        rt = _dtype_code(residual.dtype, "residual")
+        _matrix(residual, "residual", dev, rows, hidden)
+        if residual_out is None:
+            residual_out = residual
+        else:
+            _matrix(residual_out, "residual_out", dev, rows, hidden, residual.dtype)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight is not None:
+        wt = _dtype_code(weight.dtype, "weight")
+        _vector(weight, "weight", dev, hidden)
+    if ot > COLI_MOE_F16:
+        if group not in (0, 64, 128):
+            raise ValueError(f"group: 0, 64 or 128, got {group}")
+        n = -(-hidden // group) if group else 1
+        if scales is None:
+            scales = torch.empty((rows, n), dtype=torch.float32, device=dev)
+        else:
+            _matrix(scales, "scales", dev, rows, n, torch.float32)
+    else:
+        if scales is not None:
+            raise ValueError("scales belong to 8-bit outputs")
+        group = 0
+    if rows and hidden:
+        a = coli_moe_rmsnorm_t(rows, hidden, xt, rt, wt, ot, group, eps, x.data_ptr(), x.stride(0),
+                               None if residual is None else residual.data_ptr(),
+                               0 if residual is None else residual.stride(0),
+                               None if residual is None else residual_out.data_ptr(),
+                               0 if residual is None else residual_out.stride(0),
+                               None if weight is None else weight.data_ptr(), out.data_ptr(), out.stride(0),
+                               None if scales is None else scales.data_ptr(),
+                               0 if scales is None else scales.stride(0))
+        _enqueue(lambda stream: coli_moe_rmsnorm(a, stream), dev)
+    return out if scales is None else (out, scales)
+
+
+_SCORES = {"sigmoid": COLI_MOE_SCORES_SIGMOID, "softmax": COLI_MOE_SCORES_SOFTMAX}
+
+
+def _balance_args(logits, idx, alpha, scores, offsets, mask, n_seqs):
+    import torch
+    dev = logits.device
+    _matrix(logits, "logits", dev, dtype=torch.float32)
+    T, E = logits.shape
+    if scores not in _SCORES:
+        raise ValueError(f"scores: 'sigmoid' or 'softmax', got {scores!r}")
+    if idx is not None:
+        _matrix(idx, "idx", dev, T, None, torch.int32)
+        if T > 1 and idx.stride(0) != idx.shape[1]:
+            raise ValueError("idx: expected a contiguous tensor")
+    if offsets is not None:
+        _vector(offsets, "offsets", dev, n_seqs + 1, torch.int32)
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
+        _vector(mask, "mask", dev, T)
+    return coli_moe_balance_t(T, E, 1 if idx is None else idx.shape[1], n_seqs, _SCORES[scores], alpha,
+                              logits.data_ptr(), logits.stride(0), None if idx is None else idx.data_ptr(),
+                              None if offsets is None else offsets.data_ptr(),
+                              None if mask is None else mask.data_ptr())
+
+
+def balance_loss(logits, idx, alpha: float, scores: str = "sigmoid", offsets=None, mask=None):
+    """Balance loss of router choices idx [T, k] (int32, -1 in dropped slots)
+    with logits [T, E] (float32), per sequence: offsets int32 [S + 1] gives
+    the sequences' rows (default: one sequence of all tokens), mask [T] the
+    valid tokens (default: all).
+
+    Returns (loss [S], counts [S, E] int32, coef [S, E]); balance_grad takes
+    coef.  coli_moe_balance in include/coli_moe.h gives the formulas."""
+    import torch
+    n_seqs = 1 if offsets is None else offsets.numel() - 1
+    a = _balance_args(logits, idx, alpha, scores, offsets, mask, n_seqs)
+    dev, E = logits.device, logits.shape[1]
+    loss = torch.empty(max(n_seqs, 0), dtype=torch.float32, device=dev)
+    counts = torch.empty((max(n_seqs, 0), E), dtype=torch.int32, device=dev)
+    coef = torch.empty((max(n_seqs, 0), E), dtype=torch.float32, device=dev)
+    nbytes = coli_moe_balance_workspace_bytes(a.tokens, E, n_seqs)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _enqueue(lambda stream: coli_moe_balance(a, loss.data_ptr(), counts.data_ptr(), coef.data_ptr(), ws.data_ptr(),
+                                             nbytes, stream), dev)
+    return loss, counts, coef
+
+
+def balance_grad(logits, coef, dloss=None, scores: str = "sigmoid", offsets=None, mask=None, out=None):
+    """Gradient [T, E] of sum_s dloss[s] * loss[s] (dloss default: ones) with
+    respect to the logits, from balance_loss's coef and the same logits,
+    scores, offsets and mask.  Rows of tokens in no sequence are left as they
+    were in `out` (a fresh result holds zeros there)."""
+    import torch
+    n_seqs = 1 if offsets is None else offsets.numel() - 1
+    a = _balance_args(logits, None, 0.0, scores, offsets, mask, n_seqs)
+    dev, (T, E) = logits.device, logits.shape
+    _matrix(coef, "coef", dev, n_seqs, E, torch.float32)
+    if n_seqs > 1 and coef.stride(0) != E:
+        raise ValueError("coef: expected a contiguous tensor")
+    if dloss is not None:
+        _vector(dloss, "dloss", dev, n_seqs, torch.float32)
+    if out is None:
+        out = (torch.empty if offsets is None else torch.zeros)((T, E), dtype=torch.float32, device=dev)
+    else:
+        _matrix(out, "out", dev, T, E, torch.float32)
+    _enqueue(lambda stream: coli_moe_balance_grad(a, coef.data_ptr(), None if dloss is None else dloss.data_ptr(),
+                                                  out.data_ptr(), out.stride(0), stream), dev)
+    return out
+
+
 # ---------------------------------------------------------------------------
 # Convenience wrapper over torch device tensors.
 # ---------------------------------------------------------------------------
@@ -386,7 +637,52 @@ def make_config(hidden, n_experts, top_k, inter, n_shared, routed_scaling_factor
                              routed_scaling_factor=routed_scaling_factor, weight_format=weight_format)
 
 
-class MoELayer:
+def _stream_of(stream: int, device):
+    """Context in which `stream` is torch's current stream on `device`."""
+    import contextlib
+
+    import torch
+    if torch.cuda.current_stream(device).cuda_stream == stream:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
+
+
+class _RoutedCalls:
+    """What a resident and a cached layer have in common beside their forward:
+    needs `cfg`, `workspace`, `stream` and `_layer()`."""
+
+    def forward_normed(self, x, norm_weight=None, eps: float = 1e-6, residual=None, out=None):
+        """The layer on the norm of x (of x + residual, stored in the residual,
+        if one is given): forward(rms_norm(x, norm_weight, eps, residual)), on
+        the layer's stream.  x and the residual may be float32, bf16 or f16;
+        the result is the layer's float32 output, to be added to the residual
+        by the next norm."""
+        import torch
+        with _stream_of(self.stream, x.device):
+            hidden = rms_norm(x, norm_weight, eps, residual=residual, out_dtype=torch.float32)
+            return self.forward(hidden, out)
+
+    def last_logits(self):
+        """Router logits [T, E] of the last forward."""
+        import torch
+        dev = self.workspace.device
+        with _stream_of(self.stream, dev):
+            T = coli_moe_last_routing(self._layer(), stream=self.stream)
+            z = torch.empty((T, self.cfg.n_experts), dtype=torch.float32, device=dev)
+            if T:
+                coli_moe_last_logits(self._layer(), z.data_ptr(), self.stream)
+        return z
+
+    def balance(self, alpha: float, scores: str = "sigmoid", offsets=None, mask=None):
+        """balance_loss of the last forward's routing: (loss [S], counts
+        [S, E], coef [S, E])."""
+        z = self.last_logits()
+        T, routing = self.last_routing()
+        with _stream_of(self.stream, z.device):
+            return balance_loss(z, routing["idx"].view(T, self.cfg.top_k), alpha, scores, offsets, mask)
+
+
+class MoELayer(_RoutedCalls):
     """One layer on the current torch device.
 
     `tensors` maps names to device tensors: router_w [h,E] f32, sel_bias [E]
@@ -421,6 +717,9 @@ class MoELayer:
         return out
 
     __call__ = forward
+
+    def _layer(self):
+        return self.handle
 
     def set_routing(self, k_use: int | None = None, top_p: float = 1.0):
         """Lossy run-time routing limits for later forwards (warns when they
@@ -463,7 +762,7 @@ class MoELayer:
             pass
 
 
-class ExpertCache:
+class ExpertCache(_RoutedCalls):
     """One layer whose routed experts live in pinned host memory, copied on
     demand into `n_slots` HBM slots (torch device tensors hold the slots and
     the workspace).  `resident` maps router_w, sel_bias and sh_* to device
@@ -501,6 +800,9 @@ class ExpertCache:
         return out
 
     __call__ = forward
+
+    def _layer(self):
+        return coli_moe_cache_layer(self.handle)
 
     def prefetch(self, hidden, n_predict: int):
         return coli_moe_cache_prefetch(self.handle, hidden.data_ptr(), hidden.shape[0], n_predict, self.stream)

@@ -564,6 +564,15 @@ int coli_moe_last_routing(const coli_moe_t *mc, int32_t *idx, float *w, int32_t 
   return m->last_T;
 }
 
+int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream) {
+  if (!m || !logits || !aligned(logits, 4)) return COLI_MOE_EARG;
+  const size_t bytes = (size_t)m->last_T * m->cfg.n_experts * 4;
+  if (bytes && hipMemcpyAsync(logits, m->ws + m->L.logits, bytes, hipMemcpyDeviceToDevice,
+                              static_cast<hipStream_t>(stream)) != hipSuccess)
+    return COLI_MOE_EDEVICE;
+  return m->last_T;
+}
+
 static_assert(coli::kSpinLimit == COLI_MOE_DEFAULT_SPIN_LIMIT, "one default bound");
 
 int coli_moe_status(coli_moe_t *m, void *stream) {

@@ -1,0 +1,102 @@
+// Element types of the operators around the layer (COLI_MOE_F32 ...): eight
+// consecutive elements at a time between memory and float registers.  Wide
+// accesses do not need 16-byte alignment (gfx950 takes global loads and
+// stores of any width at element alignment), so rows of any length and
+// stride take the same path; only the last, partial eight of a row go one
+// element at a time.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "coli_moe.h"
+
+namespace coli {
+
+inline __host__ __device__ size_t type_bytes(int type) {
+  return type == COLI_MOE_F32 ? 4 : type == COLI_MOE_BF16 || type == COLI_MOE_F16 ? 2 : 1;
+}
+inline bool float_type(int type) { return type >= COLI_MOE_F32 && type <= COLI_MOE_F16; }
+inline bool byte_type(int type) { return type == COLI_MOE_INT8 || type == COLI_MOE_E4M3; }
+
+__device__ __forceinline__ float from_bf16(uint32_t low16) { return __uint_as_float(low16 << 16); }
+
+// Round to nearest, ties to even; a NaN keeps its sign and stays a NaN.
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ uint16_t to_f16(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+
+// Element i of an array of 16- or 32-bit floats.
+__device__ __forceinline__ float load1(const void *base, int type, int64_t i) {
+  if (type == COLI_MOE_F32) return static_cast<const float *>(base)[i];
+  const uint16_t u = static_cast<const uint16_t *>(base)[i];
+  return type == COLI_MOE_BF16 ? from_bf16(u) : (float)__builtin_bit_cast(_Float16, u);
+}
+
+__device__ __forceinline__ void store1(void *base, int type, int64_t i, float v) {
+  if (type == COLI_MOE_F32)
+    static_cast<float *>(base)[i] = v;
+  else
+    static_cast<uint16_t *>(base)[i] = type == COLI_MOE_BF16 ? to_bf16(v) : to_f16(v);
+}
+
+// v = elements i .. i + 7; those at n and beyond are 0 and not read.
+__device__ __forceinline__ void load8(const void *base, int type, int64_t i, int n, float (&v)[8]) {
+  if (n >= 8) {
+    if (type == COLI_MOE_F32) {
+      __builtin_memcpy(v, static_cast<const float *>(base) + i, 32);
+      return;
+    }
+    uint32_t u[4];
+    __builtin_memcpy(u, static_cast<const uint16_t *>(base) + i, 16);
+    if (type == COLI_MOE_BF16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = from_bf16(u[j]);
+        v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = (float)__builtin_bit_cast(_Float16, (uint16_t)u[j]);
+        v[2 * j + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[j] >> 16));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? load1(base, type, i + j) : 0.0f;
+  }
+}
+
+// v rounded to the 16-bit type (as float32 values; unchanged for F32).
+__device__ __forceinline__ void round8(int type, float (&v)[8]) {
+  if (type == COLI_MOE_F32) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = type == COLI_MOE_BF16 ? from_bf16(to_bf16(v[j])) : (float)(_Float16)v[j];
+}
+
+// Elements i .. i + 7 (those below n) = v, rounded to the type.
+__device__ __forceinline__ void store8(void *base, int type, int64_t i, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    if (type == COLI_MOE_F32) {
+      __builtin_memcpy(static_cast<float *>(base) + i, v, 32);
+      return;
+    }
+    uint32_t u[4];
+    if (type == COLI_MOE_BF16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = to_bf16(v[2 * j]) | ((uint32_t)to_bf16(v[2 * j + 1]) << 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = to_f16(v[2 * j]) | ((uint32_t)to_f16(v[2 * j + 1]) << 16);
+    }
+    __builtin_memcpy(static_cast<uint16_t *>(base) + i, u, 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) store1(base, type, i + j, v[j]);
+  }
+}
+
+}  // namespace coli

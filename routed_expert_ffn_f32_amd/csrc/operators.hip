@@ -1,0 +1,107 @@
+// C ABI of the operators around the layer: argument checks, then the launch.
+#include "operators.h"
+
+#include "coli_moe.h"
+#include "element_types.h"
+#include "internal.h"
+
+namespace {
+
+bool aligned_to(const void *p, size_t a) { return p && ((uintptr_t)p % a) == 0; }
+
+// A [rows] array of rows of `cols` elements: pointer and stride usable.
+// Rows that are written must not overlap (a stride of 0 reads one row for all).
+bool rows_ok(const void *p, int type, int64_t stride, int64_t cols, int64_t rows, bool written) {
+  return aligned_to(p, coli::type_bytes(type)) && stride >= 0 && stride <= (int64_t)1 << 40 &&
+         (!written || rows <= 1 || stride >= cols);
+}
+
+}  // namespace
+
+extern "C" {
+
+int coli_moe_rmsnorm(const coli_moe_rmsnorm_t *a, void *stream) {
+  using namespace coli;
+  if (!a || a->rows < 0 || a->hidden < 1 || a->hidden > 32768 || !(a->eps >= 0.0f)) return COLI_MOE_EARG;
+  if (!float_type(a->x_type) || (!float_type(a->out_type) && !byte_type(a->out_type))) return COLI_MOE_EARG;
+  if (byte_type(a->out_type) ? a->group != 0 && a->group != 64 && a->group != 128 : a->group != 0)
+    return COLI_MOE_EARG;
+  if ((a->residual == nullptr) != (a->residual_out == nullptr)) return COLI_MOE_EARG;
+  if (a->residual && !float_type(a->residual_type)) return COLI_MOE_EARG;
+  if (a->weight && !float_type(a->weight_type)) return COLI_MOE_EARG;
+  if (a->rows == 0) return COLI_MOE_OK;
+  if (!rows_ok(a->x, a->x_type, a->x_stride, a->hidden, a->rows, false) ||
+      !rows_ok(a->out, a->out_type, a->out_stride, a->hidden, a->rows, true))
+    return COLI_MOE_EARG;
+  if (a->residual && (!rows_ok(a->residual, a->residual_type, a->residual_stride, a->hidden, a->rows, false) ||
+                      !rows_ok(a->residual_out, a->residual_type, a->residual_out_stride, a->hidden, a->rows, true)))
+    return COLI_MOE_EARG;
+  // in place is element for element, or the rows would overwrite each other's input
+  if (a->residual && a->residual == a->residual_out && a->rows > 1 && a->residual_stride != a->residual_out_stride)
+    return COLI_MOE_EARG;
+  if (a->out == a->x && (a->out_type != a->x_type || (a->rows > 1 && a->out_stride != a->x_stride)))
+    return COLI_MOE_EARG;
+  if (a->weight && !aligned_to(a->weight, type_bytes(a->weight_type))) return COLI_MOE_EARG;
+  if (byte_type(a->out_type)) {
+    const int64_t n = a->group ? (a->hidden + a->group - 1) / a->group : 1;
+    if (!rows_ok(a->scales, COLI_MOE_F32, a->scales_stride, n, a->rows, true)) return COLI_MOE_EARG;
+  }
+  return launch_rmsnorm(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? COLI_MOE_OK : COLI_MOE_EDEVICE;
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int32_t kMaxSeqs = 65536;
+
+int balance_check(const coli_moe_balance_t *a) {
+  if (!a || a->tokens < 0 || a->n_seqs < 1 || a->n_seqs > kMaxSeqs) return COLI_MOE_EARG;
+  if (a->n_experts < 1 || a->n_experts > coli::kMaxExperts || a->top_k < 1 || a->top_k > a->n_experts ||
+      a->top_k > coli::kMaxTopK)
+    return COLI_MOE_EROUTING;
+  if ((int64_t)a->tokens * a->top_k > INT32_MAX - (1 << 20)) return COLI_MOE_EARG;
+  if (a->scores != COLI_MOE_SCORES_SIGMOID && a->scores != COLI_MOE_SCORES_SOFTMAX) return COLI_MOE_EARG;
+  if (a->seq_offsets ? !aligned_to(a->seq_offsets, 4) : a->n_seqs != 1) return COLI_MOE_EARG;
+  if (a->tokens > 0 && !rows_ok(a->logits, COLI_MOE_F32, a->logits_stride, a->n_experts, a->tokens, false))
+    return COLI_MOE_EARG;
+  return COLI_MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t coli_moe_balance_workspace_bytes(int32_t tokens, int32_t n_experts, int32_t n_seqs) {
+  if (tokens < 0 || n_experts < 1 || n_experts > coli::kMaxExperts || n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
+  return coli::balance_workspace_bytes(tokens, n_experts, n_seqs);
+}
+
+int coli_moe_balance(const coli_moe_balance_t *a, float *loss, int32_t *counts, float *coef, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  const int code = balance_check(a);
+  if (code != COLI_MOE_OK) return code;
+  if (a->tokens > 0 && !aligned_to(a->idx, 4)) return COLI_MOE_EARG;
+  if (!aligned_to(loss, 4) || !aligned_to(counts, 4) || !aligned_to(coef, 4) || !aligned_to(workspace, 16))
+    return COLI_MOE_EARG;
+  if (workspace_bytes < coli::balance_workspace_bytes(a->tokens, a->n_experts, a->n_seqs)) return COLI_MOE_ECAPACITY;
+  return coli::launch_balance(*a, loss, counts, coef, static_cast<float *>(workspace),
+                              static_cast<hipStream_t>(stream)) == hipSuccess
+             ? COLI_MOE_OK
+             : COLI_MOE_EDEVICE;
+}
+
+int coli_moe_balance_grad(const coli_moe_balance_t *a, const float *coef, const float *dloss, float *dlogits,
+                          int64_t dlogits_stride, void *stream) {
+  const int code = balance_check(a);
+  if (code != COLI_MOE_OK) return code;
+  if (!aligned_to(coef, 4) || (dloss && !aligned_to(dloss, 4))) return COLI_MOE_EARG;
+  if (a->tokens == 0) return COLI_MOE_OK;
+  if (!rows_ok(dlogits, COLI_MOE_F32, dlogits_stride, a->n_experts, a->tokens, true)) return COLI_MOE_EARG;
+  return coli::launch_balance_grad(*a, coef, dloss, dlogits, dlogits_stride, static_cast<hipStream_t>(stream)) ==
+                 hipSuccess
+             ? COLI_MOE_OK
+             : COLI_MOE_EDEVICE;
+}
+
+}  // extern "C"

@@ -1,0 +1,248 @@
+"""GPU parity of coli_moe_balance and coli_moe_balance_grad against the
+formulas in 64 bits on the host, and of the gradient against differences of
+the loss.
+
+Tolerances, in units u = 2^-23 (two half steps of float32).  A score is an
+exponential (argument reduced with a two-part ln 2: at most 3 u) and for
+sigmoid a quotient (2 u, the derivative 3 u); its sum over the experts adds
+at most 14 float32 additions of positive terms (7 u), a share one division
+and one product: 14 u.  A loss adds the shares of positive weight in float32
+over the at most 4 + 8 additions a wave and its workgroup make of a chunk of
+32 tokens (6 u) and continues in float64: 22 u.  An element of the gradient is scale * slope
+* (c - m), with m a sum of 14 terms c_j p_j of any sign: its error is at most
+48 u of scale * slope * (|c| + sum |c_j| p_j)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import routed_expert_ffn_f32_amd as cm
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -23
+ALPHA = 0.01
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def make(T, E, k, seed, drop=0.1):
+    rng = np.random.default_rng(seed)
+    z = (rng.standard_normal((T, E)) * 2 + rng.standard_normal(E)).astype(np.float32)
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :k].astype(np.int32)
+    idx[rng.random((T, k)) < drop] = -1
+    return z, np.ascontiguousarray(idx), rng
+
+
+def shares(z, scores):
+    """(shares, derivative factor) of rows z in float64."""
+    z = z.astype(np.float64)
+    if scores == "softmax":
+        top = np.max(z, axis=1, keepdims=True)
+        e = np.exp(z - np.where(np.isfinite(top), top, 0.0))
+        d = e
+    else:
+        e = 1 / (1 + np.exp(-z))
+        d = e * (1 / (1 + np.exp(z)))
+    tot = e.sum(1, keepdims=True)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        return np.where(tot > 0, e / tot, 0.0), np.where(tot > 0, d / tot, 0.0)
+
+
+def reference(z, idx, off, mask, scores, alpha, dloss):
+    """loss, counts, coef, gradient (NaN in rows of no sequence) and the gradient's error unit."""
+    (T, E), S = z.shape, len(off) - 1
+    loss, counts, coef = np.zeros(S), np.zeros((S, E), np.int64), np.zeros((S, E))
+    d, unit = np.full((T, E), np.nan), np.zeros((T, E))
+    for s in range(S):
+        rows = np.arange(off[s], off[s + 1])
+        d[rows] = 0.0
+        rows = rows[mask[rows]]
+        ids = idx[rows]
+        ids = ids[(ids >= 0) & (ids < E)]
+        counts[s] = np.bincount(ids, minlength=E)
+        if len(rows) == 0:
+            continue
+        p, slope = shares(z[rows], scores)
+        if len(ids):
+            coef[s] = alpha / len(rows) * (E * counts[s] / len(ids) - 1)
+            loss[s] = alpha * np.sum(E * counts[s] / len(ids) * p.sum(0) / len(rows))
+        m = p @ coef[s]
+        d[rows] = dloss[s] * slope * (coef[s] - m[:, None])
+        unit[rows] = abs(dloss[s]) * slope * (np.abs(coef[s]) + (p @ np.abs(coef[s]))[:, None])
+    return loss, counts, coef, d, unit
+
+
+def check(dev, z, idx, off, mask, scores, dloss=None, alpha=ALPHA, tokens_per_chunk=32, stride_pad=0):
+    T, E = z.shape
+    S = len(off) - 1
+    up = np.ones(S) if dloss is None else dloss.astype(np.float64)
+    loss, counts, coef, d, unit = reference(z, idx, off, np.ones(T, bool) if mask is None else mask, scores,
+                                            float(np.float32(alpha)), up)
+    zd = torch.full((T, E + stride_pad), float("nan"), device=dev)
+    zd[:, :E] = torch.from_numpy(z)
+    zd = zd[:, :E]
+    kw = dict(scores=scores, offsets=torch.from_numpy(np.asarray(off, np.int32)).to(dev),
+              mask=None if mask is None else torch.from_numpy(mask).to(dev))
+    gl, gc, gf = cm.balance_loss(zd, torch.from_numpy(idx).to(dev), alpha, **kw)
+    out = torch.full((T, E + stride_pad), 7.0, device=dev)
+    cm.balance_grad(zd, gf, None if dloss is None else torch.from_numpy(dloss).to(dev), out=out[:, :E], **kw)
+    torch.cuda.synchronize()
+    assert np.array_equal(gc.cpu().numpy(), counts)
+    extra = max(0, tokens_per_chunk - 32) / 8  # additions of a wave beyond the four of 32 tokens
+    gl = gl.cpu().numpy().astype(np.float64)
+    assert (np.abs(gl - loss) <= (22 + extra / 2) * U * np.abs(loss)).all(), (gl, loss)
+    cmax = np.abs(coef) + alpha * 1e-30
+    assert (np.abs(gf.cpu().numpy() - coef) <= 2 * U * cmax).all()
+    g = out.cpu().numpy().astype(np.float64)
+    assert (g[:, E:] == 7.0).all()
+    g = g[:, :E]
+    none = np.isnan(d[:, 0])
+    assert (g[none] == 7.0).all(), "rows of no sequence were written"
+    err = np.abs(g[~none] - d[~none])
+    assert (err <= 48 * U * unit[~none] + 1e-37).all(), float((err / (unit[~none] + 1e-300)).max() / U)
+    return gl, gc, gf, g
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 2, 1), (2, 8, 2), (5, 63, 3), (64, 64, 8), (33, 65, 4), (31, 128, 6),
+                                   (257, 200, 8), (300, 256, 8), (100, 257, 32), (77, 512, 16)])
+def test_sizes(dev, T, E, k, scores):
+    z, idx, rng = make(T, E, k, T * 1000 + E)
+    check(dev, z, idx, [0, T], None, scores)
+    # ragged sequences (empty ones among them), masked tokens, rows before the first and behind the last
+    cuts = np.sort(rng.integers(0, T + 1, size=6))
+    check(dev, z, idx, cuts, rng.random(T) < 0.7, scores, rng.standard_normal(5).astype(np.float32), stride_pad=3)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_long_and_many_sequences(dev, scores):
+    """More tokens than the sums' largest number of workgroups takes at 32
+    each; a sequence per token; one sequence over every workgroup."""
+    z, idx, rng = make(20011, 40, 4, 1)
+    per = -(-20011 // 512)
+    check(dev, z, idx, [0, 20011], rng.random(20011) < 0.9, scores, tokens_per_chunk=per)
+    check(dev, z[:700], idx[:700], np.arange(701), None, scores)
+    check(dev, z[:700], idx[:700], np.repeat([0, 5, 5, 300, 700], 50), None, scores)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_masked_and_infinite_logits(dev, scores):
+    """Masked rows hold NaN and Inf and are not looked at; -Inf takes an
+    expert out of a token's reach; a token and a sequence with nothing left
+    give zeros; every slot dropped gives loss 0 and gradient 0."""
+    z, idx, rng = make(48, 70, 5, 9)
+    mask = rng.random(48) < 0.6
+    mask[:16] = False           # the first sequence is masked altogether
+    z[~mask] = rng.choice([np.nan, np.inf, -np.inf], size=(int((~mask).sum()), 70))
+    mask[20] = mask[21] = True
+    z[20] = -np.inf             # a token without any expert
+    z[21, 1:] = -np.inf         # and one with a single one
+    z[21, 0] = 1.5
+    z[mask] = np.where(rng.random((int(mask.sum()), 70)) < 0.2, -np.inf, z[mask])
+    z[21, 0] = 1.5
+    idx[32:] = -1               # the last sequence kept no assignment
+    idx[30, 0], idx[31, 0] = 70, 1 << 30  # not experts
+    mask[30] = mask[31] = True
+    z[30:32] = rng.standard_normal((2, 70))
+    gl, gc, gf, g = check(dev, z, idx, [0, 16, 32, 48], mask, scores)
+    assert gl[0] == 0 and gl[2] == 0 and not g[:16].any() and not g[20].any() and not g[32:].any()
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_extreme_logits(dev, scores):
+    """Logits of large magnitude overflow nothing."""
+    rng = np.random.default_rng(4)
+    z = (rng.standard_normal((40, 33)) * np.exp(rng.uniform(-3, 5, size=(40, 1)))).astype(np.float32)
+    z[0], z[1], z[2] = 3e38, -80.0, 80.0
+    z[3, :5] = [1e30, -1e30, 0, 88, -88]
+    z[4] = 0
+    idx = np.argsort(-z, axis=1)[:, :4].astype(np.int32)
+    with np.errstate(over="ignore"):
+        check(dev, z, np.ascontiguousarray(idx), [0, 11, 40], None, scores)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_gradient_against_differences(dev, scores):
+    """Central differences of the loss (counts held) in 64 bits: their own
+    error is about h^2 and 2^-53 / h of the loss."""
+    z, idx, rng = make(6, 12, 3, 3, drop=0.2)
+    off, up = [0, 4, 6], np.array([1.5, -0.5], np.float32)
+    _, counts, _, g = check(dev, z, idx, off, None, scores, up)
+    counts = counts.cpu().numpy()
+
+    def total(zz):
+        v = 0.0
+        for s in range(2):
+            p, _ = shares(zz[off[s]:off[s + 1]], scores)
+            f = 12 * counts[s] / counts[s].sum()
+            v += float(up[s]) * ALPHA * np.sum(f * p.mean(0))
+        return v
+
+    h = 1e-4
+    for t in range(6):
+        for e in range(12):
+            a, b = z.astype(np.float64), z.astype(np.float64)
+            a[t, e] += h
+            b[t, e] -= h
+            assert abs((total(a) - total(b)) / (2 * h) - g[t, e]) <= 1e-6 * ALPHA, (t, e)
+
+
+def test_default_arguments_and_repeatability(dev):
+    """No offsets, mask or upstream gradient; the same call twice gives the
+    same bits."""
+    z, idx, _ = make(5000, 256, 8, 6)
+    zd, id_ = torch.from_numpy(z).to(dev), torch.from_numpy(idx).to(dev)
+    a = cm.balance_loss(zd, id_, ALPHA)
+    b = cm.balance_loss(zd, id_, ALPHA)
+    ga, gb = cm.balance_grad(zd, a[2]), cm.balance_grad(zd, b[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip((*a, ga), (*b, gb)))
+    loss, counts, _, d, unit = reference(z, idx, [0, 5000], np.ones(5000, bool), "sigmoid", float(np.float32(ALPHA)),
+                                         [1.0])
+    assert np.array_equal(a[1].cpu().numpy(), counts)
+    assert abs(float(a[0]) - loss[0]) <= 22 * U * loss[0]
+    assert (np.abs(ga.cpu().numpy() - d) <= 48 * U * unit).all()
+
+
+def test_no_tokens(dev):
+    loss, counts, coef = cm.balance_loss(torch.empty(0, 16, device=dev), torch.empty(0, 2, dtype=torch.int32, device=dev),
+                                         ALPHA, offsets=torch.zeros(4, dtype=torch.int32, device=dev))
+    g = cm.balance_grad(torch.empty(0, 16, device=dev), coef, offsets=torch.zeros(4, dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    assert not loss.any() and not counts.any() and not coef.any() and loss.shape == (3,) and g.shape == (0, 16)
+
+
+def test_graph_replays_and_two_graphs(dev):
+    """Two captured graphs, replayed in turn with eager work between them, on
+    new inputs each time: every result is the eager one."""
+    data = [make(3000, 256, 8, 50 + i)[:2] for i in range(3)]
+    data = [(torch.from_numpy(z).to(dev), torch.from_numpy(i).to(dev)) for z, i in data]
+    off = torch.tensor([0, 1000, 1010, 2990], dtype=torch.int32, device=dev)
+    want = []
+    for z, i in data:
+        loss, counts, coef = cm.balance_loss(z, i, ALPHA, offsets=off)
+        want.append((loss, counts, coef, cm.balance_grad(z, coef, offsets=off)))
+    graphs = []
+    for _ in range(2):
+        z, i = data[0][0].clone(), data[0][1].clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            loss, counts, coef = cm.balance_loss(z, i, ALPHA, offsets=off)
+            d = cm.balance_grad(z, coef, offsets=off)
+        graphs.append((g, z, i, (loss, counts, coef, d)))
+    for rep in range(4):
+        for n, (g, z, i, out) in enumerate(graphs):
+            k = (rep + n) % 3
+            z.copy_(data[k][0])
+            i.copy_(data[k][1])
+            g.replay()
+            eager = cm.balance_loss(*data[(k + 1) % 3], ALPHA, offsets=off)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want[k])), (rep, n)
+            assert all(torch.equal(a, b) for a, b in zip(eager, want[(k + 1) % 3][:3]))

@@ -1,0 +1,102 @@
+"""The operators around the layer without a GPU: every refusal is made on the
+host before any HIP call, by the C entry points (error codes) and by the
+Python functions (ValueError), and calls with nothing to do succeed."""
+import ctypes
+
+import pytest
+
+import routed_expert_ffn_f32_amd as cm
+
+torch = pytest.importorskip("torch")
+
+A = 0x7f0000001000  # addresses that are checked but never read
+
+
+def norm_args(**kw):
+    a = dict(rows=0, hidden=64, x_type=0, residual_type=0, weight_type=0, out_type=0, group=0, eps=1e-6, x=A,
+             x_stride=64, residual=None, residual_stride=0, residual_out=None, residual_out_stride=0, weight=A,
+             out=A + 0x10000, out_stride=64, scales=None, scales_stride=0)
+    a.update(kw)
+    return cm.coli_moe_rmsnorm_t(**a)
+
+
+def norm_rc(**kw):
+    return cm.load_library().coli_moe_rmsnorm(norm_args(**kw), None)
+
+
+def test_rmsnorm_refusals():
+    assert cm.load_library().coli_moe_rmsnorm(None, None) == -4
+    assert norm_rc() == 0  # no rows: a dry run
+    for bad in (dict(rows=-1), dict(hidden=0), dict(hidden=32769), dict(eps=-1.0), dict(eps=float("nan")),
+                dict(x_type=3), dict(x_type=-1), dict(out_type=5), dict(out_type=-1), dict(group=64),
+                dict(out_type=3, group=32), dict(out_type=4, group=-64), dict(weight_type=4),
+                dict(residual=A), dict(residual_out=A), dict(residual=A, residual_out=A, residual_type=3)):
+        assert norm_rc(**bad) == -4, bad
+    two = dict(rows=2)
+    for bad in (dict(x=None), dict(out=None), dict(x=A + 2), dict(out=A + 0x10002), dict(weight=A + 1),
+                dict(x_type=1, x=A + 1), dict(out_stride=63), dict(out_stride=-64), dict(x_stride=-1),
+                dict(x_stride=1 << 41), dict(out_type=3), dict(out_type=3, scales=A + 2, scales_stride=1),
+                dict(out_type=3, scales=A, scales_stride=0),
+                dict(out_type=4, group=64, hidden=65, x_stride=65, out_stride=65, scales=A, scales_stride=1),
+                dict(residual=A, residual_stride=64, residual_out=A + 0x20000, residual_out_stride=63),
+                dict(residual=A, residual_stride=128, residual_out=A, residual_out_stride=64),
+                dict(residual=A, residual_stride=0, residual_out=A, residual_out_stride=0),
+                dict(out=A, out_type=1), dict(out=A, x_stride=128)):
+        assert norm_rc(**two, **bad) == -4, bad
+    with pytest.raises(cm.ColiMoeError) as e:
+        cm.coli_moe_rmsnorm(norm_args(hidden=0))
+    assert e.value.code == -4
+
+
+def balance_args(**kw):
+    a = dict(tokens=0, n_experts=8, top_k=2, n_seqs=1, scores=0, alpha=0.01, logits=A, logits_stride=8, idx=A,
+             seq_offsets=None, mask=None)
+    a.update(kw)
+    return cm.coli_moe_balance_t(**a)
+
+
+def balance_rc(loss=A, counts=A, coef=A, ws=A, nbytes=1 << 30, **kw):
+    return cm.load_library().coli_moe_balance(balance_args(**kw), loss, counts, coef, ws, nbytes, None)
+
+
+def grad_rc(coef=A, dloss=None, out=A, stride=8, **kw):
+    return cm.load_library().coli_moe_balance_grad(balance_args(**kw), coef, dloss, out, stride, None)
+
+
+def test_balance_refusals():
+    lib = cm.load_library()
+    assert lib.coli_moe_balance(None, A, A, A, A, 1 << 30, None) == -4
+    assert lib.coli_moe_balance_grad(None, A, None, A, 8, None) == -4
+    assert grad_rc() == 0  # no tokens
+    sizes = [(dict(tokens=-1), -4), (dict(n_seqs=0), -4), (dict(n_seqs=65537, seq_offsets=A), -4),
+             (dict(n_experts=0), -2), (dict(n_experts=513, top_k=1), -2), (dict(top_k=0), -2), (dict(top_k=9), -2),
+             (dict(n_experts=64, top_k=33), -2), (dict(tokens=1 << 30, top_k=2), -4), (dict(scores=2), -4),
+             (dict(n_seqs=2), -4), (dict(n_seqs=2, seq_offsets=A + 2), -4), (dict(tokens=4, logits=None), -4),
+             (dict(tokens=4, logits=A + 2), -4), (dict(tokens=4, logits_stride=-1), -4)]
+    for bad, code in sizes:
+        assert balance_rc(**bad) == code, bad
+        assert grad_rc(**bad) == code, bad
+    for bad in (dict(loss=None), dict(counts=None), dict(coef=None), dict(ws=None), dict(ws=A + 8), dict(loss=A + 1),
+                dict(tokens=4, idx=None), dict(tokens=4, idx=A + 1)):
+        assert balance_rc(**bad) == -4, bad
+    assert balance_rc(tokens=100, nbytes=cm.coli_moe_balance_workspace_bytes(100, 8, 1) - 1) == -1
+    for bad in (dict(coef=None), dict(tokens=4, out=None), dict(tokens=4, stride=7), dict(dloss=A + 1)):
+        assert grad_rc(**bad) == -4, bad
+    for bad in ((-1, 8, 1), (4, 0, 1), (4, 513, 1), (4, 8, 0), (4, 8, 65537)):
+        assert cm.coli_moe_balance_workspace_bytes(*bad) == 0
+    assert lib.coli_moe_last_logits(None, A, None) == -4
+
+
+def test_python_functions_refuse_host_tensors_and_wrong_shapes():
+    x = torch.zeros(2, 64)
+    with pytest.raises(ValueError, match="GPU"):
+        cm.rms_norm(x)
+    with pytest.raises(ValueError, match="2-D"):
+        cm.rms_norm(x[0])
+    with pytest.raises(ValueError, match="GPU"):
+        cm.balance_loss(x, torch.zeros(2, 2, dtype=torch.int32), 0.01)
+    with pytest.raises(ValueError, match="GPU"):
+        cm.balance_grad(x, torch.zeros(1, 64))
+    m = torch.zeros(2, 64, device="meta")
+    with pytest.raises(ValueError):
+        cm.rms_norm(m)
