@@ -541,6 +541,54 @@ typedef struct {
 int coli_moe_rmsnorm(const coli_moe_rmsnorm_t *a, void *stream);
 
 /*
+ * Dense product with its epilogue:
+ *   out[i][j] = act(sx_i sw_j sum_l x[i][l] w[j][l] + bias_j) + residual[i][j]
+ * for i < m, j < n, l < k (sx sw: 8-bit types only), or with SwiGLU, where w
+ * holds n gate rows and then n up rows (w_scale and bias likewise 2 n),
+ *   out[i][j] = silu(gate_ij) * up_ij + residual[i][j].
+ * x and w are both BF16, F16, INT8 or E4M3; 8-bit rows carry one float32
+ * scale each, the format that coli_moe_rmsnorm writes with group 0 and the
+ * layer's int8 tables use (COLI_MOE_WEIGHTS_INT8_ROW).  Sums are exact in
+ * int32 for INT8 and float32 otherwise; scales, bias, activation and residual
+ * are float32, and the result is rounded once to out_type.
+ *   ACT_GELU       v Phi(v) (erf);  ACT_GELU_TANH  its tanh form
+ *   ACT_SILU       v sigma(v);      ACT_RELU       max(v, 0)
+ * Any m and n; k a multiple of 8 (16-bit types) or 16 (8-bit types), and the
+ * rows of x and w 16-byte aligned (pointer and stride).  Nothing outside the
+ * m x n outputs is written, and rows' elements past k are not used.
+ */
+#define COLI_MOE_ACT_NONE 0
+#define COLI_MOE_ACT_RELU 1
+#define COLI_MOE_ACT_SILU 2
+#define COLI_MOE_ACT_GELU 3
+#define COLI_MOE_ACT_GELU_TANH 4
+#define COLI_MOE_ACT_SWIGLU 5
+typedef struct {
+  int32_t m;             /* rows of x, 0..2^22; 0 checks the arguments and enqueues nothing */
+  int32_t n;             /* columns of out, 1..2^22 */
+  int32_t k;             /* 8..65536 */
+  int32_t type;          /* of x and w: BF16, F16, INT8 or E4M3 */
+  int32_t out_type;      /* of out and residual: F32, BF16 or F16 */
+  int32_t bias_type;     /* F32, BF16 or F16 */
+  int32_t act;           /* COLI_MOE_ACT_* */
+  const void *x;
+  int64_t ldx;           /* elements between rows; at most 2^23 bytes */
+  const void *w;
+  int64_t ldw;
+  const float *x_scale;  /* 8-bit types: [m], else NULL */
+  const float *w_scale;  /* 8-bit types: [n] (SwiGLU [2 n]), else NULL */
+  const void *bias;      /* [n] (SwiGLU [2 n]); NULL: none */
+  const void *residual;  /* NULL: none; may be `out` itself */
+  int64_t ldr;
+  void *out;             /* no overlap with x, w, scales or bias */
+  int64_t ldo;
+} coli_moe_linear_t;
+
+/* Errors: -4 NULL or misaligned pointer, unsupported type, dimension or
+ * stride; -3 HIP launch error. */
+int coli_moe_linear(const coli_moe_linear_t *a, void *stream);
+
+/*
  * Balance of the router's choices over each of n_seqs sequences (token rows
  * seq_offsets[s] .. seq_offsets[s+1]-1).  With the valid tokens t of a
  * sequence (mask[t] != 0), V their number, n_e the kept assignments among

@@ -89,6 +89,22 @@ class coli_moe_rmsnorm_t(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("scales_stride", ctypes.c_int64)]
 
 
+COLI_MOE_ACT_NONE = 0
+COLI_MOE_ACT_RELU = 1
+COLI_MOE_ACT_SILU = 2
+COLI_MOE_ACT_GELU = 3
+COLI_MOE_ACT_GELU_TANH = 4
+COLI_MOE_ACT_SWIGLU = 5
+
+
+class coli_moe_linear_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("m", "n", "k", "type", "out_type", "bias_type", "act")] + \
+               [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("x_scale", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("ldo", ctypes.c_int64)]
+
+
 class coli_moe_balance_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "n_experts", "top_k", "n_seqs", "scores")] + \
                [("alpha", ctypes.c_float), ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
@@ -179,6 +195,8 @@ def load_library():
         L.coli_moe_test_cache_policy.restype = ctypes.c_int
         L.coli_moe_rmsnorm.argtypes = [ctypes.POINTER(coli_moe_rmsnorm_t), vp]
         L.coli_moe_rmsnorm.restype = ctypes.c_int
+        L.coli_moe_linear.argtypes = [ctypes.POINTER(coli_moe_linear_t), vp]
+        L.coli_moe_linear.restype = ctypes.c_int
         bp = ctypes.POINTER(coli_moe_balance_t)
         L.coli_moe_balance_workspace_bytes.argtypes = [i32, i32, i32]
         L.coli_moe_balance_workspace_bytes.restype = sz
@@ -405,6 +423,10 @@ def coli_moe_rmsnorm(args: coli_moe_rmsnorm_t, stream: int = 0) -> int:
     return _check(load_library().coli_moe_rmsnorm(args, stream), "coli_moe_rmsnorm")
 
 
+def coli_moe_linear(args: coli_moe_linear_t, stream: int = 0) -> int:
+    return _check(load_library().coli_moe_linear(args, stream), "coli_moe_linear")
+
+
 def coli_moe_balance_workspace_bytes(tokens: int, n_experts: int, n_seqs: int) -> int:
     return int(load_library().coli_moe_balance_workspace_bytes(int(tokens), int(n_experts), int(n_seqs)))
 
@@ -542,6 +564,65 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
                                0 if scales is None else scales.stride(0))
         _enqueue(lambda stream: coli_moe_rmsnorm(a, stream), dev)
     return out if scales is None else (out, scales)
+
+
+_ACTS = {"none": COLI_MOE_ACT_NONE, "relu": COLI_MOE_ACT_RELU, "silu": COLI_MOE_ACT_SILU, "gelu": COLI_MOE_ACT_GELU,
+         "gelu_tanh": COLI_MOE_ACT_GELU_TANH, "swiglu": COLI_MOE_ACT_SWIGLU}
+
+
+def linear(x, w, x_scale=None, w_scale=None, bias=None, act: str = "none", residual=None, out=None, out_dtype=None):
+    """act(x w^T [* x_scale w_scale] + bias) + residual for x [m, k] and w
+    [n, k] of one type (bf16, f16, int8 or float8_e4m3fn; 8 bits with float32
+    scales per row, [m] or [m, 1] and [n] or [n, 1]).  act is one of none,
+    relu, silu, gelu, gelu_tanh and swiglu; for swiglu w, w_scale and bias hold the gate rows
+    and then as many up rows, and n is half of w's rows.  The result [m, n]
+    has out_dtype (float32, bf16 or f16; default: the residual's type, else
+    x's, or bf16 for 8 bits), which is also the residual's type; out may be
+    the residual.  coli_moe_linear in include/coli_moe.h gives the formulas."""
+    import torch
+    dev = x.device
+    _matrix(x, "x", dev)
+    m, k = x.shape
+    _matrix(w, "w", dev, None, k, x.dtype)
+    code = _dtype_code(x.dtype, "x", True)
+    if act not in _ACTS:
+        raise ValueError(f"act: one of {', '.join(_ACTS)}, got {act!r}")
+    rows = w.shape[0]
+    n = rows // 2 if act == "swiglu" else rows
+    if act == "swiglu" and rows % 2:
+        raise ValueError(f"w: an even number of rows for swiglu, got {rows}")
+    if code > COLI_MOE_F16:
+        if x_scale is None or w_scale is None:
+            raise ValueError("x_scale and w_scale: 8-bit rows carry scales")
+        _vector(x_scale.flatten() if x_scale.dim() == 2 else x_scale, "x_scale", dev, m, torch.float32)
+        _vector(w_scale.flatten() if w_scale.dim() == 2 else w_scale, "w_scale", dev, rows, torch.float32)
+        if not (x_scale.is_contiguous() and w_scale.is_contiguous()):
+            raise ValueError("x_scale, w_scale: expected contiguous tensors")
+    elif x_scale is not None or w_scale is not None:
+        raise ValueError("x_scale, w_scale: only 8-bit rows carry scales")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else residual.dtype if residual is not None else \
+            torch.bfloat16 if code > COLI_MOE_F16 else x.dtype
+    ot = _dtype_code(out_dtype, "out")
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    else:
+        _matrix(out, "out", dev, m, n, out_dtype)
+    if residual is not None:
+        _matrix(residual, "residual", dev, m, n, out_dtype)
+    bt = 0
+    if bias is not None:
+        bt = _dtype_code(bias.dtype, "bias")
+        _vector(bias, "bias", dev, rows)
+    if m and n:
+        a = coli_moe_linear_t(m, n, k, code, ot, bt, _ACTS[act], x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0),
+                              None if x_scale is None else x_scale.data_ptr(),
+                              None if w_scale is None else w_scale.data_ptr(),
+                              None if bias is None else bias.data_ptr(),
+                              None if residual is None else residual.data_ptr(),
+                              0 if residual is None else residual.stride(0), out.data_ptr(), out.stride(0))
+        _enqueue(lambda stream: coli_moe_linear(a, stream), dev)
+    return out
 
 
 _SCORES = {"sigmoid": COLI_MOE_SCORES_SIGMOID, "softmax": COLI_MOE_SCORES_SOFTMAX}

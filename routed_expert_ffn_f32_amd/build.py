@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libcoli_moe.so")
 SOURCES = ["coli_moe.hip", "expert_cache.hip", "router.hip", "dispatch.hip", "expert_gemv.hip", "expert_batch.hip",
-           "expert_mfma.hip", "probes.hip", "operators.hip", "rmsnorm.hip", "balance.hip"]
+           "expert_mfma.hip", "probes.hip", "operators.hip", "rmsnorm.hip", "balance.hip",
+           "linear.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -26,6 +26,7 @@
 
 #include "coli_moe.h"
 #include "operators.h"
+#include "scalar_math.h"
 
 namespace coli {
 namespace {
@@ -43,17 +44,6 @@ __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
   return v;
-}
-
-// exp(x) for x <= 0: x = n ln 2 + r with ln 2 in two parts (n r exact enough
-// that r keeps full precision), 2^(r / ln 2) on the transcendental unit, n
-// through the exponent.  -Inf gives 0.
-__device__ __forceinline__ float exp_neg(float x) {
-  constexpr float kLog2e = 1.44269504f, kLn2Hi = 0.693359375f, kLn2Lo = -2.12194440e-4f;
-  x = fmaxf(x, -110.0f);  // below: 0 anyway (a NaN becomes 0 here; masked rows never come here)
-  const float n = rintf(x * kLog2e);
-  const float r = __builtin_fmaf(-n, kLn2Lo, __builtin_fmaf(-n, kLn2Hi, x));
-  return __builtin_ldexpf(__builtin_amdgcn_exp2f(r * kLog2e), (int)n);
 }
 
 // A token's scores: v = exp(z - max) (softmax) or sigma(z), slope = its own

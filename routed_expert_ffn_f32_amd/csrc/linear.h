@@ -1,0 +1,168 @@
+// What the kernels of coli_moe_linear share: the products of 16-byte operand
+// pieces on the matrix cores, and the epilogue.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "coli_moe.h"
+#include "element_types.h"
+#include "lds_dma.h"
+#include "scalar_math.h"
+#include "wave.h"
+
+namespace coli {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Operand types: kPieces 16-byte pieces of a row form one operand of an
+// MFMA.  The matrix cores sum over K in any order the two operands agree on,
+// so both take the same pieces of their rows and the layout within K does
+// not matter.  int8 products accumulate exactly in int32, the others in
+// float32; every type runs at the rate of its 32-byte-per-lane form (int8 and
+// e4m3 twice the 16-bit rate).
+template <int TYPE>
+struct Operand;
+
+template <>
+struct Operand<COLI_MOE_BF16> {
+  static constexpr int kPieces = 1;
+  typedef f32x16 Acc32;
+  typedef f32x4 Acc16;
+  static __device__ __forceinline__ Acc32 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc32 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a[0]), __builtin_bit_cast(bf16x8, b[0]),
+                                                   c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ Acc16 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc16 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[0]), __builtin_bit_cast(bf16x8, b[0]),
+                                                   c, 0, 0, 0);
+  }
+};
+
+template <>
+struct Operand<COLI_MOE_F16> {
+  static constexpr int kPieces = 1;
+  typedef f32x16 Acc32;
+  typedef f32x4 Acc16;
+  static __device__ __forceinline__ Acc32 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc32 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a[0]), __builtin_bit_cast(f16x8, b[0]), c,
+                                                  0, 0, 0);
+  }
+  static __device__ __forceinline__ Acc16 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc16 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a[0]), __builtin_bit_cast(f16x8, b[0]), c,
+                                                  0, 0, 0);
+  }
+};
+
+template <>
+struct Operand<COLI_MOE_INT8> {
+  static constexpr int kPieces = 1;
+  typedef i32x16 Acc32;
+  typedef i32x4 Acc16;
+  static __device__ __forceinline__ Acc32 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc32 c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a[0]), __builtin_bit_cast(i32x4, b[0]), c, 0,
+                                                 0, 0);
+  }
+  static __device__ __forceinline__ Acc16 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc16 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a[0]), __builtin_bit_cast(i32x4, b[0]), c, 0,
+                                                 0, 0);
+  }
+};
+
+// e4m3 on the 16-bit matrix cores: every code is a half exactly, so sums are
+// float32 sums.  (The 8-bit float MFMAs add each group of 8 products with
+// about 15 bits below the largest of them: measured, 2^16 + 7 * 1 within a
+// group gives 2^16, and the worst error of 64 random products was 2^-12.3 of
+// the largest.)
+template <>
+struct Operand<COLI_MOE_E4M3> {
+  static constexpr int kPieces = 1;
+  typedef f32x16 Acc32;
+  typedef f32x4 Acc16;
+  // codes 8 h .. 8 h + 7 of a piece
+  static __device__ __forceinline__ f16x8 halves(const uint4 &v, int h) {
+    const int lo = (int)(h ? v.z : v.x), hi = (int)(h ? v.w : v.y);
+    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const auto b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const auto c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const auto d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return f16x8{(_Float16)a[0], (_Float16)a[1], (_Float16)b[0], (_Float16)b[1],
+                 (_Float16)c[0], (_Float16)c[1], (_Float16)d[0], (_Float16)d[1]};
+  }
+  static __device__ __forceinline__ Acc32 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc32 c) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(halves(a[0], 0), halves(b[0], 0), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(halves(a[0], 1), halves(b[0], 1), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ Acc16 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc16 c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(a[0], 0), halves(b[0], 0), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(a[0], 1), halves(b[0], 1), c, 0, 0, 0);
+  }
+};
+
+// 16 zero bytes: where the copies past a row's end come from.
+__device__ const uint4 kZeroPiece = {0u, 0u, 0u, 0u};
+
+__device__ __forceinline__ float activate(int act, float v) {
+  switch (act) {
+    case COLI_MOE_ACT_RELU: return fmaxf(v, 0.0f);
+    case COLI_MOE_ACT_SILU: return v * sigmoid(v);
+    case COLI_MOE_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678f);
+    // tanh(u) = 2 sigma(2 u) - 1
+    case COLI_MOE_ACT_GELU_TANH: return v * sigmoid(1.59576912f * (v + 0.044715f * v * v * v));
+    default: return v;
+  }
+}
+
+// Epilogue of 8 neighbouring outputs (row m, columns n .. n + 7, those below
+// a.n stored): v = the products' sums (up: those of the up rows, SwiGLU
+// only), float32.
+__device__ __forceinline__ void finish8(const coli_moe_linear_t &a, int m, int n, float (&v)[8], float (&up)[8]) {
+  const int cnt = a.n - n;
+  if (cnt <= 0) return;
+  const bool gated = a.act == COLI_MOE_ACT_SWIGLU;
+  if (a.x_scale) {
+    const float sx = a.x_scale[m];
+    float sw[8];
+    load8(a.w_scale, COLI_MOE_F32, n, cnt, sw);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= sx * sw[j];
+    if (gated) {
+      load8(a.w_scale, COLI_MOE_F32, (int64_t)a.n + n, cnt, sw);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) up[j] *= sx * sw[j];
+    }
+  }
+  if (a.bias) {
+    float b[8];
+    load8(a.bias, a.bias_type, n, cnt, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += b[j];
+    if (gated) {
+      load8(a.bias, a.bias_type, (int64_t)a.n + n, cnt, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) up[j] += b[j];
+    }
+  }
+  if (gated) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * sigmoid(v[j]) * up[j];
+  } else if (a.act != COLI_MOE_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = activate(a.act, v[j]);
+  }
+  if (a.residual) {
+    float r[8];
+    load8(a.residual, a.out_type, (int64_t)m * a.ldr + n, cnt, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += r[j];
+  }
+  store8(a.out, a.out_type, (int64_t)m * a.ldo + n, cnt, v);
+}
+
+}  // namespace coli

@@ -1,0 +1,345 @@
+// Dense products with their epilogue (coli_moe_linear) for more than a few
+// rows: out = act(x w^T [* sx sw] + bias) + residual.
+//
+// Bound by the matrix cores: 2 m n k operations on (m + n) k elements.  A
+// workgroup computes a tile of BM x BN outputs over all of K in steps of 128
+// bytes of every row (64 16-bit or 128 8-bit elements: one whole cache line a
+// row).  Rows of x and w go straight into LDS by LDS-DMA, kStages steps deep,
+// 16-byte piece c of row r in position c ^ ((r >> 1) & 7), so that the 16
+// rows that neighbouring lanes read fall into different banks.  Each wave
+// holds MB x NB accumulators of 32 x 32; its operands for the next K piece
+// are read from LDS while the current ones are multiplied.
+//
+// K that is not a multiple of the step: the pieces of the last step that lie
+// past the rows' ends are copied from a piece of zeros.  Rows past the last
+// of x or w: the last row again, results not stored.
+//
+// SwiGLU: w holds the n gate rows and then the n up rows.  A tile takes BN/2
+// of each in alternating blocks of 32, so that a wave holds the gate and the
+// up sum of the same outputs.
+//
+// Blocks are mapped so that each XCD (hardware block b runs on XCD b mod 8)
+// works on neighbouring tiles, 8 tiles high: the rows that they share come
+// from that XCD's L2.
+#include <type_traits>
+
+#include "internal.h"
+#include "linear.h"
+#include "operators.h"
+
+namespace coli {
+namespace {
+
+constexpr int kXcds = 8;
+constexpr int kStepBytes = 128;  // of a row, per K step
+
+template <int TYPE, int MB, int NB, int WM, int WN, int STAGES, bool GATED>
+struct Tile {
+  typedef Operand<TYPE> Op;
+  typedef typename Op::Acc32 Acc;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int BM = 32 * MB * WM, BN = 32 * NB * WN;  // rows of x and of w
+  static constexpr int kOutN = GATED ? BN / 2 : BN;           // output columns
+  static constexpr int kStageBytes = (BM + BN) * kStepBytes;
+  // the epilogue's transpose: 32 rows of the wave's columns, rows padded so
+  // that the two half-waves' rows (4 apart) fall into different banks
+  static constexpr int kRowFloats = 32 * NB + 8;
+  static constexpr int kEpilogueBytes = kWaves * 32 * kRowFloats * 4;
+  static constexpr int kRing = STAGES * kStageBytes;
+  static constexpr int kLds = kRing > kEpilogueBytes ? kRing : kEpilogueBytes;
+  static_assert(kLds <= 160 * 1024, "the ring exceeds a CU's LDS");
+  static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "copies of 8 rows, as many for each wave");
+  static_assert(!GATED || NB == 2, "gate and up blocks of a wave");
+  static constexpr int kCopiesA = BM / 8 / kWaves, kCopiesB = BN / 8 / kWaves, kCopies = kCopiesA + kCopiesB;
+
+  // Where this lane's copies come from, relative to the tile's first rows.
+  struct Sources {
+    const char *x, *w, *up;  // tile's first row of x, of w (and of its up rows)
+    uint32_t xo[kCopiesA], wo[kCopiesB];
+    int64_t k_bytes;
+  };
+
+  // Copy i of a wave: rows 8 c .. 8 c + 7 of the tile's x or w rows, c = i
+  // kWaves + wave; lane l copies position l % 8 of row 8 c + l / 8.
+  static __device__ __forceinline__ uint32_t piece(int row, int lane) {
+    return (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+  }
+
+  static __device__ __forceinline__ void copy(const Sources &S, int i, int64_t at, uint32_t lds, int wave, int lane) {
+    const bool a = i < kCopiesA;
+    const int c = (a ? i : i - kCopiesA) * kWaves + wave;
+    const char *base = a ? S.x : (GATED && (c & 4)) ? S.up : S.w;
+    const uint32_t off = a ? S.xo[a ? i : 0] : S.wo[a ? 0 : i - kCopiesA];
+    const uint32_t to = lds + (uint32_t)((a ? 0 : BM * kStepBytes) + c * 8 * kStepBytes);
+    if (at + kStepBytes <= S.k_bytes) {
+      dma16(to, base + at, off);
+    } else {  // the last, partial step
+      const int row = 8 * c + (lane >> 3);
+      const bool real = at + (int64_t)piece(row, lane) < S.k_bytes;
+      dma16v(to, real ? base + at + off : reinterpret_cast<const char *>(&kZeroPiece));
+    }
+  }
+
+  static __device__ __forceinline__ void run(const coli_moe_linear_t &a, char *lds_mem) {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    // this block's tile
+    const int tiles_n = (a.n + kOutN - 1) / kOutN, tiles_m = (a.m + BM - 1) / BM, tiles = tiles_m * tiles_n;
+    const int b = blockIdx.x, xcd = b % kXcds;
+    const int t = xcd * (tiles / kXcds) + min(xcd, tiles % kXcds) + b / kXcds;
+    const int first = t / (kXcds * tiles_n) * kXcds, high = min(kXcds, tiles_m - first);
+    const int in = t - first * tiles_n;
+    const int m0 = (first + in % high) * BM, n0 = in / high * kOutN;
+
+    constexpr size_t esz = TYPE == COLI_MOE_BF16 || TYPE == COLI_MOE_F16 ? 2 : 1;
+    const size_t ldx = (size_t)a.ldx * esz, ldw = (size_t)a.ldw * esz;
+    Sources S;
+    S.x = static_cast<const char *>(a.x) + (size_t)m0 * ldx;
+    S.w = static_cast<const char *>(a.w) + (size_t)n0 * ldw;
+    S.up = S.w + (size_t)a.n * ldw;
+    S.k_bytes = (int64_t)a.k * esz;
+#pragma unroll
+    for (int i = 0; i < kCopiesA; ++i) {
+      const int row = 8 * (i * kWaves + wave) + (lane >> 3);
+      S.xo[i] = (uint32_t)(min(row, a.m - 1 - m0) * ldx) + piece(row, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kCopiesB; ++i) {
+      const int row = 8 * (i * kWaves + wave) + (lane >> 3);
+      const int col = GATED ? (row >> 6) * 32 + (row & 31) : row;  // output column of the row
+      S.wo[i] = (uint32_t)(min(col, a.n - 1 - n0) * ldw) + piece(row, lane);
+    }
+
+    const uint32_t lds = lds_addr(lds_mem);
+    const int G = (int)((S.k_bytes + kStepBytes - 1) / kStepBytes);
+    Acc acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = Acc{};
+
+    if constexpr (kWaves == 8)
+      alternate(S, G, lds, lds_mem, wm, wn, wave, lane, acc);
+    else
+      together(S, G, lds, lds_mem, wm, wn, wave, lane, acc);
+    block_barrier();  // the ring is free
+    epilogue(a, m0, n0, wm, wn, wave, lane, acc, reinterpret_cast<float *>(lds_mem));
+  }
+
+  // Every wave reads and multiplies at its own pace, one barrier a step; other
+  // workgroups of the CU fill the gaps.
+  static __device__ __forceinline__ void together(const Sources &S, int G, uint32_t lds, const char *lds_mem, int wm,
+                                                  int wn, int wave, int lane, Acc (&acc)[MB][NB]) {
+    for (int g = 0; g < STAGES - 1 && g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) copy(S, i, (int64_t)g * kStepBytes, lds + g * kStageBytes, wave, lane);
+
+    int slot = 0, fill = STAGES - 1;  // slots of the step to compute and of the step to copy
+    for (int g = 0; g < G; ++g) {
+      // this wave's copies of step g have arrived; then every wave's have,
+      // and every wave is done with the slot to be filled
+      if (STAGES > 2 && g + STAGES - 2 < G)
+        dma_wait<kCopies *(STAGES - 2)>();
+      else
+        dma_wait<0>();
+      block_barrier();
+      const bool more = g + STAGES - 1 < G;
+      const int64_t at = (int64_t)(g + STAGES - 1) * kStepBytes;
+      compute(lds_mem + slot * kStageBytes, wm, wn, lane, acc, [&](int i) {
+        if (more) copy(S, i, at, lds + fill * kStageBytes, wave, lane);
+      });
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+      fill = fill + 1 == STAGES ? 0 : fill + 1;
+    }
+  }
+
+  // Two groups of four waves, one of each on every SIMD, take turns: while one
+  // group's waves multiply, the other's read their next operands (half a K
+  // step) from LDS and issue copies; a barrier ends each turn.  With the
+  // turns of a step numbered 4 g .. 4 g + 3, group 0 reads in turns 4 g and
+  // 4 g + 2 and multiplies in the other two; group 1 does the same one turn
+  // later.  Step g - 1's slot was last read in turn 4 g - 1 (group 1), so step
+  // g + 1 is copied into it from turn 4 g (group 0) and 4 g + 1 (group 1) on;
+  // both groups' copies are awaited before the barrier that ends turn 4 g + 3,
+  // behind which turn 4 g + 4 reads them.
+  static __device__ __forceinline__ void alternate(const Sources &S, int G, uint32_t lds, const char *lds_mem, int wm,
+                                                   int wn, int wave, int lane, Acc (&acc)[MB][NB]) {
+    static_assert(STAGES == 2, "one step computed, one copied");
+    const bool second = wave >= 4;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy(S, i, 0, lds, wave, lane);
+    dma_wait<0>();
+    turn();
+    if (second) turn();
+    for (int g = 0; g < G; ++g) {
+      const char *stage = lds_mem + (g & 1) * kStageBytes;
+      const bool more = g + 1 < G;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 af[MB][2], bf[NB][2];
+        fetch_half(stage, wm, wn, lane, h, af, bf);
+        if (h == 0 && more) {
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i)
+            copy(S, i, (int64_t)(g + 1) * kStepBytes, lds + ((g + 1) & 1) * kStageBytes, wave, lane);
+        }
+        if (h == 1 && second) dma_wait<0>();
+        lds_wait();
+        turn();
+        __builtin_amdgcn_s_setprio(1);
+        multiply_half(af, bf, acc);
+        __builtin_amdgcn_s_setprio(0);
+        if (h == 1 && !second) dma_wait<0>();
+        turn();
+      }
+    }
+    if (!second) turn();
+  }
+
+  static __device__ __forceinline__ void turn() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  static __device__ __forceinline__ void lds_wait() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+
+  // This lane's operands of half h of a step: 2 pieces of each of its rows.
+  static __device__ __forceinline__ void fetch_half(const char *stage, int wm, int wn, int lane, int h,
+                                                    uint4 (&af)[MB][2], uint4 (&bf)[NB][2]) {
+    const int nl = lane & 31, half = lane >> 5, swz = (nl >> 1) & 7;
+    const char *A = stage + (wm * MB * 32 + nl) * kStepBytes;
+    const char *B = stage + (BM + wn * NB * 32 + nl) * kStepBytes;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int pos = ((4 * half + 2 * h + p) ^ swz) * 16;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) bf[nb][p] = *reinterpret_cast<const uint4 *>(B + nb * 32 * kStepBytes + pos);
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) af[mb][p] = *reinterpret_cast<const uint4 *>(A + mb * 32 * kStepBytes + pos);
+    }
+  }
+
+  static __device__ __forceinline__ void multiply_half(const uint4 (&af)[MB][2], const uint4 (&bf)[NB][2],
+                                                       Acc (&acc)[MB][NB]) {
+    if constexpr (Op::kPieces == 2) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = Op::mma(af[mb], bf[nb], acc[mb][nb]);
+    } else {
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const uint4 a[1] = {af[mb][p]}, b[1] = {bf[nb][p]};
+            acc[mb][nb] = Op::mma(a, b, acc[mb][nb]);
+          }
+    }
+  }
+
+  // One K step; copies are issued between the products.
+  template <class Copy>
+  static __device__ __forceinline__ void compute(const char *stage, int wm, int wn, int lane, Acc (&acc)[MB][NB],
+                                                 const Copy &copy_one) {
+    constexpr int P = Op::kPieces, kJ = 4 / P;  // operand groups of the step; a half-wave holds half the pieces
+    const int nl = lane & 31, half = lane >> 5, swz = (nl >> 1) & 7;
+    const char *A = stage + (wm * MB * 32 + nl) * kStepBytes;
+    const char *B = stage + (BM + wn * NB * 32 + nl) * kStepBytes;
+    uint4 af[2][MB][P], bf[2][NB][P];
+    auto fetch = [&](int buf, int j) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int pos = ((4 * half + j * P + p) ^ swz) * 16;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          bf[buf][nb][p] = *reinterpret_cast<const uint4 *>(B + nb * 32 * kStepBytes + pos);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+          af[buf][mb][p] = *reinterpret_cast<const uint4 *>(A + mb * 32 * kStepBytes + pos);
+      }
+    };
+    fetch(0, 0);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      if (j + 1 < kJ) fetch((j + 1) & 1, j + 1);
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = Op::mma(af[j & 1][mb], bf[j & 1][nb], acc[mb][nb]);
+#pragma unroll
+      for (int i = j * kCopies / kJ; i < (j + 1) * kCopies / kJ; ++i) copy_one(i);
+    }
+  }
+
+  // Accumulators -> LDS (each wave its own rows) -> 8 neighbouring outputs a
+  // thread.  Register i of a 32 x 32 block is row 8 (i / 4) + 4 half + i % 4,
+  // the lane's column is lane % 32.
+  static __device__ __forceinline__ void epilogue(const coli_moe_linear_t &a, int m0, int n0, int wm, int wn, int wave,
+                                                  int lane, const Acc (&acc)[MB][NB], float *lds) {
+    float *mine = lds + wave * 32 * kRowFloats;
+    constexpr int kCols = GATED ? 32 : 32 * NB, kPerRow = kCols / 8, kRows = 64 / kPerRow;
+    const int nl = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const int row0 = m0 + (wm * MB + mb) * 32;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          mine[(8 * (i >> 2) + 4 * half + (i & 3)) * kRowFloats + 32 * nb + nl] = (float)acc[mb][nb][i];
+      const int c = lane % kPerRow * 8, n = n0 + wn * kCols + c;
+#pragma unroll
+      for (int r = lane / kPerRow; r < 32; r += kRows) {
+        if (row0 + r >= a.m) break;
+        float v[8], up[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] = mine[r * kRowFloats + c + j];
+          up[j] = GATED ? mine[r * kRowFloats + 32 + c + j] : 0.0f;
+        }
+        finish8(a, row0 + r, n, v, up);
+      }
+    }
+  }
+};
+
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void linear_tile_kernel(coli_moe_linear_t a) {
+  __shared__ __attribute__((aligned(16))) char lds[T::kLds];
+  T::run(a, lds);
+}
+
+template <int TYPE, int MB, int NB, int WM, int WN, int STAGES>
+hipError_t launch_tiles(const coli_moe_linear_t &a, hipStream_t s) {
+  auto go = [&](auto gated) -> hipError_t {
+    typedef Tile<TYPE, MB, NB, WM, WN, STAGES, decltype(gated)::value> T;
+    const int64_t tiles = (int64_t)((a.m + T::BM - 1) / T::BM) * ((a.n + T::kOutN - 1) / T::kOutN);
+    return launch(linear_tile_kernel<T>, dim3((uint32_t)tiles), dim3(T::kThreads), 0, s, a);
+  };
+  return a.act == COLI_MOE_ACT_SWIGLU ? go(std::true_type()) : go(std::false_type());
+}
+
+template <int TYPE>
+hipError_t launch_type(const coli_moe_linear_t &a, hipStream_t s) {
+  const int64_t wn = a.act == COLI_MOE_ACT_SWIGLU ? 2 * (int64_t)a.n : a.n;
+  if ((int64_t)((a.m + 255) / 256) * ((wn + 255) / 256) >= 192) return launch_tiles<TYPE, 4, 2, 2, 4, 2>(a, s);
+  return launch_tiles<TYPE, 2, 2, 2, 2, 4>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_linear(const coli_moe_linear_t &a, hipStream_t s) {
+  switch (a.type) {
+    case COLI_MOE_BF16: return launch_type<COLI_MOE_BF16>(a, s);
+    case COLI_MOE_F16: return launch_type<COLI_MOE_F16>(a, s);
+    case COLI_MOE_INT8: return launch_type<COLI_MOE_INT8>(a, s);
+    default: return launch_type<COLI_MOE_E4M3>(a, s);
+  }
+}
+
+}  // namespace coli

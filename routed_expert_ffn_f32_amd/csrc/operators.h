@@ -18,4 +18,6 @@ hipError_t launch_balance(const coli_moe_balance_t &a, float *loss, int32_t *cou
 hipError_t launch_balance_grad(const coli_moe_balance_t &a, const float *coef, const float *dloss, float *dlogits,
                                int64_t stride, hipStream_t s);  // tokens >= 1
 
+hipError_t launch_linear(const coli_moe_linear_t &a, hipStream_t s);  // m, n >= 1
+
 }  // namespace coli

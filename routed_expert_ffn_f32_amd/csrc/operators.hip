@@ -16,6 +16,11 @@ bool rows_ok(const void *p, int type, int64_t stride, int64_t cols, int64_t rows
          (!written || rows <= 1 || stride >= cols);
 }
 
+struct Rows {
+  const void *p;
+  int64_t ld, rows;
+};
+
 }  // namespace
 
 extern "C" {
@@ -47,6 +52,33 @@ int coli_moe_rmsnorm(const coli_moe_rmsnorm_t *a, void *stream) {
     if (!rows_ok(a->scales, COLI_MOE_F32, a->scales_stride, n, a->rows, true)) return COLI_MOE_EARG;
   }
   return launch_rmsnorm(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? COLI_MOE_OK : COLI_MOE_EDEVICE;
+}
+
+int coli_moe_linear(const coli_moe_linear_t *a, void *stream) {
+  using namespace coli;
+  constexpr int32_t kMaxRows = 1 << 22, kMaxK = 1 << 16;
+  constexpr int64_t kMaxRowBytes = (int64_t)1 << 23;  // a tile's row offsets are 32-bit
+  if (!a || a->m < 0 || a->m > kMaxRows || a->n < 1 || a->n > kMaxRows || a->k < 1 || a->k > kMaxK)
+    return COLI_MOE_EARG;
+  const bool bytes = byte_type(a->type);
+  if (!bytes && a->type != COLI_MOE_BF16 && a->type != COLI_MOE_F16) return COLI_MOE_EARG;
+  if (!float_type(a->out_type) || a->act < COLI_MOE_ACT_NONE || a->act > COLI_MOE_ACT_SWIGLU) return COLI_MOE_EARG;
+  if (a->bias && !float_type(a->bias_type)) return COLI_MOE_EARG;
+  const int64_t esz = (int64_t)type_bytes(a->type);
+  if (a->k * esz % 16) return COLI_MOE_EARG;
+  if (a->m == 0) return COLI_MOE_OK;
+  const int64_t wrows = a->act == COLI_MOE_ACT_SWIGLU ? 2 * (int64_t)a->n : a->n;
+  for (const auto &[p, ld, rows] : {Rows{a->x, a->ldx, a->m}, Rows{a->w, a->ldw, wrows}})
+    if (!aligned_to(p, 16) ||
+        (rows > 1 && (ld < 0 || ld > kMaxRowBytes || ld * esz > kMaxRowBytes || ld * esz % 16)))
+      return COLI_MOE_EARG;
+  if (bytes ? !aligned_to(a->x_scale, 4) || !aligned_to(a->w_scale, 4) : a->x_scale || a->w_scale)
+    return COLI_MOE_EARG;
+  if (a->bias && !aligned_to(a->bias, type_bytes(a->bias_type))) return COLI_MOE_EARG;
+  if (!rows_ok(a->out, a->out_type, a->ldo, a->n, a->m, true)) return COLI_MOE_EARG;
+  if (a->residual && !rows_ok(a->residual, a->out_type, a->ldr, a->n, a->m, false)) return COLI_MOE_EARG;
+  if (a->residual == a->out && a->m > 1 && a->ldr != a->ldo) return COLI_MOE_EARG;
+  return launch_linear(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? COLI_MOE_OK : COLI_MOE_EDEVICE;
 }
 
 }  // extern "C"

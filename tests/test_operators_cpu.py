@@ -100,3 +100,40 @@ def test_python_functions_refuse_host_tensors_and_wrong_shapes():
     m = torch.zeros(2, 64, device="meta")
     with pytest.raises(ValueError):
         cm.rms_norm(m)
+
+
+def linear_args(**kw):
+    a = dict(m=0, n=8, k=64, type=1, out_type=0, bias_type=0, act=0, x=A, ldx=64, w=A, ldw=64, x_scale=None,
+             w_scale=None, bias=None, residual=None, ldr=0, out=A, ldo=8)
+    a.update(kw)
+    return cm.coli_moe_linear_t(**a)
+
+
+def linear_rc(**kw):
+    return cm.load_library().coli_moe_linear(linear_args(**kw), None)
+
+
+def test_linear_refusals():
+    assert cm.load_library().coli_moe_linear(None, None) == -4
+    assert linear_rc() == 0  # no rows
+    for bad in (dict(m=-1), dict(m=(1 << 22) + 1), dict(n=0), dict(n=(1 << 22) + 1), dict(k=0), dict(k=65552),
+                dict(k=4), dict(k=60), dict(type=3, k=72), dict(type=4, k=8), dict(type=0), dict(type=5),
+                dict(type=-1), dict(out_type=3), dict(out_type=-1), dict(act=-1), dict(act=6),
+                dict(bias=A, bias_type=3)):
+        assert linear_rc(**bad) == -4, bad
+    for bad in (dict(x=None), dict(w=None), dict(out=None), dict(x=A + 8), dict(w=A + 2), dict(out=A + 2),
+                dict(out_type=1, out=A + 1), dict(ldx=63), dict(ldx=-64), dict(ldw=68), dict(ldx=1 << 23),
+                dict(ldw=1 << 40), dict(ldo=7), dict(bias=A + 2), dict(bias=A + 1, bias_type=1),
+                dict(residual=A + 2), dict(residual=A + 64, ldr=-1), dict(residual=A, ldr=16),
+                dict(x_scale=A), dict(w_scale=A), dict(type=3), dict(type=3, x_scale=A),
+                dict(type=4, x_scale=A, w_scale=A + 2), dict(type=3, ldx=72, x_scale=A, w_scale=A)):
+        assert linear_rc(m=2, **bad) == -4, bad
+    with pytest.raises(cm.ColiMoeError) as e:
+        cm.coli_moe_linear(linear_args(k=0))
+    assert e.value.code == -4
+
+
+def test_linear_python_refusals():
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        cm.linear(x, w)
