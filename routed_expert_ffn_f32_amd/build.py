@@ -22,7 +22,7 @@ LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libcoli_moe.so")
 SOURCES = ["coli_moe.hip", "expert_cache.hip", "router.hip", "dispatch.hip", "expert_gemv.hip", "expert_batch.hip",
            "expert_mfma.hip", "probes.hip", "operators.hip", "rmsnorm.hip", "balance.hip",
-           "linear.hip"]
+           "linear.hip", "linear_rows.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -41,15 +41,15 @@ struct Tile {
   static constexpr int BM = 32 * MB * WM, BN = 32 * NB * WN;  // rows of x and of w
   static constexpr int kOutN = GATED ? BN / 2 : BN;           // output columns
   static constexpr int kStageBytes = (BM + BN) * kStepBytes;
-  // the epilogue's transpose: 32 rows of the wave's columns, rows padded so
-  // that the two half-waves' rows (4 apart) fall into different banks
-  static constexpr int kRowFloats = 32 * NB + 8;
-  static constexpr int kEpilogueBytes = kWaves * 32 * kRowFloats * 4;
+  // the epilogue's slab: 32 rows of every wave row, padded so that the two
+  // half-waves' rows (4 apart) fall into different banks
+  static constexpr int kRowFloats = BN + 8;
+  static constexpr int kEpilogueBytes = WM * 32 * kRowFloats * 4;
   static constexpr int kRing = STAGES * kStageBytes;
   static constexpr int kLds = kRing > kEpilogueBytes ? kRing : kEpilogueBytes;
   static_assert(kLds <= 160 * 1024, "the ring exceeds a CU's LDS");
   static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "copies of 8 rows, as many for each wave");
-  static_assert(!GATED || NB == 2, "gate and up blocks of a wave");
+  static_assert(!GATED || BN % 64 == 0, "pairs of gate and up blocks");
   static constexpr int kCopiesA = BM / 8 / kWaves, kCopiesB = BN / 8 / kWaves, kCopies = kCopiesA + kCopiesB;
 
   // Where this lane's copies come from, relative to the tile's first rows.
@@ -63,6 +63,14 @@ struct Tile {
   // kWaves + wave; lane l copies position l % 8 of row 8 c + l / 8.
   static __device__ __forceinline__ uint32_t piece(int row, int lane) {
     return (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+  }
+
+  static __device__ __forceinline__ void copy_whole(const Sources &S, int i, int64_t at, uint32_t lds, int wave) {
+    const bool a = i < kCopiesA;
+    const int c = (a ? i : i - kCopiesA) * kWaves + wave;
+    const char *base = a ? S.x : (GATED && (c & 4)) ? S.up : S.w;
+    dma16(lds + (uint32_t)((a ? 0 : BM * kStepBytes) + c * 8 * kStepBytes), base + at,
+          a ? S.xo[a ? i : 0] : S.wo[a ? 0 : i - kCopiesA]);
   }
 
   static __device__ __forceinline__ void copy(const Sources &S, int i, int64_t at, uint32_t lds, int wave, int lane) {
@@ -118,12 +126,20 @@ struct Tile {
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = Acc{};
 
-    if constexpr (kWaves == 8)
-      alternate(S, G, lds, lds_mem, wm, wn, wave, lane, acc);
-    else
+    if constexpr (kWaves == 8) {
+      const int whole = (int)(S.k_bytes / kStepBytes);
+      if (whole) {
+        if (wave >= 4)
+          alternate<true>(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
+        else
+          alternate<false>(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
+      }
+      if (whole < G) remainder(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
+    } else {
       together(S, G, lds, lds_mem, wm, wn, wave, lane, acc);
+    }
     block_barrier();  // the ring is free
-    epilogue(a, m0, n0, wm, wn, wave, lane, acc, reinterpret_cast<float *>(lds_mem));
+    epilogue(a, m0, n0, wm, wn, lane, acc, reinterpret_cast<float *>(lds_mem));
   }
 
   // Every wave reads and multiplies at its own pace, one barrier a step; other
@@ -154,46 +170,78 @@ struct Tile {
   }
 
   // Two groups of four waves, one of each on every SIMD, take turns: while one
-  // group's waves multiply, the other's read their next operands (half a K
-  // step) from LDS and issue copies; a barrier ends each turn.  With the
-  // turns of a step numbered 4 g .. 4 g + 3, group 0 reads in turns 4 g and
-  // 4 g + 2 and multiplies in the other two; group 1 does the same one turn
-  // later.  Step g - 1's slot was last read in turn 4 g - 1 (group 1), so step
-  // g + 1 is copied into it from turn 4 g (group 0) and 4 g + 1 (group 1) on;
-  // both groups' copies are awaited before the barrier that ends turn 4 g + 3,
-  // behind which turn 4 g + 4 reads them.
+  // group's waves multiply, the other's read their next operands, half a K
+  // step, from LDS; a barrier ends each turn.  With the turns of step g
+  // numbered 4 g .. 4 g + 3, the first group reads in turns 4 g and 4 g + 2
+  // and multiplies in the other two; the second does the same one turn later.
+  // Step g - 1's slot was last read in turn 4 g - 1 (second group), so step
+  // g + 1 is copied into it from turn 4 g on: half of a wave's copies go out
+  // with the reads of the step's first half (turn 4 g or 4 g + 1), the others
+  // between products, in turn 4 g + 1 (first group) and 4 g (second group,
+  // with its last products of step g - 1).  Both groups await their copies
+  // before the barrier that ends turn 4 g + 3, behind which turn 4 g + 4 reads
+  // them.  (8192^3 bf16: 827 us; all copies with the reads 894 us, all between
+  // products 843 us; without the raised priority of the multiplying waves
+  // 903 us; every wave at its own pace, one barrier a step, 1100 us.)  The
+  // copies have no conditions: past the last step they fetch it again, into
+  // the slot that is not read any more (a branch a copy, between the products,
+  // cost 23%).
+  template <bool SECOND>
   static __device__ __forceinline__ void alternate(const Sources &S, int G, uint32_t lds, const char *lds_mem, int wm,
                                                    int wn, int wave, int lane, Acc (&acc)[MB][NB]) {
     static_assert(STAGES == 2, "one step computed, one copied");
-    const bool second = wave >= 4;
+    auto copy_step = [&](int g, int i) {
+      copy_whole(S, i, (int64_t)min(g, G - 1) * kStepBytes, lds + (g & 1) * kStageBytes, wave);
+    };
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy(S, i, 0, lds, wave, lane);
+    for (int i = 0; i < kCopies; ++i) copy_step(0, i);
     dma_wait<0>();
     turn();
-    if (second) turn();
+    constexpr int kInRead = kCopies / 2;  // copies issued in a read turn, the others between products
+    if (SECOND) {
+#pragma unroll
+      for (int i = kInRead; i < kCopies; ++i) copy_step(1, i);
+      turn();
+    }
     for (int g = 0; g < G; ++g) {
       const char *stage = lds_mem + (g & 1) * kStageBytes;
-      const bool more = g + 1 < G;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint4 af[MB][2], bf[NB][2];
         fetch_half(stage, wm, wn, lane, h, af, bf);
-        if (h == 0 && more) {
+        if (h == 0)
 #pragma unroll
-          for (int i = 0; i < kCopies; ++i)
-            copy(S, i, (int64_t)(g + 1) * kStepBytes, lds + ((g + 1) & 1) * kStageBytes, wave, lane);
-        }
-        if (h == 1 && second) dma_wait<0>();
+          for (int i = 0; i < kInRead; ++i) copy_step(g + 1, i);
+        if (h == 1 && SECOND) dma_wait<0>();
         lds_wait();
         turn();
         __builtin_amdgcn_s_setprio(1);
-        multiply_half(af, bf, acc);
+        multiply_half(af, bf, acc, [&](int i) {
+          if (SECOND == (h == 1) && i >= kInRead) copy_step(g + 1 + h, i);
+        });
         __builtin_amdgcn_s_setprio(0);
-        if (h == 1 && !second) dma_wait<0>();
+        if (h == 1 && !SECOND) dma_wait<0>();
         turn();
       }
     }
-    if (!second) turn();
+    if (!SECOND) turn();
+    dma_wait<0>();
+  }
+
+  // The last step of a K that is no multiple of it.
+  static __device__ __forceinline__ void remainder(const Sources &S, int G, uint32_t lds, const char *lds_mem, int wm,
+                                                   int wn, int wave, int lane, Acc (&acc)[MB][NB]) {
+    block_barrier();
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy(S, i, (int64_t)G * kStepBytes, lds, wave, lane);
+    dma_wait<0>();
+    block_barrier();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 af[MB][2], bf[NB][2];
+      fetch_half(lds_mem, wm, wn, lane, h, af, bf);
+      multiply_half(af, bf, acc, [](int) {});
+    }
   }
 
   static __device__ __forceinline__ void turn() {
@@ -222,24 +270,24 @@ struct Tile {
     }
   }
 
+  // The products of half a step, copy i of the wave's kCopies issued after an
+  // equal share of them.
+  template <class Copy>
   static __device__ __forceinline__ void multiply_half(const uint4 (&af)[MB][2], const uint4 (&bf)[NB][2],
-                                                       Acc (&acc)[MB][NB]) {
-    if constexpr (Op::kPieces == 2) {
+                                                       Acc (&acc)[MB][NB], const Copy &copy_one) {
+    constexpr int kAll = 2 * MB * NB;
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = Op::mma(af[mb], bf[nb], acc[mb][nb]);
-    } else {
+        for (int nb = 0; nb < NB; ++nb) {
+          const uint4 a[1] = {af[mb][p]}, b[1] = {bf[nb][p]};
+          acc[mb][nb] = Op::mma(a, b, acc[mb][nb]);
+          const int done = (p * MB + mb) * NB + nb;
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const uint4 a[1] = {af[mb][p]}, b[1] = {bf[nb][p]};
-            acc[mb][nb] = Op::mma(a, b, acc[mb][nb]);
-          }
-    }
+          for (int i = done * kCopies / kAll; i < (done + 1) * kCopies / kAll; ++i) copy_one(i);
+        }
   }
 
   // One K step; copies are issued between the products.
@@ -276,33 +324,35 @@ struct Tile {
     }
   }
 
-  // Accumulators -> LDS (each wave its own rows) -> 8 neighbouring outputs a
-  // thread.  Register i of a 32 x 32 block is row 8 (i / 4) + 4 half + i % 4,
-  // the lane's column is lane % 32.
-  static __device__ __forceinline__ void epilogue(const coli_moe_linear_t &a, int m0, int n0, int wm, int wn, int wave,
-                                                  int lane, const Acc (&acc)[MB][NB], float *lds) {
-    float *mine = lds + wave * 32 * kRowFloats;
-    constexpr int kCols = GATED ? 32 : 32 * NB, kPerRow = kCols / 8, kRows = 64 / kPerRow;
+  // Accumulators -> LDS -> 8 neighbouring outputs a thread, 32 rows of every
+  // wave row at a time.  Register i of a 32 x 32 block is row 8 (i / 4) +
+  // 4 half + i % 4, the lane's column is lane % 32.
+  static __device__ __forceinline__ void epilogue(const coli_moe_linear_t &a, int m0, int n0, int wm, int wn, int lane,
+                                                  const Acc (&acc)[MB][NB], float *sums) {
     const int nl = lane & 31, half = lane >> 5;
+    constexpr int kParts = kOutN / 8;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-      const int row0 = m0 + (wm * MB + mb) * 32;
+      if (mb) __syncthreads();
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          mine[(8 * (i >> 2) + 4 * half + (i & 3)) * kRowFloats + 32 * nb + nl] = (float)acc[mb][nb][i];
-      const int c = lane % kPerRow * 8, n = n0 + wn * kCols + c;
-#pragma unroll
-      for (int r = lane / kPerRow; r < 32; r += kRows) {
-        if (row0 + r >= a.m) break;
+          sums[(wm * 32 + 8 * (i >> 2) + 4 * half + (i & 3)) * kRowFloats + 32 * (wn * NB + nb) + nl] =
+              (float)acc[mb][nb][i];
+      __syncthreads();
+      for (int q = threadIdx.x; q < WM * 32 * kParts; q += kThreads) {
+        const int r = q / kParts, c = q % kParts * 8;  // row of the slab, output column of the tile
+        const int m = m0 + ((r >> 5) * MB + mb) * 32 + (r & 31);
+        if (m >= a.m) continue;
+        const float *from = sums + r * kRowFloats + (GATED ? (c >> 5) * 64 + (c & 31) : c);
         float v[8], up[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          v[j] = mine[r * kRowFloats + c + j];
-          up[j] = GATED ? mine[r * kRowFloats + 32 + c + j] : 0.0f;
+          v[j] = from[j];
+          up[j] = GATED ? from[32 + j] : 0.0f;
         }
-        finish8(a, row0 + r, n, v, up);
+        finish8(a, m, n0 + c, v, up);
       }
     }
   }
@@ -324,21 +374,65 @@ hipError_t launch_tiles(const coli_moe_linear_t &a, hipStream_t s) {
   return a.act == COLI_MOE_ACT_SWIGLU ? go(std::true_type()) : go(std::false_type());
 }
 
+// The shapes a product of more than kLinearRowsMax rows can take, with what
+// they cost: microseconds measured at 12288 bytes of K (6144 bf16 elements;
+// n = 6144, m from 64 to 4096, three sets of operands in turn) for up to one
+// block a CU, and for a full chip where two blocks share a CU.
+struct Shape {
+  int bm, bn;         // rows of x and of w of a block
+  int per_cu;         // blocks a CU holds
+  int one, full;      // cost with at most one block a CU, and with per_cu of them
+};
+constexpr int kCus = 256;
+constexpr Shape kShapes[] = {
+    {64, 32, 1, 17, 17},     // linear_rows: m = 64 in 18 us, 128 in 34, 256 in 50
+    {64, 64, 1, 28, 28},     // linear_rows: m = 128 in 29 us, 256 in 55
+    {128, 64, 2, 53, 64},    // four waves: m = 256 in 53 us, 512 in 64, 1024 in 125
+    {128, 128, 2, 63, 110},  // eight waves: m = 512 in 64 us, 1024 in 111, 2048 in 207
+    {256, 192, 1, 137, 137}, // m = 2048 in 142 us, 4096 in 274 (two full rounds)
+    {256, 256, 1, 150, 150}, // m = 2048 in 150 us, 4096 in 300 (two rounds, the second half empty)
+};
+
+// The shape with the least cost: rounds of blocks over the CUs times the
+// cost of a round.  Large blocks read less per product, small ones leave
+// fewer CUs idle.
+int pick_shape(int64_t m, int64_t wrows) {
+  int best = 0;
+  int64_t least = 0;
+  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
+    const Shape &s = kShapes[i];
+    const int64_t blocks = ((m + s.bm - 1) / s.bm) * ((wrows + s.bn - 1) / s.bn);
+    const int64_t slots = (int64_t)kCus * s.per_cu, rest = blocks % slots;
+    const int64_t cost = blocks / slots * s.full + (rest == 0 ? 0 : rest <= kCus ? s.one : s.full);
+    if (i == 0 || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  return best;
+}
+
 template <int TYPE>
-hipError_t launch_type(const coli_moe_linear_t &a, hipStream_t s) {
-  const int64_t wn = a.act == COLI_MOE_ACT_SWIGLU ? 2 * (int64_t)a.n : a.n;
-  if ((int64_t)((a.m + 255) / 256) * ((wn + 255) / 256) >= 192) return launch_tiles<TYPE, 4, 2, 2, 4, 2>(a, s);
-  return launch_tiles<TYPE, 2, 2, 2, 2, 4>(a, s);
+hipError_t launch_type(const coli_moe_linear_t &a, int shape, hipStream_t s) {
+  switch (shape) {
+    case 2: return launch_tiles<TYPE, 2, 1, 2, 2, 3>(a, s);
+    case 3: return launch_tiles<TYPE, 2, 1, 2, 4, 2>(a, s);
+    case 4: return launch_tiles<TYPE, 2, 3, 4, 2, 2>(a, s);
+    default: return launch_tiles<TYPE, 4, 2, 2, 4, 2>(a, s);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_linear(const coli_moe_linear_t &a, hipStream_t s) {
+  if (a.m <= kLinearRowsMax) return launch_linear_rows(a, 32, s);
+  const int shape = pick_shape(a.m, a.act == COLI_MOE_ACT_SWIGLU ? 2 * (int64_t)a.n : a.n);
+  if (shape < 2) return launch_linear_rows(a, kShapes[shape].bn, s);
   switch (a.type) {
-    case COLI_MOE_BF16: return launch_type<COLI_MOE_BF16>(a, s);
-    case COLI_MOE_F16: return launch_type<COLI_MOE_F16>(a, s);
-    case COLI_MOE_INT8: return launch_type<COLI_MOE_INT8>(a, s);
-    default: return launch_type<COLI_MOE_E4M3>(a, s);
+    case COLI_MOE_BF16: return launch_type<COLI_MOE_BF16>(a, shape, s);
+    case COLI_MOE_F16: return launch_type<COLI_MOE_F16>(a, shape, s);
+    case COLI_MOE_INT8: return launch_type<COLI_MOE_INT8>(a, shape, s);
+    default: return launch_type<COLI_MOE_E4M3>(a, shape, s);
   }
 }
 

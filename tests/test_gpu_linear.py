@@ -102,9 +102,31 @@ def test_sizes_exactly(dev, m, n, k, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("m,n,k", [(3500, 3600, 136), (4096, 3585, 64), (3329, 4000, 520)])
-def test_many_tiles_exactly(dev, m, n, k, kind):
+@pytest.mark.parametrize("m,n,k", [(129, 8200, 136), (500, 4096, 328), (700, 5000, 200), (4000, 6100, 136),
+                                   (3500, 3600, 264), (3329, 4000, 520), (4096, 3585, 64), (300, 5000, 8)])
+def test_every_block_shape_exactly(dev, m, n, k, kind):
+    """Sizes that the choice of blocks sends to each of its shapes beyond the
+    smallest; K of less than a step, of whole steps, and with a rest."""
     exact_case(dev, m, n, k, kind, "none", m, bias=True, residual=True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n,k", [(1, 5, 64), (7, 100, 520), (30, 129, 264), (60, 300, 136), (129, 4099, 136),
+                                   (500, 2049, 72), (700, 2500, 200), (4000, 3050, 72), (3500, 1801, 136)])
+def test_swiglu_on_every_block_shape(dev, m, n, k, kind):
+    """Gate and up sums are exact integers here, so only the activation's own
+    8 u |gate up| and the product's 2 u remain."""
+    g = torch.Generator().manual_seed(n)
+    k = step(k, kind)
+    x, w = ints((m, k), 2, g), ints((2 * n, k), 2, g)
+    sx, sw = torch.full((m,), 0.25), torch.full((2 * n,), 0.125)
+    kw = dict(x_scale=sx.to(dev), w_scale=sw.to(dev)) if kind in (I8, E4) else {}
+    v = (x.float() @ w.float().t()).double() * (0.03125 if kw else 1.0)
+    gate, up = v[:, :n], v[:, n:]
+    want = gate / (1 + torch.exp(-gate)) * up
+    got = cm.linear(padded(x, kind, dev, 0), padded(w, kind, dev, 0), act="swiglu", out_dtype=F32, **kw)
+    err = (got.cpu().double() - want).abs()
+    assert (err <= 10 * U * (gate * up).abs()).all(), float((err / ((gate * up).abs() + 1e-30)).max() / U)
 
 
 @pytest.mark.parametrize("out", [BF16, F16])
