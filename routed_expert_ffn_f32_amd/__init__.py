@@ -470,14 +470,16 @@ def _dtype_code(dtype, what: str, bytes_too: bool = False) -> int:
 
 
 def _matrix(t, what: str, device, rows=None, cols=None, dtype=None):
-    """Checks a 2-D device tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows, got shape {tuple(t.shape)}, "
-                         f"strides {tuple(t.stride())}")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
-    _on(t, what, device, dtype)
-    return t
+    """Checks a 2-D device tensor whose rows are contiguous; its row stride."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows, got shape {tuple(shape)}, "
+                         f"strides {tuple(strides)}")
+    if (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{what}: expected shape {(rows, cols)}, got {tuple(shape)}")
+    if t.device != device or (dtype is not None and t.dtype != dtype):
+        _refuse_place(t, what, device, dtype)
+    return strides[0]
 
 
 def _vector(t, what: str, device, n: int, dtype=None):
@@ -485,26 +487,45 @@ def _vector(t, what: str, device, n: int, dtype=None):
     if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous elements, got shape {tuple(t.shape)}, "
                          f"strides {tuple(t.stride())}")
-    _on(t, what, device, dtype)
-    return t
+    if t.device != device or (dtype is not None and t.dtype != dtype):
+        _refuse_place(t, what, device, dtype)
 
 
-def _on(t, what: str, device, dtype):
-    if t.device != device or t.device.type != "cuda":
-        raise ValueError(f"{what}: expected a tensor on {device if device.type == 'cuda' else 'the GPU'}, got one on "
-                         f"{t.device}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-
-
-def _enqueue(call, device):
-    """call(stream) with `device` current."""
+def _scale_vector(t, what: str, device, n: int):
+    """Checks contiguous float32 scales [n] or [n, 1]."""
     import torch
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        return call(stream)
-    with torch.cuda.device(device):
-        return call(stream)
+    if t.shape not in ((n,), (n, 1)) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous scales, got shape {tuple(t.shape)}, "
+                         f"strides {tuple(t.stride())}")
+    if t.device != device or t.dtype != torch.float32:
+        _refuse_place(t, what, device, torch.float32)
+
+
+def _refuse_place(t, what: str, device, dtype):
+    if t.device != device:
+        raise ValueError(f"{what}: expected a tensor on {device}, got one on {t.device}")
+    raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+
+
+def _gpu(t, what: str):
+    """The tensor's device, which has to be a GPU."""
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError(f"{what}: expected a tensor on the GPU, got one on {device}")
+    return device
+
+
+def _enqueue(entry: str, device, *args) -> None:
+    """Calls a C entry point, whose last argument is the stream, with `device`
+    current and on its current stream."""
+    import torch
+    index = device.index
+    call = getattr(load_library(), entry)
+    if torch.cuda.current_device() == index:
+        _check(call(*args, torch._C._cuda_getCurrentRawStream(index)), entry)
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, torch._C._cuda_getCurrentRawStream(index)), entry)
 
 
 def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None, out=None, scales=None,
@@ -518,51 +539,48 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
     [rows, ceil(hidden / group)] for a group of 64 or 128 columns.
     coli_moe_rmsnorm in include/coli_moe.h gives the formulas."""
     import torch
-    dev = x.device
-    _matrix(x, "x", dev)
+    dev = _gpu(x, "x")
+    ldx = _matrix(x, "x", dev)
     rows, hidden = x.shape
     if out_dtype is None:
         out_dtype = x.dtype if out is None else out.dtype
     xt, ot = _dtype_code(x.dtype, "x"), _dtype_code(out_dtype, "out", True)
     if out is None:
-        out = torch.empty((rows, hidden), dtype=out_dtype, device=dev)
+        out, ldo = torch.empty((rows, hidden), dtype=out_dtype, device=dev), hidden
     else:
-        _matrix(out, "out", dev, rows, hidden, out_dtype)
-    rt = wt = 0
+        ldo = _matrix(out, "out", dev, rows, hidden, out_dtype)
+    rt = wt = ldr = ldro = lds = 0
+    rp = rop = wp = sp = None
     if residual is not None:
         rt = _dtype_code(residual.dtype, "residual")
-        _matrix(residual, "residual", dev, rows, hidden)
-        if residual_out is None:
-            residual_out = residual
-        else:
-            _matrix(residual_out, "residual_out", dev, rows, hidden, residual.dtype)
+        ldr = ldro = _matrix(residual, "residual", dev, rows, hidden)
+        rp = rop = residual.data_ptr()
+        if residual_out is not None:
+            ldro = _matrix(residual_out, "residual_out", dev, rows, hidden, residual.dtype)
+            rop = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if weight is not None:
         wt = _dtype_code(weight.dtype, "weight")
         _vector(weight, "weight", dev, hidden)
+        wp = weight.data_ptr()
     if ot > COLI_MOE_F16:
         if group not in (0, 64, 128):
             raise ValueError(f"group: 0, 64 or 128, got {group}")
         n = -(-hidden // group) if group else 1
         if scales is None:
-            scales = torch.empty((rows, n), dtype=torch.float32, device=dev)
+            scales, lds = torch.empty((rows, n), dtype=torch.float32, device=dev), n
         else:
-            _matrix(scales, "scales", dev, rows, n, torch.float32)
+            lds = _matrix(scales, "scales", dev, rows, n, torch.float32)
+        sp = scales.data_ptr()
     else:
         if scales is not None:
             raise ValueError("scales belong to 8-bit outputs")
         group = 0
     if rows and hidden:
-        a = coli_moe_rmsnorm_t(rows, hidden, xt, rt, wt, ot, group, eps, x.data_ptr(), x.stride(0),
-                               None if residual is None else residual.data_ptr(),
-                               0 if residual is None else residual.stride(0),
-                               None if residual is None else residual_out.data_ptr(),
-                               0 if residual is None else residual_out.stride(0),
-                               None if weight is None else weight.data_ptr(), out.data_ptr(), out.stride(0),
-                               None if scales is None else scales.data_ptr(),
-                               0 if scales is None else scales.stride(0))
-        _enqueue(lambda stream: coli_moe_rmsnorm(a, stream), dev)
+        _enqueue("coli_moe_rmsnorm", dev,
+                 coli_moe_rmsnorm_t(rows, hidden, xt, rt, wt, ot, group, eps, x.data_ptr(), ldx, rp, ldr, rop, ldro,
+                                    wp, out.data_ptr(), ldo, sp, lds))
     return out if scales is None else (out, scales)
 
 
@@ -574,30 +592,33 @@ def linear(x, w, x_scale=None, w_scale=None, bias=None, act: str = "none", resid
     """act(x w^T [* x_scale w_scale] + bias) + residual for x [m, k] and w
     [n, k] of one type (bf16, f16, int8 or float8_e4m3fn; 8 bits with float32
     scales per row, [m] or [m, 1] and [n] or [n, 1]).  act is one of none,
-    relu, silu, gelu, gelu_tanh and swiglu; for swiglu w, w_scale and bias hold the gate rows
-    and then as many up rows, and n is half of w's rows.  The result [m, n]
-    has out_dtype (float32, bf16 or f16; default: the residual's type, else
-    x's, or bf16 for 8 bits), which is also the residual's type; out may be
-    the residual.  coli_moe_linear in include/coli_moe.h gives the formulas."""
+    relu, silu, gelu, gelu_tanh and swiglu; for swiglu w, w_scale and bias
+    hold the gate rows and then as many up rows, and n is half of w's rows.
+    The result [m, n] has out_dtype (float32, bf16 or f16; default: the
+    residual's type, else x's, or bf16 for 8 bits), which is also the
+    residual's type; out may be the residual.  coli_moe_linear in
+    include/coli_moe.h gives the formulas."""
     import torch
-    dev = x.device
-    _matrix(x, "x", dev)
+    dev = _gpu(x, "x")
+    ldx = _matrix(x, "x", dev)
     m, k = x.shape
-    _matrix(w, "w", dev, None, k, x.dtype)
+    ldw = _matrix(w, "w", dev, None, k, x.dtype)
     code = _dtype_code(x.dtype, "x", True)
     if act not in _ACTS:
         raise ValueError(f"act: one of {', '.join(_ACTS)}, got {act!r}")
-    rows = w.shape[0]
-    n = rows // 2 if act == "swiglu" else rows
-    if act == "swiglu" and rows % 2:
-        raise ValueError(f"w: an even number of rows for swiglu, got {rows}")
+    n = rows = w.shape[0]
+    if act == "swiglu":
+        if rows % 2:
+            raise ValueError(f"w: an even number of rows for swiglu, got {rows}")
+        n = rows // 2
+    sxp = swp = bp = rp = None
+    bt = ldr = 0
     if code > COLI_MOE_F16:
         if x_scale is None or w_scale is None:
             raise ValueError("x_scale and w_scale: 8-bit rows carry scales")
-        _vector(x_scale.flatten() if x_scale.dim() == 2 else x_scale, "x_scale", dev, m, torch.float32)
-        _vector(w_scale.flatten() if w_scale.dim() == 2 else w_scale, "w_scale", dev, rows, torch.float32)
-        if not (x_scale.is_contiguous() and w_scale.is_contiguous()):
-            raise ValueError("x_scale, w_scale: expected contiguous tensors")
+        _scale_vector(x_scale, "x_scale", dev, m)
+        _scale_vector(w_scale, "w_scale", dev, rows)
+        sxp, swp = x_scale.data_ptr(), w_scale.data_ptr()
     elif x_scale is not None or w_scale is not None:
         raise ValueError("x_scale, w_scale: only 8-bit rows carry scales")
     if out_dtype is None:
@@ -605,50 +626,51 @@ def linear(x, w, x_scale=None, w_scale=None, bias=None, act: str = "none", resid
             torch.bfloat16 if code > COLI_MOE_F16 else x.dtype
     ot = _dtype_code(out_dtype, "out")
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+        out, ldo = torch.empty((m, n), dtype=out_dtype, device=dev), n
     else:
-        _matrix(out, "out", dev, m, n, out_dtype)
+        ldo = _matrix(out, "out", dev, m, n, out_dtype)
     if residual is not None:
-        _matrix(residual, "residual", dev, m, n, out_dtype)
-    bt = 0
+        ldr = _matrix(residual, "residual", dev, m, n, out_dtype)
+        rp = residual.data_ptr()
     if bias is not None:
         bt = _dtype_code(bias.dtype, "bias")
         _vector(bias, "bias", dev, rows)
+        bp = bias.data_ptr()
     if m and n:
-        a = coli_moe_linear_t(m, n, k, code, ot, bt, _ACTS[act], x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0),
-                              None if x_scale is None else x_scale.data_ptr(),
-                              None if w_scale is None else w_scale.data_ptr(),
-                              None if bias is None else bias.data_ptr(),
-                              None if residual is None else residual.data_ptr(),
-                              0 if residual is None else residual.stride(0), out.data_ptr(), out.stride(0))
-        _enqueue(lambda stream: coli_moe_linear(a, stream), dev)
+        _enqueue("coli_moe_linear", dev,
+                 coli_moe_linear_t(m, n, k, code, ot, bt, _ACTS[act], x.data_ptr(), ldx, w.data_ptr(), ldw, sxp, swp,
+                                   bp, rp, ldr, out.data_ptr(), ldo))
     return out
 
 
 _SCORES = {"sigmoid": COLI_MOE_SCORES_SIGMOID, "softmax": COLI_MOE_SCORES_SOFTMAX}
 
 
-def _balance_args(logits, idx, alpha, scores, offsets, mask, n_seqs):
+def _balance_args(logits, idx, alpha, scores, offsets, mask):
+    """(struct, device, tokens, experts, sequences) of checked arguments."""
     import torch
-    dev = logits.device
-    _matrix(logits, "logits", dev, dtype=torch.float32)
+    dev = _gpu(logits, "logits")
+    ld = _matrix(logits, "logits", dev, dtype=torch.float32)
     T, E = logits.shape
     if scores not in _SCORES:
         raise ValueError(f"scores: 'sigmoid' or 'softmax', got {scores!r}")
+    n_seqs, k, ip, op, mp = 1, 1, None, None, None
     if idx is not None:
-        _matrix(idx, "idx", dev, T, None, torch.int32)
-        if T > 1 and idx.stride(0) != idx.shape[1]:
+        if _matrix(idx, "idx", dev, T, None, torch.int32) != idx.shape[1] and T > 1:
             raise ValueError("idx: expected a contiguous tensor")
+        k, ip = idx.shape[1], idx.data_ptr()
     if offsets is not None:
+        n_seqs = offsets.numel() - 1
         _vector(offsets, "offsets", dev, n_seqs + 1, torch.int32)
+        if n_seqs < 1:
+            raise ValueError("offsets: expected the bounds of at least one sequence")
+        op = offsets.data_ptr()
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
         _vector(mask, "mask", dev, T)
-    return coli_moe_balance_t(T, E, 1 if idx is None else idx.shape[1], n_seqs, _SCORES[scores], alpha,
-                              logits.data_ptr(), logits.stride(0), None if idx is None else idx.data_ptr(),
-                              None if offsets is None else offsets.data_ptr(),
-                              None if mask is None else mask.data_ptr())
+        mp = mask.data_ptr()
+    return coli_moe_balance_t(T, E, k, n_seqs, _SCORES[scores], alpha, logits.data_ptr(), ld, ip, op, mp), dev, T, E, n_seqs
 
 
 def balance_loss(logits, idx, alpha: float, scores: str = "sigmoid", offsets=None, mask=None):
@@ -660,16 +682,13 @@ def balance_loss(logits, idx, alpha: float, scores: str = "sigmoid", offsets=Non
     Returns (loss [S], counts [S, E] int32, coef [S, E]); balance_grad takes
     coef.  coli_moe_balance in include/coli_moe.h gives the formulas."""
     import torch
-    n_seqs = 1 if offsets is None else offsets.numel() - 1
-    a = _balance_args(logits, idx, alpha, scores, offsets, mask, n_seqs)
-    dev, E = logits.device, logits.shape[1]
-    loss = torch.empty(max(n_seqs, 0), dtype=torch.float32, device=dev)
-    counts = torch.empty((max(n_seqs, 0), E), dtype=torch.int32, device=dev)
-    coef = torch.empty((max(n_seqs, 0), E), dtype=torch.float32, device=dev)
-    nbytes = coli_moe_balance_workspace_bytes(a.tokens, E, n_seqs)
+    a, dev, T, E, S = _balance_args(logits, idx, alpha, scores, offsets, mask)
+    loss = torch.empty(S, dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    coef = torch.empty((S, E), dtype=torch.float32, device=dev)
+    nbytes = coli_moe_balance_workspace_bytes(T, E, S)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _enqueue(lambda stream: coli_moe_balance(a, loss.data_ptr(), counts.data_ptr(), coef.data_ptr(), ws.data_ptr(),
-                                             nbytes, stream), dev)
+    _enqueue("coli_moe_balance", dev, a, loss.data_ptr(), counts.data_ptr(), coef.data_ptr(), ws.data_ptr(), nbytes)
     return loss, counts, coef
 
 
@@ -679,20 +698,17 @@ def balance_grad(logits, coef, dloss=None, scores: str = "sigmoid", offsets=None
     scores, offsets and mask.  Rows of tokens in no sequence are left as they
     were in `out` (a fresh result holds zeros there)."""
     import torch
-    n_seqs = 1 if offsets is None else offsets.numel() - 1
-    a = _balance_args(logits, None, 0.0, scores, offsets, mask, n_seqs)
-    dev, (T, E) = logits.device, logits.shape
-    _matrix(coef, "coef", dev, n_seqs, E, torch.float32)
-    if n_seqs > 1 and coef.stride(0) != E:
+    a, dev, T, E, S = _balance_args(logits, None, 0.0, scores, offsets, mask)
+    if _matrix(coef, "coef", dev, S, E, torch.float32) != E and S > 1:
         raise ValueError("coef: expected a contiguous tensor")
     if dloss is not None:
-        _vector(dloss, "dloss", dev, n_seqs, torch.float32)
+        _vector(dloss, "dloss", dev, S, torch.float32)
     if out is None:
-        out = (torch.empty if offsets is None else torch.zeros)((T, E), dtype=torch.float32, device=dev)
+        out, ldo = (torch.empty if offsets is None else torch.zeros)((T, E), dtype=torch.float32, device=dev), E
     else:
-        _matrix(out, "out", dev, T, E, torch.float32)
-    _enqueue(lambda stream: coli_moe_balance_grad(a, coef.data_ptr(), None if dloss is None else dloss.data_ptr(),
-                                                  out.data_ptr(), out.stride(0), stream), dev)
+        ldo = _matrix(out, "out", dev, T, E, torch.float32)
+    _enqueue("coli_moe_balance_grad", dev, a, coef.data_ptr(), None if dloss is None else dloss.data_ptr(),
+             out.data_ptr(), ldo)
     return out
 
 

@@ -32,19 +32,11 @@ namespace coli {
 namespace {
 
 constexpr int kTok = 4;              // tokens a wave works on at once
-constexpr int kSumWaves = 8;         // waves of a workgroup of the sums
+constexpr int kSumWaves = 16;        // waves of a workgroup of the sums
 constexpr int kSumThreads = 64 * kSumWaves;
-constexpr int kMaxChunks = 512;      // workgroups of the sums
-constexpr int kMinChunkTokens = 32;  // one batch of four tokens a wave
-constexpr int kGradTokens = 32;      // tokens of a workgroup of the gradient
-constexpr int kGradWaves = 4;
-
-// Largest over the 64 lanes, in every lane.
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
-}
+constexpr int kMaxChunks = 256;      // workgroups of the sums
+constexpr int kBatchTokens = kTok * kSumWaves;  // tokens they take at a time
+constexpr int kGradWaves = 4;        // waves of a workgroup of the gradient, four tokens each
 
 // A token's scores: v = exp(z - max) (softmax) or sigma(z), slope = its own
 // derivative (softmax: v again), total their sum over the experts.
@@ -66,7 +58,7 @@ __device__ __forceinline__ void score_tokens(const float (&z)[kTok][NE], int lan
       top[t] = m;
     }
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) top[t] = wave_max(top[t]);
+    for (int t = 0; t < kTok; ++t) top[t] = lanes_max<64>(top[t]);
   }
 #pragma unroll
   for (int t = 0; t < kTok; ++t) {
@@ -82,7 +74,7 @@ __device__ __forceinline__ void score_tokens(const float (&z)[kTok][NE], int lan
         // a = exp(-|z|): sigma and sigma (1 - sigma) = a / (1 + a)^2 without
         // overflow or cancellation
         const float a = exp_neg(-fabsf(z[t][i]));
-        const float q = 1.0f / (1.0f + a);
+        const float q = __builtin_amdgcn_rcpf(1.0f + a);
         v = (z[t][i] >= 0.0f ? 1.0f : a) * q;
         d = a * q * q;
       }
@@ -103,107 +95,171 @@ __device__ __forceinline__ int seq_at(const coli_moe_balance_t &a, int s) {
   return min(max(a.seq_offsets[s], 0), a.tokens);
 }
 
-// First sequence that ends behind token t (n_seqs: none).
-__device__ __forceinline__ int first_seq(const coli_moe_balance_t &a, int t) {
-  int lo = 0, hi = a.n_seqs;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_at(a, mid + 1) > t)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo;
-}
+// The sequences' bounds, 64 at a time in the wave's lanes (a load for each
+// bound would be a memory round trip in front of everything else).
+struct Bounds {
+  int first, value;  // lane l holds the start of sequence first + l
 
+  __device__ __forceinline__ void load(const coli_moe_balance_t &a, int s) {
+    first = s;
+    value = seq_at(a, min(s + (int)(threadIdx.x & 63), a.n_seqs));
+  }
+  // Start of sequence s (s = n_seqs: the end of the last), s >= first.
+  __device__ __forceinline__ int at(const coli_moe_balance_t &a, int s) {
+    if (s - first >= 64) load(a, s);
+    return __builtin_amdgcn_readlane(value, s - first);
+  }
+  // Starts at the first sequence that ends behind token t (n_seqs: none):
+  // the number of ends at or before t, narrowed 64-fold a load.  For up to 63
+  // sequences load(a, 0), issued earlier, is all it needs.
+  __device__ __forceinline__ int seek(const coli_moe_balance_t &a, int t) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = a.n_seqs;  // among sequences lo .. lo + n - 1 or behind them
+    if (n > 63) {
+      do {
+        const int step = (n + 62) / 63, probe = min(lo + step * (lane + 1), lo + n);
+        const int before = __popcll(__ballot(seq_at(a, probe) <= t));  // probes are ends, ascending
+        const int skip = min(before * step, n);
+        lo += skip;
+        n = min(step, n - skip);
+      } while (n > 63);
+      load(a, lo);
+    }
+    return lo + __popcll(__ballot(lane >= 1 && lane <= n && value <= t));
+  }
+};
+
+// A wave's next four tokens, t0 + t step: logits and mask as they stand.
+// Masked tokens' logits are loaded (beside the mask, not behind it) but not
+// looked at.
 template <int NE>
-__device__ __forceinline__ void load_tokens(const coli_moe_balance_t &a, int t0, int step, int end, int lane,
-                                            float (&z)[kTok][NE], bool (&on)[kTok]) {
+struct Tokens {
+  float raw[kTok][NE];
+  uint8_t valid[kTok];
+
+  __device__ __forceinline__ void load(const coli_moe_balance_t &a, int t0, int step, int end, int lane) {
 #pragma unroll
-  for (int t = 0; t < kTok; ++t) {
-    const int tok = t0 + t * step;
-    on[t] = tok < end && (!a.mask || a.mask[tok]);
+    for (int t = 0; t < kTok; ++t) {
+      const int tok = min(t0 + t * step, end - 1);
+      valid[t] = a.mask ? a.mask[tok] : 1;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = lane + 64 * i;
-      z[t][i] = on[t] && e < a.n_experts ? a.logits[(int64_t)tok * a.logits_stride + e] : -__builtin_inff();
+      for (int i = 0; i < NE; ++i)
+        raw[t][i] = a.logits[(int64_t)tok * a.logits_stride + min(lane + 64 * i, a.n_experts - 1)];
     }
   }
-}
+  __device__ __forceinline__ void look(int t0, int step, int end, int lane, int E, float (&z)[kTok][NE],
+                                       bool (&on)[kTok]) const {
+#pragma unroll
+    for (int t = 0; t < kTok; ++t) {
+      on[t] = t0 + t * step < end && valid[t] != 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) z[t][i] = on[t] && lane + 64 * i < E ? raw[t][i] : -__builtin_inff();
+    }
+  }
+};
 
 // Sums of one piece: share sums [E], counts [E], valid tokens (as float32
 // words: E floats, then E + 1 ints).
 __host__ __device__ inline size_t slot_words(int E) { return 2 * (size_t)E + 1; }
 
+// A workgroup takes its tokens 64 at a time, four a wave; their loads need no
+// knowledge of the sequences and go out first.  A piece's sums stay in
+// registers (shares) and LDS (counts) until the piece ends.
 template <int NE, bool SOFTMAX>
 __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(coli_moe_balance_t a, int chunk_tokens,
                                                                    float *slots) {
+  constexpr int kBatch = kBatchTokens, kIdx = kBatch * kMaxTopK / kSumThreads;
   __shared__ float mass[kSumWaves][64 * NE];
   __shared__ int hist[64 * NE];
   __shared__ int valid;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), E = a.n_experts, k = a.top_k;
   const int lo = blockIdx.x * chunk_tokens, hi = min(lo + chunk_tokens, a.tokens);
-  for (int s = first_seq(a, lo); s < a.n_seqs; ++s) {
-    const int begin = max(seq_at(a, s), lo), end = min(seq_at(a, s + 1), hi);
-    if (begin >= hi) break;
-    if (begin >= end) continue;
-    for (int i = threadIdx.x; i < E; i += kSumThreads) hist[i] = 0;
-    if (threadIdx.x == 0) valid = 0;
-    __syncthreads();
-    // counts of the kept assignments
-    const int n = (end - begin) * k;
-    const int32_t *idx = a.idx + (int64_t)begin * k;
-    for (int i = threadIdx.x; i < n; i += kSumThreads) {
-      const int e = idx[i];
-      if ((uint32_t)e < (uint32_t)E && (!a.mask || a.mask[begin + (uint32_t)i / (uint32_t)k])) atomicAdd(&hist[e], 1);
-    }
-    // shares
-    float acc[NE];
+  Tokens<NE> now;
+  int expert[kIdx], of[kIdx];  // this thread's assignments of the batch and their tokens
+  uint8_t counted[kIdx];       // whether those tokens are valid
+  auto load = [&](int t0) {
+    now.load(a, t0 + wave, kSumWaves, hi, lane);
 #pragma unroll
-    for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
-    int seen = 0;
-    for (int t0 = begin + wave; t0 < end; t0 += kTok * kSumWaves) {
-      float z[kTok][NE];
-      bool on[kTok];
-      load_tokens<NE>(a, t0, kSumWaves, end, lane, z, on);
-      Scores<NE, SOFTMAX> sc[kTok];
-      score_tokens<NE, SOFTMAX>(z, lane, E, sc);
+    for (int q = 0; q < kIdx; ++q) {
+      const int i = threadIdx.x + q * kSumThreads;
+      of[q] = t0 + (int)((uint32_t)i / (uint32_t)k);
+      of[q] = i < kBatch * k && of[q] < hi ? of[q] : -1;
+      expert[q] = of[q] >= 0 ? a.idx[(int64_t)t0 * k + i] : -1;
+      counted[q] = a.mask && of[q] >= 0 ? a.mask[of[q]] : 1;
+    }
+  };
+  Bounds bounds;
+  bounds.load(a, 0);
+  load(lo);
+  int s = bounds.seek(a, lo);
+  for (int i = threadIdx.x; i < E; i += kSumThreads) hist[i] = 0;
+  if (threadIdx.x == 0) valid = 0;
+  __syncthreads();
+  float acc[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+  int seen = 0;
+  for (int t0 = lo; t0 < hi; t0 += kBatch) {
+    float z[kTok][NE];
+    bool on[kTok];
+    now.look(t0 + wave, kSumWaves, hi, lane, E, z, on);
+    int e_now[kIdx], of_now[kIdx];
+#pragma unroll
+    for (int q = 0; q < kIdx; ++q) {
+      e_now[q] = counted[q] ? expert[q] : -1;
+      of_now[q] = of[q];
+    }
+    if (t0 + kBatch < hi) load(t0 + kBatch);
+    Scores<NE, SOFTMAX> sc[kTok];
+    score_tokens<NE, SOFTMAX>(z, lane, E, sc);
+    float inv[kTok];
+#pragma unroll
+    for (int t = 0; t < kTok; ++t) inv[t] = on[t] && sc[t].total > 0.0f ? 1.0f / sc[t].total : 0.0f;
+    const int stop = min(t0 + kBatch, hi);
+    for (; s < a.n_seqs; ++s) {
+      const int begin = bounds.at(a, s), end = bounds.at(a, s + 1);
+      if (begin >= stop) break;
+      if (begin >= end) continue;
 #pragma unroll
       for (int t = 0; t < kTok; ++t) {
-        const float inv = on[t] && sc[t].total > 0.0f ? 1.0f / sc[t].total : 0.0f;
+        const int tok = t0 + wave + t * kSumWaves;
+        const bool in = tok >= begin && tok < end;
+        const float w = in ? inv[t] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) acc[i] = __builtin_fmaf(sc[t].v[i], inv, acc[i]);
-        seen += on[t] ? 1 : 0;
+        for (int i = 0; i < NE; ++i) acc[i] = __builtin_fmaf(sc[t].v[i], w, acc[i]);
+        seen += in && on[t] ? 1 : 0;
       }
-    }
 #pragma unroll
-    for (int i = 0; i < NE; ++i) mass[wave][lane + 64 * i] = acc[i];
-    if (lane == 0) atomicAdd(&valid, seen);
-    __syncthreads();
-    float *slot = slots + (size_t)(blockIdx.x + s) * slot_words(E);
-    int *cnt = reinterpret_cast<int *>(slot + E);
-    for (int e = threadIdx.x; e < E; e += kSumThreads) {
-      float m = 0.0f;
+      for (int q = 0; q < kIdx; ++q)
+        if ((uint32_t)e_now[q] < (uint32_t)E && of_now[q] >= begin && of_now[q] < end) atomicAdd(&hist[e_now[q]], 1);
+      if (end > stop && stop < hi) break;  // goes on in the workgroup's next batch
+      // the piece ends: its sums to its slot
 #pragma unroll
-      for (int w = 0; w < kSumWaves; ++w) m += mass[w][e];
-      slot[e] = m;
-      cnt[e] = hist[e];
+      for (int i = 0; i < NE; ++i) {
+        mass[wave][lane + 64 * i] = acc[i];
+        acc[i] = 0.0f;
+      }
+      if (lane == 0) atomicAdd(&valid, seen);
+      seen = 0;
+      __syncthreads();
+      float *slot = slots + (size_t)(blockIdx.x + s) * slot_words(E);
+      int *cnt = reinterpret_cast<int *>(slot + E);
+      for (int e = threadIdx.x; e < E; e += kSumThreads) {
+        float m = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSumWaves; ++w) m += mass[w][e];
+        slot[e] = m;
+        cnt[e] = hist[e];
+        hist[e] = 0;
+      }
+      if (threadIdx.x == 0) {
+        cnt[E] = valid;
+        valid = 0;
+      }
+      __syncthreads();
+      if (end > stop) break;  // the workgroup's last batch
     }
-    if (threadIdx.x == 0) cnt[E] = valid;
-    __syncthreads();
   }
-}
-
-// Sum of v over a workgroup of 1024 threads, in every thread.
-__device__ __forceinline__ double block_sum(double v, double *scratch) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double t = 0.0;
-  for (int i = 0; i < 16; ++i) t += scratch[i];
-  return t;
 }
 
 // One workgroup per sequence: its pieces' sums, then loss, counts and coef.
@@ -212,10 +268,10 @@ template <int NE>
 __global__ __launch_bounds__(1024) void balance_finish_kernel(coli_moe_balance_t a, int chunk_tokens,
                                                               const float *slots, float *loss, int32_t *counts,
                                                               float *coef) {
-  constexpr int kCols = 64 * NE, kGroups = 1024 / kCols;
+  constexpr int kCols = 64 * NE, kGroups = 1024 / kCols, kAhead = 8;
   __shared__ double mass[1024];
   __shared__ int cnts[1024];
-  __shared__ double scratch[16];
+  __shared__ double totals[3][16];
   const int s = blockIdx.x, E = a.n_experts, col = threadIdx.x % kCols, grp = threadIdx.x / kCols;
   const int begin = seq_at(a, s), end = seq_at(a, s + 1);
   const size_t words = slot_words(E);
@@ -223,17 +279,25 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(coli_moe_balance_t
   int c = 0, v = 0;
   if (begin < end) {
     const int first = begin / chunk_tokens, last = (end - 1) / chunk_tokens;
-#pragma unroll 4
-    for (int p = first + grp; p <= last; p += kGroups) {
-      const float *slot = slots + (size_t)(p + s) * words;
-      const int *cnt = reinterpret_cast<const int *>(slot + E);
-      if (col < E) {
-        m += (double)slot[col];
-        c += cnt[col];
+    for (int p0 = first + grp; p0 <= last; p0 += kGroups * kAhead) {
+      float part[kAhead];
+      int cnt[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {  // kAhead pieces' loads in flight
+        const int p = p0 + q * kGroups;
+        const float *slot = slots + (size_t)(min(p, last) + s) * words;
+        part[q] = slot[min(col, E - 1)];
+        cnt[q] = reinterpret_cast<const int *>(slot)[E + min(col, E - 1)];
       }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+        if (p0 + q * kGroups <= last && col < E) {
+          m += (double)part[q];
+          c += cnt[q];
+        }
     }
     for (int p = first + (int)threadIdx.x; p <= last; p += 1024)
-      v += reinterpret_cast<const int *>(slots + (size_t)(p + s) * words + E)[E];
+      v += reinterpret_cast<const int *>(slots + (size_t)(p + s) * words)[2 * E];
   }
   mass[threadIdx.x] = m;
   cnts[threadIdx.x] = c;
@@ -248,14 +312,25 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(coli_moe_balance_t
     m = 0.0;
     c = 0;
   }
-  const double V = block_sum((double)v, scratch);
-  const double N = block_sum((double)c, scratch);
-  const double dot = block_sum((double)c * m, scratch);
+  // valid tokens, kept assignments (whole numbers, exact) and their product with the shares
+  const double sums[3] = {lanes_sum64<64>((double)v), lanes_sum64<64>((double)c), lanes_sum64<64>((double)c * m)};
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) totals[i][threadIdx.x >> 6] = sums[i];
+  __syncthreads();
+  double V = 0.0, N = 0.0, dot = 0.0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    V += totals[0][i];
+    N += totals[1][i];
+    dot += totals[2][i];
+  }
   const bool some = V > 0.0 && N > 0.0;
-  if (threadIdx.x == 0) loss[s] = some ? (float)((double)a.alpha * E * dot / (N * V)) : 0.0f;
+  const double per_token = some ? (double)a.alpha / V : 0.0, share = some ? E / N : 0.0;
+  if (threadIdx.x == 0) loss[s] = (float)(per_token * share * dot);
   if (grp == 0 && col < E) {
     counts[(size_t)s * E + col] = c;
-    coef[(size_t)s * E + col] = some ? (float)((double)a.alpha / V * ((double)c * E / N - 1.0)) : 0.0f;
+    coef[(size_t)s * E + col] = (float)(per_token * ((double)c * share - 1.0));
   }
 }
 
@@ -264,45 +339,46 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(coli_moe_
                                                                        const float *dloss, float *dlogits,
                                                                        int64_t stride) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), E = a.n_experts;
-  const int lo = blockIdx.x * kGradTokens, hi = min(lo + kGradTokens, a.tokens);
-  for (int s = first_seq(a, lo); s < a.n_seqs; ++s) {
-    const int begin = max(seq_at(a, s), lo), end = min(seq_at(a, s + 1), hi);
+  const int lo = (blockIdx.x * kGradWaves + wave) * kTok, hi = min(lo + kTok, a.tokens);  // the wave's tokens
+  if (lo >= hi) return;
+  Bounds bounds;
+  bounds.load(a, 0);
+  Tokens<NE> tokens;
+  tokens.load(a, lo, 1, hi, lane);
+  int s = bounds.seek(a, lo);
+  float z[kTok][NE];
+  bool on[kTok];
+  tokens.look(lo, 1, hi, lane, E, z, on);
+  Scores<NE, SOFTMAX> sc[kTok];
+  score_tokens<NE, SOFTMAX>(z, lane, E, sc);
+  for (; s < a.n_seqs; ++s) {
+    const int begin = bounds.at(a, s), end = bounds.at(a, s + 1);
     if (begin >= hi) break;
     if (begin >= end) continue;
     float c[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = lane + 64 * i;
-      c[i] = e < E ? coef[(size_t)s * E + e] : 0.0f;
-    }
+    for (int i = 0; i < NE; ++i) c[i] = lane + 64 * i < E ? coef[(size_t)s * E + lane + 64 * i] : 0.0f;
     const float up = dloss ? dloss[s] : 1.0f;
-    for (int t0 = begin + wave; t0 < end; t0 += kTok * kGradWaves) {
-      float z[kTok][NE];
-      bool on[kTok];
-      load_tokens<NE>(a, t0, kGradWaves, end, lane, z, on);
-      Scores<NE, SOFTMAX> sc[kTok];
-      score_tokens<NE, SOFTMAX>(z, lane, E, sc);
-      float dot[kTok];
+    float dot[kTok];
 #pragma unroll
-      for (int t = 0; t < kTok; ++t) {
-        dot[t] = 0.0f;
+    for (int t = 0; t < kTok; ++t) {
+      dot[t] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) dot[t] = __builtin_fmaf(c[i], sc[t].v[i], dot[t]);
-      }
+      for (int i = 0; i < NE; ++i) dot[t] = __builtin_fmaf(c[i], sc[t].v[i], dot[t]);
+    }
 #pragma unroll
-      for (int t = 0; t < kTok; ++t) dot[t] = wave_sum(dot[t]);
+    for (int t = 0; t < kTok; ++t) dot[t] = wave_sum(dot[t]);
 #pragma unroll
-      for (int t = 0; t < kTok; ++t) {
-        const int tok = t0 + t * kGradWaves;
-        if (tok >= end) continue;
-        const bool some = on[t] && sc[t].total > 0.0f;
-        const float inv = some ? 1.0f / sc[t].total : 0.0f;
-        const float mean = dot[t] * inv, scale = up * inv;
+    for (int t = 0; t < kTok; ++t) {
+      const int tok = lo + t;
+      if (tok < begin || tok >= min(end, hi)) continue;
+      const bool some = on[t] && sc[t].total > 0.0f;
+      const float inv = some ? 1.0f / sc[t].total : 0.0f;
+      const float mean = dot[t] * inv, scale = up * inv;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          const int e = lane + 64 * i;
-          if (e < E) dlogits[(int64_t)tok * stride + e] = some ? scale * sc[t].slope[i] * (c[i] - mean) : 0.0f;
-        }
+      for (int i = 0; i < NE; ++i) {
+        const int e = lane + 64 * i;
+        if (e < E) dlogits[(int64_t)tok * stride + e] = some ? scale * sc[t].slope[i] * (c[i] - mean) : 0.0f;
       }
     }
   }
@@ -311,7 +387,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(coli_moe_
 // Tokens of one workgroup of the sums.
 int chunk_tokens_of(int tokens) {
   const int c = (tokens + kMaxChunks - 1) / kMaxChunks;
-  return c < kMinChunkTokens ? kMinChunkTokens : c;
+  return (c < 1 ? 1 : (c + kBatchTokens - 1) / kBatchTokens) * kBatchTokens;
 }
 
 int chunks_of(int tokens) {
@@ -352,7 +428,7 @@ hipError_t launch_balance(const coli_moe_balance_t &a, float *loss, int32_t *cou
 
 hipError_t launch_balance_grad(const coli_moe_balance_t &a, const float *coef, const float *dloss, float *dlogits,
                                int64_t stride, hipStream_t s) {
-  const dim3 grid((a.tokens + kGradTokens - 1) / kGradTokens), block(64 * kGradWaves);
+  const dim3 grid((a.tokens + kTok * kGradWaves - 1) / (kTok * kGradWaves)), block(64 * kGradWaves);
   return by_experts(a.n_experts, [&](auto ne) {
     constexpr int NE = decltype(ne)::value;
     return a.scores == COLI_MOE_SCORES_SOFTMAX

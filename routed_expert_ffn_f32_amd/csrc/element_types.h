@@ -26,13 +26,6 @@ __device__ __forceinline__ float from_bf16(uint32_t low16) { return __uint_as_fl
 __device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ __forceinline__ uint16_t to_f16(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 
-// Element i of an array of 16- or 32-bit floats.
-__device__ __forceinline__ float load1(const void *base, int type, int64_t i) {
-  if (type == COLI_MOE_F32) return static_cast<const float *>(base)[i];
-  const uint16_t u = static_cast<const uint16_t *>(base)[i];
-  return type == COLI_MOE_BF16 ? from_bf16(u) : (float)__builtin_bit_cast(_Float16, u);
-}
-
 __device__ __forceinline__ void store1(void *base, int type, int64_t i, float v) {
   if (type == COLI_MOE_F32)
     static_cast<float *>(base)[i] = v;
@@ -40,31 +33,69 @@ __device__ __forceinline__ void store1(void *base, int type, int64_t i, float v)
     static_cast<uint16_t *>(base)[i] = type == COLI_MOE_BF16 ? to_bf16(v) : to_f16(v);
 }
 
-// v = elements i .. i + 7; those at n and beyond are 0 and not read.
-__device__ __forceinline__ void load8(const void *base, int type, int64_t i, int n, float (&v)[8]) {
-  if (n >= 8) {
-    if (type == COLI_MOE_F32) {
-      __builtin_memcpy(v, static_cast<const float *>(base) + i, 32);
-      return;
+// Eight elements as they stand in memory (16-bit types: in lo alone), so that
+// loads of several arrays can be in flight before the first is looked at.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+struct Raw8 {
+  u32x4 lo, hi;
+};
+
+__device__ __forceinline__ u32x4 load16(const char *p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
+// Elements i .. i + 7.
+__device__ __forceinline__ Raw8 load_raw8(const void *base, int type, int64_t i) {
+  Raw8 r;
+  if (type == COLI_MOE_F32) {
+    const char *p = static_cast<const char *>(base) + i * 4;
+    r.lo = load16(p);
+    r.hi = load16(p + 16);
+  } else {
+    r.lo = load16(static_cast<const char *>(base) + i * 2);
+  }
+  return r;
+}
+
+// The same, those at n and beyond 0 and not read.
+__device__ __forceinline__ Raw8 load_raw8(const void *base, int type, int64_t i, int n) {
+  if (n >= 8) return load_raw8(base, type, i);
+  Raw8 r = {u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
+  if (type == COLI_MOE_F32) {
+    const uint32_t *p = static_cast<const uint32_t *>(base) + i;
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < n) (j < 4 ? r.lo : r.hi)[j & 3] = p[j];
+  } else {
+    const uint16_t *p = static_cast<const uint16_t *>(base) + i;
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < n) r.lo[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+  }
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(int type, const Raw8 &r, float (&v)[8]) {
+  if (type == COLI_MOE_F32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __uint_as_float(r.lo[j]);
+      v[j + 4] = __uint_as_float(r.hi[j]);
     }
-    uint32_t u[4];
-    __builtin_memcpy(u, static_cast<const uint16_t *>(base) + i, 16);
-    if (type == COLI_MOE_BF16) {
+  } else if (type == COLI_MOE_BF16) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = from_bf16(u[j]);
-        v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = (float)__builtin_bit_cast(_Float16, (uint16_t)u[j]);
-        v[2 * j + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[j] >> 16));
-      }
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = from_bf16(r.lo[j]);
+      v[2 * j + 1] = __uint_as_float(r.lo[j] & 0xFFFF0000u);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? load1(base, type, i + j) : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = (float)__builtin_bit_cast(_Float16, (uint16_t)r.lo[j]);
+      v[2 * j + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.lo[j] >> 16));
+    }
   }
 }
 
@@ -76,27 +107,32 @@ __device__ __forceinline__ void round8(int type, float (&v)[8]) {
     v[j] = type == COLI_MOE_BF16 ? from_bf16(to_bf16(v[j])) : (float)(_Float16)v[j];
 }
 
-// Elements i .. i + 7 (those below n) = v, rounded to the type.
-__device__ __forceinline__ void store8(void *base, int type, int64_t i, int n, const float (&v)[8]) {
-  if (n >= 8) {
-    if (type == COLI_MOE_F32) {
-      __builtin_memcpy(static_cast<float *>(base) + i, v, 32);
-      return;
-    }
-    uint32_t u[4];
-    if (type == COLI_MOE_BF16) {
+// Elements i .. i + 7 = v, rounded to the type.
+__device__ __forceinline__ void store8(void *base, int type, int64_t i, const float (&v)[8]) {
+  if (type == COLI_MOE_F32) {
+    __builtin_memcpy(static_cast<float *>(base) + i, v, 32);
+    return;
+  }
+  uint32_t u[4];
+  if (type == COLI_MOE_BF16) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = to_bf16(v[2 * j]) | ((uint32_t)to_bf16(v[2 * j + 1]) << 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = to_f16(v[2 * j]) | ((uint32_t)to_f16(v[2 * j + 1]) << 16);
-    }
-    __builtin_memcpy(static_cast<uint16_t *>(base) + i, u, 16);
+    for (int j = 0; j < 4; ++j) u[j] = to_bf16(v[2 * j]) | ((uint32_t)to_bf16(v[2 * j + 1]) << 16);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) store1(base, type, i + j, v[j]);
+    for (int j = 0; j < 4; ++j) u[j] = to_f16(v[2 * j]) | ((uint32_t)to_f16(v[2 * j + 1]) << 16);
   }
+  __builtin_memcpy(static_cast<uint16_t *>(base) + i, u, 16);
+}
+
+// The same, those below n.
+__device__ __forceinline__ void store8(void *base, int type, int64_t i, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    store8(base, type, i, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 7; ++j)
+    if (j < n) store1(base, type, i + j, v[j]);
 }
 
 }  // namespace coli

@@ -108,61 +108,86 @@ struct Operand<COLI_MOE_E4M3> {
 // 16 zero bytes: where the copies past a row's end come from.
 __device__ const uint4 kZeroPiece = {0u, 0u, 0u, 0u};
 
-__device__ __forceinline__ float activate(int act, float v) {
-  switch (act) {
-    case COLI_MOE_ACT_RELU: return fmaxf(v, 0.0f);
-    case COLI_MOE_ACT_SILU: return v * sigmoid(v);
-    case COLI_MOE_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678f);
-    // tanh(u) = 2 sigma(2 u) - 1
-    case COLI_MOE_ACT_GELU_TANH: return v * sigmoid(1.59576912f * (v + 0.044715f * v * v * v));
-    default: return v;
-  }
+// Elements i .. i + 7 of an array as float32; WHOLE: all of them exist, else
+// those at i + n and beyond are 0 and not read.
+template <bool WHOLE>
+__device__ __forceinline__ void fetch8(const void *base, int type, int64_t i, int n, float (&v)[8]) {
+  unpack8(type, WHOLE ? load_raw8(base, type, i) : load_raw8(base, type, i, n), v);
 }
 
-// Epilogue of 8 neighbouring outputs (row m, columns n .. n + 7, those below
-// a.n stored): v = the products' sums (up: those of the up rows, SwiGLU
-// only), float32.
-__device__ __forceinline__ void finish8(const coli_moe_linear_t &a, int m, int n, float (&v)[8], float (&up)[8]) {
+// The epilogue up to the residual of 8 neighbouring outputs (row m, columns n
+// .. n + 7): v = the products' sums (up: those of the up rows, SwiGLU only),
+// float32.  WHOLE: n + 7 < a.n.
+template <bool WHOLE>
+__device__ __forceinline__ void activate8(const coli_moe_linear_t &a, int m, int n, float (&v)[8], float (&up)[8]) {
   const int cnt = a.n - n;
-  if (cnt <= 0) return;
   const bool gated = a.act == COLI_MOE_ACT_SWIGLU;
+  float w[8];
   if (a.x_scale) {
     const float sx = a.x_scale[m];
-    float sw[8];
-    load8(a.w_scale, COLI_MOE_F32, n, cnt, sw);
+    fetch8<WHOLE>(a.w_scale, COLI_MOE_F32, n, cnt, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= sx * sw[j];
+    for (int j = 0; j < 8; ++j) v[j] *= sx * w[j];
     if (gated) {
-      load8(a.w_scale, COLI_MOE_F32, (int64_t)a.n + n, cnt, sw);
+      fetch8<WHOLE>(a.w_scale, COLI_MOE_F32, (int64_t)a.n + n, cnt, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) up[j] *= sx * sw[j];
+      for (int j = 0; j < 8; ++j) up[j] *= sx * w[j];
     }
   }
   if (a.bias) {
-    float b[8];
-    load8(a.bias, a.bias_type, n, cnt, b);
+    fetch8<WHOLE>(a.bias, a.bias_type, n, cnt, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += b[j];
+    for (int j = 0; j < 8; ++j) v[j] += w[j];
     if (gated) {
-      load8(a.bias, a.bias_type, (int64_t)a.n + n, cnt, b);
+      fetch8<WHOLE>(a.bias, a.bias_type, (int64_t)a.n + n, cnt, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) up[j] += b[j];
+      for (int j = 0; j < 8; ++j) up[j] += w[j];
     }
   }
-  if (gated) {
+  switch (a.act) {
+    case COLI_MOE_ACT_RELU:
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * sigmoid(v[j]) * up[j];
-  } else if (a.act != COLI_MOE_ACT_NONE) {
+      for (int j = 0; j < 8; ++j) v[j] = fmaxf(v[j], 0.0f);
+      break;
+    case COLI_MOE_ACT_SILU:
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate(a.act, v[j]);
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * sigmoid(v[j]);
+      break;
+    case COLI_MOE_ACT_GELU:
+#pragma nounroll
+      for (int j = 0; j < 8; ++j) {  // a long function: one copy of it, on rotating values
+        const float y = 0.5f * v[0] * erfcf(v[0] * -0.70710678f);
+#pragma unroll
+        for (int q = 0; q < 7; ++q) v[q] = v[q + 1];
+        v[7] = y;
+      }
+      break;
+    case COLI_MOE_ACT_GELU_TANH:  // tanh(u) = 2 sigma(2 u) - 1
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = v[j] * sigmoid(1.59576912f * (v[j] + 0.044715f * v[j] * v[j] * v[j]));
+      break;
+    case COLI_MOE_ACT_SWIGLU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * sigmoid(v[j]) * up[j];
+      break;
+    default: break;
   }
+}
+
+// The rest of it: adds the residual (as loaded) and stores.
+template <bool WHOLE>
+__device__ __forceinline__ void store_out8(const coli_moe_linear_t &a, int m, int n, float (&v)[8], const Raw8 &res) {
   if (a.residual) {
     float r[8];
-    load8(a.residual, a.out_type, (int64_t)m * a.ldr + n, cnt, r);
+    unpack8(a.out_type, res, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += r[j];
   }
-  store8(a.out, a.out_type, (int64_t)m * a.ldo + n, cnt, v);
+  if (WHOLE)
+    store8(a.out, a.out_type, (int64_t)m * a.ldo + n, v);
+  else
+    store8(a.out, a.out_type, (int64_t)m * a.ldo + n, a.n - n, v);
 }
 
 }  // namespace coli

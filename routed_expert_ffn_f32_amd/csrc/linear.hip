@@ -324,36 +324,89 @@ struct Tile {
     }
   }
 
-  // Accumulators -> LDS -> 8 neighbouring outputs a thread, 32 rows of every
-  // wave row at a time.  Register i of a 32 x 32 block is row 8 (i / 4) +
-  // 4 half + i % 4, the lane's column is lane % 32.
+  // Accumulators -> LDS -> 8 neighbouring outputs a thread, a slab of 32 rows
+  // of every wave row at a time.  Register i of a 32 x 32 block is row
+  // 8 (i / 4) + 4 half + i % 4, the lane's column is lane % 32.  The loop over
+  // the slabs stays a loop (only the accumulators' registers differ), and
+  // tiles that end inside 8 columns take their own copy of the code: it runs
+  // once a tile, straight from memory.
   static __device__ __forceinline__ void epilogue(const coli_moe_linear_t &a, int m0, int n0, int wm, int wn, int lane,
                                                   const Acc (&acc)[MB][NB], float *sums) {
     const int nl = lane & 31, half = lane >> 5;
-    constexpr int kParts = kOutN / 8;
-#pragma unroll
+    const bool whole = n0 + kOutN <= a.n;
+#pragma nounroll
     for (int mb = 0; mb < MB; ++mb) {
       if (mb) __syncthreads();
+      float *to = sums + (wm * 32 + 4 * half) * kRowFloats + 32 * wn * NB + nl;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int q = 0; q < MB; ++q)
+        if (q == mb) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          sums[(wm * 32 + 8 * (i >> 2) + 4 * half + (i & 3)) * kRowFloats + 32 * (wn * NB + nb) + nl] =
-              (float)acc[mb][nb][i];
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) to[(8 * (i >> 2) + (i & 3)) * kRowFloats + 32 * nb] = (float)acc[q][nb][i];
+        }
       __syncthreads();
-      for (int q = threadIdx.x; q < WM * 32 * kParts; q += kThreads) {
-        const int r = q / kParts, c = q % kParts * 8;  // row of the slab, output column of the tile
-        const int m = m0 + ((r >> 5) * MB + mb) * 32 + (r & 31);
-        if (m >= a.m) continue;
-        const float *from = sums + r * kRowFloats + (GATED ? (c >> 5) * 64 + (c & 31) : c);
-        float v[8], up[8];
+      if (whole)
+        finish_slab<true>(a, m0, n0, mb, sums);
+      else
+        finish_slab<false>(a, m0, n0, mb, sums);
+    }
+  }
+
+  // One slab: scales, bias and activation in LDS (a loop: one copy of that
+  // code), then residual and store; every residual of the slab is on its way
+  // before that.  Each thread stays with its own outputs.
+  template <bool WHOLE>
+  static __device__ __forceinline__ void finish_slab(const coli_moe_linear_t &a, int m0, int n0, int mb, float *sums) {
+    constexpr int kParts = kOutN / 8, kTurns = WM * 32 * kParts / kThreads;
+    static_assert(kTurns * kThreads == WM * 32 * kParts, "whole turns of the threads");
+    auto row = [&](int i) {
+      const int r = (threadIdx.x + i * kThreads) / kParts;
+      return m0 + ((r >> 5) * MB + mb) * 32 + (r & 31);
+    };
+    auto column = [&](int i) { return n0 + (int)(threadIdx.x + i * kThreads) % kParts * 8; };
+    auto place = [&](int i) {
+      const int q = threadIdx.x + i * kThreads, r = q / kParts, c = q % kParts * 8;
+      return sums + r * kRowFloats + (GATED ? (c >> 5) * 64 + (c & 31) : c);
+    };
+    Raw8 res[kTurns];
+    if (WHOLE && a.residual) {  // rows past the last read the last
+      if (a.out_type == COLI_MOE_F32) {
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i)
+          res[i] = load_raw8(a.residual, COLI_MOE_F32, (int64_t)min(row(i), a.m - 1) * a.ldr + column(i));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i)
+          res[i] = load_raw8(a.residual, COLI_MOE_BF16, (int64_t)min(row(i), a.m - 1) * a.ldr + column(i));
+      }
+    }
+    float v[8], up[8];
+    if (a.x_scale || a.bias || a.act != COLI_MOE_ACT_NONE) {
+#pragma nounroll
+      for (int i = 0; i < kTurns; ++i) {
+        if (row(i) >= a.m || column(i) >= a.n) continue;
+        float *at = place(i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          v[j] = from[j];
-          up[j] = GATED ? from[32 + j] : 0.0f;
+          v[j] = at[j];
+          up[j] = GATED ? at[32 + j] : 0.0f;
         }
-        finish8(a, m, n0 + c, v, up);
+        activate8<WHOLE>(a, row(i), column(i), v, up);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) at[j] = v[j];
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      if (row(i) >= a.m || column(i) >= a.n) continue;
+      const float *at = place(i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = at[j];
+      if (!WHOLE && a.residual)
+        res[i] = load_raw8(a.residual, a.out_type, (int64_t)row(i) * a.ldr + column(i), a.n - column(i));
+      store_out8<WHOLE>(a, row(i), column(i), v, res[i]);
     }
   }
 };

@@ -161,6 +161,10 @@ struct Rows {
     for (int i = threadIdx.x; i < MR * kParts; i += 64 * kWaves) {
       const int token = i / kParts, part = i % kParts * 8;
       if (m0 + token >= a.m) break;
+      if (n0 + part >= a.n) continue;
+      Raw8 res;
+      if (a.residual)
+        res = load_raw8(a.residual, a.out_type, (int64_t)(m0 + token) * a.ldr + n0 + part, a.n - n0 - part);
       float v[8], u[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -174,7 +178,8 @@ struct Rows {
         v[e] = (float)s;
         u[e] = (float)su;
       }
-      finish8(a, m0 + token, n0 + part, v, u);
+      activate8<false>(a, m0 + token, n0 + part, v, u);
+      store_out8<false>(a, m0 + token, n0 + part, v, res);
     }
   }
 };

@@ -115,6 +115,53 @@ __device__ __forceinline__ float quad_max(float v) {
   return v;
 }
 
+// Max of v over LANES (4, 8, 16 or 64) neighbouring lanes, in every one of
+// them: within a quad, then the other quad of 8 (half mirror), the other half
+// of a 16-lane row (mirror), the other rows (16- and 32-lane swaps).
+constexpr int kDppRowMirror = 0x140, kDppRowHalfMirror = 0x141;
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+  v = quad_max(v);
+  if constexpr (LANES >= 8) v = fmaxf(v, dpp_f<kDppRowHalfMirror>(v));
+  if constexpr (LANES >= 16) v = fmaxf(v, dpp_f<kDppRowMirror>(v));
+  if constexpr (LANES >= 64) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  }
+  return v;
+}
+
+// Sum of v over LANES (16 or 64) neighbouring lanes, in every one of them, in
+// float64 (the same order on every run).
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)dpp_i<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp_i<CTRL>((int)(uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, lo | ((uint64_t)hi << 32));
+}
+template <int LANES>
+__device__ __forceinline__ double lanes_sum64(double v) {
+  v += dpp_d<kDppQuadXor1>(v);
+  v += dpp_d<kDppQuadXor2>(v);
+  v += dpp_d<kDppRowHalfMirror>(v);
+  v += dpp_d<kDppRowMirror>(v);
+  if constexpr (LANES == 16) return v;
+  const auto swapped = [](double x, bool across32) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+    const auto a = across32 ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false)
+                            : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    const auto b = across32 ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false)
+                            : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    return __builtin_bit_cast(double, a[0] | ((uint64_t)b[0] << 32)) +
+           __builtin_bit_cast(double, a[1] | ((uint64_t)b[1] << 32));
+  };
+  v = swapped(v, false);
+  return swapped(v, true);
+}
+
 // ---------------------------------------------------------------------------
 // Digit-plane activations.
 //

@@ -7,8 +7,8 @@ exponential (argument reduced with a two-part ln 2: at most 3 u) and for
 sigmoid a quotient (2 u, the derivative 3 u); its sum over the experts adds
 at most 14 float32 additions of positive terms (7 u), a share one division
 and one product: 14 u.  A loss adds the shares of positive weight in float32
-over the at most 4 + 8 additions a wave and its workgroup make of a chunk of
-32 tokens (6 u) and continues in float64: 22 u.  An element of the gradient is scale * slope
+over the at most 4 + 16 additions a wave and its workgroup make of a chunk of
+64 tokens (10 u, half a step each) and continues in float64: 26 u.  An element of the gradient is scale * slope
 * (c - m), with m a sum of 14 terms c_j p_j of any sign: its error is at most
 48 u of scale * slope * (|c| + sum |c_j| p_j)."""
 import numpy as np
@@ -78,7 +78,7 @@ def reference(z, idx, off, mask, scores, alpha, dloss):
     return loss, counts, coef, d, unit
 
 
-def check(dev, z, idx, off, mask, scores, dloss=None, alpha=ALPHA, tokens_per_chunk=32, stride_pad=0):
+def check(dev, z, idx, off, mask, scores, dloss=None, alpha=ALPHA, tokens_per_chunk=64, stride_pad=0):
     T, E = z.shape
     S = len(off) - 1
     up = np.ones(S) if dloss is None else dloss.astype(np.float64)
@@ -94,9 +94,9 @@ def check(dev, z, idx, off, mask, scores, dloss=None, alpha=ALPHA, tokens_per_ch
     cm.balance_grad(zd, gf, None if dloss is None else torch.from_numpy(dloss).to(dev), out=out[:, :E], **kw)
     torch.cuda.synchronize()
     assert np.array_equal(gc.cpu().numpy(), counts)
-    extra = max(0, tokens_per_chunk - 32) / 8  # additions of a wave beyond the four of 32 tokens
+    extra = max(0, tokens_per_chunk - 64) / 16  # additions of a wave beyond the four of 64 tokens
     gl = gl.cpu().numpy().astype(np.float64)
-    assert (np.abs(gl - loss) <= (22 + extra / 2) * U * np.abs(loss)).all(), (gl, loss)
+    assert (np.abs(gl - loss) <= (26 + extra / 2) * U * np.abs(loss)).all(), (gl, loss)
     cmax = np.abs(coef) + alpha * 1e-30
     assert (np.abs(gf.cpu().numpy() - coef) <= 2 * U * cmax).all()
     g = out.cpu().numpy().astype(np.float64)
@@ -122,13 +122,17 @@ def test_sizes(dev, T, E, k, scores):
 
 @pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
 def test_long_and_many_sequences(dev, scores):
-    """More tokens than the sums' largest number of workgroups takes at 32
+    """More tokens than the sums' largest number of workgroups takes at 64
     each; a sequence per token; one sequence over every workgroup."""
     z, idx, rng = make(20011, 40, 4, 1)
-    per = -(-20011 // 512)
+    per = -(-20011 // 256)
     check(dev, z, idx, [0, 20011], rng.random(20011) < 0.9, scores, tokens_per_chunk=per)
     check(dev, z[:700], idx[:700], np.arange(701), None, scores)
     check(dev, z[:700], idx[:700], np.repeat([0, 5, 5, 300, 700], 50), None, scores)
+    # more sequences than one load of bounds shows, most of them empty
+    rng = np.random.default_rng(8)
+    for n in (64, 65, 130, 5000):
+        check(dev, z[:900], idx[:900], np.sort(rng.integers(3, 890, size=n + 1)), None, scores)
 
 
 @pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
@@ -206,7 +210,7 @@ def test_default_arguments_and_repeatability(dev):
     loss, counts, _, d, unit = reference(z, idx, [0, 5000], np.ones(5000, bool), "sigmoid", float(np.float32(ALPHA)),
                                          [1.0])
     assert np.array_equal(a[1].cpu().numpy(), counts)
-    assert abs(float(a[0]) - loss[0]) <= 22 * U * loss[0]
+    assert abs(float(a[0]) - loss[0]) <= 26 * U * loss[0]
     assert (np.abs(ga.cpu().numpy() - d) <= 48 * U * unit).all()
 
 

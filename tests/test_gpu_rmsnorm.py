@@ -88,9 +88,12 @@ def run(dev, x, weight, eps, residual=None, in_place=False, **kw):
     return got, None if stored is None else stored.cpu()
 
 
-# every launch shape: 1 wave x 1, 2 pieces; 4 waves x 1, 2, 3; 16 waves x 1, 2, 4
-SIZES = [(1, 1), (3, 7), (5, 64), (2, 511), (9, 512), (4, 513), (7, 1024), (3, 1025), (2, 2047), (5, 2048), (2, 2056),
-         (3, 4096), (1, 6144), (65, 6144), (3, 6145), (2, 8192), (2, 8193), (2, 16384), (1, 16391), (2, 32768)]
+# every launch shape: 1, 2, 4, 6, 8, 12 and 16 waves of one piece a thread, 8 (many rows)
+# and 16 of 2, 16 of 4; parts of a wave up to 128 columns
+SIZES = [(1, 1), (3, 7), (5, 64), (17, 120), (16, 128), (7, 129), (2, 511), (9, 512), (4, 513), (7, 1024), (3, 1025), (2, 2047), (5, 2048), (2, 2056),
+         (3, 2600), (3, 4096), (2, 5001), (1, 6144), (65, 6144), (3, 6145), (2, 8192), (2, 8193), (2, 16384), (1, 16391),
+         (2, 32768),
+         (1025, 5000)]
 
 
 @pytest.mark.parametrize("rows,hidden", SIZES)
@@ -171,9 +174,32 @@ def test_extreme_rows(dev):
     stored, y64, _ = reference(x[4:5], None, 0.0)
     got, _ = run(dev, x[4:5], None, 0.0)
     check_float(got.cpu(), y64, F32)
+    zeros = torch.zeros(2, h, device=dev)
+    assert not cm.rms_norm(zeros, None, 0.0).any() and not cm.rms_norm(zeros, None, 0.0, out_dtype=E4)[0].float().any()
     same = cm.rms_norm(x[4:5].to(dev).expand(3, h), None, 0.0)
     assert torch.equal(same.cpu(), got.cpu().expand(3, h))
     assert cm.rms_norm(torch.empty(0, h, device=dev)).shape == (0, h)
+
+
+@pytest.mark.parametrize("exponent", [-148, -140, -126, -100, -70, -61, -60, -59, 50, 99, 100, 101, 110, 119])
+def test_codes_at_every_magnitude(dev, exponent):
+    """Scales down to float32's subnormals and up to its largest values: the
+    codes are those of a correctly rounded division all the same."""
+    h = 256
+    x = make(3, h, F32, 12) * 3
+    w = torch.full((h,), 2.0 ** (exponent / 2 if exponent % 2 == 0 else (exponent + 1) / 2)) * 1.0
+    w = w * torch.tensor(2.0 ** (exponent - (exponent // 2 if exponent % 2 == 0 else (exponent + 1) // 2)), dtype=F32)
+    stored, y64, y32 = reference(x, w, 1e-6)
+    for dtype in (I8, E4):
+        for group in (0, 64):
+            (codes, scales), _ = run(dev, x, w, 1e-6, out_dtype=dtype, group=group)
+            q = 127.0 if dtype == I8 else 448.0
+            s = y32.view(3, -1, group or h).abs().amax(2) / q
+            assert torch.equal(scales.cpu(), s)
+            wide = s.repeat_interleave(group or h, 1)
+            v = torch.where(wide > 0, y32 / wide, torch.zeros_like(y32)).clamp(-q, q)
+            want = (v.round() if dtype == I8 else v).to(dtype)
+            assert torch.equal(codes.cpu().view(torch.int8), want.view(torch.int8)), (exponent, dtype, group)
 
 
 def test_in_place(dev):

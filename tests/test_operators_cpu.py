@@ -91,8 +91,6 @@ def test_python_functions_refuse_host_tensors_and_wrong_shapes():
     x = torch.zeros(2, 64)
     with pytest.raises(ValueError, match="GPU"):
         cm.rms_norm(x)
-    with pytest.raises(ValueError, match="2-D"):
-        cm.rms_norm(x[0])
     with pytest.raises(ValueError, match="GPU"):
         cm.balance_loss(x, torch.zeros(2, 2, dtype=torch.int32), 0.01)
     with pytest.raises(ValueError, match="GPU"):
