@@ -510,9 +510,10 @@ int coli_moe_test_cache_policy(int32_t n_experts, int32_t n_slots, int32_t reser
  * shorter), Q = 127 (int8) or 448 (e4m3):
  *   scales[row][g] = max|y| / Q over the group (float32 division),
  *   out = round(y / scale), to the nearest, ties to even, |out| <= Q;
- * a group of zeros has scale 0 and codes 0.  Inputs must be finite; a row
- * that holds Inf or NaN gets an unspecified output, other rows are not
- * affected.
+ * a group of zeros has scale 0 and codes 0, and a row of zeros stays zero
+ * without eps too.  Inputs must be finite; a row that holds Inf or NaN gets an
+ * unspecified output, other rows are not affected.  The stride of a single
+ * row is not looked at.
  */
 typedef struct {
   int32_t rows;           /* >= 0; 0 checks the arguments and enqueues nothing */
@@ -578,7 +579,7 @@ typedef struct {
   const float *x_scale;  /* 8-bit types: [m], else NULL */
   const float *w_scale;  /* 8-bit types: [n] (SwiGLU [2 n]), else NULL */
   const void *bias;      /* [n] (SwiGLU [2 n]); NULL: none */
-  const void *residual;  /* NULL: none; may be `out` itself */
+  const void *residual;  /* NULL: none; may be `out` itself, else no overlap with it */
   int64_t ldr;
   void *out;             /* no overlap with x, w, scales or bias */
   int64_t ldo;
@@ -615,13 +616,15 @@ int coli_moe_linear(const coli_moe_linear_t *a, void *stream);
  * is 0; gradient rows of tokens in no sequence (before the first or behind
  * the last) are left as they were.  Offsets outside [0, tokens] are clamped;
  * offsets that decrease give unspecified results within the output arrays.
- * Sums over tokens: float32 within a workgroup, then float64, in a fixed
- * order, so the same call gives the same bits.
+ * A valid token with a NaN or +Inf logit has unspecified shares.  Outputs may
+ * not overlap inputs.
+ * Sums over tokens: float32 within a workgroup (at most 4096 tokens), then
+ * float64, in a fixed order, so the same call gives the same bits.
  */
 #define COLI_MOE_SCORES_SIGMOID 0
 #define COLI_MOE_SCORES_SOFTMAX 1
 typedef struct {
-  int32_t tokens;             /* rows of logits, idx and mask; >= 0 */
+  int32_t tokens;             /* rows of logits, idx and mask; 0..2^26 */
   int32_t n_experts;          /* 1..512 */
   int32_t top_k;              /* 1..32, <= n_experts */
   int32_t n_seqs;             /* 1..65536 */

@@ -604,6 +604,8 @@ def linear(x, w, x_scale=None, w_scale=None, bias=None, act: str = "none", resid
     m, k = x.shape
     ldw = _matrix(w, "w", dev, None, k, x.dtype)
     code = _dtype_code(x.dtype, "x", True)
+    if code == COLI_MOE_F32:
+        raise ValueError("x: unsupported type torch.float32 (bf16, f16, int8 or float8_e4m3fn)")
     if act not in _ACTS:
         raise ValueError(f"act: one of {', '.join(_ACTS)}, got {act!r}")
     n = rows = w.shape[0]

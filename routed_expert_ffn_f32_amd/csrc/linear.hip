@@ -1,7 +1,12 @@
 // Dense products with their epilogue (coli_moe_linear) for more than a few
 // rows: out = act(x w^T [* sx sw] + bias) + residual.
 //
-// Bound by the matrix cores: 2 m n k operations on (m + n) k elements.  A
+// Bound by the matrix cores: 2 m n k operations on (m + n) k elements.  8192^3
+// runs at 1.33 PFLOP/s in bf16 (the library's product: 1.49), 4096 x 6144 x
+// 6144 at 1.12 (the library's: 1.12); there the chip is held by its power:
+// the same call on zeros takes two thirds of the time, and reading every
+// operand row from the L2 alone changes less.  4096 x 2 2048 x 6144 in int8
+// with SwiGLU runs at 2.26 PFLOP/s, e4m3 on the 16-bit cores at 1.29.  A
 // workgroup computes a tile of BM x BN outputs over all of K in steps of 128
 // bytes of every row (64 16-bit or 128 8-bit elements: one whole cache line a
 // row).  Rows of x and w go straight into LDS by LDS-DMA, kStages steps deep,

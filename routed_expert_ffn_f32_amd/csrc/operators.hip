@@ -12,8 +12,9 @@ bool aligned_to(const void *p, size_t a) { return p && ((uintptr_t)p % a) == 0; 
 // A [rows] array of rows of `cols` elements: pointer and stride usable.
 // Rows that are written must not overlap (a stride of 0 reads one row for all).
 bool rows_ok(const void *p, int type, int64_t stride, int64_t cols, int64_t rows, bool written) {
-  return aligned_to(p, coli::type_bytes(type)) && stride >= 0 && stride <= (int64_t)1 << 40 &&
-         (!written || rows <= 1 || stride >= cols);
+  constexpr int64_t kMaxOffset = (int64_t)1 << 56;  // elements; no array is that long
+  return aligned_to(p, coli::type_bytes(type)) &&
+         (rows <= 1 || (stride >= 0 && stride <= kMaxOffset / rows && (!written || stride >= cols)));
 }
 
 struct Rows {
@@ -85,14 +86,13 @@ int coli_moe_linear(const coli_moe_linear_t *a, void *stream) {
 
 namespace {
 
-constexpr int32_t kMaxSeqs = 65536;
+constexpr int32_t kMaxSeqs = 65536, kMaxTokens = 1 << 26;
 
 int balance_check(const coli_moe_balance_t *a) {
-  if (!a || a->tokens < 0 || a->n_seqs < 1 || a->n_seqs > kMaxSeqs) return COLI_MOE_EARG;
+  if (!a || a->tokens < 0 || a->tokens > kMaxTokens || a->n_seqs < 1 || a->n_seqs > kMaxSeqs) return COLI_MOE_EARG;
   if (a->n_experts < 1 || a->n_experts > coli::kMaxExperts || a->top_k < 1 || a->top_k > a->n_experts ||
       a->top_k > coli::kMaxTopK)
     return COLI_MOE_EROUTING;
-  if ((int64_t)a->tokens * a->top_k > INT32_MAX - (1 << 20)) return COLI_MOE_EARG;
   if (a->scores != COLI_MOE_SCORES_SIGMOID && a->scores != COLI_MOE_SCORES_SOFTMAX) return COLI_MOE_EARG;
   if (a->seq_offsets ? !aligned_to(a->seq_offsets, 4) : a->n_seqs != 1) return COLI_MOE_EARG;
   if (a->tokens > 0 && !rows_ok(a->logits, COLI_MOE_F32, a->logits_stride, a->n_experts, a->tokens, false))
@@ -105,7 +105,7 @@ int balance_check(const coli_moe_balance_t *a) {
 extern "C" {
 
 size_t coli_moe_balance_workspace_bytes(int32_t tokens, int32_t n_experts, int32_t n_seqs) {
-  if (tokens < 0 || n_experts < 1 || n_experts > coli::kMaxExperts || n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
+  if (tokens < 0 || tokens > kMaxTokens || n_experts < 1 || n_experts > coli::kMaxExperts || n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
   return coli::balance_workspace_bytes(tokens, n_experts, n_seqs);
 }
 

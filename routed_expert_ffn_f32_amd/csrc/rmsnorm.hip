@@ -85,15 +85,18 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
   __shared__ float max_of[WAVES];
   const int wave = WAVES == 1 ? 0 : (int)(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int tid = WAVES == 1 ? lane % LANES : (int)threadIdx.x;
-  int64_t row = blockIdx.x;
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  int64_t row = block;
   if constexpr (WAVES == 1) {
-    row = row * (256 / LANES) + threadIdx.x / LANES;
+    row = block * (256 / LANES) + threadIdx.x / LANES;
     if constexpr (LANES == 64) row = uniform((int)row);
     // whole waves without a row leave; in a wave with some, the lanes of the
     // missing rows repeat the last row, with the same results
-    const int64_t wave_row = (int64_t)blockIdx.x * (256 / LANES) + (threadIdx.x & ~63) / LANES;
+    const int64_t wave_row = block * (256 / LANES) + (threadIdx.x & ~63) / LANES;
     if (wave_row >= a.rows) return;
     row = row < a.rows ? row : a.rows - 1;
+  } else if (row >= a.rows) {
+    return;
   }
   const int h = a.hidden;
 
@@ -228,7 +231,10 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
 template <int LANES, int WAVES, int NCH>
 hipError_t launch_shape(const coli_moe_rmsnorm_t &a, hipStream_t s) {
   constexpr int kRows = WAVES == 1 ? 256 / LANES : 1;
-  const dim3 grid((uint32_t)(((int64_t)a.rows + kRows - 1) / kRows)), block(WAVES == 1 ? 256 : 64 * WAVES);
+  // threads along one axis of a grid are counted in 32 bits
+  constexpr uint32_t kMaxX = 1u << 20;
+  const uint32_t blocks = (uint32_t)(((int64_t)a.rows + kRows - 1) / kRows);
+  const dim3 grid(blocks < kMaxX ? blocks : kMaxX, (blocks + kMaxX - 1) / kMaxX), block(WAVES == 1 ? 256 : 64 * WAVES);
   return a.hidden % kVec == 0 ? launch(rmsnorm_kernel<LANES, WAVES, NCH, true>, grid, block, 0, s, a)
                               : launch(rmsnorm_kernel<LANES, WAVES, NCH, false>, grid, block, 0, s, a);
 }

@@ -35,7 +35,7 @@ def test_rmsnorm_refusals():
     two = dict(rows=2)
     for bad in (dict(x=None), dict(out=None), dict(x=A + 2), dict(out=A + 0x10002), dict(weight=A + 1),
                 dict(x_type=1, x=A + 1), dict(out_stride=63), dict(out_stride=-64), dict(x_stride=-1),
-                dict(x_stride=1 << 41), dict(out_type=3), dict(out_type=3, scales=A + 2, scales_stride=1),
+                dict(x_stride=1 << 56), dict(out_type=3), dict(out_type=3, scales=A + 2, scales_stride=1),
                 dict(out_type=3, scales=A, scales_stride=0),
                 dict(out_type=4, group=64, hidden=65, x_stride=65, out_stride=65, scales=A, scales_stride=1),
                 dict(residual=A, residual_stride=64, residual_out=A + 0x20000, residual_out_stride=63),
@@ -70,7 +70,7 @@ def test_balance_refusals():
     assert grad_rc() == 0  # no tokens
     sizes = [(dict(tokens=-1), -4), (dict(n_seqs=0), -4), (dict(n_seqs=65537, seq_offsets=A), -4),
              (dict(n_experts=0), -2), (dict(n_experts=513, top_k=1), -2), (dict(top_k=0), -2), (dict(top_k=9), -2),
-             (dict(n_experts=64, top_k=33), -2), (dict(tokens=1 << 30, top_k=2), -4), (dict(scores=2), -4),
+             (dict(n_experts=64, top_k=33), -2), (dict(tokens=(1 << 26) + 1), -4), (dict(scores=2), -4),
              (dict(n_seqs=2), -4), (dict(n_seqs=2, seq_offsets=A + 2), -4), (dict(tokens=4, logits=None), -4),
              (dict(tokens=4, logits=A + 2), -4), (dict(tokens=4, logits_stride=-1), -4)]
     for bad, code in sizes:
@@ -82,7 +82,7 @@ def test_balance_refusals():
     assert balance_rc(tokens=100, nbytes=cm.coli_moe_balance_workspace_bytes(100, 8, 1) - 1) == -1
     for bad in (dict(coef=None), dict(tokens=4, out=None), dict(tokens=4, stride=7), dict(dloss=A + 1)):
         assert grad_rc(**bad) == -4, bad
-    for bad in ((-1, 8, 1), (4, 0, 1), (4, 513, 1), (4, 8, 0), (4, 8, 65537)):
+    for bad in ((-1, 8, 1), ((1 << 26) + 1, 8, 1), (4, 0, 1), (4, 513, 1), (4, 8, 0), (4, 8, 65537)):
         assert cm.coli_moe_balance_workspace_bytes(*bad) == 0
     assert lib.coli_moe_last_logits(None, A, None) == -4
 
