@@ -685,11 +685,10 @@ def balance_loss(logits, idx, alpha: float, scores: str = "sigmoid", offsets=Non
     coef.  coli_moe_balance in include/coli_moe.h gives the formulas."""
     import torch
     a, dev, T, E, S = _balance_args(logits, idx, alpha, scores, offsets, mask)
-    loss = torch.empty(S, dtype=torch.float32, device=dev)
-    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-    coef = torch.empty((S, E), dtype=torch.float32, device=dev)
+    loss, coef = logits.new_empty((S,)), logits.new_empty((S, E))
+    counts = logits.new_empty((S, E), dtype=torch.int32)
     nbytes = coli_moe_balance_workspace_bytes(T, E, S)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = logits.new_empty(((nbytes + 3) // 4,))
     _enqueue("coli_moe_balance", dev, a, loss.data_ptr(), counts.data_ptr(), coef.data_ptr(), ws.data_ptr(), nbytes)
     return loss, counts, coef
 

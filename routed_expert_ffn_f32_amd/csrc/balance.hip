@@ -40,6 +40,7 @@ constexpr int kSumWaves = 16;        // waves of a workgroup of the sums
 constexpr int kSumThreads = 64 * kSumWaves;
 constexpr int kMaxChunks = 256;      // workgroups of the sums, up to 2^20 tokens
 constexpr int kBatchTokens = kTok * kSumWaves;  // tokens they take at a time
+constexpr int kAloneSeqs = 8;        // sequences of one batch that its workgroup finishes itself, one by one
 constexpr int kGradWaves = 4;        // waves of a workgroup of the gradient, four tokens each
 
 // A token's scores: v = exp(z - max) (softmax) or sigma(z), slope = its own
@@ -166,12 +167,46 @@ struct Tokens {
 // words: E floats, then E + 1 ints).
 __host__ __device__ inline size_t slot_words(int E) { return 2 * (size_t)E + 1; }
 
+// What the sums of a sequence give: V valid tokens, N kept assignments, dot =
+// sum_e n_e sum_t p_te, and thread `col`'s own count c.
+__device__ __forceinline__ void finish_sequence(const coli_moe_balance_t &a, int s, int col, bool mine, int c, double V,
+                                                double N, double dot, float *loss, int32_t *counts, float *coef) {
+  const bool some = V > 0.0 && N > 0.0;
+  const double per_token = some ? (double)a.alpha / V : 0.0, share = some ? a.n_experts / N : 0.0;
+  if (threadIdx.x == 0) loss[s] = (float)(per_token * share * dot);
+  if (mine) {
+    counts[(size_t)s * a.n_experts + col] = c;
+    coef[(size_t)s * a.n_experts + col] = (float)(per_token * ((double)c * share - 1.0));
+  }
+}
+
+// Totals of N values over a workgroup of 1024 threads, in every thread.
+template <int N>
+__device__ __forceinline__ void block_totals(double (&v)[N], double (*scratch)[16]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = lanes_sum64<64>(v[i]);
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) scratch[i][threadIdx.x >> 6] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = 0.0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v[i] += scratch[i][w];
+  }
+}
+
 // A workgroup takes its tokens 64 at a time, four a wave; their loads need no
 // knowledge of the sequences and go out first.  A piece's sums stay in
-// registers (shares) and LDS (counts) until the piece ends.
-template <int NE, bool SOFTMAX>
-__global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(coli_moe_balance_t a, int chunk_tokens,
-                                                                   float *slots) {
+// registers (shares) and LDS (counts) until the piece ends.  ALONE: one
+// workgroup and one batch hold every token, so each piece is a whole sequence
+// and is finished on the spot (64 tokens: one launch of 5.6 us instead of two
+// of 5.0 and 3.9 us and the gap between them).
+template <int NE, bool SOFTMAX, bool ALONE>
+__global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(coli_moe_balance_t a, int chunk_tokens, float *slots,
+                                                                   float *loss, int32_t *counts, float *coef) {
+  __shared__ double totals[2][16];
   constexpr int kBatch = kBatchTokens, kIdx = kBatch * kMaxTopK / kSumThreads;
   __shared__ float mass[kSumWaves][64 * NE];
   __shared__ int hist[64 * NE];
@@ -195,7 +230,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(coli_moe_bala
   Bounds bounds;
   bounds.load(a, 0);
   load(lo);
-  int s = bounds.seek(a, lo);
+  int s = ALONE ? 0 : bounds.seek(a, lo);
   for (int i = threadIdx.x; i < E; i += kSumThreads) hist[i] = 0;
   if (threadIdx.x == 0) valid = 0;
   __syncthreads();
@@ -222,8 +257,11 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(coli_moe_bala
     const int stop = min(t0 + kBatch, hi);
     for (; s < a.n_seqs; ++s) {
       const int begin = bounds.at(a, s), end = bounds.at(a, s + 1);
-      if (begin >= stop) break;
-      if (begin >= end) continue;
+      if (!ALONE && begin >= stop) break;
+      if (begin >= end) {
+        if (ALONE) finish_sequence(a, s, threadIdx.x, (int)threadIdx.x < E, 0, 0.0, 0.0, 0.0, loss, counts, coef);
+        continue;
+      }
 #pragma unroll
       for (int t = 0; t < kTok; ++t) {
         const int tok = t0 + wave + t * kSumWaves;
@@ -236,7 +274,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(coli_moe_bala
 #pragma unroll
       for (int q = 0; q < kIdx; ++q)
         if ((uint32_t)e_now[q] < (uint32_t)E && of_now[q] >= begin && of_now[q] < end) atomicAdd(&hist[e_now[q]], 1);
-      if (end > stop && stop < hi) break;  // goes on in the workgroup's next batch
+      if (!ALONE && end > stop && stop < hi) break;  // goes on in the workgroup's next batch
       // the piece ends: its sums to its slot
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
@@ -246,22 +284,34 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(coli_moe_bala
       if (lane == 0) atomicAdd(&valid, seen);
       seen = 0;
       __syncthreads();
-      float *slot = slots + (size_t)(blockIdx.x + s) * slot_words(E);
-      int *cnt = reinterpret_cast<int *>(slot + E);
-      for (int e = threadIdx.x; e < E; e += kSumThreads) {
-        float m = 0.0f;
+      static_assert(64 * NE <= kSumThreads, "an expert a thread");
+      const int e = threadIdx.x;
+      float m = 0.0f;
+      int c = 0;
+      const int valid_now = valid;
+      if (e < E) {
 #pragma unroll
         for (int w = 0; w < kSumWaves; ++w) m += mass[w][e];
-        slot[e] = m;
-        cnt[e] = hist[e];
+        c = hist[e];
         hist[e] = 0;
       }
-      if (threadIdx.x == 0) {
-        cnt[E] = valid;
-        valid = 0;
+      if constexpr (ALONE) {
+        double sums[2] = {(double)c, (double)c * (double)m};
+        block_totals(sums, totals);
+        finish_sequence(a, s, e, e < E, c, (double)valid_now, sums[0], sums[1], loss, counts, coef);
+      } else {
+        float *slot = slots + (size_t)(blockIdx.x + s) * slot_words(E);
+        int *cnt = reinterpret_cast<int *>(slot + E);
+        if (e < E) {
+          slot[e] = m;
+          cnt[e] = c;
+        }
+        if (e == 0) cnt[E] = valid_now;
       }
       __syncthreads();
-      if (end > stop) break;  // the workgroup's last batch
+      if (threadIdx.x == 0) valid = 0;
+      __syncthreads();
+      if (!ALONE && end > stop) break;  // the workgroup's last batch
     }
   }
 }
@@ -317,25 +367,9 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(coli_moe_balance_t
     c = 0;
   }
   // valid tokens, kept assignments (whole numbers, exact) and their product with the shares
-  const double sums[3] = {lanes_sum64<64>((double)v), lanes_sum64<64>((double)c), lanes_sum64<64>((double)c * m)};
-  if ((threadIdx.x & 63) == 0)
-#pragma unroll
-    for (int i = 0; i < 3; ++i) totals[i][threadIdx.x >> 6] = sums[i];
-  __syncthreads();
-  double V = 0.0, N = 0.0, dot = 0.0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    V += totals[0][i];
-    N += totals[1][i];
-    dot += totals[2][i];
-  }
-  const bool some = V > 0.0 && N > 0.0;
-  const double per_token = some ? (double)a.alpha / V : 0.0, share = some ? E / N : 0.0;
-  if (threadIdx.x == 0) loss[s] = (float)(per_token * share * dot);
-  if (grp == 0 && col < E) {
-    counts[(size_t)s * E + col] = c;
-    coef[(size_t)s * E + col] = (float)(per_token * ((double)c * share - 1.0));
-  }
+  double sums[3] = {(double)v, (double)c, (double)c * m};
+  block_totals(sums, totals);
+  finish_sequence(a, s, col, grp == 0 && col < E, c, sums[0], sums[1], sums[2], loss, counts, coef);
 }
 
 template <int NE, bool SOFTMAX>
@@ -423,10 +457,16 @@ hipError_t launch_balance(const coli_moe_balance_t &a, float *loss, int32_t *cou
   const int chunk = chunk_tokens_of(a.tokens), n = chunks_of(a.tokens);
   return by_experts(a.n_experts, [&](auto ne) {
     constexpr int NE = decltype(ne)::value;
+    const auto sums = [&](auto softmax, auto alone) {
+      return launch(balance_sums_kernel<NE, decltype(softmax)::value, decltype(alone)::value>, dim3(n),
+                    dim3(kSumThreads), 0, s, a, chunk, slots, loss, counts, coef);
+    };
+    const bool softmax = a.scores == COLI_MOE_SCORES_SOFTMAX;
+    if (n == 1 && a.tokens <= kBatchTokens && a.n_seqs <= kAloneSeqs)
+      return softmax ? sums(std::true_type(), std::true_type()) : sums(std::false_type(), std::true_type());
     if (n > 0) {
-      const hipError_t e = a.scores == COLI_MOE_SCORES_SOFTMAX
-                               ? launch(balance_sums_kernel<NE, true>, dim3(n), dim3(kSumThreads), 0, s, a, chunk, slots)
-                               : launch(balance_sums_kernel<NE, false>, dim3(n), dim3(kSumThreads), 0, s, a, chunk, slots);
+      const hipError_t e =
+          softmax ? sums(std::true_type(), std::false_type()) : sums(std::false_type(), std::false_type());
       if (e != hipSuccess) return e;
     }
     return launch(balance_finish_kernel<NE>, dim3(a.n_seqs), dim3(1024), 0, s, a, chunk, slots, loss, counts, coef);

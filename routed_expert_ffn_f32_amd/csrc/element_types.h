@@ -59,20 +59,27 @@ __device__ __forceinline__ Raw8 load_raw8(const void *base, int type, int64_t i)
   return r;
 }
 
-// The same, those at n and beyond 0 and not read.
+// The same, those at n and beyond 0 and not read.  The last, partial eight
+// loads its elements from indices held below n, without conditions: a branch
+// around each made one wait for the other (a row of 2047 halves: 7 memory
+// round trips for every array).
 __device__ __forceinline__ Raw8 load_raw8(const void *base, int type, int64_t i, int n) {
   if (n >= 8) return load_raw8(base, type, i);
   Raw8 r = {u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
+  if (n <= 0) return r;
+  uint32_t t[7];
   if (type == COLI_MOE_F32) {
     const uint32_t *p = static_cast<const uint32_t *>(base) + i;
 #pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (j < n) (j < 4 ? r.lo : r.hi)[j & 3] = p[j];
+    for (int j = 0; j < 7; ++j) t[j] = p[min(j, n - 1)];
+#pragma unroll
+    for (int j = 0; j < 7; ++j) (j < 4 ? r.lo : r.hi)[j & 3] = j < n ? t[j] : 0u;
   } else {
     const uint16_t *p = static_cast<const uint16_t *>(base) + i;
 #pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (j < n) r.lo[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+    for (int j = 0; j < 7; ++j) t[j] = p[min(j, n - 1)];
+#pragma unroll
+    for (int j = 0; j < 7; ++j) r.lo[j / 2] |= (j < n ? t[j] : 0u) << (16 * (j & 1));
   }
   return r;
 }
