@@ -52,6 +52,7 @@ struct Tile {
   static constexpr int kEpilogueBytes = WM * 32 * kRowFloats * 4;
   static constexpr int kRing = STAGES * kStageBytes;
   static constexpr int kLds = kRing > kEpilogueBytes ? kRing : kEpilogueBytes;
+  static constexpr int kPerCu = 160 * 1024 / kLds;
   static_assert(kLds <= 160 * 1024, "the ring exceeds a CU's LDS");
   static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "copies of 8 rows, as many for each wave");
   static_assert(!GATED || BN % 64 == 0, "pairs of gate and up blocks");
@@ -180,12 +181,14 @@ struct Tile {
   // numbered 4 g .. 4 g + 3, the first group reads in turns 4 g and 4 g + 2
   // and multiplies in the other two; the second does the same one turn later.
   // Step g - 1's slot was last read in turn 4 g - 1 (second group), so step
-  // g + 1 is copied into it from turn 4 g on: half of a wave's copies go out
-  // with the reads of the step's first half (turn 4 g or 4 g + 1), the others
-  // between products, in turn 4 g + 1 (first group) and 4 g (second group,
-  // with its last products of step g - 1).  Both groups await their copies
-  // before the barrier that ends turn 4 g + 3, behind which turn 4 g + 4 reads
-  // them.  (8192^3 bf16: 827 us; all copies with the reads 894 us, all between
+  // g + STAGES - 1 is copied into it from turn 4 g on: half of a wave's copies
+  // go out with the reads of the step's first half (turn 4 g or 4 g + 1), the
+  // others between products, in turn 4 g + 1 (first group) and 4 g (second
+  // group, with its last products of step g - 1).  Both groups await their
+  // copies of step g + 1, those of later steps still going, before the barrier
+  // that ends turn 4 g + 3, behind which turn 4 g + 4 reads them.  A third
+  // stage pays where it fits beside one workgroup a CU (256 x 128: m = 1024 in
+  // 82 us, with two 110).  (8192^3 bf16: 827 us; all copies with the reads 894 us, all between
   // products 843 us; without the raised priority of the multiplying waves
   // 903 us; every wave at its own pace, one barrier a step, 1100 us.)  The
   // copies have no conditions: past the last step they fetch it again, into
@@ -194,40 +197,51 @@ struct Tile {
   template <bool SECOND>
   static __device__ __forceinline__ void alternate(const Sources &S, int G, uint32_t lds, const char *lds_mem, int wm,
                                                    int wn, int wave, int lane, Acc (&acc)[MB][NB]) {
-    static_assert(STAGES == 2, "one step computed, one copied");
-    auto copy_step = [&](int g, int i) {
-      copy_whole(S, i, (int64_t)min(g, G - 1) * kStepBytes, lds + (g & 1) * kStageBytes, wave);
-    };
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy_step(0, i);
-    dma_wait<0>();
-    turn();
+    constexpr int kAhead = STAGES - 1;    // steps between a copy and its use
     constexpr int kInRead = kCopies / 2;  // copies issued in a read turn, the others between products
+    // copy i of step g into the slot that the ring gives it
+    auto copy_step = [&](int g, int slot, int i) {
+      copy_whole(S, i, (int64_t)min(g, G - 1) * kStepBytes, lds + slot * kStageBytes, wave);
+    };
+    auto next = [](int slot) { return slot + 1 == STAGES ? 0 : slot + 1; };
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g)
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) copy_step(g, g, i);
+    dma_wait<kCopies *(STAGES - 2)>();
+    turn();
     if (SECOND) {
 #pragma unroll
-      for (int i = kInRead; i < kCopies; ++i) copy_step(1, i);
+      for (int i = kInRead; i < kCopies; ++i) copy_step(kAhead, kAhead, i);
       turn();
     }
+    int slot = 0, fill = kAhead;  // slots of step g and of step g + kAhead
     for (int g = 0; g < G; ++g) {
-      const char *stage = lds_mem + (g & 1) * kStageBytes;
+      if constexpr (STAGES == 2) {
+        slot = g & 1;
+        fill = slot ^ 1;
+      }
+      const char *stage = lds_mem + slot * kStageBytes;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint4 af[MB][2], bf[NB][2];
         fetch_half(stage, wm, wn, lane, h, af, bf);
         if (h == 0)
 #pragma unroll
-          for (int i = 0; i < kInRead; ++i) copy_step(g + 1, i);
-        if (h == 1 && SECOND) dma_wait<0>();
+          for (int i = 0; i < kInRead; ++i) copy_step(g + kAhead, fill, i);
+        if (h == 1 && SECOND) dma_wait<kCopies *(STAGES - 2)>();
         lds_wait();
         turn();
         __builtin_amdgcn_s_setprio(1);
         multiply_half(af, bf, acc, [&](int i) {
-          if (SECOND == (h == 1) && i >= kInRead) copy_step(g + 1 + h, i);
+          if (SECOND == (h == 1) && i >= kInRead) copy_step(g + kAhead + h, h ? (STAGES == 2 ? slot : next(fill)) : fill, i);
         });
         __builtin_amdgcn_s_setprio(0);
-        if (h == 1 && !SECOND) dma_wait<0>();
+        if (h == 1 && !SECOND) dma_wait<kCopies *(STAGES - 2)>();
         turn();
       }
+      slot = next(slot);
+      fill = next(fill);
     }
     if (!SECOND) turn();
     dma_wait<0>();
@@ -366,13 +380,19 @@ struct Tile {
   static __device__ __forceinline__ void finish_slab(const coli_moe_linear_t &a, int m0, int n0, int mb, float *sums) {
     constexpr int kParts = kOutN / 8, kTurns = WM * 32 * kParts / kThreads;
     static_assert(kTurns * kThreads == WM * 32 * kParts, "whole turns of the threads");
+    // The slabs' loop leaves each thread's columns alone, and the compiler would
+    // compute every address of every turn ahead of it and keep them all (100
+    // registers, of which other workgroups of the CU have no use); an index
+    // that it cannot see through keeps them in the loop.
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
     auto row = [&](int i) {
-      const int r = (threadIdx.x + i * kThreads) / kParts;
+      const int r = (tid + i * kThreads) / kParts;
       return m0 + ((r >> 5) * MB + mb) * 32 + (r & 31);
     };
-    auto column = [&](int i) { return n0 + (int)(threadIdx.x + i * kThreads) % kParts * 8; };
+    auto column = [&](int i) { return n0 + (tid + i * kThreads) % kParts * 8; };
     auto place = [&](int i) {
-      const int q = threadIdx.x + i * kThreads, r = q / kParts, c = q % kParts * 8;
+      const int q = tid + i * kThreads, r = q / kParts, c = q % kParts * 8;
       return sums + r * kRowFloats + (GATED ? (c >> 5) * 64 + (c & 31) : c);
     };
     Raw8 res[kTurns];
@@ -416,8 +436,10 @@ struct Tile {
   }
 };
 
+// kPerCu workgroups of the shape share a CU by their LDS; the registers have
+// to leave room for as many.
 template <class T>
-__global__ __launch_bounds__(T::kThreads) void linear_tile_kernel(coli_moe_linear_t a) {
+__global__ __launch_bounds__(T::kThreads, T::kPerCu * T::kWaves / 4) void linear_tile_kernel(coli_moe_linear_t a) {
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
   T::run(a, lds);
 }
@@ -435,20 +457,22 @@ hipError_t launch_tiles(const coli_moe_linear_t &a, hipStream_t s) {
 // The shapes a product of more than kLinearRowsMax rows can take, with what
 // they cost: microseconds measured at 12288 bytes of K (6144 bf16 elements;
 // n = 6144, m from 64 to 4096, three sets of operands in turn) for up to one
-// block a CU, and for a full chip where two blocks share a CU.
+// block a CU, and for a round that fills the chip (per_cu blocks on every CU,
+// the clock held by the power).  (128 x 128 blocks with two stages, two a CU,
+// took 63 us at m = 512 and 103 at 1024: never the least.)
 struct Shape {
   int bm, bn;         // rows of x and of w of a block
   int per_cu;         // blocks a CU holds
-  int one, full;      // cost with at most one block a CU, and with per_cu of them
+  int one, full;      // cost of a round with fewer blocks, and of a full one
 };
 constexpr int kCus = 256;
 constexpr Shape kShapes[] = {
-    {64, 32, 1, 17, 17},     // linear_rows: m = 64 in 18 us, 128 in 34, 256 in 50
-    {64, 64, 1, 28, 28},     // linear_rows: m = 128 in 29 us, 256 in 55
-    {128, 64, 2, 53, 64},    // four waves: m = 256 in 53 us, 512 in 64, 1024 in 125
-    {128, 128, 2, 63, 110},  // eight waves: m = 512 in 64 us, 1024 in 111, 2048 in 207
-    {256, 192, 1, 137, 137}, // m = 2048 in 142 us, 4096 in 274 (two full rounds)
-    {256, 256, 1, 150, 150}, // m = 2048 in 150 us, 4096 in 300 (two rounds, the second half empty)
+    {64, 32, 1, 17, 17},      // linear_rows: m = 64 in 18 us, 128 in 34, 256 in 50
+    {64, 64, 1, 27, 27},      // linear_rows: m = 128 in 26 to 29 us, 256 in 48 to 55
+    {128, 64, 2, 50, 62},     // four waves: m = 256 in 48 to 53 us, 512 in 60 to 64, 1024 in 120
+    {256, 128, 1, 84, 91},    // eight waves: m = 1024 in 82 us (192 blocks), 4096 in 273 (three full rounds)
+    {256, 192, 1, 136, 136},  // m = 2048 in 140 us, 4096 in 272 (two full rounds)
+    {256, 256, 1, 150, 150},  // m = 2048 in 152 us, 4096 in 296 (two rounds, the second half empty)
 };
 
 // The shape with the least cost: rounds of blocks over the CUs times the
@@ -474,7 +498,7 @@ template <int TYPE>
 hipError_t launch_type(const coli_moe_linear_t &a, int shape, hipStream_t s) {
   switch (shape) {
     case 2: return launch_tiles<TYPE, 2, 1, 2, 2, 3>(a, s);
-    case 3: return launch_tiles<TYPE, 2, 1, 2, 4, 2>(a, s);
+    case 3: return launch_tiles<TYPE, 2, 2, 4, 2, 3>(a, s);
     case 4: return launch_tiles<TYPE, 2, 3, 4, 2, 2>(a, s);
     default: return launch_tiles<TYPE, 4, 2, 2, 4, 2>(a, s);
   }

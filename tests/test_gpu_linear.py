@@ -102,7 +102,8 @@ def test_sizes_exactly(dev, m, n, k, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("m,n,k", [(129, 8200, 136), (500, 4096, 328), (700, 5000, 200), (4000, 6100, 136),
+@pytest.mark.parametrize("m,n,k", [(129, 8200, 136), (500, 4096, 328), (1000, 6100, 200), (1000, 5000, 8),
+                                   (4000, 6100, 136),
                                    (3500, 3600, 264), (3329, 4000, 520), (4096, 3585, 64), (300, 5000, 8)])
 def test_every_block_shape_exactly(dev, m, n, k, kind):
     """Sizes that the choice of blocks sends to each of its shapes beyond the
@@ -112,7 +113,7 @@ def test_every_block_shape_exactly(dev, m, n, k, kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("m,n,k", [(1, 5, 64), (7, 100, 520), (30, 129, 264), (60, 300, 136), (129, 4099, 136),
-                                   (500, 2049, 72), (700, 2500, 200), (4000, 3050, 72), (3500, 1801, 136)])
+                                   (500, 2049, 72), (1000, 3050, 200), (4000, 3050, 72), (3500, 1801, 136)])
 def test_swiglu_on_every_block_shape(dev, m, n, k, kind):
     """Gate and up sums are exact integers here, so only the activation's own
     8 u |gate up| and the product's 2 u remain."""
