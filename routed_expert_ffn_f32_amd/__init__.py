@@ -520,12 +520,14 @@ def _enqueue(entry: str, device, *args) -> None:
     current and on its current stream."""
     import torch
     index = device.index
-    call = getattr(load_library(), entry)
-    if torch.cuda.current_device() == index:
-        _check(call(*args, torch._C._cuda_getCurrentRawStream(index)), entry)
+    call = getattr(_lib or load_library(), entry)
+    if torch._C._cuda_getDevice() == index:
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _check(call(*args, torch._C._cuda_getCurrentRawStream(index)), entry)
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc < 0:
+        raise ColiMoeError(rc, entry)
 
 
 def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None, out=None, scales=None,
@@ -546,7 +548,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
         out_dtype = x.dtype if out is None else out.dtype
     xt, ot = _dtype_code(x.dtype, "x"), _dtype_code(out_dtype, "out", True)
     if out is None:
-        out, ldo = torch.empty((rows, hidden), dtype=out_dtype, device=dev), hidden
+        out, ldo = x.new_empty((rows, hidden), dtype=out_dtype), hidden
     else:
         ldo = _matrix(out, "out", dev, rows, hidden, out_dtype)
     rt = wt = ldr = ldro = lds = 0
@@ -569,7 +571,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
             raise ValueError(f"group: 0, 64 or 128, got {group}")
         n = -(-hidden // group) if group else 1
         if scales is None:
-            scales, lds = torch.empty((rows, n), dtype=torch.float32, device=dev), n
+            scales, lds = x.new_empty((rows, n), dtype=torch.float32), n
         else:
             lds = _matrix(scales, "scales", dev, rows, n, torch.float32)
         sp = scales.data_ptr()
@@ -628,7 +630,7 @@ def linear(x, w, x_scale=None, w_scale=None, bias=None, act: str = "none", resid
             torch.bfloat16 if code > COLI_MOE_F16 else x.dtype
     ot = _dtype_code(out_dtype, "out")
     if out is None:
-        out, ldo = torch.empty((m, n), dtype=out_dtype, device=dev), n
+        out, ldo = x.new_empty((m, n), dtype=out_dtype), n
     else:
         ldo = _matrix(out, "out", dev, m, n, out_dtype)
     if residual is not None:
@@ -705,7 +707,7 @@ def balance_grad(logits, coef, dloss=None, scores: str = "sigmoid", offsets=None
     if dloss is not None:
         _vector(dloss, "dloss", dev, S, torch.float32)
     if out is None:
-        out, ldo = (torch.empty if offsets is None else torch.zeros)((T, E), dtype=torch.float32, device=dev), E
+        out, ldo = (logits.new_empty if offsets is None else logits.new_zeros)((T, E)), E
     else:
         ldo = _matrix(out, "out", dev, T, E, torch.float32)
     _enqueue("coli_moe_balance_grad", dev, a, coef.data_ptr(), None if dloss is None else dloss.data_ptr(),
