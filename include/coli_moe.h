@@ -511,9 +511,9 @@ int coli_moe_test_cache_policy(int32_t n_experts, int32_t n_slots, int32_t reser
  *   scales[row][g] = max|y| / Q over the group (float32 division),
  *   out = round(y / scale), to the nearest, ties to even, |out| <= Q;
  * a group of zeros has scale 0 and codes 0, and a row of zeros stays zero
- * without eps too.  Inputs must be finite; a row that holds Inf or NaN gets an
- * unspecified output, other rows are not affected.  The stride of a single
- * row is not looked at.
+ * without eps too.  A row whose s holds Inf or NaN becomes NaN (8 bits: its
+ * scales NaN, its codes 0); other rows are not affected.  Weights must be
+ * finite.  The stride of a single row is not looked at.
  */
 typedef struct {
   int32_t rows;           /* >= 0; 0 checks the arguments and enqueues nothing */
@@ -523,15 +523,15 @@ typedef struct {
   int32_t weight_type;    /* F32, BF16 or F16 */
   int32_t out_type;       /* any type */
   int32_t group;          /* 8-bit out: columns per scale, 64 or 128; 0 = the whole row.  Else 0 */
-  float eps;              /* >= 0 */
+  float eps;              /* >= 0, finite */
   const void *x;
   int64_t x_stride;
   const void *residual;   /* NULL: none */
   int64_t residual_stride;
-  void *residual_out;     /* may be `residual` itself; NULL exactly when residual is */
+  void *residual_out;     /* may be `residual` itself, or x with equal type and stride; NULL exactly when residual is */
   int64_t residual_out_stride;
   const void *weight;     /* [hidden]; NULL: ones */
-  void *out;              /* no overlap with an input, except out == x with equal type and stride */
+  void *out;              /* no overlap with residual_out or an input, except out == x with equal type and stride */
   int64_t out_stride;
   float *scales;          /* 8-bit out: [rows][1 or ceil(hidden / group)] */
   int64_t scales_stride;
@@ -616,8 +616,10 @@ int coli_moe_linear(const coli_moe_linear_t *a, void *stream);
  * is 0; gradient rows of tokens in no sequence (before the first or behind
  * the last) are left as they were.  Offsets outside [0, tokens] are clamped;
  * offsets that decrease give unspecified results within the output arrays.
- * A valid token with a NaN or +Inf logit has unspecified shares.  Outputs may
- * not overlap inputs.
+ * Scores are float32: those below 2^-126 count as 0, and a token whose scores
+ * are all 0 has shares and gradient 0.  A NaN logit of a valid token (softmax:
+ * +Inf too) makes its sequence's loss and its row of the gradient NaN.
+ * Outputs may not overlap inputs.
  * Sums over tokens: float32 within a workgroup (at most 4096 tokens), then
  * float64, in a fixed order, so the same call gives the same bits.
  */

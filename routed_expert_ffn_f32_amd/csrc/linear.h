@@ -147,7 +147,7 @@ __device__ __forceinline__ void activate8(const coli_moe_linear_t &a, int m, int
   switch (a.act) {
     case COLI_MOE_ACT_RELU:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fmaxf(v[j], 0.0f);
+      for (int j = 0; j < 8; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];  // keeps a NaN
       break;
     case COLI_MOE_ACT_SILU:
 #pragma unroll

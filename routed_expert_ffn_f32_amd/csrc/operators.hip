@@ -28,7 +28,7 @@ extern "C" {
 
 int coli_moe_rmsnorm(const coli_moe_rmsnorm_t *a, void *stream) {
   using namespace coli;
-  if (!a || a->rows < 0 || a->hidden < 1 || a->hidden > 32768 || !(a->eps >= 0.0f)) return COLI_MOE_EARG;
+  if (!a || a->rows < 0 || a->hidden < 1 || a->hidden > 32768 || !(a->eps >= 0.0f && a->eps <= 0x1.fffffep+127f)) return COLI_MOE_EARG;
   if (!float_type(a->x_type) || (!float_type(a->out_type) && !byte_type(a->out_type))) return COLI_MOE_EARG;
   if (byte_type(a->out_type) ? a->group != 0 && a->group != 64 && a->group != 128 : a->group != 0)
     return COLI_MOE_EARG;
@@ -46,6 +46,10 @@ int coli_moe_rmsnorm(const coli_moe_rmsnorm_t *a, void *stream) {
   if (a->residual && a->residual == a->residual_out && a->rows > 1 && a->residual_stride != a->residual_out_stride)
     return COLI_MOE_EARG;
   if (a->out == a->x && (a->out_type != a->x_type || (a->rows > 1 && a->out_stride != a->x_stride)))
+    return COLI_MOE_EARG;
+  if (a->residual_out && (a->residual_out == a->out || a->residual == a->out ||
+                          (a->residual_out == a->x && (a->residual_type != a->x_type ||
+                                                       (a->rows > 1 && a->residual_out_stride != a->x_stride)))))
     return COLI_MOE_EARG;
   if (a->weight && !aligned_to(a->weight, type_bytes(a->weight_type))) return COLI_MOE_EARG;
   if (byte_type(a->out_type)) {
@@ -79,6 +83,7 @@ int coli_moe_linear(const coli_moe_linear_t *a, void *stream) {
   if (!rows_ok(a->out, a->out_type, a->ldo, a->n, a->m, true)) return COLI_MOE_EARG;
   if (a->residual && !rows_ok(a->residual, a->out_type, a->ldr, a->n, a->m, false)) return COLI_MOE_EARG;
   if (a->residual == a->out && a->m > 1 && a->ldr != a->ldo) return COLI_MOE_EARG;
+  if (a->out == a->x || a->out == a->w) return COLI_MOE_EARG;
   return launch_linear(*a, static_cast<hipStream_t>(stream)) == hipSuccess ? COLI_MOE_OK : COLI_MOE_EDEVICE;
 }
 

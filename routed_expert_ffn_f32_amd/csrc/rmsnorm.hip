@@ -158,7 +158,8 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
     for (int i = 0; i < WAVES; ++i) sum += sum_of[i];
   }
   const double mean = sum / (double)h + (double)a.eps;
-  const float r = mean > 0.0 ? rsqrt64(mean) : 0.0f;  // a row of zeros without eps: zeros
+  // a row of zeros without eps: zeros; of Inf or NaN: NaN (for Inf, by the Newton steps)
+  const float r = mean != 0.0 ? rsqrt64(mean) : 0.0f;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
 #pragma unroll
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
 
   // 8 bits: the largest magnitude of the row or of each group (pieces past
   // the row's end hold zeros), then the codes
-  const bool e4m3 = a.out_type == COLI_MOE_E4M3;
+  const bool e4m3 = a.out_type == COLI_MOE_E4M3, finite = r == r;  // the maxima leave NaNs out
   const float q = e4m3 ? 448.0f : 127.0f;
   float m[NCH];
 #pragma unroll
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
 #pragma unroll
       for (int i = 0; i < WAVES; ++i) all = fmaxf(all, max_of[i]);
     }
-    const float scale = all / q;
+    const float scale = finite ? all / q : r;
     if (tid == 0) a.scales[row * a.scales_stride] = scale;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) m[i] = scale;
@@ -211,6 +212,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       m[i] = (a.group == 64 ? lanes_max<8>(m[i]) : lanes_max<16>(m[i])) / q;
+      if (!finite) m[i] = r;
       const int c = kVec * (i * kThreads + tid);
       if (c < h && c % a.group == 0) a.scales[row * a.scales_stride + c / a.group] = m[i];
     }

@@ -250,3 +250,40 @@ def test_graph_replays_and_two_graphs(dev):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want[k])), (rep, n)
             assert all(torch.equal(a, b) for a, b in zip(eager, want[(k + 1) % 3][:3]))
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E", [(48, 70), (300, 256), (300, 20)])
+def test_nan_stays_visible_and_where_it_is(dev, T, E, scores):
+    """A valid token's NaN logit makes its sequence's loss and its own row of
+    the gradient NaN, and nothing else; so does +Inf under softmax."""
+    z, idx, _ = make(T, E, 4, 77)
+    off = [0, 10, 20, T - 9, T]
+    od = torch.tensor(off, dtype=torch.int32, device=dev)
+    zd, ids = torch.from_numpy(z).to(dev), torch.from_numpy(idx).to(dev)
+    want = cm.balance_loss(zd, ids, ALPHA, scores, od)
+    dwant = cm.balance_grad(zd, want[2], None, scores, od)
+    for bad in [float("nan")] + ([float("inf")] if scores == "softmax" else []):
+        zn = zd.clone()
+        zn[13, E // 2] = bad
+        loss, counts, coef = cm.balance_loss(zn, ids, ALPHA, scores, od)
+        d = cm.balance_grad(zn, coef, None, scores, od)
+        assert loss.isnan().tolist() == [False, True, False, False]
+        assert torch.equal(loss[[0, 2, 3]], want[0][[0, 2, 3]]) and torch.equal(counts, want[1])
+        assert torch.equal(coef, want[2])
+        assert d[13].isnan().all() and torch.equal(d[:13], dwant[:13]) and torch.equal(d[14:], dwant[14:])
+
+
+def test_scores_at_the_end_of_their_range(dev):
+    """All of a token's sigmoid scores just above 2^-126: shares and gradient
+    hold, also with a large upstream gradient.  All below: shares and
+    gradient 0."""
+    z, idx, rng = make(20, 12, 3, 5)
+    z = (rng.uniform(-87.3, -84.0, size=z.shape)).astype(np.float32)  # exp(-87.3) = 2^-125.95
+    up = np.array([3e4, -3e4], np.float32)
+    # the error unit of d carries dloss: 3e4 * alpha / 20 * 48 U, far above 1e-37
+    check(dev, z, idx, [0, 10, 20], None, "sigmoid", up)
+    low = torch.full((20, 12), -95.0, device=dev)
+    ids = torch.from_numpy(idx).to(dev)
+    loss, _, coef = cm.balance_loss(low, ids, ALPHA)
+    assert loss.tolist() == [0.0] and not cm.balance_grad(low, coef).any()

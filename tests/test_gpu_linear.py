@@ -253,3 +253,22 @@ def test_another_stream_and_graph_replays(dev):
             torch.cuda.synchronize()
             assert torch.equal(y, want[i]), (m, i)
             block(xs[0])
+
+
+@pytest.mark.parametrize("m", [1, 20, 60, 200, 600])
+def test_nan_stays_visible(dev, m):
+    """A NaN in a row of x makes that row of the result NaN, one in w or the
+    bias its column, under every activation; the others are as without it."""
+    g = torch.Generator().manual_seed(m)
+    x, w = torch.randn(m, 136, generator=g).to(dev, BF16), torch.randn(2 * 96, 136, generator=g).to(dev, BF16)
+    bias = torch.randn(2 * 96, generator=g).to(dev)
+    xn, wn, bn = x.clone(), w.clone(), bias.clone()
+    xn[m // 2, 135], wn[5, 0], bn[90] = float("nan"), float("nan"), float("nan")
+    for act in ACTS:
+        rows = 2 * 96 if act == "swiglu" else 96
+        want = cm.linear(x, w[:rows], bias=bias[:rows], act=act, out_dtype=F32)
+        got = cm.linear(xn, wn[:rows], bias=bn[:rows], act=act, out_dtype=F32)
+        nan = torch.zeros(m, 96, dtype=torch.bool, device=dev)
+        nan[m // 2], nan[:, 5], nan[:, 90] = True, True, True
+        assert torch.equal(got.isnan(), nan), act
+        assert torch.equal(got[~nan], want[~nan]), act

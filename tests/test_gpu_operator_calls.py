@@ -73,10 +73,11 @@ def test_int8_at_its_largest(dev, m):
     assert (got == 2.0 ** 30).all()
 
 
-def test_many_short_rows(dev):
-    """More workgroups than one axis of the grid is given."""
-    rows = (1 << 20) * 16 + 5
-    x = torch.zeros(rows, 8, dtype=BF16, device=dev)
+@pytest.mark.parametrize("rows,hidden", [((1 << 20) * 16 + 5, 8), ((1 << 20) * 4 + 5, 136), ((1 << 20) + 3, 520)])
+def test_many_short_rows(dev, rows, hidden):
+    """More workgroups than one axis of the grid is given: several rows a wave,
+    a row a wave, a row a workgroup."""
+    x = torch.zeros(rows, hidden, dtype=BF16, device=dev)
     x[-3:] = 2.0
     out = cm.rms_norm(x, None, 0.0)
     assert (out[-3:] == 1).all() and not out[:-3].any()

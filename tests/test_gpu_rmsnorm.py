@@ -239,3 +239,28 @@ def test_another_stream_and_graph_replays(dev):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((codes, scales, r), want[i])), i
         cm.rms_norm(xs[i], w)  # eager work between replays
+
+
+@pytest.mark.parametrize("hidden", [40, 300, 2050, 6144])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_rows_that_are_not_finite_stay_visible(dev, bad, hidden):
+    """A row with NaN or Inf is NaN from end to end (8 bits: every scale, with
+    codes 0), its stored sum is the plain one, and the rows beside it are
+    those of a call without it."""
+    x, r = make(5, hidden, BF16, 40).to(dev), make(5, hidden, F32, 41).to(dev)
+    x[1, hidden - 1] = bad
+    x[3, 3] = bad
+    ok, nan = [0, 2, 4], [1, 3]
+    w = (1 + 0.1 * make(1, hidden, F32, 42)[0]).to(dev)
+    for out in (F32, BF16, F16):
+        s = r.clone()
+        got = cm.rms_norm(x, w, residual=s, out_dtype=out)
+        assert got[nan].isnan().all()
+        assert torch.equal(got[ok], cm.rms_norm(x[ok], w, residual=r[ok], out_dtype=out))
+        assert torch.equal(s.nan_to_num(7.0), (x.float() + r).nan_to_num(7.0))
+    for out in (I8, E4):
+        for group in (0, 64, 128):
+            codes, scales = cm.rms_norm(x, w, out_dtype=out, group=group)
+            assert scales[nan].isnan().all() and not codes[nan].view(torch.int8).any()
+            want = cm.rms_norm(x[ok], w, out_dtype=out, group=group)
+            assert torch.equal(codes[ok].view(torch.int8), want[0].view(torch.int8)) and torch.equal(scales[ok], want[1])

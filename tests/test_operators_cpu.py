@@ -135,3 +135,14 @@ def test_linear_python_refusals():
     x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU"):
         cm.linear(x, w)
+
+
+def test_overlapping_results_are_refused():
+    """Arrays that begin at the same address and cannot be the same array."""
+    res = dict(rows=2, residual=A + 0x40000, residual_stride=64, residual_out=A + 0x40000, residual_out_stride=64)
+    for bad in (dict(out=A + 0x40000), dict(residual_out=A + 0x10000),  # out is the residual, or the sum
+                dict(residual_out=A, residual_type=1), dict(residual_out=A, residual_out_stride=72)):
+        assert norm_rc(**{**res, **bad}) == -4, bad
+    assert norm_rc(eps=float("inf")) == -4
+    for bad in (dict(x=A + 0x10000, w=A, out=A), dict(x=A, w=A + 0x10000, out=A)):
+        assert linear_rc(m=2, **bad) == -4, bad
