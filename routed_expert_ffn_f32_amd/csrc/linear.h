@@ -21,56 +21,52 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// Operand types: kPieces 16-byte pieces of a row form one operand of an
-// MFMA.  The matrix cores sum over K in any order the two operands agree on,
-// so both take the same pieces of their rows and the layout within K does
-// not matter.  int8 products accumulate exactly in int32, the others in
-// float32; every type runs at the rate of its 32-byte-per-lane form (int8 and
-// e4m3 twice the 16-bit rate).
+// Operand types: a 16-byte piece of a row in every lane is one operand of an
+// MFMA (e4m3: of two).  The matrix cores sum over K in any order the two
+// operands agree on, so both take the same pieces of their rows and the layout
+// within K does not matter.  int8 products accumulate exactly in int32, at
+// twice the 16-bit rate, the others in float32.
 template <int TYPE>
 struct Operand;
 
 template <>
 struct Operand<COLI_MOE_BF16> {
-  static constexpr int kPieces = 1;
   typedef f32x16 Acc32;
   typedef f32x4 Acc16;
-  static __device__ __forceinline__ Acc32 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc32 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a[0]), __builtin_bit_cast(bf16x8, b[0]),
+  static __device__ __forceinline__ Acc32 mma(uint4 a, uint4 b, Acc32 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                    c, 0, 0, 0);
   }
-  static __device__ __forceinline__ Acc16 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc16 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[0]), __builtin_bit_cast(bf16x8, b[0]),
+  static __device__ __forceinline__ Acc16 mma(uint4 a, uint4 b, Acc16 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                    c, 0, 0, 0);
   }
 };
 
 template <>
 struct Operand<COLI_MOE_F16> {
-  static constexpr int kPieces = 1;
   typedef f32x16 Acc32;
   typedef f32x4 Acc16;
-  static __device__ __forceinline__ Acc32 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc32 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a[0]), __builtin_bit_cast(f16x8, b[0]), c,
+  static __device__ __forceinline__ Acc32 mma(uint4 a, uint4 b, Acc32 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
                                                   0, 0, 0);
   }
-  static __device__ __forceinline__ Acc16 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc16 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a[0]), __builtin_bit_cast(f16x8, b[0]), c,
+  static __device__ __forceinline__ Acc16 mma(uint4 a, uint4 b, Acc16 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
                                                   0, 0, 0);
   }
 };
 
 template <>
 struct Operand<COLI_MOE_INT8> {
-  static constexpr int kPieces = 1;
   typedef i32x16 Acc32;
   typedef i32x4 Acc16;
-  static __device__ __forceinline__ Acc32 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc32 c) {
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a[0]), __builtin_bit_cast(i32x4, b[0]), c, 0,
+  static __device__ __forceinline__ Acc32 mma(uint4 a, uint4 b, Acc32 c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0,
                                                  0, 0);
   }
-  static __device__ __forceinline__ Acc16 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc16 c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a[0]), __builtin_bit_cast(i32x4, b[0]), c, 0,
+  static __device__ __forceinline__ Acc16 mma(uint4 a, uint4 b, Acc16 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0,
                                                  0, 0);
   }
 };
@@ -82,7 +78,6 @@ struct Operand<COLI_MOE_INT8> {
 // the largest.)
 template <>
 struct Operand<COLI_MOE_E4M3> {
-  static constexpr int kPieces = 1;
   typedef f32x16 Acc32;
   typedef f32x4 Acc16;
   // codes 8 h .. 8 h + 7 of a piece
@@ -95,13 +90,13 @@ struct Operand<COLI_MOE_E4M3> {
     return f16x8{(_Float16)a[0], (_Float16)a[1], (_Float16)b[0], (_Float16)b[1],
                  (_Float16)c[0], (_Float16)c[1], (_Float16)d[0], (_Float16)d[1]};
   }
-  static __device__ __forceinline__ Acc32 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc32 c) {
-    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(halves(a[0], 0), halves(b[0], 0), c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(halves(a[0], 1), halves(b[0], 1), c, 0, 0, 0);
+  static __device__ __forceinline__ Acc32 mma(uint4 a, uint4 b, Acc32 c) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(halves(a, 0), halves(b, 0), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(halves(a, 1), halves(b, 1), c, 0, 0, 0);
   }
-  static __device__ __forceinline__ Acc16 mma(const uint4 (&a)[1], const uint4 (&b)[1], Acc16 c) {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(a[0], 0), halves(b[0], 0), c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(a[0], 1), halves(b[0], 1), c, 0, 0, 0);
+  static __device__ __forceinline__ Acc16 mma(uint4 a, uint4 b, Acc16 c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(a, 0), halves(b, 0), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(halves(a, 1), halves(b, 1), c, 0, 0, 0);
   }
 };
 

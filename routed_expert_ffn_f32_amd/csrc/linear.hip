@@ -5,8 +5,8 @@
 // runs at 1.33 PFLOP/s in bf16 (the library's product: 1.49), 4096 x 6144 x
 // 6144 at 1.12 (the library's: 1.12); there the chip is held by its power:
 // the same call on zeros takes two thirds of the time, and reading every
-// operand row from the L2 alone changes less.  4096 x 2 2048 x 6144 in int8
-// with SwiGLU runs at 2.26 PFLOP/s, e4m3 on the 16-bit cores at 1.29.  A
+// operand row from the L2 alone changes less.  4096 rows of 6144 int8 on 2048
+// gate and 2048 up rows with SwiGLU run at 2.26 PFLOP/s, e4m3 on the 16-bit cores at 1.29.  A
 // workgroup computes a tile of BM x BN outputs over all of K in steps of 128
 // bytes of every row (64 16-bit or 128 8-bit elements: one whole cache line a
 // row).  Rows of x and w go straight into LDS by LDS-DMA, kStages steps deep,
@@ -188,9 +188,10 @@ struct Tile {
   // copies of step g + 1, those of later steps still going, before the barrier
   // that ends turn 4 g + 3, behind which turn 4 g + 4 reads them.  A third
   // stage pays where it fits beside one workgroup a CU (256 x 128: m = 1024 in
-  // 82 us, with two 110).  (8192^3 bf16: 827 us; all copies with the reads 894 us, all between
-  // products 843 us; without the raised priority of the multiplying waves
-  // 903 us; every wave at its own pace, one barrier a step, 1100 us.)  The
+  // 82 us, with two 110).  (8192^3 bf16: 827 us; all copies with the reads 894
+  // us, all between products 843 us; without the raised priority of the
+  // multiplying waves 903 us.  4096 x 6144 x 6144 with bias and SiLU: 305 us a
+  // call, 451 with every wave at its own pace, one barrier a step.)  The
   // copies have no conditions: past the last step they fetch it again, into
   // the slot that is not read any more (a branch a copy, between the products,
   // cost 23%).
@@ -301,8 +302,7 @@ struct Tile {
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const uint4 a[1] = {af[mb][p]}, b[1] = {bf[nb][p]};
-          acc[mb][nb] = Op::mma(a, b, acc[mb][nb]);
+          acc[mb][nb] = Op::mma(af[mb][p], bf[nb][p], acc[mb][nb]);
           const int done = (p * MB + mb) * NB + nb;
 #pragma unroll
           for (int i = done * kCopies / kAll; i < (done + 1) * kCopies / kAll; ++i) copy_one(i);
@@ -313,22 +313,17 @@ struct Tile {
   template <class Copy>
   static __device__ __forceinline__ void compute(const char *stage, int wm, int wn, int lane, Acc (&acc)[MB][NB],
                                                  const Copy &copy_one) {
-    constexpr int P = Op::kPieces, kJ = 4 / P;  // operand groups of the step; a half-wave holds half the pieces
+    constexpr int kJ = 4;  // pieces of the step in each half-wave
     const int nl = lane & 31, half = lane >> 5, swz = (nl >> 1) & 7;
     const char *A = stage + (wm * MB * 32 + nl) * kStepBytes;
     const char *B = stage + (BM + wn * NB * 32 + nl) * kStepBytes;
-    uint4 af[2][MB][P], bf[2][NB][P];
+    uint4 af[2][MB], bf[2][NB];
     auto fetch = [&](int buf, int j) {
+      const int pos = ((4 * half + j) ^ swz) * 16;
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int pos = ((4 * half + j * P + p) ^ swz) * 16;
+      for (int nb = 0; nb < NB; ++nb) bf[buf][nb] = *reinterpret_cast<const uint4 *>(B + nb * 32 * kStepBytes + pos);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          bf[buf][nb][p] = *reinterpret_cast<const uint4 *>(B + nb * 32 * kStepBytes + pos);
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-          af[buf][mb][p] = *reinterpret_cast<const uint4 *>(A + mb * 32 * kStepBytes + pos);
-      }
+      for (int mb = 0; mb < MB; ++mb) af[buf][mb] = *reinterpret_cast<const uint4 *>(A + mb * 32 * kStepBytes + pos);
     };
     fetch(0, 0);
 #pragma unroll

@@ -1,20 +1,22 @@
 // Dense products with their epilogue (coli_moe_linear) for few rows of x
 // (up to kLinearRowsMax): decode steps and small batches.
 //
-// Bound by the bytes of w, each read once.  A workgroup owns 16 rows of w
-// (SwiGLU: 8 gate rows and the 8 up rows of the same outputs) and splits K
-// over its four waves: each wave takes every fourth chunk of CB bytes of
-// every row, copies it with the matching chunk of x into its own two-slot
-// ring in LDS by LDS-DMA, and multiplies it on 16x16 matrix instructions (16
-// rows of w by 16 rows of x).  A chunk is long (256 or 512 bytes of a row)
-// because short pieces of rows read HBM poorly, and goes through LDS because
-// the instructions want 16 rows by 64 bytes.  The waves never wait for each
-// other before the end, where their sums meet in LDS in wave order.
+// Bound by the bytes of w, each read once (beyond kLinearRowsMax rows, where
+// few large blocks would leave most CUs idle: once per 64 rows of x).  A
+// workgroup owns 16, 32 or 64 rows of w (SwiGLU: half of them gate rows, half
+// the up rows of the same outputs) and splits K over its four waves: each wave
+// takes every fourth chunk of CB bytes of every row, copies it with the
+// matching chunk of x into its own ring of 2 or 3 slots in LDS by LDS-DMA, and
+// multiplies it on 16x16 matrix instructions (16 rows of w by 16 rows of x).
+// Up to 32 rows of x a chunk is long (256 or 512 bytes of a row), because
+// short pieces of rows read HBM poorly; it goes through LDS because the
+// instructions want 16 rows by 64 bytes.  The waves never wait for each other
+// before the end, where their sums meet in LDS in wave order.
 //
-// 16-byte piece p of row r sits in position p ^ (r mod 16), so that the 16
-// rows that neighbouring lanes read fall into different banks.  Rows past the
-// last of x or w: the last row again, results not stored.  Pieces past K come
-// from a piece of zeros.
+// The 16-byte pieces of a row change places with the row (swizzle below), so
+// that the 16 rows that neighbouring lanes read fall into different banks.
+// Rows past the last of x or w: the last row again, results not stored.
+// Pieces past K come from a piece of zeros.
 #include <type_traits>
 
 #include "internal.h"
@@ -130,12 +132,12 @@ struct Rows {
 #pragma unroll
       for (int j = 0; j < CB / 64; ++j) {
         const int pw = ((4 * j + g) ^ swizzle(r)) * 16, px = ((4 * j + g) ^ swizzle(rx)) * 16;
-        uint4 wf[RT][1];
+        uint4 wf[RT];
 #pragma unroll
-        for (int q = 0; q < RT; ++q) wf[q][0] = *reinterpret_cast<const uint4 *>(W + q * 16 * CB + pw);
+        for (int q = 0; q < RT; ++q) wf[q] = *reinterpret_cast<const uint4 *>(W + q * 16 * CB + pw);
 #pragma unroll
         for (int t = 0; t < kTokens; ++t) {
-          const uint4 xf[1] = {*reinterpret_cast<const uint4 *>(X + t * 16 * CB + px)};
+          const uint4 xf = *reinterpret_cast<const uint4 *>(X + t * 16 * CB + px);
 #pragma unroll
           for (int q = 0; q < RT; ++q) acc[q][t] = Op::mma(wf[q], xf, acc[q][t]);
         }
