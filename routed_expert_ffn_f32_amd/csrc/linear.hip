@@ -9,11 +9,12 @@
 // gate and 2048 up rows with SwiGLU run at 2.26 PFLOP/s, e4m3 on the 16-bit cores at 1.29.  A
 // workgroup computes a tile of BM x BN outputs over all of K in steps of 128
 // bytes of every row (64 16-bit or 128 8-bit elements: one whole cache line a
-// row).  Rows of x and w go straight into LDS by LDS-DMA, kStages steps deep,
+// row).  Rows of x and w go straight into LDS by LDS-DMA, STAGES steps deep,
 // 16-byte piece c of row r in position c ^ ((r >> 1) & 7), so that the 16
 // rows that neighbouring lanes read fall into different banks.  Each wave
-// holds MB x NB accumulators of 32 x 32; its operands for the next K piece
-// are read from LDS while the current ones are multiplied.
+// holds MB x NB accumulators of 32 x 32; operands are read from LDS while
+// others are multiplied, by the same wave (blocks of four waves) or by the
+// other wave of its SIMD (blocks of eight).
 //
 // K that is not a multiple of the step: the pieces of the last step that lie
 // past the rows' ends are copied from a piece of zeros.  Rows past the last
@@ -52,7 +53,6 @@ struct Tile {
   static constexpr int kEpilogueBytes = WM * 32 * kRowFloats * 4;
   static constexpr int kRing = STAGES * kStageBytes;
   static constexpr int kLds = kRing > kEpilogueBytes ? kRing : kEpilogueBytes;
-  static constexpr int kPerCu = 160 * 1024 / kLds;
   static_assert(kLds <= 160 * 1024, "the ring exceeds a CU's LDS");
   static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "copies of 8 rows, as many for each wave");
   static_assert(!GATED || BN % 64 == 0, "pairs of gate and up blocks");
@@ -132,47 +132,80 @@ struct Tile {
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = Acc{};
 
-    if constexpr (kWaves == 8) {
-      const int whole = (int)(S.k_bytes / kStepBytes);
-      if (whole) {
-        if (wave >= 4)
-          alternate<true>(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
-        else
-          alternate<false>(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
-      }
-      if (whole < G) remainder(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
-    } else {
-      together(S, G, lds, lds_mem, wm, wn, wave, lane, acc);
+    const int whole = (int)(S.k_bytes / kStepBytes);
+    if (whole) {
+      if constexpr (kWaves == 4)
+        pipelined(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
+      else if (wave >= 4)
+        alternate<true>(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
+      else
+        alternate<false>(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
     }
+    if (whole < G) remainder(S, whole, lds, lds_mem, wm, wn, wave, lane, acc);
     block_barrier();  // the ring is free
     epilogue(a, m0, n0, wm, wn, lane, acc, reinterpret_cast<float *>(lds_mem));
   }
 
-  // Every wave reads and multiplies at its own pace, one barrier a step; other
-  // workgroups of the CU fill the gaps.
-  static __device__ __forceinline__ void together(const Sources &S, int G, uint32_t lds, const char *lds_mem, int wm,
-                                                  int wn, int wave, int lane, Acc (&acc)[MB][NB]) {
-    for (int g = 0; g < STAGES - 1 && g < G; ++g)
+  // Four waves, one on every SIMD: while a wave multiplies step g, it reads its
+  // operands of step g + 1 into other registers, a few reads and copies after
+  // each product, so that nothing waits for LDS.  Step g + 1 has arrived for
+  // every wave at the barrier in front of step g; step g - 1's slot, whose
+  // operands were in registers before step g - 1's products, takes step g +
+  // STAGES - 1 from then on.  As in alternate, copies past the last step fetch
+  // it again.  (256 x 6144 x 6144 bf16 in 128 x 64 blocks: 30 us; with the reads
+  // in front of each step's products, also over six stages, 46 us; eight waves
+  // taking turns 45 us; three stages, two blocks a CU, 59 us.  Reads spread over
+  // all of a step's products, or within the first quarter, are as fast.)
+  static __device__ __forceinline__ void pipelined(const Sources &S, int G, uint32_t lds, const char *lds_mem, int wm,
+                                                   int wn, int wave, int lane, Acc (&acc)[MB][NB]) {
+    constexpr int kAhead = STAGES - 1, kAll = 4 * MB * NB, kReads = 4 * (MB + NB);
+    const int nl = lane & 31, half = lane >> 5, swz = (nl >> 1) & 7;
+    const int at_a = (wm * MB * 32 + nl) * kStepBytes, at_b = (BM + wn * NB * 32 + nl) * kStepBytes;
+    uint4 op[2][4][MB + NB];  // operands of this step and of the next, by piece: rows of w, then of x
+    auto read = [&](const char *stage, int buf, int r) {
+      const int p = r / (MB + NB), q = r % (MB + NB), pos = ((4 * half + p) ^ swz) * 16;
+      op[buf][p][q] = *reinterpret_cast<const uint4 *>(
+          stage + (q < NB ? at_b + q * 32 * kStepBytes : at_a + (q - NB) * 32 * kStepBytes) + pos);
+    };
+    auto copy_step = [&](int g, int slot, int i) {
+      copy_whole(S, i, (int64_t)min(g, G - 1) * kStepBytes, lds + slot * kStageBytes, wave);
+    };
+    auto next = [](int slot) { return slot + 1 == STAGES ? 0 : slot + 1; };
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) copy(S, i, (int64_t)g * kStepBytes, lds + g * kStageBytes, wave, lane);
-
-    int slot = 0, fill = STAGES - 1;  // slots of the step to compute and of the step to copy
-    for (int g = 0; g < G; ++g) {
-      // this wave's copies of step g have arrived; then every wave's have,
-      // and every wave is done with the slot to be filled
-      if (STAGES > 2 && g + STAGES - 2 < G)
-        dma_wait<kCopies *(STAGES - 2)>();
-      else
-        dma_wait<0>();
-      block_barrier();
-      const bool more = g + STAGES - 1 < G;
-      const int64_t at = (int64_t)(g + STAGES - 1) * kStepBytes;
-      compute(lds_mem + slot * kStageBytes, wm, wn, lane, acc, [&](int i) {
-        if (more) copy(S, i, at, lds + fill * kStageBytes, wave, lane);
-      });
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
-      fill = fill + 1 == STAGES ? 0 : fill + 1;
+    for (int g = 0; g < kAhead; ++g)
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) copy_step(g, g, i);
+    dma_wait<kCopies *(STAGES - 2)>();
+    turn();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(lds_mem, 0, r);
+    int ahead = next(0), fill = kAhead;  // slots of step g + 1 and of step g + kAhead
+    auto step = [&](int g, auto buf_) {
+      constexpr int buf = decltype(buf_)::value;
+      dma_wait<kCopies *(STAGES - 3)>();
+      turn();
+      const char *stage = lds_mem + ahead * kStageBytes;
+#pragma unroll
+      for (int j = 0; j < kAll; ++j) {
+        const int p = j / (MB * NB), mb = j / NB % MB, nb = j % NB;
+        acc[mb][nb] = Op::mma(op[buf][p][NB + mb], op[buf][p][nb], acc[mb][nb]);
+#pragma unroll
+        for (int r = kReads * min(2 * j, kAll) / kAll; r < kReads * min(2 * j + 2, kAll) / kAll; ++r)
+          read(stage, buf ^ 1, r);
+#pragma unroll
+        for (int i = j * kCopies / kAll; i < (j + 1) * kCopies / kAll; ++i) copy_step(g + kAhead, fill, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      ahead = next(ahead);
+      fill = next(fill);
+    };
+    int g = 0;
+    for (; g + 1 < G; g += 2) {
+      step(g, std::integral_constant<int, 0>());
+      step(g + 1, std::integral_constant<int, 1>());
     }
+    if (g < G) step(g, std::integral_constant<int, 0>());
+    dma_wait<0>();
   }
 
   // Two groups of four waves, one of each on every SIMD, take turns: while one
@@ -309,35 +342,6 @@ struct Tile {
         }
   }
 
-  // One K step; copies are issued between the products.
-  template <class Copy>
-  static __device__ __forceinline__ void compute(const char *stage, int wm, int wn, int lane, Acc (&acc)[MB][NB],
-                                                 const Copy &copy_one) {
-    constexpr int kJ = 4;  // pieces of the step in each half-wave
-    const int nl = lane & 31, half = lane >> 5, swz = (nl >> 1) & 7;
-    const char *A = stage + (wm * MB * 32 + nl) * kStepBytes;
-    const char *B = stage + (BM + wn * NB * 32 + nl) * kStepBytes;
-    uint4 af[2][MB], bf[2][NB];
-    auto fetch = [&](int buf, int j) {
-      const int pos = ((4 * half + j) ^ swz) * 16;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) bf[buf][nb] = *reinterpret_cast<const uint4 *>(B + nb * 32 * kStepBytes + pos);
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) af[buf][mb] = *reinterpret_cast<const uint4 *>(A + mb * 32 * kStepBytes + pos);
-    };
-    fetch(0, 0);
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      if (j + 1 < kJ) fetch((j + 1) & 1, j + 1);
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = Op::mma(af[j & 1][mb], bf[j & 1][nb], acc[mb][nb]);
-#pragma unroll
-      for (int i = j * kCopies / kJ; i < (j + 1) * kCopies / kJ; ++i) copy_one(i);
-    }
-  }
-
   // Accumulators -> LDS -> 8 neighbouring outputs a thread, a slab of 32 rows
   // of every wave row at a time.  Register i of a 32 x 32 block is row
   // 8 (i / 4) + 4 half + i % 4, the lane's column is lane % 32.  The loop over
@@ -431,10 +435,9 @@ struct Tile {
   }
 };
 
-// kPerCu workgroups of the shape share a CU by their LDS; the registers have
-// to leave room for as many.
+// One workgroup a CU, by its LDS: one or two waves on each SIMD share its registers.
 template <class T>
-__global__ __launch_bounds__(T::kThreads, T::kPerCu * T::kWaves / 4) void linear_tile_kernel(coli_moe_linear_t a) {
+__global__ __launch_bounds__(T::kThreads, T::kWaves / 4) void linear_tile_kernel(coli_moe_linear_t a) {
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
   T::run(a, lds);
 }
@@ -449,25 +452,24 @@ hipError_t launch_tiles(const coli_moe_linear_t &a, hipStream_t s) {
   return a.act == COLI_MOE_ACT_SWIGLU ? go(std::true_type()) : go(std::false_type());
 }
 
-// The shapes a product of more than kLinearRowsMax rows can take, with what
-// they cost: microseconds measured at 12288 bytes of K (6144 bf16 elements;
-// n = 6144, m from 64 to 4096, three sets of operands in turn) for up to one
-// block a CU, and for a round that fills the chip (per_cu blocks on every CU,
-// the clock held by the power).  (128 x 128 blocks with two stages, two a CU,
-// took 63 us at m = 512 and 103 at 1024: never the least.)
+// The shapes a product of more than kLinearRowsMax rows can take, one block a
+// CU, with what they cost: microseconds measured at 12288 bytes of K (6144
+// bf16 elements; n = 6144, m from 64 to 4096, three sets of operands in turn)
+// for up to one block a CU, and for a round that fills the chip (the clock
+// held by the power).
 struct Shape {
-  int bm, bn;         // rows of x and of w of a block
-  int per_cu;         // blocks a CU holds
-  int one, full;      // cost of a round with fewer blocks, and of a full one
+  int bm, bn;     // rows of x and of w of a block
+  int one, full;  // cost of a round with fewer blocks, and of a full one
 };
 constexpr int kCus = 256;
 constexpr Shape kShapes[] = {
-    {64, 32, 1, 17, 17},      // linear_rows: m = 64 in 18 us, 128 in 34, 256 in 50
-    {64, 64, 1, 27, 27},      // linear_rows: m = 128 in 26 to 29 us, 256 in 48 to 55
-    {128, 64, 2, 50, 62},     // four waves: m = 256 in 48 to 53 us, 512 in 60 to 64, 1024 in 120
-    {256, 128, 1, 84, 91},    // eight waves: m = 1024 in 82 us (192 blocks), 4096 in 273 (three full rounds)
-    {256, 192, 1, 136, 136},  // m = 2048 in 140 us, 4096 in 272 (two full rounds)
-    {256, 256, 1, 150, 150},  // m = 2048 in 152 us, 4096 in 296 (two rounds, the second half empty)
+    {64, 32, 17, 17},      // linear_rows: m = 64 in 18 to 20 us, 128 in 34, 256 in 50
+    {64, 64, 21, 25},      // four waves: m = 128 in 21 us, 256 (384 blocks) in 41, 512 (three full rounds) in 81
+    {128, 64, 30, 38},     // the same: m = 256 in 30 us, 512 (384 blocks) in 62, 1024 (three full rounds) in 124
+    {128, 128, 48, 57},    // the same: m = 384 in 39 us, 512 in 46 to 58, 640 in 60, 1024 (384 blocks) in 115
+    {256, 128, 84, 91},    // eight waves: m = 1024 in 82 us (192 blocks), 4096 in 273 (three full rounds)
+    {256, 192, 136, 136},  // m = 2048 in 140 us, 4096 in 272 (two full rounds)
+    {256, 256, 150, 150},  // m = 2048 in 152 us, 4096 in 296 (two rounds, the second half empty)
 };
 
 // The shape with the least cost: rounds of blocks over the CUs times the
@@ -479,8 +481,7 @@ int pick_shape(int64_t m, int64_t wrows) {
   for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
     const Shape &s = kShapes[i];
     const int64_t blocks = ((m + s.bm - 1) / s.bm) * ((wrows + s.bn - 1) / s.bn);
-    const int64_t slots = (int64_t)kCus * s.per_cu, rest = blocks % slots;
-    const int64_t cost = blocks / slots * s.full + (rest == 0 ? 0 : rest <= kCus ? s.one : s.full);
+    const int64_t cost = blocks / kCus * s.full + (blocks % kCus ? s.one : 0);
     if (i == 0 || cost < least) {
       best = i;
       least = cost;
@@ -492,9 +493,11 @@ int pick_shape(int64_t m, int64_t wrows) {
 template <int TYPE>
 hipError_t launch_type(const coli_moe_linear_t &a, int shape, hipStream_t s) {
   switch (shape) {
-    case 2: return launch_tiles<TYPE, 2, 1, 2, 2, 3>(a, s);
-    case 3: return launch_tiles<TYPE, 2, 2, 4, 2, 3>(a, s);
-    case 4: return launch_tiles<TYPE, 2, 3, 4, 2, 2>(a, s);
+    case 1: return launch_tiles<TYPE, 1, 1, 2, 2, 8>(a, s);
+    case 2: return launch_tiles<TYPE, 2, 1, 2, 2, 6>(a, s);
+    case 3: return launch_tiles<TYPE, 2, 2, 2, 2, 4>(a, s);
+    case 4: return launch_tiles<TYPE, 2, 2, 4, 2, 3>(a, s);
+    case 5: return launch_tiles<TYPE, 2, 3, 4, 2, 2>(a, s);
     default: return launch_tiles<TYPE, 4, 2, 2, 4, 2>(a, s);
   }
 }
@@ -502,9 +505,9 @@ hipError_t launch_type(const coli_moe_linear_t &a, int shape, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_linear(const coli_moe_linear_t &a, hipStream_t s) {
-  if (a.m <= kLinearRowsMax) return launch_linear_rows(a, 32, s);
+  if (a.m <= kLinearRowsMax) return launch_linear_rows(a, s);
   const int shape = pick_shape(a.m, a.act == COLI_MOE_ACT_SWIGLU ? 2 * (int64_t)a.n : a.n);
-  if (shape < 2) return launch_linear_rows(a, kShapes[shape].bn, s);
+  if (shape == 0) return launch_linear_rows(a, s);
   switch (a.type) {
     case COLI_MOE_BF16: return launch_type<COLI_MOE_BF16>(a, shape, s);
     case COLI_MOE_F16: return launch_type<COLI_MOE_F16>(a, shape, s);

@@ -3,7 +3,7 @@
 //
 // Bound by the bytes of w, each read once (beyond kLinearRowsMax rows, where
 // few large blocks would leave most CUs idle: once per 64 rows of x).  A
-// workgroup owns 16, 32 or 64 rows of w (SwiGLU: half of them gate rows, half
+// workgroup owns 16 or 32 rows of w (SwiGLU: half of them gate rows, half
 // the up rows of the same outputs) and splits K over its four waves: each wave
 // takes every fourth chunk of CB bytes of every row, copies it with the
 // matching chunk of x into its own ring of 2 or 3 slots in LDS by LDS-DMA, and
@@ -202,31 +202,29 @@ hipError_t launch_shape(const coli_moe_linear_t &a, hipStream_t s) {
   return a.act == COLI_MOE_ACT_SWIGLU ? go(std::true_type()) : go(std::false_type());
 }
 
-// w_rows: rows of w a block of more than 32 rows of x owns (32 or 64).
 // Up to 16 rows of x, LDS is kept small enough for two workgroups a CU: 16
 // rows of bf16 on 6144 x 6144 take 13.9 us with 256-byte chunks (64 KB) and
 // 17.0 us with 512-byte ones (128 KB), one row 12.9 us against 14.5 us with a
 // third slot.  From 17 rows on, 32 rows of w share each chunk of x: 32 rows
 // take 16.2 us, 18.9 us with 16 rows of w.
 template <int TYPE>
-hipError_t launch_type(const coli_moe_linear_t &a, int w_rows, hipStream_t s) {
+hipError_t launch_type(const coli_moe_linear_t &a, hipStream_t s) {
   if (a.m <= 2) return launch_shape<TYPE, 2, 1, 512, 2>(a, s);
   if (a.m <= 4) return launch_shape<TYPE, 4, 1, 512, 2>(a, s);
   if (a.m <= 8) return launch_shape<TYPE, 8, 1, 256, 3>(a, s);
   if (a.m <= 16) return launch_shape<TYPE, 16, 1, 256, 2>(a, s);
   if (a.m <= 32) return launch_shape<TYPE, 32, 2, 256, 2>(a, s);
-  if (w_rows == 32) return launch_shape<TYPE, 64, 2, 128, 2>(a, s);
-  return launch_shape<TYPE, 64, 4, 128, 2>(a, s);
+  return launch_shape<TYPE, 64, 2, 128, 2>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_linear_rows(const coli_moe_linear_t &a, int w_rows, hipStream_t s) {
+hipError_t launch_linear_rows(const coli_moe_linear_t &a, hipStream_t s) {
   switch (a.type) {
-    case COLI_MOE_BF16: return launch_type<COLI_MOE_BF16>(a, w_rows, s);
-    case COLI_MOE_F16: return launch_type<COLI_MOE_F16>(a, w_rows, s);
-    case COLI_MOE_INT8: return launch_type<COLI_MOE_INT8>(a, w_rows, s);
-    default: return launch_type<COLI_MOE_E4M3>(a, w_rows, s);
+    case COLI_MOE_BF16: return launch_type<COLI_MOE_BF16>(a, s);
+    case COLI_MOE_F16: return launch_type<COLI_MOE_F16>(a, s);
+    case COLI_MOE_INT8: return launch_type<COLI_MOE_INT8>(a, s);
+    default: return launch_type<COLI_MOE_E4M3>(a, s);
   }
 }
 

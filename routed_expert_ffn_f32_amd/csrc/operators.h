@@ -20,6 +20,6 @@ hipError_t launch_balance_grad(const coli_moe_balance_t &a, const float *coef, c
 
 hipError_t launch_linear(const coli_moe_linear_t &a, hipStream_t s);  // m, n >= 1
 constexpr int kLinearRowsMax = 32;  // rows of x up to which every product takes launch_linear_rows
-hipError_t launch_linear_rows(const coli_moe_linear_t &a, int w_rows, hipStream_t s);
+hipError_t launch_linear_rows(const coli_moe_linear_t &a, hipStream_t s);
 
 }  // namespace coli
