@@ -272,3 +272,18 @@ def test_nan_stays_visible(dev, m):
         nan[m // 2], nan[:, 5], nan[:, 90] = True, True, True
         assert torch.equal(got.isnan(), nan), act
         assert torch.equal(got[~nan], want[~nan]), act
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n", [(100, 6000), (250, 6100), (380, 5990)])
+@pytest.mark.parametrize("k", [8, 64, 128, 192, 320, 576, 1088, 2056])
+def test_rings_of_the_small_blocks(dev, m, n, k, kind):
+    """Blocks of 64 x 64, 128 x 64 and 128 x 128 with fewer K steps than their
+    rings have stages, as many, several times as many, odd and even numbers."""
+    exact_case(dev, m, n, k, kind, "none", m + k, bias=False, residual=True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n,k", [(100, 3000, 1096), (250, 3050, 1480), (380, 2990, 968)])
+def test_swiglu_on_the_small_blocks(dev, m, n, k, kind):
+    test_swiglu_on_every_block_shape(dev, m, n, k, kind)
