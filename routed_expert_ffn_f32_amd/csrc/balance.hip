@@ -111,10 +111,13 @@ struct Bounds {
     first = s;
     value = seq_at(a, min(s + (int)(threadIdx.x & 63), a.n_seqs));
   }
-  // Start of sequence s (s = n_seqs: the end of the last), s >= first.
-  __device__ __forceinline__ int at(const coli_moe_balance_t &a, int s) {
-    if (s - first >= 64) load(a, s);
-    return __builtin_amdgcn_readlane(value, s - first);
+  // Start and end of sequence s < n_seqs, s >= first.  A window without the
+  // end is moved to start at s itself, never behind it: the caller may ask for
+  // s again, for the tokens of its next batch.
+  __device__ __forceinline__ void of(const coli_moe_balance_t &a, int s, int &begin, int &end) {
+    if (s + 1 - first >= 64) load(a, s);
+    begin = __builtin_amdgcn_readlane(value, s - first);
+    end = __builtin_amdgcn_readlane(value, s + 1 - first);
   }
   // Starts at the first sequence that ends behind token t (n_seqs: none):
   // the number of ends at or before t, narrowed 64-fold a load.  For up to 63
@@ -258,7 +261,8 @@ __global__ __launch_bounds__(kSumThreads) void balance_sums_kernel(coli_moe_bala
     for (int t = 0; t < kTok; ++t) inv[t] = on[t] && sc[t].total != 0.0f ? 1.0f / sc[t].total : 0.0f;
     const int stop = min(t0 + kBatch, hi);
     for (; s < a.n_seqs; ++s) {
-      const int begin = bounds.at(a, s), end = bounds.at(a, s + 1);
+      int begin, end;
+      bounds.of(a, s, begin, end);
       if (!ALONE && begin >= stop) break;
       if (begin >= end) {
         if (ALONE) finish_sequence(a, s, threadIdx.x, (int)threadIdx.x < E, 0, 0.0, 0.0, 0.0, loss, counts, coef);
@@ -391,7 +395,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(coli_moe_
   Scores<NE, SOFTMAX> sc[kTok];
   score_tokens<NE, SOFTMAX>(z, lane, E, sc);
   for (; s < a.n_seqs; ++s) {
-    const int begin = bounds.at(a, s), end = bounds.at(a, s + 1);
+    int begin, end;
+    bounds.of(a, s, begin, end);
     if (begin >= hi) break;
     if (begin >= end) continue;
     float c[NE];

@@ -287,3 +287,71 @@ def test_scores_at_the_end_of_their_range(dev):
     ids = torch.from_numpy(idx).to(dev)
     loss, _, coef = cm.balance_loss(low, ids, ALPHA)
     assert loss.tolist() == [0.0] and not cm.balance_grad(low, coef).any()
+
+
+def many_sequences(kind):
+    rng = np.random.default_rng(31)
+    if kind == "63 short, one long":    # the long one is the last that the first window of bounds shows
+        return 32768, np.r_[np.arange(64), 32768]
+    if kind == "64 short, one long":
+        return 32768, np.r_[np.arange(65), 32768]
+    if kind == "random":
+        return 65536, np.r_[0, np.sort(rng.integers(0, 65537, 3899)), 65536]
+    if kind == "equal":
+        return 78000, np.arange(0, 78001, 20)
+    if kind == "empty between":         # rows before the first and behind the last, windows of empty sequences
+        return 40000, np.sort(np.r_[np.repeat([5, 5, 700, 20001], 100), rng.integers(5, 39001, 200)])
+    return 1 << 20, np.r_[0, np.sort(rng.integers(0, (1 << 20) + 1, 16383)), 1 << 20]
+
+
+@pytest.mark.parametrize("kind", ["63 short, one long", "64 short, one long", "random", "equal", "empty between", "largest"])
+def test_many_sequences_over_several_batches(dev, kind):
+    """More sequences than one load of bounds shows, in workgroups of several
+    batches: every token and choice is counted once, in its own sequence.  The
+    workspace holds NaN before the call, so that a sum of anything unwritten
+    shows.  The logits are equal, so every token's shares are 1 / E, and E = 4
+    makes the shares and their sums (under 2^24 tokens of 1/4) exact: a loss
+    is alpha up to the float32 rounding of alpha's product, 2 half steps."""
+    T, off = many_sequences(kind)
+    S, E, k = len(off) - 1, 4, 2
+    rng = np.random.default_rng(T)
+    idx = rng.integers(-1, E, size=(T, k)).astype(np.int32)
+    mask = rng.random(T) < 0.9
+    seq = np.searchsorted(off[1:], np.arange(T), side="right")
+    inside = (np.arange(T) >= off[0]) & (seq < S) & mask
+    rows = np.repeat(np.where(inside, seq, S), k)
+    flat = idx.reshape(-1)
+    keep = (flat >= 0) & (rows < S)
+    counts = np.zeros((S, E), np.int64)
+    np.add.at(counts, (rows[keep], flat[keep]), 1)
+    valid = np.bincount(seq[inside], minlength=S)[:S]
+    n = counts.sum(1)
+    some = (n > 0) & (valid > 0)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        coef = np.where(some[:, None], float(np.float32(ALPHA)) / valid[:, None] * (E * counts / n[:, None] - 1), 0.0)
+    z = torch.zeros(T, E, device=dev)
+    it, ot, mt = (torch.from_numpy(np.ascontiguousarray(v)).to(dev) for v in (idx, off.astype(np.int32), mask))
+    loss, cnt = torch.full((S,), float("nan"), device=dev), torch.full((S, E), -1, dtype=torch.int32, device=dev)
+    cf = torch.full((S, E), float("nan"), device=dev)
+    ws = torch.full((cm.coli_moe_balance_workspace_bytes(T, E, S) // 4,), float("nan"), device=dev)
+    args = cm.coli_moe_balance_t(T, E, k, S, cm.COLI_MOE_SCORES_SOFTMAX, ALPHA, z.data_ptr(), E, it.data_ptr(),
+                                 ot.data_ptr(), mt.data_ptr())
+    cm.coli_moe_balance(args, loss.data_ptr(), cnt.data_ptr(), cf.data_ptr(), ws.data_ptr(), 4 * ws.numel(),
+                        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert np.array_equal(cnt.cpu().numpy(), counts)
+    want = np.where(some, float(np.float32(ALPHA)), 0.0)
+    assert (np.abs(loss.cpu().numpy() - want) <= U * want).all()
+    # one rounding to float32; in 64 bits a quotient, a product and a difference, each off by 2^-53 of E n_e / N or 1
+    got = cf.cpu().numpy().astype(np.float64)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        off64 = np.where(some[:, None], 4 * 2.0 ** -53 * ALPHA / valid[:, None] * (E * counts / n[:, None] + 1), 0.0)
+    assert (np.abs(got - coef) <= U * np.abs(coef) + off64).all()
+    dl = torch.full((T, E), 7.0, device=dev)
+    cm.coli_moe_balance_grad(args, cf.data_ptr(), None, dl.data_ptr(), E, torch.cuda.current_stream().cuda_stream)
+    d = dl.cpu().numpy().astype(np.float64)
+    nowhere = (np.arange(T) < off[0]) | (seq >= S)
+    assert (d[nowhere] == 7.0).all() and not d[~nowhere & ~mask].any()
+    c = got[seq[inside]]
+    unit = 0.25 * (np.abs(c) + 0.25 * np.abs(c).sum(1, keepdims=True))
+    assert (np.abs(d[inside] - 0.25 * (c - c.mean(1, keepdims=True))) <= 48 * U * unit + 1e-37).all()
