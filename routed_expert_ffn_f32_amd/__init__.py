@@ -15,6 +15,7 @@ first call raises, naming the build command.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -677,6 +678,21 @@ def _balance_args(logits, idx, alpha, scores, offsets, mask):
     return coli_moe_balance_t(T, E, k, n_seqs, _SCORES[scores], alpha, logits.data_ptr(), ld, ip, op, mp), dev, T, E, n_seqs
 
 
+def _balance_loss(logits, idx, alpha, scores, offsets, mask):
+    """(results, enqueue) of a balance_loss call: arguments checked and buffers
+    allocated, the launch left to enqueue()."""
+    import torch
+    a, dev, T, E, S = _balance_args(logits, idx, alpha, scores, offsets, mask)
+    loss, coef = logits.new_empty((S,)), logits.new_empty((S, E))
+    counts = logits.new_empty((S, E), dtype=torch.int32)
+    nbytes = coli_moe_balance_workspace_bytes(T, E, S)
+    ws = logits.new_empty(((nbytes + 3) // 4,))
+
+    def enqueue():
+        _enqueue("coli_moe_balance", dev, a, loss.data_ptr(), counts.data_ptr(), coef.data_ptr(), ws.data_ptr(), nbytes)
+    return (loss, counts, coef), enqueue
+
+
 def balance_loss(logits, idx, alpha: float, scores: str = "sigmoid", offsets=None, mask=None):
     """Balance loss of router choices idx [T, k] (int32, -1 in dropped slots)
     with logits [T, E] (float32), per sequence: offsets int32 [S + 1] gives
@@ -685,14 +701,9 @@ def balance_loss(logits, idx, alpha: float, scores: str = "sigmoid", offsets=Non
 
     Returns (loss [S], counts [S, E] int32, coef [S, E]); balance_grad takes
     coef.  coli_moe_balance in include/coli_moe.h gives the formulas."""
-    import torch
-    a, dev, T, E, S = _balance_args(logits, idx, alpha, scores, offsets, mask)
-    loss, coef = logits.new_empty((S,)), logits.new_empty((S, E))
-    counts = logits.new_empty((S, E), dtype=torch.int32)
-    nbytes = coli_moe_balance_workspace_bytes(T, E, S)
-    ws = logits.new_empty(((nbytes + 3) // 4,))
-    _enqueue("coli_moe_balance", dev, a, loss.data_ptr(), counts.data_ptr(), coef.data_ptr(), ws.data_ptr(), nbytes)
-    return loss, counts, coef
+    results, enqueue = _balance_loss(logits, idx, alpha, scores, offsets, mask)
+    enqueue()
+    return results
 
 
 def balance_grad(logits, coef, dloss=None, scores: str = "sigmoid", offsets=None, mask=None, out=None):
@@ -737,19 +748,34 @@ def make_config(hidden, n_experts, top_k, inter, n_shared, routed_scaling_factor
                              routed_scaling_factor=routed_scaling_factor, weight_format=weight_format)
 
 
-def _stream_of(stream: int, device):
-    """Context in which `stream` is torch's current stream on `device`."""
-    import contextlib
-
+def _layer_stream(stream: int, device):
+    """Context in which work goes to a layer's `stream`.  Where torch's current
+    stream is another one, the layer's first waits for it and it then waits for
+    the layer's, so that tensors may be allocated (before the context), made,
+    used and freed on the current stream as if all were one stream."""
     import torch
-    if torch.cuda.current_stream(device).cuda_stream == stream:
+    current = torch.cuda.current_stream(device)
+    if current.cuda_stream == stream:
         return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
+    return _crossing(current, torch.cuda.ExternalStream(stream, device=device))
+
+
+@contextlib.contextmanager
+def _crossing(current, own):
+    import torch
+    own.wait_stream(current)
+    try:
+        with torch.cuda.stream(own):
+            yield
+    finally:
+        current.wait_stream(own)
 
 
 class _RoutedCalls:
     """What a resident and a cached layer have in common beside their forward:
-    needs `cfg`, `workspace`, `stream` and `_layer()`."""
+    needs `cfg`, `workspace`, `stream` and `_layer()`.  These calls run on the
+    layer's stream; on another current stream they wait for its work, and its
+    later work for them (_layer_stream)."""
 
     def forward_normed(self, x, norm_weight=None, eps: float = 1e-6, residual=None, out=None):
         """The layer on the norm of x (of x + residual, stored in the residual,
@@ -758,17 +784,20 @@ class _RoutedCalls:
         the result is the layer's float32 output, to be added to the residual
         by the next norm."""
         import torch
-        with _stream_of(self.stream, x.device):
-            hidden = rms_norm(x, norm_weight, eps, residual=residual, out_dtype=torch.float32)
+        hidden = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+        if out is None:
+            out = torch.empty_like(hidden)
+        with _layer_stream(self.stream, x.device):
+            rms_norm(x, norm_weight, eps, residual=residual, out=hidden)
             return self.forward(hidden, out)
 
     def last_logits(self):
         """Router logits [T, E] of the last forward."""
         import torch
         dev = self.workspace.device
-        with _stream_of(self.stream, dev):
-            T = coli_moe_last_routing(self._layer(), stream=self.stream)
-            z = torch.empty((T, self.cfg.n_experts), dtype=torch.float32, device=dev)
+        T = coli_moe_last_routing(self._layer())
+        z = torch.empty((T, self.cfg.n_experts), dtype=torch.float32, device=dev)
+        with _layer_stream(self.stream, dev):
             if T:
                 coli_moe_last_logits(self._layer(), z.data_ptr(), self.stream)
         return z
@@ -776,10 +805,18 @@ class _RoutedCalls:
     def balance(self, alpha: float, scores: str = "sigmoid", offsets=None, mask=None):
         """balance_loss of the last forward's routing: (loss [S], counts
         [S, E], coef [S, E])."""
-        z = self.last_logits()
-        T, routing = self.last_routing()
-        with _stream_of(self.stream, z.device):
-            return balance_loss(z, routing["idx"].view(T, self.cfg.top_k), alpha, scores, offsets, mask)
+        import torch
+        dev = self.workspace.device
+        T = coli_moe_last_routing(self._layer())
+        z = torch.empty((T, self.cfg.n_experts), dtype=torch.float32, device=dev)
+        idx = torch.empty((T, self.cfg.top_k), dtype=torch.int32, device=dev)
+        results, enqueue = _balance_loss(z, idx, alpha, scores, offsets, mask)
+        with _layer_stream(self.stream, dev):
+            if T:
+                coli_moe_last_logits(self._layer(), z.data_ptr(), self.stream)
+                coli_moe_last_routing(self._layer(), idx.data_ptr(), stream=self.stream)
+            enqueue()
+        return results
 
 
 class MoELayer(_RoutedCalls):
@@ -845,9 +882,10 @@ class MoELayer(_RoutedCalls):
         r = dict(idx=torch.empty(n, **i32), w=torch.empty(n, dtype=torch.float32, device=dev),
                  offsets=torch.empty(E + 1, **i32), sorted_ids=torch.empty(n, **i32),
                  inv=torch.empty(n, **i32), active=torch.empty(E, **i32), n_active=torch.empty(1, **i32))
-        coli_moe_last_routing(self.handle, *(r[key].data_ptr() for key in
-                                             ("idx", "w", "offsets", "sorted_ids", "inv", "active",
-                                              "n_active")), stream=self.stream)
+        with _layer_stream(self.stream, dev):
+            coli_moe_last_routing(self.handle, *(r[key].data_ptr() for key in
+                                                 ("idx", "w", "offsets", "sorted_ids", "inv", "active",
+                                                  "n_active")), stream=self.stream)
         return T, r
 
     def close(self):
@@ -938,9 +976,10 @@ class ExpertCache(_RoutedCalls):
         r = dict(idx=torch.empty(n, **i32), w=torch.empty(n, dtype=torch.float32, device=dev),
                  offsets=torch.empty(E + 1, **i32), sorted_ids=torch.empty(n, **i32),
                  inv=torch.empty(n, **i32), active=torch.empty(E, **i32), n_active=torch.empty(1, **i32))
-        coli_moe_last_routing(layer, *(r[key].data_ptr() for key in
-                                       ("idx", "w", "offsets", "sorted_ids", "inv", "active", "n_active")),
-                              stream=self.stream)
+        with _layer_stream(self.stream, dev):
+            coli_moe_last_routing(layer, *(r[key].data_ptr() for key in
+                                           ("idx", "w", "offsets", "sorted_ids", "inv", "active", "n_active")),
+                                  stream=self.stream)
         return T, r
 
     def close(self):

@@ -215,3 +215,57 @@ def test_refusals_on_the_device(dev):
             call()
         assert e.value.code == code, i
     torch.cuda.synchronize()
+
+
+def test_layer_on_its_own_stream(dev):
+    """A layer on one stream, called while another is current, with work still
+    going on both: arguments made on the current stream just before a call are
+    read as made, results can be used there, and memory that the calls drop or
+    that the caller reuses afterwards is not written late."""
+    shape = synth.TINY
+    L = DeviceLayer(shape, 1, 0, dev, max_tokens=16)
+    own, side = torch.cuda.Stream(), torch.cuda.Stream()
+    a = torch.randn(2048, 2048, device=dev)
+
+    def delay():
+        for _ in range(20):
+            torch.mm(a, a)
+
+    try:
+        T, h = 16, shape.hidden
+        x0 = torch.from_numpy(synth.hidden(shape, 1, T)).to(dev)
+        res0, off0 = torch.randn(T, h, device=dev), torch.tensor([0, 5, T], dtype=torch.int32, device=dev)
+        keep0 = torch.arange(T, device=dev) % 3 != 0
+        r = res0.clone()
+        want = (L.moe.forward_normed(x0, residual=r).clone(), r.clone(), *L.moe.balance(0.01, offsets=off0, mask=keep0),
+                L.moe.last_logits(), L.moe.last_routing()[1]["idx"])
+        x, res, off, keep = torch.zeros_like(x0), torch.zeros_like(res0), torch.zeros_like(off0), torch.zeros_like(keep0)
+        torch.cuda.synchronize()
+        L.moe.stream = own.cuda_stream
+        for _ in range(3):
+            with torch.cuda.stream(own):
+                delay()
+            with torch.cuda.stream(side):
+                delay()
+                for dst, src in ((x, x0), (res, res0), (off, off0), (keep, keep0)):
+                    dst.copy_(src)
+                out = L.moe.forward_normed(x, residual=res)
+                x.fill_(float("nan"))                                  # the caller's again
+                got = [out.clone(), res.clone()]
+                with torch.cuda.stream(own):
+                    delay()
+                got += L.moe.balance(0.01, offsets=off, mask=keep)
+                off.zero_(), keep.zero_()
+                # blocks of the sizes that balance has just dropped
+                later = [torch.full((n,), -7, dtype=torch.int32, device=dev)
+                         for n in (T * shape.top_k, T * shape.n_experts, shape.n_experts, 1) for _ in range(8)]
+                with torch.cuda.stream(own):
+                    delay()
+                got += [L.moe.last_logits(), L.moe.last_routing()[1]["idx"]]
+                got = [t.clone() for t in got]
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
+            assert all((t == -7).all() for t in later)
+    finally:
+        torch.cuda.synchronize()
+        L.close()
