@@ -749,15 +749,17 @@ def make_config(hidden, n_experts, top_k, inter, n_shared, routed_scaling_factor
 
 
 def _layer_stream(stream: int, device):
-    """Context in which work goes to a layer's `stream`.  Where torch's current
-    stream is another one, the layer's first waits for it and it then waits for
-    the layer's, so that tensors may be allocated (before the context), made,
-    used and freed on the current stream as if all were one stream."""
+    """Context in which a layer's device is current and work goes to its
+    `stream`.  Where torch's current stream of that device is another one, the
+    layer's first waits for it and it then waits for the layer's, so that
+    tensors may be allocated (before the context), made, used and freed on the
+    current stream as if all were one stream."""
     import torch
     current = torch.cuda.current_stream(device)
-    if current.cuda_stream == stream:
-        return contextlib.nullcontext()
-    return _crossing(current, torch.cuda.ExternalStream(stream, device=device))
+    if current.cuda_stream != stream:
+        return _crossing(current, torch.cuda.ExternalStream(stream, device=device))
+    # every device's default stream has the handle 0
+    return contextlib.nullcontext() if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
 @contextlib.contextmanager

@@ -146,3 +146,25 @@ def test_overlapping_results_are_refused():
     assert norm_rc(eps=float("inf")) == -4
     for bad in (dict(x=A + 0x10000, w=A, out=A), dict(x=A, w=A + 0x10000, out=A)):
         assert linear_rc(m=2, **bad) == -4, bad
+
+
+def test_a_layers_device_is_current_in_its_calls(monkeypatch):
+    """The default streams of two devices have the same handle: with another
+    device current, the layer's has to be set all the same."""
+    import contextlib
+    from types import SimpleNamespace
+    entered = []
+
+    @contextlib.contextmanager
+    def device(d):
+        entered.append(d)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    one = torch.device("cuda", 1)
+    with cm._layer_stream(0, torch.device("cuda", 0)):
+        assert not entered
+    with cm._layer_stream(0, one):
+        assert entered == [one]
