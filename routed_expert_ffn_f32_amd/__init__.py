@@ -786,10 +786,15 @@ class _RoutedCalls:
         the result is the layer's float32 output, to be added to the residual
         by the next norm."""
         import torch
-        hidden = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+        dev, h = self.workspace.device, self.cfg.hidden
+        _matrix(x, "x", dev, None, h)
+        T = x.shape[0]
         if out is None:
-            out = torch.empty_like(hidden)
-        with _layer_stream(self.stream, x.device):
+            out = torch.empty((T, h), dtype=torch.float32, device=dev)
+        elif _matrix(out, "out", dev, T, h, torch.float32) != h and T > 1:
+            raise ValueError("out: expected a contiguous tensor")
+        hidden = torch.empty((T, h), dtype=torch.float32, device=dev)
+        with _layer_stream(self.stream, dev):
             rms_norm(x, norm_weight, eps, residual=residual, out=hidden)
             return self.forward(hidden, out)
 

@@ -1,6 +1,7 @@
 """The operators around the layer without a GPU: every refusal is made on the
 host before any HIP call, by the C entry points (error codes) and by the
 Python functions (ValueError), and calls with nothing to do succeed."""
+import contextlib
 import ctypes
 
 import pytest
@@ -151,7 +152,6 @@ def test_overlapping_results_are_refused():
 def test_a_layers_device_is_current_in_its_calls(monkeypatch):
     """The default streams of two devices have the same handle: with another
     device current, the layer's has to be set all the same."""
-    import contextlib
     from types import SimpleNamespace
     entered = []
 
@@ -168,3 +168,39 @@ def test_a_layers_device_is_current_in_its_calls(monkeypatch):
         assert not entered
     with cm._layer_stream(0, one):
         assert entered == [one]
+
+
+class HostLayer(cm._RoutedCalls):
+    """A layer's public calls with nothing behind them: a norm or a forward
+    that is reached shows in `reached`."""
+
+    def __init__(self, monkeypatch):
+        self.cfg = cm.make_config(hidden=128, n_experts=8, top_k=2, inter=64, n_shared=0, routed_scaling_factor=1.0,
+                                  max_tokens=4)
+        self.workspace, self.stream, self.handle, self.reached = torch.empty(0), 0, 1, []
+        monkeypatch.setattr(cm, "rms_norm", lambda *a, **kw: self.reached.append("norm"))
+        monkeypatch.setattr(cm, "_layer_stream", lambda *a: contextlib.nullcontext())
+
+    def forward(self, hidden, out):
+        self.reached.append("forward")
+        return out
+
+    def _layer(self):
+        return self.handle
+
+
+def test_forward_normed_refuses_shapes_that_are_not_the_layers(monkeypatch):
+    """The layer reads and writes rows of its own width: narrower ones would
+    be left behind."""
+    layer = HostLayer(monkeypatch)
+    x = torch.zeros(3, 128)
+    assert layer.forward_normed(x).shape == (3, 128) and layer.reached == ["norm", "forward"]
+    assert layer.forward_normed(x[:1], out=torch.empty(1, 200)[:, :128]).shape == (1, 128)
+    layer.reached.clear()
+    for bad in (dict(x=x[:, :64]), dict(x=torch.zeros(3, 256)), dict(x=x[0]), dict(x=torch.zeros(128, 3).t()),
+                dict(x=torch.zeros(3, 128, device="meta")), dict(x=x, out=torch.zeros(2, 128)),
+                dict(x=x, out=torch.zeros(3, 64)), dict(x=x, out=x.half()), dict(x=x, out=torch.zeros(3, 256)[:, :128]),
+                dict(x=x, out=torch.zeros(3, 128, device="meta"))):
+        with pytest.raises(ValueError):
+            layer.forward_normed(**bad)
+    assert not layer.reached
