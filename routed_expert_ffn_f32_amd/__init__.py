@@ -784,7 +784,8 @@ class _RoutedCalls:
         if one is given): forward(rms_norm(x, norm_weight, eps, residual)), on
         the layer's stream.  x and the residual may be float32, bf16 or f16;
         the result is the layer's float32 output, to be added to the residual
-        by the next norm."""
+        by the next norm.  A call that is refused leaves the residual as it
+        was."""
         import torch
         dev, h = self.workspace.device, self.cfg.hidden
         _matrix(x, "x", dev, None, h)
@@ -793,6 +794,11 @@ class _RoutedCalls:
             out = torch.empty((T, h), dtype=torch.float32, device=dev)
         elif _matrix(out, "out", dev, T, h, torch.float32) != h and T > 1:
             raise ValueError("out: expected a contiguous tensor")
+        # what the layer would refuse, while the residual is still as it was
+        if T > self.cfg.max_tokens:
+            raise ColiMoeError(COLI_MOE_ECAPACITY, "forward_normed")
+        if not self.handle or out.data_ptr() % 16:
+            raise ColiMoeError(COLI_MOE_EARG, "forward_normed")
         hidden = torch.empty((T, h), dtype=torch.float32, device=dev)
         with _layer_stream(self.stream, dev):
             rms_norm(x, norm_weight, eps, residual=residual, out=hidden)

@@ -79,3 +79,25 @@ def test_balance_with_routing_limits_and_cache(dev):
     finally:
         cache.close()
         L.close()
+
+
+def test_a_refused_call_leaves_the_residual(dev):
+    """More rows than the layer takes: refused, and the same rows in two calls
+    afterwards give what two calls on the first residual give."""
+    shape = synth.TINY
+    L = DeviceLayer(shape, 1, 0, dev, max_tokens=4)
+    try:
+        x = torch.from_numpy(synth.hidden(shape, 1, 6)).to(dev)
+        res = torch.randn(6, shape.hidden, generator=torch.Generator().manual_seed(5)).to(dev)
+        before = res.clone()
+        with pytest.raises(cm.ColiMoeError) as e:
+            L.moe.forward_normed(x, residual=res)
+        assert e.value.code == cm.COLI_MOE_ECAPACITY
+        torch.cuda.synchronize()
+        assert torch.equal(res, before)
+        for lo, hi in ((0, 4), (4, 6)):
+            L.moe.forward_normed(x[lo:hi], residual=res[lo:hi])
+        torch.cuda.synchronize()
+        assert torch.equal(res, before + x)
+    finally:
+        L.close()

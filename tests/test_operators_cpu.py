@@ -204,3 +204,21 @@ def test_forward_normed_refuses_shapes_that_are_not_the_layers(monkeypatch):
         with pytest.raises(ValueError):
             layer.forward_normed(**bad)
     assert not layer.reached
+
+
+def test_forward_normed_refuses_before_the_residual_changes(monkeypatch):
+    """Calls that the layer refuses are refused before the norm stores the sum:
+    a caller that splits the batch and calls again adds once."""
+    layer = HostLayer(monkeypatch)
+    many, wide = torch.zeros(5, 128), torch.zeros(3 * 128 + 1)
+    with pytest.raises(cm.ColiMoeError) as e:
+        layer.forward_normed(many, residual=many.clone())
+    assert e.value.code == cm.COLI_MOE_ECAPACITY
+    off = wide[1:].view(3, 128) if wide.data_ptr() % 16 == 0 else wide[:-1].view(3, 128)
+    closed = HostLayer(monkeypatch)
+    closed.handle = None
+    for refused, kw in ((layer, dict(out=off)), (closed, {})):
+        with pytest.raises(cm.ColiMoeError) as e:
+            refused.forward_normed(many[:3], residual=many[:3].clone(), **kw)
+        assert e.value.code == cm.COLI_MOE_EARG
+    assert not layer.reached and not closed.reached
