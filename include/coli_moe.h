@@ -656,7 +656,11 @@ int coli_moe_balance_grad(const coli_moe_balance_t *a, const float *coef, const 
 /* Copy the router logits of the handle's last forward (T tokens) into the
  * caller's DEVICE buffer [T][n_experts], enqueued on `stream`: with the idx
  * of coli_moe_last_routing, what coli_moe_balance takes.  (The read probes
- * overwrite them.)  Returns the T of the last forward (>= 0), -4 or -3. */
+ * overwrite them.)  A coli_moe_cache_prefetch routes other rows into the same
+ * arrays: from then until the cache's next forward this call is refused, and
+ * coli_moe_last_routing gives the prefetch's choices.  Returns the T of the
+ * last forward (>= 0), -4 NULL or misaligned pointer or after a prefetch, or
+ * -3. */
 int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream);
 
 /* Static description of an error code. */

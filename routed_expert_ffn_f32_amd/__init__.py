@@ -805,7 +805,9 @@ class _RoutedCalls:
             return self.forward(hidden, out)
 
     def last_logits(self):
-        """Router logits [T, E] of the last forward."""
+        """Router logits [T, E] of the last forward.  Refused (ColiMoeError)
+        between a prefetch, which routes into the same arrays, and the next
+        forward."""
         import torch
         dev = self.workspace.device
         T = coli_moe_last_routing(self._layer())
@@ -817,7 +819,7 @@ class _RoutedCalls:
 
     def balance(self, alpha: float, scores: str = "sigmoid", offsets=None, mask=None):
         """balance_loss of the last forward's routing: (loss [S], counts
-        [S, E], coef [S, E])."""
+        [S, E], coef [S, E]).  Refused after a prefetch, as last_logits."""
         import torch
         dev = self.workspace.device
         T = coli_moe_last_routing(self._layer())

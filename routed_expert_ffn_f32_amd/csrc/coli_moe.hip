@@ -217,6 +217,7 @@ void set_up(coli_moe_t *m, const coli_moe_config_t &cfg, const coli_moe_weights_
   m->ws = ws;
   m->L = L;
   m->last_T = 0;
+  m->route_only = false;
   m->prof_calls_left = 0;
   m->prof_calls_done = 0;
   m->prof_used = 0;
@@ -276,6 +277,7 @@ int forward_phases(coli_moe_t *m, const float *hidden, float *out, int32_t T, hi
   if (T == 0) return COLI_MOE_OK;
   if (!hidden || !aligned(hidden, 16)) return COLI_MOE_EARG;
   if ((phase & kPhaseExperts) && (!out || !aligned(out, 16))) return COLI_MOE_EARG;
+  m->route_only = !(phase & kPhaseExperts);
   const coli_moe_config_t &c = m->cfg;
   const Layout &L = m->L;
   const int E = c.n_experts, k = c.top_k, h = c.hidden, I = c.inter;
@@ -565,7 +567,7 @@ int coli_moe_last_routing(const coli_moe_t *mc, int32_t *idx, float *w, int32_t 
 }
 
 int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream) {
-  if (!m || !logits || !aligned(logits, 4)) return COLI_MOE_EARG;
+  if (!m || !logits || !aligned(logits, 4) || m->route_only) return COLI_MOE_EARG;
   const size_t bytes = (size_t)m->last_T * m->cfg.n_experts * 4;
   if (bytes && hipMemcpyAsync(logits, m->ws + m->L.logits, bytes, hipMemcpyDeviceToDevice,
                               static_cast<hipStream_t>(stream)) != hipSuccess)

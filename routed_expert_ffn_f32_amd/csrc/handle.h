@@ -31,6 +31,7 @@ struct coli_moe {
   char *ws;
   Layout L;
   int last_T;
+  bool route_only;  // the last call only routed (a prefetch): its logits and choices are no forward's
   // profiling
   int prof_calls_left;
   int prof_calls_done;

@@ -101,3 +101,27 @@ def test_a_refused_call_leaves_the_residual(dev):
         assert torch.equal(res, before + x)
     finally:
         L.close()
+
+
+def test_balance_is_never_a_prefetchs(dev):
+    """A prefetch routes other rows: no logits and no balance until the next
+    forward, which gives its own."""
+    shape = synth.TINY
+    L = DeviceLayer(shape, 1, 0, dev, max_tokens=4, keep_host=True)
+    host = {k: torch.from_numpy(np.ascontiguousarray(v)).pin_memory() for k, v in L.host_routed.items()}
+    cache = cm.ExpertCache(L.moe.cfg, L.tensors, host, n_slots=8)
+    try:
+        x = torch.from_numpy(synth.hidden(shape, 1, 4)).to(dev)
+        cache(x)
+        z, want = cache.last_logits(), cache.balance(ALPHA)
+        cache.prefetch(-x[:2], 1)
+        for call in (cache.last_logits, lambda: cache.balance(ALPHA)):
+            with pytest.raises(cm.ColiMoeError) as e:
+                call()
+            assert e.value.code == cm.COLI_MOE_EARG
+        cache(x)
+        assert torch.equal(cache.last_logits(), z)
+        assert all(torch.equal(p, q) for p, q in zip(cache.balance(ALPHA), want))
+    finally:
+        cache.close()
+        L.close()
