@@ -57,6 +57,8 @@ __device__ __forceinline__ uint64_t codes8(const float (&y)[kVec], float scale, 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (e4m3) {
+#pragma unroll
+      for (int j = 4 * h; j < 4 * h + 4; ++j) v[j] = copysignf(v[j], y[j]);  // the remainder step turns -0 into +0
       int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h], v[4 * h + 1], 0, false);
       p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], p, true);
       w[h] = (uint32_t)p;

@@ -264,3 +264,17 @@ def test_rows_that_are_not_finite_stay_visible(dev, bad, hidden):
             assert scales[nan].isnan().all() and not codes[nan].view(torch.int8).any()
             want = cm.rms_norm(x[ok], w, out_dtype=out, group=group)
             assert torch.equal(codes[ok].view(torch.int8), want[0].view(torch.int8)) and torch.equal(scales[ok], want[1])
+
+
+@pytest.mark.parametrize("hidden", [8, 300, 2050])
+def test_signs_of_zero_codes(dev, hidden):
+    """e4m3 has a negative zero: the code of -0, and of a negative quotient
+    that rounds to it."""
+    x = make(3, hidden, F32, 50)
+    x[0, ::2], x[0, 1::4] = -0.0, 0.0
+    x[1, 1:] *= 2.0 ** -20
+    x[2, :4] = torch.tensor([-2.0 ** -149, -0.0, 2.0 ** -149, 0.0])
+    _, y64, y32 = reference(x, None, 1e-6)
+    for group in (0, 64):
+        (codes, scales), _ = run(dev, x, None, 1e-6, out_dtype=E4, group=group)
+        check_codes(codes.cpu(), scales.cpu(), y32, y64, E4, group)
