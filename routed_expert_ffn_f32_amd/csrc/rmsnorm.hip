@@ -29,11 +29,10 @@ constexpr int kVec = 8;  // columns of one piece
 
 // 1 / sqrt(m), m > 0: the instruction's estimate (about 2^-24) and two Newton
 // steps, far below the float32 it is rounded to.
-__device__ __forceinline__ float rsqrt64(double m) {
+__device__ __forceinline__ double rsqrt64(double m) {
   double y = __builtin_amdgcn_rsq(m);
   y = __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
-  y = __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
-  return (float)y;
+  return __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
 }
 
 // Codes of one piece: round(y / scale) to the nearest, ties to even.  With
@@ -161,7 +160,19 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
   }
   const double mean = sum / (double)h + (double)a.eps;
   // a row of zeros without eps: zeros; of Inf or NaN: NaN (for Inf, by the Newton steps)
-  const float r = mean != 0.0 ? rsqrt64(mean) : 0.0f;
+  double r64 = mean != 0.0 ? rsqrt64(mean) : 0.0;
+  // 1 / rms of a row near either end of float32's range would pass the other
+  // end, or become subnormal: a power of two goes from r to s, which is exact
+  // (elements of s that it makes subnormal give results far below that)
+  if (r64 > 0x1p+100 || r64 < 0x1p-100) {
+    const float up = r64 > 1.0 ? 0x1p+64f : 0x1p-64f;
+    r64 *= r64 > 1.0 ? 0x1p-64 : 0x1p+64;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) s[i][j] *= up;
+  }
+  const float r = (float)r64;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
 #pragma unroll

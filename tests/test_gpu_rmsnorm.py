@@ -278,3 +278,42 @@ def test_signs_of_zero_codes(dev, hidden):
     for group in (0, 64):
         (codes, scales), _ = run(dev, x, None, 1e-6, out_dtype=E4, group=group)
         check_codes(codes.cpu(), scales.cpu(), y32, y64, E4, group)
+
+
+@pytest.mark.parametrize("hidden", [8, 120, 300, 1000, 2050, 6144, 16391, 32768])
+def test_rows_at_both_ends_of_the_range(dev, hidden):
+    """Without eps, rows of float32's and bf16's subnormals and of its largest
+    values: 1 / rms is not a (normal) float32 there, the results are of order
+    1.  The reference takes the power of two from one factor to the other too,
+    which changes no rounding."""
+    g = torch.Generator().manual_seed(hidden)
+    x = torch.randn(9, hidden, generator=g)
+    x[0] = torch.randint(-3, 4, (hidden,), generator=g) * 2.0 ** -149
+    x[0, 0], x[0, hidden // 2] = 0.0, 2.0 ** -149
+    x[1] = 0
+    x[1, hidden - 1] = -2.0 ** -149
+    for row, e in ((2, -128), (3, -105), (4, -100), (5, -95), (6, 99), (7, 126)):
+        x[row] *= 2.0 ** e
+    x[8] *= 1e-37
+    x[8, 3] = 3.4e38
+    x.clamp_(-3.4e38, 3.4e38)
+    assert x[0].any() and torch.isfinite(x).all()
+    w = 1 + 0.1 * make(1, hidden, F32, 1)[0]
+    for v in (x, x.bfloat16()):
+        s = v.float()
+        ok = torch.isfinite(s).all(1)  # the largest values round to Inf in bf16: a row of NaN
+        assert ok.all() or v.dtype == BF16
+        r = 1 / (s.double().square().sum(1, keepdim=True) / hidden).sqrt()
+        r = torch.where(torch.isfinite(r), r, torch.zeros_like(r))  # and the smallest to 0: a row of zeros
+        far = torch.where(r > 2.0 ** 100, 64.0, torch.where(r < 2.0 ** -100, -64.0, 0.0)).double()
+        y32 = (s.double() * 2.0 ** far).float() * (r * 2.0 ** -far).float() * w
+        y64 = s.double() * r * w.double()
+        for out in (F32, BF16):
+            got = run(dev, v, w, 0.0, out_dtype=out)[0].cpu()
+            check_float(got[ok], y64[ok], out)
+            assert got[~ok].isnan().all()
+        for out in (I8, E4):
+            for group in (0, 64):
+                codes, scales = (t.cpu() for t in run(dev, v, w, 0.0, out_dtype=out, group=group)[0])
+                check_codes(codes[ok], scales[ok], y32[ok], y64[ok], out, group)
+                assert scales[~ok].isnan().all()
