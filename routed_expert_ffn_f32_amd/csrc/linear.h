@@ -110,6 +110,22 @@ __device__ __forceinline__ void fetch8(const void *base, int type, int64_t i, in
   unpack8(type, WHOLE ? load_raw8(base, type, i) : load_raw8(base, type, i, n), v);
 }
 
+// v[j] *= sx w[j], the sum times the row's scale first: the product of two
+// scales alone may leave float32's range where the result does not (two of
+// 1e-22 on a sum of 2^30).  A sum other than 0 lies in 2^-18 .. 2^34, so with
+// sx in 2^-90 .. 2^90 the first product is a normal float32, whatever w is;
+// rows of other scales are multiplied in float64.
+__device__ __forceinline__ void scale8(float (&v)[8], float sx, const float (&w)[8]) {
+  const float size = fabsf(sx);
+  if ((size < 0x1p-90f && size > 0.0f) || size > 0x1p+90f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)((double)v[j] * sx * w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * sx * w[j];
+  }
+}
+
 // The epilogue up to the residual of 8 neighbouring outputs (row m, columns n
 // .. n + 7): v = the products' sums (up: those of the up rows, SwiGLU only),
 // float32.  WHOLE: n + 7 < a.n.
@@ -121,12 +137,10 @@ __device__ __forceinline__ void activate8(const coli_moe_linear_t &a, int m, int
   if (a.x_scale) {
     const float sx = a.x_scale[m];
     fetch8<WHOLE>(a.w_scale, COLI_MOE_F32, n, cnt, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= sx * w[j];
+    scale8(v, sx, w);
     if (gated) {
       fetch8<WHOLE>(a.w_scale, COLI_MOE_F32, (int64_t)a.n + n, cnt, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) up[j] *= sx * w[j];
+      scale8(up, sx, w);
     }
   }
   if (a.bias) {

@@ -287,3 +287,33 @@ def test_rings_of_the_small_blocks(dev, m, n, k, kind):
 @pytest.mark.parametrize("m,n,k", [(100, 3000, 1096), (250, 3050, 1480), (380, 2990, 968)])
 def test_swiglu_on_the_small_blocks(dev, m, n, k, kind):
     test_swiglu_on_every_block_shape(dev, m, n, k, kind)
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("m,n", [(1, 37), (20, 64), (60, 300), (129, 1030), (300, 500), (1000, 6100)])
+def test_scales_of_every_magnitude(dev, m, n, kind):
+    """Scales whose product alone leaves float32's range, and zeros: what
+    counts is the sum times both.  Sums are whole numbers below 2^24, exact;
+    two products round (u |v| in all), the last perhaps to a subnormal (half
+    of 2^-149)."""
+    g = torch.Generator().manual_seed(m)
+    x, w = ints((m, 64), 9, g), ints((n, 64), 9, g)
+    x[m // 2], w[5] = 0, 0
+    x[0], w[1] = -128 if kind == I8 else 448, -128 if kind == I8 else -448
+    far = torch.tensor([1e-22, 1e22, 2.0 ** -140, 1e-38, 1e30, 2.0 ** 120, 1e-28, 1e26, 1.0, 0.0])
+    sx, sw = far[torch.randint(0, 10, (m,), generator=g)], -far[torch.randint(0, 10, (n,), generator=g)]
+    sx[0], sw[1], sw[2], sw[3] = 1e-22, -1e-22, 1e22, 1e30
+    want = (x @ w.t()) * sx[:, None].double() * sw.double()
+    xd, wd = padded(x, kind, dev, 0), padded(w, kind, dev, 0)
+    got = cm.linear(xd, wd, sx.to(dev), sw.to(dev), out_dtype=F32).cpu()
+    over = want.float().isinf()
+    assert torch.equal(got[over], want.float()[over]) and torch.isfinite(got[~over]).all()
+    err = (got.double() - want)[~over].abs()
+    assert (err <= U * want[~over].abs() + 2.0 ** -150).all()
+    # powers of two that cancel change nothing
+    one = torch.ones(m, device=dev), torch.ones(n, device=dev)
+    for act in ACTS:
+        rows, cols = (wd[:n // 2 * 2], one[1][:n // 2 * 2]) if act == "swiglu" else (wd, one[1])
+        plain = cm.linear(xd, rows, one[0], cols, act=act, out_dtype=F32)
+        for e in (-110, -80, 80, 110):
+            assert torch.equal(cm.linear(xd, rows, one[0] * 2.0 ** e, cols * 2.0 ** -e, act=act, out_dtype=F32), plain)
