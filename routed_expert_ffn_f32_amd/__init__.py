@@ -453,7 +453,9 @@ def coli_moe_last_logits(handle, logits: int, stream: int = 0) -> int:
 # the current stream of the tensors' device; results are allocated there
 # unless given.  Tensors of other devices, shapes or types than described
 # raise ValueError; sizes and alignments that the library refuses raise
-# ColiMoeError.
+# ColiMoeError.  Results carry no autograd history whatever the arguments do;
+# tensors written in place are marked as changed, so that a backward pass that
+# needs what stood there before raises.
 # ---------------------------------------------------------------------------
 
 _DTYPES: dict = {}  # torch dtype -> COLI_MOE_* element type
@@ -540,8 +542,10 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
     Returns the normed rows in out_dtype (default: x's type), or for int8 and
     float8_e4m3fn the pair (codes, scales) with scales [rows, 1], or
     [rows, ceil(hidden / group)] for a group of 64 or 128 columns.
-    coli_moe_rmsnorm in include/coli_moe.h gives the formulas."""
+    Forward only: no gradient goes through it.  coli_moe_rmsnorm in
+    include/coli_moe.h gives the formulas."""
     import torch
+    written = ()  # the caller's tensors that this call writes
     dev = _gpu(x, "x")
     ldx = _matrix(x, "x", dev)
     rows, hidden = x.shape
@@ -552,6 +556,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
         out, ldo = x.new_empty((rows, hidden), dtype=out_dtype), hidden
     else:
         ldo = _matrix(out, "out", dev, rows, hidden, out_dtype)
+        written = (out,)
     rt = wt = ldr = ldro = lds = 0
     rp = rop = wp = sp = None
     if residual is not None:
@@ -561,6 +566,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
         if residual_out is not None:
             ldro = _matrix(residual_out, "residual_out", dev, rows, hidden, residual.dtype)
             rop = residual_out.data_ptr()
+        written += (residual if residual_out is None else residual_out,)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if weight is not None:
@@ -575,6 +581,7 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
             scales, lds = x.new_empty((rows, n), dtype=torch.float32), n
         else:
             lds = _matrix(scales, "scales", dev, rows, n, torch.float32)
+            written += (scales,)
         sp = scales.data_ptr()
     else:
         if scales is not None:
@@ -584,6 +591,8 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
         _enqueue("coli_moe_rmsnorm", dev,
                  coli_moe_rmsnorm_t(rows, hidden, xt, rt, wt, ot, group, eps, x.data_ptr(), ldx, rp, ldr, rop, ldro,
                                     wp, out.data_ptr(), ldo, sp, lds))
+        if written:
+            torch._C._increment_version(written)
     return out if scales is None else (out, scales)
 
 
@@ -599,9 +608,10 @@ def linear(x, w, x_scale=None, w_scale=None, bias=None, act: str = "none", resid
     hold the gate rows and then as many up rows, and n is half of w's rows.
     The result [m, n] has out_dtype (float32, bf16 or f16; default: the
     residual's type, else x's, or bf16 for 8 bits), which is also the
-    residual's type; out may be the residual.  coli_moe_linear in
-    include/coli_moe.h gives the formulas."""
+    residual's type; out may be the residual.  Forward only: no gradient goes
+    through it.  coli_moe_linear in include/coli_moe.h gives the formulas."""
     import torch
+    given = out is not None
     dev = _gpu(x, "x")
     ldx = _matrix(x, "x", dev)
     m, k = x.shape
@@ -645,6 +655,8 @@ def linear(x, w, x_scale=None, w_scale=None, bias=None, act: str = "none", resid
         _enqueue("coli_moe_linear", dev,
                  coli_moe_linear_t(m, n, k, code, ot, bt, _ACTS[act], x.data_ptr(), ldx, w.data_ptr(), ldw, sxp, swp,
                                    bp, rp, ldr, out.data_ptr(), ldo))
+        if given:
+            torch._C._increment_version((out,))
     return out
 
 
@@ -699,8 +711,11 @@ def balance_loss(logits, idx, alpha: float, scores: str = "sigmoid", offsets=Non
     the sequences' rows (default: one sequence of all tokens), mask [T] the
     valid tokens (default: all).
 
-    Returns (loss [S], counts [S, E] int32, coef [S, E]); balance_grad takes
-    coef.  coli_moe_balance in include/coli_moe.h gives the formulas."""
+    Returns (loss [S], counts [S, E] int32, coef [S, E]).  The loss is a number
+    without history, also where the logits have one: its gradient comes from
+    balance_grad, which takes coef, and
+    logits.backward(balance_grad(logits, coef, ...)) carries it to the router.
+    coli_moe_balance in include/coli_moe.h gives the formulas."""
     results, enqueue = _balance_loss(logits, idx, alpha, scores, offsets, mask)
     enqueue()
     return results
@@ -717,12 +732,15 @@ def balance_grad(logits, coef, dloss=None, scores: str = "sigmoid", offsets=None
         raise ValueError("coef: expected a contiguous tensor")
     if dloss is not None:
         _vector(dloss, "dloss", dev, S, torch.float32)
+    given = out is not None
     if out is None:
         out, ldo = (logits.new_empty if offsets is None else logits.new_zeros)((T, E)), E
     else:
         ldo = _matrix(out, "out", dev, T, E, torch.float32)
     _enqueue("coli_moe_balance_grad", dev, a, coef.data_ptr(), None if dloss is None else dloss.data_ptr(),
              out.data_ptr(), ldo)
+    if given:
+        torch._C._increment_version((out,))
     return out
 
 

@@ -355,3 +355,38 @@ def test_many_sequences_over_several_batches(dev, kind):
     c = got[seq[inside]]
     unit = 0.25 * (np.abs(c) + 0.25 * np.abs(c).sum(1, keepdims=True))
     assert (np.abs(d[inside] - 0.25 * (c - c.mean(1, keepdims=True))) <= 48 * U * unit + 1e-37).all()
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_gradient_reaches_a_router(dev, scores):
+    """The documented way from the loss to a router's weights, against autograd
+    of the formula in 64 bits.  Tolerance: the gradient's 48 u on every element
+    and the float32 product's sum of T terms, both of sum |x| |dz|."""
+    g = torch.Generator().manual_seed(11)
+    T, E, h, k = 50, 24, 40, 3
+    x, w = torch.randn(T, h, generator=g), torch.randn(h, E, generator=g) / 6
+    wd = w.to(dev).requires_grad_()
+    logits = x.to(dev) @ wd
+    idx = torch.topk(logits.detach(), k, dim=1).indices.to(torch.int32)
+    off = torch.tensor([0, 20, T], dtype=torch.int32, device=dev)
+    loss, counts, coef = cm.balance_loss(logits, idx, ALPHA, scores, off)
+    assert not loss.requires_grad
+    d = cm.balance_grad(logits, coef, None, scores, off)
+    logits.backward(d)
+    # the same logits in 64 bits (as rounded by the product), their gradient by autograd
+    z = logits.detach().cpu().double().requires_grad_()
+    total = 0.0
+    for s in range(2):
+        zs = z[off[s]:off[s + 1]]
+        e = torch.exp(zs - zs.detach().amax(1, keepdim=True)) if scores == "softmax" else 1 / (1 + torch.exp(-zs))
+        p = e / e.sum(1, keepdim=True)
+        n = counts[s].cpu().double()
+        total = total + float(np.float32(ALPHA)) * (E * n / n.sum() * p.mean(0)).sum()
+    total.backward()
+    total = float(total.detach())
+    assert abs(float(loss.sum()) - total) <= 27 * U * total
+    _, _, _, _, unit = reference(logits.detach().cpu().numpy(), idx.cpu().numpy(), off.tolist(), np.ones(T, bool), scores,
+                                 float(np.float32(ALPHA)), np.ones(2))
+    want = x.double().t() @ z.grad
+    tol = x.double().abs().t() @ (48 * U * torch.from_numpy(unit) + T * U * z.grad.abs())
+    assert ((wd.grad.cpu().double() - want).abs() <= tol).all()

@@ -222,3 +222,31 @@ def test_forward_normed_refuses_before_the_residual_changes(monkeypatch):
             refused.forward_normed(many[:3], residual=many[:3].clone(), **kw)
         assert e.value.code == cm.COLI_MOE_EARG
     assert not layer.reached and not closed.reached
+
+
+def test_tensors_written_in_place_are_marked_as_changed(monkeypatch):
+    """A backward pass that saved the old contents of a residual or a result
+    raises; nothing else is marked."""
+    monkeypatch.setattr(cm, "_gpu", lambda t, what: t.device)
+    monkeypatch.setattr(cm, "_enqueue", lambda *a: None)
+    x, w = torch.zeros(2, 64), torch.zeros(8, 64)
+    h, q = x.bfloat16(), torch.zeros(2, 64, dtype=torch.int8)
+    res, kept, out, scales = torch.zeros(2, 64), torch.zeros(2, 64), torch.zeros(2, 64), torch.zeros(2, 1)
+    cm.rms_norm(x, residual=res)
+    assert res._version == 1
+    cm.rms_norm(x, residual=res, residual_out=kept, out=out)
+    assert (res._version, kept._version, out._version) == (1, 1, 1)
+    cm.rms_norm(x, out=q, scales=scales)
+    assert (q._version, scales._version) == (1, 1)
+    y = torch.zeros(2, 8)
+    cm.linear(h, w.bfloat16(), residual=y, out=y)
+    assert y._version == 1
+    cm.balance_grad(x, torch.zeros(1, 64), out=out)
+    assert out._version == 2
+    assert x._version == h._version == w._version == 0
+    leaf = torch.ones(2, 64, requires_grad=True)
+    stream = leaf * 1
+    square = stream * stream
+    assert not cm.rms_norm(x, residual=stream).requires_grad
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        square.sum().backward()
