@@ -627,7 +627,7 @@ int coli_moe_linear(const coli_moe_linear_t *a, void *stream);
 #define COLI_MOE_SCORES_SIGMOID 0
 #define COLI_MOE_SCORES_SOFTMAX 1
 typedef struct {
-  int32_t tokens;             /* rows of logits, idx and mask; 0..2^26 */
+  int32_t tokens;             /* rows of logits, idx and mask; 0..2^26, the loss: tokens * top_k < 2^31 */
   int32_t n_experts;          /* 1..512 */
   int32_t top_k;              /* 1..32, <= n_experts */
   int32_t n_seqs;             /* 1..65536 */

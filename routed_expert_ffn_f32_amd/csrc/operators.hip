@@ -119,6 +119,7 @@ int coli_moe_balance(const coli_moe_balance_t *a, float *loss, int32_t *counts, 
   const int code = balance_check(a);
   if (code != COLI_MOE_OK) return code;
   if (a->tokens > 0 && !aligned_to(a->idx, 4)) return COLI_MOE_EARG;
+  if ((int64_t)a->tokens * a->top_k > INT32_MAX) return COLI_MOE_EARG;  // counts are int32
   if (!aligned_to(loss, 4) || !aligned_to(counts, 4) || !aligned_to(coef, 4) || !aligned_to(workspace, 16))
     return COLI_MOE_EARG;
   if (workspace_bytes < coli::balance_workspace_bytes(a->tokens, a->n_experts, a->n_seqs)) return COLI_MOE_ECAPACITY;

@@ -250,3 +250,13 @@ def test_tensors_written_in_place_are_marked_as_changed(monkeypatch):
     assert not cm.rms_norm(x, residual=stream).requires_grad
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         square.sum().backward()
+
+
+def test_more_choices_than_a_count_holds_are_refused():
+    """2^26 tokens of 32 choices, all of which may name one expert, pass int32
+    by one.  The gradient, which reads no choices, has no such bound."""
+    most = dict(tokens=1 << 26, n_experts=32, logits_stride=32, top_k=32)
+    nbytes = cm.coli_moe_balance_workspace_bytes(1 << 26, 32, 1)
+    assert balance_rc(**most, nbytes=nbytes) == -4
+    assert balance_rc(**{**most, "top_k": 31}, nbytes=nbytes - 1) == -1  # the next check: nothing is enqueued
+    assert grad_rc(**most, stride=31) == -4
