@@ -21,8 +21,9 @@
 // of x or w: the last row again, results not stored.
 //
 // SwiGLU: w holds the n gate rows and then the n up rows.  A tile takes BN/2
-// of each in alternating blocks of 32, so that a wave holds the gate and the
-// up sum of the same outputs.
+// of each in alternating blocks of 32.  The gate and the up sum of an output
+// meet in the epilogue's slab in LDS; a wave of one or three column blocks
+// does not hold both.
 //
 // Blocks are mapped so that each XCD (hardware block b runs on XCD b mod 8)
 // works on neighbouring tiles, 8 tiles high: the rows that they share come
@@ -79,19 +80,16 @@ struct Tile {
           a ? S.xo[a ? i : 0] : S.wo[a ? 0 : i - kCopiesA]);
   }
 
-  static __device__ __forceinline__ void copy(const Sources &S, int i, int64_t at, uint32_t lds, int wave, int lane) {
+  // The same for the last, partial step: pieces past K come from a piece of zeros.
+  static __device__ __forceinline__ void copy_rest(const Sources &S, int i, int64_t at, uint32_t lds, int wave,
+                                                   int lane) {
     const bool a = i < kCopiesA;
     const int c = (a ? i : i - kCopiesA) * kWaves + wave;
     const char *base = a ? S.x : (GATED && (c & 4)) ? S.up : S.w;
     const uint32_t off = a ? S.xo[a ? i : 0] : S.wo[a ? 0 : i - kCopiesA];
-    const uint32_t to = lds + (uint32_t)((a ? 0 : BM * kStepBytes) + c * 8 * kStepBytes);
-    if (at + kStepBytes <= S.k_bytes) {
-      dma16(to, base + at, off);
-    } else {  // the last, partial step
-      const int row = 8 * c + (lane >> 3);
-      const bool real = at + (int64_t)piece(row, lane) < S.k_bytes;
-      dma16v(to, real ? base + at + off : reinterpret_cast<const char *>(&kZeroPiece));
-    }
+    const bool real = at + (int64_t)piece(8 * c + (lane >> 3), lane) < S.k_bytes;
+    dma16v(lds + (uint32_t)((a ? 0 : BM * kStepBytes) + c * 8 * kStepBytes),
+           real ? base + at + off : reinterpret_cast<const char *>(&kZeroPiece));
   }
 
   static __device__ __forceinline__ void run(const coli_moe_linear_t &a, char *lds_mem) {
@@ -286,7 +284,7 @@ struct Tile {
                                                    int wn, int wave, int lane, Acc (&acc)[MB][NB]) {
     block_barrier();
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy(S, i, (int64_t)G * kStepBytes, lds, wave, lane);
+    for (int i = 0; i < kCopies; ++i) copy_rest(S, i, (int64_t)G * kStepBytes, lds, wave, lane);
     dma_wait<0>();
     block_barrier();
 #pragma unroll
