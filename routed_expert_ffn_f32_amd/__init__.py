@@ -480,6 +480,8 @@ def _matrix(t, what: str, device, rows=None, cols=None, dtype=None):
                          f"strides {tuple(strides)}")
     if (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ValueError(f"{what}: expected shape {(rows, cols)}, got {tuple(shape)}")
+    if (shape[0] | shape[1]) >> 31:  # a size is an int32 in the C structs, where it would wrap around
+        raise ValueError(f"{what}: at most 2^31 - 1 rows and columns, got shape {tuple(shape)}")
     if t.device != device or (dtype is not None and t.dtype != dtype):
         _refuse_place(t, what, device, dtype)
     return strides[0]
@@ -679,8 +681,8 @@ def _balance_args(logits, idx, alpha, scores, offsets, mask):
     if offsets is not None:
         n_seqs = offsets.numel() - 1
         _vector(offsets, "offsets", dev, n_seqs + 1, torch.int32)
-        if n_seqs < 1:
-            raise ValueError("offsets: expected the bounds of at least one sequence")
+        if n_seqs < 1 or n_seqs >> 31:
+            raise ValueError(f"offsets: expected the bounds of 1 to 65536 sequences, got {n_seqs + 1} elements")
         op = offsets.data_ptr()
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8):

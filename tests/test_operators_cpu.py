@@ -260,3 +260,27 @@ def test_more_choices_than_a_count_holds_are_refused():
     assert balance_rc(**most, nbytes=nbytes) == -4
     assert balance_rc(**{**most, "top_k": 31}, nbytes=nbytes - 1) == -1  # the next check: nothing is enqueued
     assert grad_rc(**most, stride=31) == -4
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """They would wrap around on their way into the C structs: 2^32 + 4 rows
+    would be 4."""
+    monkeypatch.setattr(cm, "_gpu", lambda t, what: t.device)
+    monkeypatch.setattr(cm, "_enqueue", lambda *a: pytest.fail("enqueued"))
+    monkeypatch.setattr(cm, "_vector", lambda *a: None)
+    many = (1 << 32) + 4
+
+    def shaped(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    x, w, bf16 = shaped(many, 64), shaped(8, 64), torch.bfloat16
+    calls = [lambda: cm.rms_norm(x), lambda: cm.rms_norm(shaped(4, many)), lambda: cm.linear(x.to(bf16), w.to(bf16)),
+             lambda: cm.linear(w.to(bf16), x.to(bf16)),
+             lambda: cm.linear(shaped(2, many, dtype=bf16), shaped(3, many, dtype=bf16)),
+             lambda: cm.balance_loss(x, shaped(many, 2, dtype=torch.int32), 0.1),
+             lambda: cm.balance_grad(x, shaped(1, 64)),
+             lambda: cm.balance_loss(w, shaped(8, 2, dtype=torch.int32), 0.1, offsets=shaped(many, dtype=torch.int32))]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="2\\^31|65536"):
+            call()
+            pytest.fail(f"call {i} was not refused")
