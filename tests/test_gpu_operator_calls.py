@@ -269,3 +269,43 @@ def test_layer_on_its_own_stream(dev):
     finally:
         torch.cuda.synchronize()
         L.close()
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_layer_calls_captured(dev, own_stream):
+    """The norm with the layer, the balance of its routing, the gradient and
+    the logits in one graph, on the layer's stream or beside it: replays on new
+    rows, with eager calls of the same layer in between, give the eager
+    results each time."""
+    shape, T = synth.TINY, 8
+    L = DeviceLayer(shape, 1, 0, dev, max_tokens=T)
+    own, side = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.Generator().manual_seed(6)
+
+    def block(x, res):
+        out = L.moe.forward_normed(x, residual=res)
+        balance = L.moe.balance(0.01)
+        z = L.moe.last_logits()
+        return out, *balance, z, cm.balance_grad(z, balance[2]), res
+
+    try:
+        xs, rs = ([torch.randn(T, shape.hidden, generator=g).to(dev) for _ in range(3)] for _ in range(2))
+        want = [[t.clone() for t in block(x, r.clone())] for x, r in zip(xs, rs)]
+        x, res = xs[0].clone(), rs[0].clone()
+        torch.cuda.synchronize()
+        L.moe.stream = (own if own_stream else side).cuda_stream
+        with torch.cuda.stream(side):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                got = block(x, res)
+            for i in (1, 2, 0, 1):
+                x.copy_(xs[i])
+                res.copy_(rs[i])
+                graph.replay()
+                side.synchronize()
+                assert all(torch.equal(p, q) for p, q in zip(got, want[i])), i
+                block(xs[(i + 1) % 3], rs[0].clone())
+                side.synchronize()
+    finally:
+        torch.cuda.synchronize()
+        L.close()
