@@ -160,19 +160,20 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void rmsnorm_kernel(
   }
   const double mean = sum / (double)h + (double)a.eps;
   // a row of zeros without eps: zeros; of Inf or NaN: NaN (for Inf, by the Newton steps)
-  double r64 = mean != 0.0 ? rsqrt64(mean) : 0.0;
-  // 1 / rms of a row near either end of float32's range would pass the other
-  // end, or become subnormal: a power of two goes from r to s, which is exact
-  // (elements of s that it makes subnormal give results far below that)
-  if (r64 > 0x1p+100 || r64 < 0x1p-100) {
+  const double r64 = mean != 0.0 ? rsqrt64(mean) : 0.0;
+  float r = (float)r64;
+  // 1 / rms of a row near either end of float32's range passes the other end,
+  // or is subnormal: a power of two goes from r to s, which is exact (elements
+  // of s that it makes subnormal give results far below that)
+  constexpr int kNormal = 0x108;
+  if (!__builtin_amdgcn_classf(r, kNormal)) {
     const float up = r64 > 1.0 ? 0x1p+64f : 0x1p-64f;
-    r64 *= r64 > 1.0 ? 0x1p-64 : 0x1p+64;
+    r = (float)(r64 > 1.0 ? r64 * 0x1p-64 : r64 * 0x1p+64);
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
 #pragma unroll
       for (int j = 0; j < kVec; ++j) s[i][j] *= up;
   }
-  const float r = (float)r64;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
 #pragma unroll
