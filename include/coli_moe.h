@@ -513,8 +513,9 @@ int coli_moe_test_cache_policy(int32_t n_experts, int32_t n_slots, int32_t reser
  *   out = round(y / scale), to the nearest, ties to even, |out| <= Q;
  * a group of zeros has scale 0 and codes 0, and a row of zeros stays zero
  * without eps too.  A row whose s holds Inf or NaN becomes NaN (8 bits: its
- * scales NaN, its codes 0); other rows are not affected.  Weights must be
- * finite.  The stride of a single row is not looked at.
+ * scales NaN, its codes 0); other rows are not affected.  A group whose
+ * largest |y| passes float32's range has scale Inf and codes 0.  Weights must
+ * be finite.  The stride of a single row is not looked at.
  */
 typedef struct {
   int32_t rows;           /* >= 0; 0 checks the arguments and enqueues nothing */

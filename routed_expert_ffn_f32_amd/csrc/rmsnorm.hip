@@ -41,7 +41,7 @@ __device__ __forceinline__ double rsqrt64(double m) {
 // kTiny the reciprocal or the remainder could leave float32's range.
 __device__ __forceinline__ uint64_t codes8(const float (&y)[kVec], float scale, bool e4m3) {
   constexpr float kTiny = 0x1p-60f, kHuge = 0x1p+100f;
-  if (!(scale > 0.0f)) return 0;
+  if (!(scale > 0.0f && scale < __builtin_inff())) return 0;
   const float q = e4m3 ? 448.0f : 127.0f, inv = 1.0f / scale;
   const bool divide = !(scale >= kTiny && scale <= kHuge);
   float v[kVec];

@@ -317,3 +317,22 @@ def test_rows_at_both_ends_of_the_range(dev, hidden):
                 codes, scales = (t.cpu() for t in run(dev, v, w, 0.0, out_dtype=out, group=group)[0])
                 check_codes(codes[ok], scales[ok], y32[ok], y64[ok], out, group)
                 assert scales[~ok].isnan().all()
+
+
+@pytest.mark.parametrize("out", [I8, E4])
+def test_results_past_the_range_stay_visible(dev, out):
+    """A weight that takes one element past float32's largest: its group's
+    scale is Inf, every value of the group Inf * 0; the others are as without
+    it."""
+    x, w = make(4, 300, F32, 60), 1 + 0.1 * make(1, 300, F32, 61)[0]
+    x[2] *= 1e-3
+    x[2, 70] = 50.0
+    w[70] = 5e37
+    for group in (0, 64):
+        (codes, scales), _ = run(dev, x, w, 1e-6, out_dtype=out, group=group)
+        hit = slice(64, 128) if group else slice(0, 300)
+        at = 1 if group else 0
+        assert scales[2, at] == float("inf") and not codes[2, hit].view(torch.int8).any()
+        _, y64, y32 = reference(x, w, 1e-6)
+        rest = [0, 1, 3]
+        check_codes(codes.cpu()[rest], scales.cpu()[rest], y32[rest], y64[rest], out, group)
