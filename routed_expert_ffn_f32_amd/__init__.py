@@ -543,7 +543,8 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, residual_out=None
 
     Returns the normed rows in out_dtype (default: x's type), or for int8 and
     float8_e4m3fn the pair (codes, scales) with scales [rows, 1], or
-    [rows, ceil(hidden / group)] for a group of 64 or 128 columns.
+    [rows, ceil(hidden / group)] for a group of 64 or 128 columns (linear reads
+    scales of rows); for other types there are no scales and group is not used.
     Forward only: no gradient goes through it.  coli_moe_rmsnorm in
     include/coli_moe.h gives the formulas."""
     import torch
@@ -689,7 +690,8 @@ def _balance_args(logits, idx, alpha, scores, offsets, mask):
             raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
         _vector(mask, "mask", dev, T)
         mp = mask.data_ptr()
-    return coli_moe_balance_t(T, E, k, n_seqs, _SCORES[scores], alpha, logits.data_ptr(), ld, ip, op, mp), dev, T, E, n_seqs
+    a = coli_moe_balance_t(T, E, k, n_seqs, _SCORES[scores], alpha, logits.data_ptr(), ld, ip, op, mp)
+    return a, dev, T, E, n_seqs
 
 
 def _balance_loss(logits, idx, alpha, scores, offsets, mask):

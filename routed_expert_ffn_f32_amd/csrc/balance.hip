@@ -12,9 +12,12 @@
 // the logits once and writes as much.  One wave takes a token, expert e in
 // lane e mod 64, so a row's sums are wave reductions; four tokens at a time
 // give the loads and the reductions something to overlap with.  Sigmoid over
-// 256 experts: 65536 tokens take 24 us for the sums (2.8 TB/s; the scores'
-// arithmetic is as long as the loads) and 28 us for the gradient (4.8 TB/s);
-// 16384 tokens in 8 sequences 10, 5 (the joining launch) and 11 us.
+// 256 experts: 65536 tokens take 24 us for the sums and 28 us for the gradient
+// from HBM (2.8 and 4.8 TB/s), 19 and 23 us from the 256 MB cache; 16384
+// tokens in 8 sequences 10, 5 (the joining launch) and 11 us.  There a
+// workgroup of the sums has one batch of 64 tokens, whose loads, scores,
+// reductions and join in LDS run one after another; a second batch, loaded
+// meanwhile, adds 3.7 us (4.8 TB/s).
 //
 // Sums over tokens: a workgroup owns a run of consecutive tokens (a chunk)
 // and visits the pieces of sequences in it.  A piece's sums go to slot

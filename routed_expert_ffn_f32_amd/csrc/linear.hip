@@ -266,7 +266,8 @@ struct Tile {
         turn();
         __builtin_amdgcn_s_setprio(1);
         multiply_half(af, bf, acc, [&](int i) {
-          if (SECOND == (h == 1) && i >= kInRead) copy_step(g + kAhead + h, h ? (STAGES == 2 ? slot : next(fill)) : fill, i);
+          if (SECOND == (h == 1) && i >= kInRead)
+            copy_step(g + kAhead + h, h ? (STAGES == 2 ? slot : next(fill)) : fill, i);
         });
         __builtin_amdgcn_s_setprio(0);
         if (h == 1 && !SECOND) dma_wait<kCopies *(STAGES - 2)>();
@@ -454,7 +455,9 @@ hipError_t launch_tiles(const coli_moe_linear_t &a, hipStream_t s) {
 // CU, with what they cost: microseconds measured at 12288 bytes of K (6144
 // bf16 elements; n = 6144, m from 64 to 4096, three sets of operands in turn)
 // for up to one block a CU, and for a round that fills the chip (the clock
-// held by the power).
+// held by the power).  The same costs rank the shapes for every type and K,
+// though int8 takes half the matrix time and a short K is ruled by what a
+// block costs beside its steps: neither was fitted.
 struct Shape {
   int bm, bn;     // rows of x and of w of a block
   int one, full;  // cost of a round with fewer blocks, and of a full one

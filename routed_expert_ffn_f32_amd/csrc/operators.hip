@@ -28,7 +28,8 @@ extern "C" {
 
 int coli_moe_rmsnorm(const coli_moe_rmsnorm_t *a, void *stream) {
   using namespace coli;
-  if (!a || a->rows < 0 || a->hidden < 1 || a->hidden > 32768 || !(a->eps >= 0.0f && a->eps <= 0x1.fffffep+127f)) return COLI_MOE_EARG;
+  if (!a || a->rows < 0 || a->hidden < 1 || a->hidden > 32768) return COLI_MOE_EARG;
+  if (!(a->eps >= 0.0f && a->eps <= 0x1.fffffep+127f)) return COLI_MOE_EARG;
   if (!float_type(a->x_type) || (!float_type(a->out_type) && !byte_type(a->out_type))) return COLI_MOE_EARG;
   if (byte_type(a->out_type) ? a->group != 0 && a->group != 64 && a->group != 128 : a->group != 0)
     return COLI_MOE_EARG;
@@ -110,7 +111,8 @@ int balance_check(const coli_moe_balance_t *a) {
 extern "C" {
 
 size_t coli_moe_balance_workspace_bytes(int32_t tokens, int32_t n_experts, int32_t n_seqs) {
-  if (tokens < 0 || tokens > kMaxTokens || n_experts < 1 || n_experts > coli::kMaxExperts || n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
+  if (tokens < 0 || tokens > kMaxTokens || n_experts < 1 || n_experts > coli::kMaxExperts) return 0;
+  if (n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
   return coli::balance_workspace_bytes(tokens, n_experts, n_seqs);
 }
 
