@@ -6,7 +6,8 @@
 // 6144 at 1.12 (the library's: 1.12); there the chip is held by its power:
 // the same call on zeros takes two thirds of the time, and reading every
 // operand row from the L2 alone changes less.  4096 rows of 6144 int8 on 2048
-// gate and 2048 up rows with SwiGLU run at 2.26 PFLOP/s, e4m3 on the 16-bit cores at 1.29.  A
+// gate and 2048 up rows with SwiGLU run at 2.3 PFLOP/s; e4m3, on the 16-bit
+// cores, at 1.29 for 8192^3 and 1.0 for 4096 x 6144 x 2048 onto a residual.  A
 // workgroup computes a tile of BM x BN outputs over all of K in steps of 128
 // bytes of every row (64 16-bit or 128 8-bit elements: one whole cache line a
 // row).  Rows of x and w go straight into LDS by LDS-DMA, STAGES steps deep,
