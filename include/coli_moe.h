@@ -506,9 +506,10 @@ int coli_moe_test_cache_policy(int32_t n_experts, int32_t n_slots, int32_t reser
  * stream sees the numbers that were normed.  The mean is summed in float64
  * and r rounded once to float32 precision (its exponent may pass float32's:
  * rows of any magnitude are normed, subnormal ones without eps too), so the
- * result does not depend on how the kernel splits a row.  The output is y rounded to out_type, or 8-bit codes
- * with one float32 scale per `group` columns (the last group of a row may be
- * shorter), Q = 127 (int8) or 448 (e4m3):
+ * result does not depend on how the kernel splits a row.  The output is y
+ * rounded to out_type, or 8-bit codes with one float32 scale per `group`
+ * columns (the last group of a row may be shorter), Q = 127 (int8) or 448
+ * (e4m3):
  *   scales[row][g] = max|y| / Q over the group (float32 division),
  *   out = round(y / scale), to the nearest, ties to even, |out| <= Q;
  * a group of zeros has scale 0 and codes 0, and a row of zeros stays zero

@@ -811,7 +811,7 @@ class _RoutedCalls:
         import torch
         dev, h = self.workspace.device, self.cfg.hidden
         _matrix(x, "x", dev, None, h)
-        T = x.shape[0]
+        T, given = x.shape[0], out is not None
         if out is None:
             out = torch.empty((T, h), dtype=torch.float32, device=dev)
         elif _matrix(out, "out", dev, T, h, torch.float32) != h and T > 1:
@@ -824,7 +824,10 @@ class _RoutedCalls:
         hidden = torch.empty((T, h), dtype=torch.float32, device=dev)
         with _layer_stream(self.stream, dev):
             rms_norm(x, norm_weight, eps, residual=residual, out=hidden)
-            return self.forward(hidden, out)
+            self.forward(hidden, out)
+        if given:
+            torch._C._increment_version((out,))
+        return out
 
     def last_logits(self):
         """Router logits [T, E] of the last forward.  Refused (ColiMoeError)

@@ -284,3 +284,9 @@ def test_sizes_past_32_bits_are_refused(monkeypatch):
         with pytest.raises(ValueError, match="2\\^31|65536"):
             call()
             pytest.fail(f"call {i} was not refused")
+
+
+def test_a_layers_given_result_is_marked_as_changed(monkeypatch):
+    layer = HostLayer(monkeypatch)
+    x, out = torch.zeros(3, 128), torch.zeros(3, 128)
+    assert layer.forward_normed(x, out=out) is out and out._version == 1 and x._version == 0
