@@ -666,6 +666,188 @@ int coli_moe_balance_grad(const coli_moe_balance_t *a, const float *coef, const 
  * -3. */
 int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The attention side of a block: rotary positions, a paged key/value cache
+ * held in 4 bits, the attention that reads it and eviction from it.  As
+ * above: no handle, arguments in structs, device pointers, work on `stream`
+ * alone, nothing allocated or copied, so every call may be captured.
+ * Tensors of heads are [tokens][heads][dim] with strides in elements between
+ * tokens and between heads; the elements of a head are contiguous.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Rotary positions: the first `part` elements of every head, as part / 2
+ * pairs (2 i, 2 i + 1) (interleaved) or (i, i + part / 2), are turned by
+ * a = positions[t] * freq[i] (inverse: by -a):
+ *   out0 = scale (x0 cos a - x1 sin a),  out1 = scale (x0 sin a + x1 cos a);
+ * elements from `part` on are copied.  The inverse with the same scale is the
+ * transposed map, so it takes a gradient with respect to out to the one with
+ * respect to x.  The angle is a float64 product reduced in float64, so far
+ * positions lose nothing; the turn itself is float32, rounded once to the
+ * type.  `out` may be x itself with equal strides, else no overlap.
+ */
+typedef struct {
+  int32_t tokens;       /* 0..2^26; 0 checks the arguments and enqueues nothing */
+  int32_t heads;        /* 1..4096 */
+  int32_t dim;          /* 1..4096 */
+  int32_t part;         /* even, 0..dim */
+  int32_t type;         /* of x and out: F32, BF16 or F16 */
+  int32_t interleaved;  /* 0: pairs (i, i + part / 2), 1: pairs (2 i, 2 i + 1) */
+  int32_t inverse;      /* 0 or 1 */
+  int32_t wide;         /* positions are int64 (exact below 2^53 / freq's 24 bits), 0: int32 */
+  float scale;          /* finite */
+  const void *x;
+  int64_t x_token, x_head;
+  const void *positions; /* [tokens], may be negative */
+  const float *freq;     /* [part / 2] */
+  void *out;
+  int64_t out_token, out_head;
+} coli_moe_rotary_t;
+
+/* Errors: -4 NULL or misaligned pointer, unsupported type, dimension or
+ * stride; -3 HIP launch error. */
+int coli_moe_rotary(const coli_moe_rotary_t *a, void *stream);
+
+/*
+ * The cache: n_pages pages of page_size rows for each key head, in the
+ * layer's int4 format with 16-bit scales.  A row of head_dim columns is
+ * head_dim / 2 bytes (byte c / 2 holds column c, the low nibble the even one,
+ * 4-bit two's complement in [-8, 7]) and one bfloat16 scale per 64 columns;
+ * value = code * scale.  (A scale of 8 significant bits keeps every value
+ * exact in half precision's 11.)  Scales of neighbouring rows are adjacent:
+ * the attention reads them for several rows at once.
+ */
+typedef struct {
+  int32_t n_pages;    /* 1..2^31 - 1 */
+  int32_t page_size;  /* rows: 16, 32, 64, 128 or 256 */
+  int32_t kv_heads;   /* 1..1024 */
+  int32_t head_dim;   /* 64, 128 or 256 */
+  uint8_t *k_codes;   /* [n_pages][kv_heads][page_size][head_dim / 2], 16-byte aligned */
+  uint16_t *k_scales; /* [n_pages][kv_heads][head_dim / 64][page_size] bfloat16, 16-byte aligned */
+  uint8_t *v_codes;
+  uint16_t *v_scales;
+  float *weights;     /* [n_pages][kv_heads][page_size] accumulated attention weights; NULL: none are kept */
+} coli_moe_kv_t;
+
+/*
+ * Rows of sequences.  Row r of sequence s stands in page
+ * table[s][r / page_size] at r % page_size.  lengths[s] counts the rows of
+ * sequence s with its new ones: tokens offsets[s] .. offsets[s + 1] - 1 (n of
+ * them; offsets NULL: token s alone) are its rows lengths[s] - n ..
+ * lengths[s] - 1.  Rows before 0, rows beyond the table's width and rows of
+ * pages outside [0, n_pages) do not exist: nothing is written there, they
+ * read as zeros and no query sees them.  Tokens in no sequence (before
+ * offsets[0], from offsets[seqs] on) take no part.  Offsets outside
+ * [0, tokens] are clamped; offsets that decrease give unspecified results
+ * within the arrays.
+ */
+typedef struct {
+  int32_t tokens;         /* 0..2^22; offsets NULL: == seqs */
+  int32_t seqs;           /* 1..65536 */
+  int32_t table_width;    /* pages per sequence, >= 1; table_width * page_size <= 2^30 */
+  const int32_t *table;   /* [seqs][table_width] */
+  int64_t table_stride;
+  const int32_t *lengths; /* [seqs] */
+  const int32_t *offsets; /* [seqs + 1], ascending, or NULL */
+} coli_moe_kv_rows_t;
+
+/* Keys and values [tokens][kv_heads][head_dim] of a call. */
+typedef struct {
+  int32_t type;  /* F32, BF16 or F16 */
+  void *k;
+  int64_t k_token, k_head;
+  void *v;
+  int64_t v_token, v_head;
+} coli_moe_kv_values_t;
+
+/*
+ * Append: the tokens' keys and values (read only) become their rows.  Per 64
+ * columns: scale = max|x| / 7 rounded to bfloat16, code = x / scale rounded
+ * to the nearest, ties to even, held within [-7, 7]; a group of zeros has
+ * scale 0, a group that holds Inf or NaN scale NaN, both codes 0.  Where
+ * weights are kept, those of the rows become 0.  A row must be written once
+ * in a call.
+ * Read: the values of the tokens' rows, rounded once to the type (bfloat16
+ * rounds; float32 and, in its range, half precision do not).
+ * Errors: -4 NULL or misaligned pointer, unsupported type, dimension or
+ * stride; -3 HIP launch error.
+ */
+int coli_moe_kv_append(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, const coli_moe_kv_values_t *a,
+                       void *stream);
+int coli_moe_kv_read(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, const coli_moe_kv_values_t *a,
+                     void *stream);
+
+/*
+ * Attention of the tokens' queries over the cache: the query of row p sees
+ * the rows max(0, p - window + 1) .. p of its sequence (window 0: 0 .. p),
+ * through key head h / (q_heads / kv_heads),
+ *   out = sum_r softmax_r(scale q . k_r) v_r
+ * in float32, with the values of the cache exact and each weight rounded to
+ * half precision relative to the largest (half precision queries: to twice
+ * that) before the product with the values.  A query that sees no row gives
+ * zeros.  With weights_out (which needs kv->weights), also
+ *   weights_out[r] = kv->weights[r] + sum of the softmax weights of row r
+ * over the tokens of the call and the query heads of its key head, for every
+ * row that a query sees; other places are left as they were.  weights_out may
+ * be kv->weights.  (Rows that several sequences of the call see get the sum of
+ * some of them.)  The scaled scores have to be within float32's range.  Out
+ * rows of tokens in no sequence are left as they were (clear 0) or set to 0
+ * (clear 1).  The same call gives the same bits.
+ */
+typedef struct {
+  int32_t q_heads;  /* a multiple of kv_heads, at most 256 times as many */
+  int32_t type;     /* of q and out: BF16 or F16 */
+  int32_t window;   /* >= 0 */
+  int32_t clear;    /* 0 or 1 */
+  float scale;      /* finite */
+  const void *q;
+  int64_t q_token, q_head;
+  void *out;        /* no overlap with q */
+  int64_t out_token, out_head;
+  float *weights_out; /* as kv->weights; NULL: none */
+} coli_moe_kv_attention_t;
+
+/* Bytes of DEVICE workspace of the call, 0 for sizes out of range (pointers
+ * are not looked at, but for weights_out being NULL or not).  It holds
+ * nothing between calls; calls whose work may overlap need one each. */
+size_t coli_moe_kv_attention_workspace_bytes(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows,
+                                             const coli_moe_kv_attention_t *a);
+/* Errors: -4 NULL or misaligned pointer (workspace: 16 bytes), unsupported
+ * type, dimension or stride; -1 workspace too small; -3 HIP launch error. */
+int coli_moe_kv_attention(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, const coli_moe_kv_attention_t *a,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Eviction: of every sequence and key head with more than `keep` rows, the
+ * first `first` rows, the last `recent` and, of those between, the ones with
+ * the largest kv->weights (ties: the lower row; NaN above everything) are
+ * kept, `keep` in all, and all rows of shorter sequences.  In their order
+ * they are copied, weights included, to rows 0 .. of the pages of `into`
+ * (pages of the same cache, none of them in the table: other places are only
+ * read, so pages may be shared between sequences and the call repeated).
+ * kept[s][h][i] is the row that went to row i (-1 behind the last), and
+ * new_lengths[s] = min(lengths[s], keep).  Rows that do not exist have weight
+ * 0 when they compete and leave their places in `into` as they were.
+ * rows->tokens and rows->offsets are not looked at.
+ */
+typedef struct {
+  int32_t keep;         /* 1..into_width * page_size */
+  int32_t first;        /* >= 0 */
+  int32_t recent;       /* >= 0; first + recent <= keep */
+  int32_t into_width;   /* pages per sequence */
+  const int32_t *into;  /* [seqs][into_width]; not the table */
+  int64_t into_stride;
+  int32_t *kept;        /* [seqs][kv_heads][keep] */
+  int32_t *new_lengths; /* [seqs]; may not be lengths */
+} coli_moe_kv_evict_t;
+
+/* Errors: -4 NULL or misaligned pointer, unsupported dimension or stride, a
+ * cache without weights; -3 HIP launch error. */
+int coli_moe_kv_evict(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, const coli_moe_kv_evict_t *a,
+                      void *stream);
+
 /* Static description of an error code. */
 const char *coli_moe_error_string(int32_t code);
 

@@ -112,6 +112,44 @@ class coli_moe_balance_t(ctypes.Structure):
                 ("idx", ctypes.c_void_p), ("seq_offsets", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
 
 
+class coli_moe_rotary_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "heads", "dim", "part", "type", "interleaved", "inverse",
+                                              "wide")] + \
+               [("scale", ctypes.c_float), ("x", ctypes.c_void_p), ("x_token", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("positions", ctypes.c_void_p), ("freq", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64)]
+
+
+class coli_moe_kv_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "kv_heads", "head_dim")] + \
+               [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales", "weights")]
+
+
+class coli_moe_kv_rows_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "seqs", "table_width")] + \
+               [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lengths", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p)]
+
+
+class coli_moe_kv_values_t(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("k", ctypes.c_void_p), ("k_token", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v", ctypes.c_void_p), ("v_token", ctypes.c_int64),
+                ("v_head", ctypes.c_int64)]
+
+
+class coli_moe_kv_attention_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("q_heads", "type", "window", "clear")] + \
+               [("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_token", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_token", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("weights_out", ctypes.c_void_p)]
+
+
+class coli_moe_kv_evict_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("keep", "first", "recent", "into_width")] + \
+               [("into", ctypes.c_void_p), ("into_stride", ctypes.c_int64), ("kept", ctypes.c_void_p),
+                ("new_lengths", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -207,6 +245,19 @@ def load_library():
         L.coli_moe_balance_grad.restype = ctypes.c_int
         L.coli_moe_last_logits.argtypes = [vp, vp, vp]
         L.coli_moe_last_logits.restype = ctypes.c_int
+        L.coli_moe_rotary.argtypes = [ctypes.POINTER(coli_moe_rotary_t), vp]
+        L.coli_moe_rotary.restype = ctypes.c_int
+        kvp, rp = ctypes.POINTER(coli_moe_kv_t), ctypes.POINTER(coli_moe_kv_rows_t)
+        for name in ("coli_moe_kv_append", "coli_moe_kv_read"):
+            getattr(L, name).argtypes = [kvp, rp, ctypes.POINTER(coli_moe_kv_values_t), vp]
+            getattr(L, name).restype = ctypes.c_int
+        ap = ctypes.POINTER(coli_moe_kv_attention_t)
+        L.coli_moe_kv_attention_workspace_bytes.argtypes = [kvp, rp, ap]
+        L.coli_moe_kv_attention_workspace_bytes.restype = sz
+        L.coli_moe_kv_attention.argtypes = [kvp, rp, ap, vp, sz, vp]
+        L.coli_moe_kv_attention.restype = ctypes.c_int
+        L.coli_moe_kv_evict.argtypes = [kvp, rp, ctypes.POINTER(coli_moe_kv_evict_t), vp]
+        L.coli_moe_kv_evict.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -442,6 +493,34 @@ def coli_moe_balance_grad(args: coli_moe_balance_t, coef: int, dloss, dlogits: i
                           stream: int = 0) -> int:
     return _check(load_library().coli_moe_balance_grad(args, coef, dloss, dlogits, dlogits_stride, stream),
                   "coli_moe_balance_grad")
+
+
+def coli_moe_rotary(args: coli_moe_rotary_t, stream: int = 0) -> int:
+    return _check(load_library().coli_moe_rotary(args, stream), "coli_moe_rotary")
+
+
+def coli_moe_kv_append(kv: coli_moe_kv_t, rows: coli_moe_kv_rows_t, args: coli_moe_kv_values_t,
+                       stream: int = 0) -> int:
+    return _check(load_library().coli_moe_kv_append(kv, rows, args, stream), "coli_moe_kv_append")
+
+
+def coli_moe_kv_read(kv: coli_moe_kv_t, rows: coli_moe_kv_rows_t, args: coli_moe_kv_values_t, stream: int = 0) -> int:
+    return _check(load_library().coli_moe_kv_read(kv, rows, args, stream), "coli_moe_kv_read")
+
+
+def coli_moe_kv_attention_workspace_bytes(kv: coli_moe_kv_t, rows: coli_moe_kv_rows_t,
+                                          args: coli_moe_kv_attention_t) -> int:
+    return int(load_library().coli_moe_kv_attention_workspace_bytes(kv, rows, args))
+
+
+def coli_moe_kv_attention(kv: coli_moe_kv_t, rows: coli_moe_kv_rows_t, args: coli_moe_kv_attention_t, workspace: int,
+                          workspace_bytes: int, stream: int = 0) -> int:
+    return _check(load_library().coli_moe_kv_attention(kv, rows, args, workspace, workspace_bytes, stream),
+                  "coli_moe_kv_attention")
+
+
+def coli_moe_kv_evict(kv: coli_moe_kv_t, rows: coli_moe_kv_rows_t, args: coli_moe_kv_evict_t, stream: int = 0) -> int:
+    return _check(load_library().coli_moe_kv_evict(kv, rows, args, stream), "coli_moe_kv_evict")
 
 
 def coli_moe_last_logits(handle, logits: int, stream: int = 0) -> int:
@@ -746,6 +825,291 @@ def balance_grad(logits, coef, dloss=None, scores: str = "sigmoid", offsets=None
     if given:
         torch._C._increment_version((out,))
     return out
+
+
+# ---------------------------------------------------------------------------
+# The attention side of a block: rotary positions and the 4-bit cache.
+# ---------------------------------------------------------------------------
+
+def _heads(t, what: str, device, heads=None, dim=None, dtype=None, tokens=None):
+    """Checks a [tokens, heads, dim] device tensor whose heads are contiguous;
+    its token and head strides."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
+        raise ValueError(f"{what}: expected a [tokens, heads, dim] tensor with contiguous heads, got shape "
+                         f"{tuple(shape)}, strides {tuple(strides)}")
+    if (tokens is not None and shape[0] != tokens) or (heads is not None and shape[1] != heads) or \
+            (dim is not None and shape[2] != dim):
+        raise ValueError(f"{what}: expected shape {(tokens, heads, dim)}, got {tuple(shape)}")
+    if (shape[0] | shape[1] | shape[2]) >> 31:
+        raise ValueError(f"{what}: at most 2^31 - 1 tokens, heads and columns, got shape {tuple(shape)}")
+    if t.device != device or (dtype is not None and t.dtype != dtype):
+        _refuse_place(t, what, device, dtype)
+    return strides[0], strides[1]
+
+
+def rotary_frequencies(part: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(frequencies float32 [part / 2], scale) of rotary positions:
+    base^(-2 i / part), for contexts `factor` times as long as the `original`
+    one scaled by
+
+    none    not at all;
+    linear  every frequency / factor;
+    base    base * factor^(part / (part - 2)), which leaves the fastest pair as it is and divides the slowest by
+            factor;
+    parts   pairs that turn more than beta_fast times in the original context as they are, those that turn less than
+            beta_slow times / factor, a linear blend by pair index between; scale 0.1 ln(factor) + 1.
+
+    The scale (1 but for parts) is rotary's."""
+    import math
+    import torch
+    if part < 2 or part % 2:
+        raise ValueError(f"part: a positive even number, got {part}")
+    if not base > 1 or not factor >= 1 or not original >= 1:
+        raise ValueError(f"base > 1, factor >= 1 and original >= 1, got {base}, {factor} and {original}")
+    i = torch.arange(part // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "base":
+        if part < 4:
+            raise ValueError("part: at least 4 for scaling 'base'")
+        base = base * factor ** (part / (part - 2))
+    freq = base ** (-2 * i / part)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "parts":
+        if not beta_fast > beta_slow > 0:
+            raise ValueError(f"beta_fast > beta_slow > 0, got {beta_fast} and {beta_slow}")
+        pair = lambda turns: part * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), part // 2 - 1)
+        slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - slow) + freq / factor * slow
+        scale = 0.1 * math.log(factor) + 1
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"scaling: none, linear, base or parts, got {scaling!r}")
+    return freq.to(torch.float32).to(device), scale
+
+
+def rotary(x, positions, freq, interleaved: bool = False, scale: float = 1.0, inverse: bool = False, out=None):
+    """Rotary positions on x [tokens, heads, dim] (float32, bf16 or f16; heads
+    contiguous, other strides any, so a view of a fused projection's query and
+    key heads is one call): pair i of each head, elements (i, i + n) or
+    (2 i, 2 i + 1) if interleaved for the n frequencies `freq` (float32, n <=
+    dim / 2), is turned by positions[t] * freq[i] and multiplied by scale;
+    elements behind the pairs are copied.  positions: int32 or int64 [tokens].
+    inverse turns the other way: with the same scale it takes the gradient of
+    the result to that of x.  out may be x.  No gradient goes through it by
+    itself.  coli_moe_rotary in include/coli_moe.h gives the formulas."""
+    import torch
+    given = out is not None
+    dev = _gpu(x, "x")
+    xt, xh = _heads(x, "x", dev)
+    tokens, heads, dim = x.shape
+    code = _dtype_code(x.dtype, "x")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"positions: expected int32 or int64, got {positions.dtype}")
+    _vector(positions, "positions", dev, tokens)
+    n = freq.shape[0] if freq.dim() == 1 else -1
+    _vector(freq, "freq", dev, n, torch.float32)
+    if 2 * n > dim:
+        raise ValueError(f"freq: at most {dim // 2} frequencies for heads of {dim}, got {n}")
+    if out is None:
+        out, ot, oh = x.new_empty((tokens, heads, dim)), heads * dim, dim
+    else:
+        ot, oh = _heads(out, "out", dev, heads, dim, x.dtype, tokens)
+    if tokens and heads and dim:
+        _enqueue("coli_moe_rotary", dev,
+                 coli_moe_rotary_t(tokens, heads, dim, 2 * n, code, bool(interleaved), bool(inverse),
+                                   positions.dtype == torch.int64, scale, x.data_ptr(), xt, xh, positions.data_ptr(),
+                                   freq.data_ptr(), out.data_ptr(), ot, oh))
+        if given:
+            torch._C._increment_version((out,))
+    return out
+
+
+class KVCache:
+    """A paged key/value cache held in 4 bits (coli_moe_kv_t in
+    include/coli_moe.h has the layout): uint8 codes [pages, kv heads, page
+    size, head dim / 2] and bfloat16 scales [pages, kv heads, head dim / 64,
+    page size] of keys and values, and float32 weights [pages, kv heads, page
+    size] where accumulated attention weights are kept.  The tensors are the
+    caller's (KVCache.empty makes them); which page belongs to whom too.
+
+    All calls take the pages of each sequence, table int32 [S, width]; its
+    rows including the call's new ones, lengths int32 [S]; and, unless every
+    sequence has exactly one new token, offsets int32 [S + 1]: tokens
+    offsets[s] .. offsets[s + 1] - 1 are the last rows of sequence s.  Work is
+    enqueued on the current stream of the cache's device."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, weights=None):
+        import torch
+        dev = _gpu(k_codes, "k_codes")
+        if k_codes.dim() != 4:
+            raise ValueError(f"k_codes: expected 4 dimensions, got shape {tuple(k_codes.shape)}")
+        pages, heads, page_size, half = k_codes.shape
+        codes, scales = (pages, heads, page_size, half), (pages, heads, half // 32, page_size)
+        for what, t, shape, dtype in (("k_codes", k_codes, codes, torch.uint8), ("v_codes", v_codes, codes, torch.uint8),
+                                      ("k_scales", k_scales, scales, torch.bfloat16),
+                                      ("v_scales", v_scales, scales, torch.bfloat16),
+                                      ("weights", weights, (pages, heads, page_size), torch.float32)):
+            if t is None and what == "weights":
+                continue
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{what}: expected a contiguous tensor of shape {shape}, got shape {tuple(t.shape)}, "
+                                 f"strides {tuple(t.stride())}")
+            if t.device != dev or t.dtype != dtype:
+                _refuse_place(t, what, dev, dtype)
+        if half not in (32, 64, 128) or page_size not in (16, 32, 64, 128, 256) or not 1 <= heads <= 1024 or \
+                not 1 <= pages < 1 << 31:
+            raise ValueError(f"a cache has heads of 64, 128 or 256 columns, pages of 16, 32, 64, 128 or 256 rows and 1 "
+                             f"to 1024 key heads; got codes of shape {codes}")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.weights, self.device = weights, dev
+        self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, 2 * half
+        self._kv = coli_moe_kv_t(pages, page_size, heads, 2 * half, k_codes.data_ptr(), k_scales.data_ptr(),
+                                 v_codes.data_ptr(), v_scales.data_ptr(),
+                                 None if weights is None else weights.data_ptr())
+        self._written = tuple(t for t in (k_codes, k_scales, v_codes, v_scales, weights) if t is not None)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, page_size: int = 64, weights: bool = False, device=None):
+        """A cache of its own tensors on the device (default: the current
+        GPU), rows of zeros."""
+        import torch
+        if dim not in (64, 128, 256):
+            raise ValueError(f"dim: 64, 128 or 256, got {dim}")
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        codes = [torch.zeros((pages, heads, page_size, dim // 2), dtype=torch.uint8, device=device) for _ in "kv"]
+        scales = [torch.zeros((pages, heads, dim // 64, page_size), dtype=torch.bfloat16, device=device) for _ in "kv"]
+        w = torch.zeros((pages, heads, page_size), device=device) if weights else None
+        return cls(codes[0], scales[0], codes[1], scales[1], w)
+
+    def _rows(self, tokens: int, table, lengths, offsets):
+        import torch
+        dev = self.device
+        stride = _matrix(table, "table", dev, dtype=torch.int32)
+        S, width = table.shape
+        _vector(lengths, "lengths", dev, S, torch.int32)
+        op = None
+        if offsets is not None:
+            _vector(offsets, "offsets", dev, S + 1, torch.int32)
+            op = offsets.data_ptr()
+        elif tokens != S:
+            raise ValueError(f"{tokens} tokens for {S} sequences: without offsets each sequence has one")
+        return coli_moe_kv_rows_t(tokens, S, width, table.data_ptr(), stride, lengths.data_ptr(), op)
+
+    def append(self, k, v, table, lengths, offsets=None) -> None:
+        """Keys and values [tokens, kv heads, dim] (float32, bf16 or f16, heads
+        contiguous) become the tokens' rows, 4 bits each with a scale per 64
+        columns; kept weights of the rows become 0.  Rows whose page is not
+        there are dropped."""
+        import torch
+        kt, kh = _heads(k, "k", self.device, self.heads, self.dim)
+        vt, vh = _heads(v, "v", self.device, self.heads, self.dim, k.dtype, k.shape[0])
+        code = _dtype_code(k.dtype, "k")
+        rows = self._rows(k.shape[0], table, lengths, offsets)
+        if rows.tokens and rows.seqs:
+            _enqueue("coli_moe_kv_append", self.device, self._kv, rows,
+                     coli_moe_kv_values_t(code, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh))
+            torch._C._increment_version(self._written)
+
+    def read(self, tokens: int, table, lengths, offsets=None, dtype=None):
+        """(keys, values) [tokens, kv heads, dim] of the tokens' rows in the
+        type (default bf16; float32 holds them exactly).  Rows that are not
+        there, and tokens in no sequence, are 0."""
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        code = _dtype_code(dtype, "dtype")
+        rows = self._rows(tokens, table, lengths, offsets)
+        new = self.k_codes.new_empty if offsets is None else self.k_codes.new_zeros
+        shape = (tokens, self.heads, self.dim)
+        k, v = new(shape, dtype=dtype), new(shape, dtype=dtype)
+        if tokens and rows.seqs:
+            t, h = self.heads * self.dim, self.dim
+            _enqueue("coli_moe_kv_read", self.device, self._kv, rows,
+                     coli_moe_kv_values_t(code, k.data_ptr(), t, h, v.data_ptr(), t, h))
+        return k, v
+
+    def attention(self, q, table, lengths, offsets=None, scale: float | None = None, window: int = 0, out=None,
+                  accumulate: bool = False, weights_out=None):
+        """Attention of q [tokens, q heads, dim] (bf16 or f16, heads contiguous)
+        over the rows of its sequence up to its own (the last `window` of them
+        if window > 0); q heads a multiple of the key heads, neighbours sharing
+        one.  scale: default 1 / sqrt(dim).  accumulate adds each row's softmax
+        weights, over the tokens and the heads that share its key head, to the
+        cache's weights, or, with weights_out (a tensor like them), stores the
+        sums there.  A token that sees no row gives zeros; tokens in no
+        sequence are left as they were in `out` (a fresh result holds zeros).
+        Forward only: no gradient goes through it.  coli_moe_kv_attention in
+        include/coli_moe.h gives the formulas."""
+        import torch
+        dev = self.device
+        qt, qh = _heads(q, "q", dev, None, self.dim)
+        tokens, heads, dim = q.shape
+        code = _dtype_code(q.dtype, "q")
+        if code == COLI_MOE_F32:
+            raise ValueError("q: unsupported type torch.float32 (bf16 or f16)")
+        if heads < 1 or heads % self.heads:
+            raise ValueError(f"q: a multiple of {self.heads} heads, got {heads}")
+        given = out is not None
+        if out is None:
+            out, ot, oh = q.new_empty((tokens, heads, dim)), heads * dim, dim
+        else:
+            ot, oh = _heads(out, "out", dev, heads, dim, q.dtype, tokens)
+        wp = None
+        if accumulate or weights_out is not None:
+            if self.weights is None:
+                raise ValueError("the cache keeps no weights")
+            w = self.weights if weights_out is None else weights_out
+            if w.shape != self.weights.shape or not w.is_contiguous():
+                raise ValueError(f"weights_out: expected a contiguous tensor of shape {tuple(self.weights.shape)}, got "
+                                 f"shape {tuple(w.shape)}, strides {tuple(w.stride())}")
+            if w.device != dev or w.dtype != torch.float32:
+                _refuse_place(w, "weights_out", dev, torch.float32)
+            wp = w.data_ptr()
+        if not 0 <= window < 1 << 31:
+            raise ValueError(f"window: 0 <= window < 2^31, got {window}")
+        rows = self._rows(tokens, table, lengths, offsets)
+        a = coli_moe_kv_attention_t(heads, code, window, not given, dim ** -0.5 if scale is None else scale,
+                                    q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, wp)
+        if tokens and rows.seqs:
+            lib = _lib or load_library()
+            nbytes = lib.coli_moe_kv_attention_workspace_bytes(self._kv, rows, a)
+            ws = q.new_empty((nbytes,), dtype=torch.uint8)
+            _enqueue("coli_moe_kv_attention", dev, self._kv, rows, a, ws.data_ptr(), nbytes)
+            written = ((out,) if given else ()) + ((w,) if wp is not None else ())
+            if written:
+                torch._C._increment_version(written)
+        return out
+
+    def evict(self, keep: int, table, lengths, into, first: int = 4, recent: int = 0):
+        """Of every sequence and key head with more than `keep` rows keeps the
+        first `first`, the last `recent` and the heaviest between them (the
+        cache's weights; ties: the lower row), `keep` in all, and copies them
+        in their order, with their weights, to rows 0 .. of the pages `into`
+        int32 [S, width] (none of them in the table).  Returns (kept int32 [S,
+        kv heads, keep], the row each came from or -1; new lengths int32
+        [S])."""
+        import torch
+        dev = self.device
+        if self.weights is None:
+            raise ValueError("the cache keeps no weights")
+        S = table.shape[0] if table.dim() == 2 else 0
+        rows = self._rows(S, table, lengths, None)
+        stride = _matrix(into, "into", dev, S, None, torch.int32)
+        width = into.shape[1]
+        if not 1 <= keep <= width * self.page_size:
+            raise ValueError(f"keep: 1 to the {width * self.page_size} rows of `into`, got {keep}")
+        if first < 0 or recent < 0 or first + recent > keep:
+            raise ValueError(f"first and recent: at least 0 and {keep} together at most, got {first} and {recent}")
+        kept = table.new_empty((S, self.heads, keep))
+        new = table.new_empty((S,))
+        if S:
+            _enqueue("coli_moe_kv_evict", dev, self._kv, rows,
+                     coli_moe_kv_evict_t(keep, first, recent, width, into.data_ptr(), stride, kept.data_ptr(),
+                                         new.data_ptr()))
+            torch._C._increment_version(self._written)
+        return kept, new
 
 
 # ---------------------------------------------------------------------------

@@ -4,6 +4,7 @@
 #include "coli_moe.h"
 #include "element_types.h"
 #include "internal.h"
+#include "kv_cache.h"
 
 namespace {
 
@@ -142,6 +143,149 @@ int coli_moe_balance_grad(const coli_moe_balance_t *a, const float *coef, const 
                  hipSuccess
              ? COLI_MOE_OK
              : COLI_MOE_EDEVICE;
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+
+// A [tokens][heads] array of heads of `dim` elements: pointer and strides
+// usable.  Heads that are written must not overlap.
+bool heads_ok(const void *p, int type, int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim,
+              bool written) {
+  if (!aligned_to(p, coli::type_bytes(type))) return false;
+  if ((tokens > 1 && (token < 0 || token > kMaxStride)) || (heads > 1 && (head < 0 || head > kMaxStride))) return false;
+  if (!written) return true;
+  if ((heads > 1 && head < dim) || (tokens > 1 && token < dim)) return false;
+  // one stride steps over the whole of the other
+  return tokens <= 1 || heads <= 1 || token >= (heads - 1) * head + dim || head >= (tokens - 1) * token + dim;
+}
+
+int kv_check(const coli_moe_kv_t *kv) {
+  if (!kv || kv->n_pages < 1 || kv->kv_heads < 1 || kv->kv_heads > 1024) return COLI_MOE_EARG;
+  if (kv->page_size < 16 || kv->page_size > 256 || (kv->page_size & (kv->page_size - 1))) return COLI_MOE_EARG;
+  return kv->head_dim == 64 || kv->head_dim == 128 || kv->head_dim == 256 ? COLI_MOE_OK : COLI_MOE_EARG;
+}
+
+bool kv_pointers_ok(const coli_moe_kv_t *kv) {
+  return aligned_to(kv->k_codes, 16) && aligned_to(kv->k_scales, 16) && aligned_to(kv->v_codes, 16) &&
+         aligned_to(kv->v_scales, 16) && (!kv->weights || aligned_to(kv->weights, 16));
+}
+
+constexpr int32_t kMaxKvTokens = 1 << 22;
+
+int kv_rows_check(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *r) {
+  if (!r || r->seqs < 1 || r->seqs > kMaxSeqs || r->table_width < 1) return COLI_MOE_EARG;
+  return (int64_t)r->table_width * kv->page_size <= (int64_t)1 << 30 ? COLI_MOE_OK : COLI_MOE_EARG;
+}
+
+int kv_tokens_check(const coli_moe_kv_rows_t *r) {
+  if (r->tokens < 0 || r->tokens > kMaxKvTokens) return COLI_MOE_EARG;
+  return r->offsets || r->tokens == r->seqs ? COLI_MOE_OK : COLI_MOE_EARG;
+}
+
+bool kv_row_pointers_ok(const coli_moe_kv_rows_t *r) {
+  return aligned_to(r->table, 4) && aligned_to(r->lengths, 4) && (!r->offsets || aligned_to(r->offsets, 4)) &&
+         (r->seqs == 1 || (r->table_stride >= 0 && r->table_stride <= kMaxStride));
+}
+
+// Arguments of append and (written) of read.
+int kv_values_check(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *r, const coli_moe_kv_values_t *a, bool written) {
+  int code = kv_check(kv);
+  if (code == COLI_MOE_OK) code = kv_rows_check(kv, r);
+  if (code == COLI_MOE_OK) code = kv_tokens_check(r);
+  if (code != COLI_MOE_OK) return code;
+  if (!a || !coli::float_type(a->type) || !kv_pointers_ok(kv) || !kv_row_pointers_ok(r)) return COLI_MOE_EARG;
+  if (r->tokens == 0) return COLI_MOE_OK;
+  if (!heads_ok(a->k, a->type, r->tokens, a->k_token, kv->kv_heads, a->k_head, kv->head_dim, written) ||
+      !heads_ok(a->v, a->type, r->tokens, a->v_token, kv->kv_heads, a->v_head, kv->head_dim, written))
+    return COLI_MOE_EARG;
+  return written && a->k == a->v ? COLI_MOE_EARG : COLI_MOE_OK;
+}
+
+bool finite(float v) { return v >= -0x1.fffffep+127f && v <= 0x1.fffffep+127f; }
+
+int kv_attention_check(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *r, const coli_moe_kv_attention_t *a) {
+  int code = kv_check(kv);
+  if (code == COLI_MOE_OK) code = kv_rows_check(kv, r);
+  if (code == COLI_MOE_OK) code = kv_tokens_check(r);
+  if (code != COLI_MOE_OK) return code;
+  if (!a || (a->type != COLI_MOE_BF16 && a->type != COLI_MOE_F16)) return COLI_MOE_EARG;
+  if (a->q_heads < kv->kv_heads || a->q_heads % kv->kv_heads || a->q_heads / kv->kv_heads > 256) return COLI_MOE_EARG;
+  return a->window >= 0 && (a->clear & ~1) == 0 && finite(a->scale) ? COLI_MOE_OK : COLI_MOE_EARG;
+}
+
+int launched(hipError_t e) { return e == hipSuccess ? COLI_MOE_OK : COLI_MOE_EDEVICE; }
+
+}  // namespace
+
+extern "C" {
+
+int coli_moe_rotary(const coli_moe_rotary_t *a, void *stream) {
+  using namespace coli;
+  if (!a || a->tokens < 0 || a->tokens > kMaxTokens || a->heads < 1 || a->heads > 4096 || a->dim < 1 || a->dim > 4096)
+    return COLI_MOE_EARG;
+  if (a->part < 0 || a->part > a->dim || a->part % 2 || !float_type(a->type) || !finite(a->scale)) return COLI_MOE_EARG;
+  if ((a->interleaved | a->inverse | a->wide) & ~1) return COLI_MOE_EARG;
+  if (a->tokens == 0) return COLI_MOE_OK;
+  if (!heads_ok(a->x, a->type, a->tokens, a->x_token, a->heads, a->x_head, a->dim, false) ||
+      !heads_ok(a->out, a->type, a->tokens, a->out_token, a->heads, a->out_head, a->dim, true))
+    return COLI_MOE_EARG;
+  if (!aligned_to(a->positions, a->wide ? 8 : 4) || (a->part > 0 && !aligned_to(a->freq, 4))) return COLI_MOE_EARG;
+  if (a->out == a->x && ((a->tokens > 1 && a->out_token != a->x_token) || (a->heads > 1 && a->out_head != a->x_head)))
+    return COLI_MOE_EARG;
+  return launched(launch_rotary(*a, static_cast<hipStream_t>(stream)));
+}
+
+int coli_moe_kv_append(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, const coli_moe_kv_values_t *a,
+                       void *stream) {
+  const int code = kv_values_check(kv, rows, a, false);
+  if (code != COLI_MOE_OK || rows->tokens == 0) return code;
+  return launched(coli::launch_kv_append(*kv, *rows, *a, static_cast<hipStream_t>(stream)));
+}
+
+int coli_moe_kv_read(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, const coli_moe_kv_values_t *a,
+                     void *stream) {
+  const int code = kv_values_check(kv, rows, a, true);
+  if (code != COLI_MOE_OK || rows->tokens == 0) return code;
+  return launched(coli::launch_kv_read(*kv, *rows, *a, static_cast<hipStream_t>(stream)));
+}
+
+size_t coli_moe_kv_attention_workspace_bytes(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows,
+                                             const coli_moe_kv_attention_t *a) {
+  return kv_attention_check(kv, rows, a) == COLI_MOE_OK ? coli::kv_attention_workspace_bytes(*kv, *rows, *a) : 0;
+}
+
+int coli_moe_kv_attention(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, const coli_moe_kv_attention_t *a,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  const int code = kv_attention_check(kv, rows, a);
+  if (code != COLI_MOE_OK) return code;
+  if (!kv_pointers_ok(kv) || !kv_row_pointers_ok(rows)) return COLI_MOE_EARG;
+  if (a->weights_out && (!kv->weights || !aligned_to(a->weights_out, 16))) return COLI_MOE_EARG;
+  if (rows->tokens == 0) return COLI_MOE_OK;
+  if (!heads_ok(a->q, a->type, rows->tokens, a->q_token, a->q_heads, a->q_head, kv->head_dim, false) ||
+      !heads_ok(a->out, a->type, rows->tokens, a->out_token, a->q_heads, a->out_head, kv->head_dim, true) ||
+      a->out == a->q || !aligned_to(workspace, 16))
+    return COLI_MOE_EARG;
+  if (workspace_bytes < coli::kv_attention_workspace_bytes(*kv, *rows, *a)) return COLI_MOE_ECAPACITY;
+  return launched(coli::launch_kv_attention(*kv, *rows, *a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int coli_moe_kv_evict(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, const coli_moe_kv_evict_t *a,
+                      void *stream) {
+  int code = kv_check(kv);
+  if (code == COLI_MOE_OK) code = kv_rows_check(kv, rows);
+  if (code != COLI_MOE_OK) return code;
+  if (!a || a->into_width < 1 || (int64_t)a->into_width * kv->page_size > (int64_t)1 << 30) return COLI_MOE_EARG;
+  if (a->keep < 1 || a->keep > a->into_width * kv->page_size) return COLI_MOE_EARG;
+  if (a->first < 0 || a->recent < 0 || a->first > a->keep || a->recent > a->keep - a->first) return COLI_MOE_EARG;
+  if (!kv_pointers_ok(kv) || !kv->weights || !kv_row_pointers_ok(rows)) return COLI_MOE_EARG;
+  if (!aligned_to(a->into, 4) || !aligned_to(a->kept, 4) || !aligned_to(a->new_lengths, 4)) return COLI_MOE_EARG;
+  if (rows->seqs > 1 && (a->into_stride < 0 || a->into_stride > kMaxStride)) return COLI_MOE_EARG;
+  if (a->into == rows->table || a->new_lengths == rows->lengths) return COLI_MOE_EARG;
+  return launched(coli::launch_kv_evict(*kv, *rows, *a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
