@@ -1,0 +1,95 @@
+// What the kernels of attention over the 4-bit cache share: the call, codes
+// as halves, and where keys stand.
+#pragma once
+
+#include "element_types.h"
+#include "internal.h"
+#include "kv_cache.h"
+#include "wave.h"
+
+namespace coli {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float float2_t __attribute__((ext_vector_type(2)));
+typedef float float4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kTileThreads = 256;
+constexpr int kTileWaves = kTileThreads / 64;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Power of two that brings v (>= 0) into [2^14, 2^15), within float32's range,
+// and its inverse.
+__device__ __forceinline__ int lift_exponent(float v) { return max((int)(__float_as_uint(v) >> 23) & 255, 20); }
+__device__ __forceinline__ float lift(int ex) { return __uint_as_float((uint32_t)(268 - ex) << 23); }
+__device__ __forceinline__ float unlift(int ex) { return __uint_as_float((uint32_t)(ex - 14) << 23); }
+
+// u - 8 of the nibbles at bits 0 and 16 (4 and 20) of w.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
+  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) | 0x64006400u);
+  return __builtin_bit_cast(uint32_t, v + half2_t{(_Float16)-1032.0f, (_Float16)-1032.0f});
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
+  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x00F000F0u) | 0x64006400u);
+  const half2_t by = {(_Float16)0.0625f, (_Float16)0.0625f}, off = {(_Float16)-72.0f, (_Float16)-72.0f};
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, by, off));
+}
+
+// The 8 codes of a dword as halves, in the order (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ half8_t codes_of(uint32_t w) {
+  w ^= 0x88888888u;
+  u32x4 r;
+  r[0] = low_codes(w);
+  r[1] = high_codes(w);
+  w >>= 8;
+  r[2] = low_codes(w);
+  r[3] = high_codes(w);
+  return __builtin_bit_cast(half8_t, r);
+}
+
+struct Call {
+  KvView kv;
+  coli_moe_kv_rows_t rows;
+  coli_moe_kv_attention_t a;
+  int group;       // query heads of a key head
+  int tiles;       // tiles of a sequence's key head that the grid has
+  int tile_waves;  // of them in one workgroup (1, 2 or 4)
+  int few_rows;    // a key head's query rows up to which a sequence takes the tiles of 16 columns
+  int splits, prompt_splits;  // of the keys, by the tiles and by the prompts' kernel
+  int part_splits;  // the larger
+  float *part_o;   // [row][split][D], row = token * q_heads + head
+  float2 *part_ml; // [row][split] maximum (of scores times log2 e) and sum
+  float2 *ml;      // [row], for the weights; NULL: not wanted
+};
+
+// Where 16 keys stand (they share a page): byte offsets are 64-bit and uniform.
+struct SubPlace {
+  int64_t ph;  // page * heads + head
+  int slot;
+  bool ok;
+};
+
+__device__ __forceinline__ SubPlace sub_place(const Call &c, const int32_t *table, int h, int key) {
+  const int page = row_page(c.kv, table, c.rows.table_width, key);
+  return {(int64_t)max(page, 0) * c.kv.p.kv_heads + h, key & (c.kv.p.page_size - 1), page >= 0};
+}
+
+// Range of keys that the rows r0 .. r1 of a sequence's key head see.
+struct KeyRange {
+  int64_t lo, hi;
+};
+__device__ __forceinline__ KeyRange keys_of_rows(const Call &c, SeqSpan span, int64_t len, int r0, int r1) {
+  const int64_t p0 = len - span.n + r0 / c.group, p1 = len - span.n + r1 / c.group;
+  const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
+  KeyRange k;
+  k.hi = min(p1 + 1, cap);
+  k.lo = c.a.window ? max(p0 - c.a.window + 1, (int64_t)0) : 0;
+  return k;
+}
+
+// Rows of a workgroup of the prompts' kernel.  D = 256 has four waves of twice
+// the registers: the results of 32 rows alone fill half of 256.
+constexpr int prompt_rows(int dim) { return dim == 256 ? 128 : 256; }
+hipError_t launch_attention_prompts(const Call &c, hipStream_t s);
+
+}  // namespace coli

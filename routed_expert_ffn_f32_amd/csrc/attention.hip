@@ -19,22 +19,10 @@
 // as subnormal halves, need no addition, but the matrix core aligns its
 // products by exponents that it does not normalise: next to a large product
 // everything below 2^-17 of it was lost.)
-#include "element_types.h"
-#include "internal.h"
-#include "kv_cache.h"
-#include "wave.h"
+#include "attention.h"
 
 namespace coli {
 namespace {
-
-typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
-typedef float float2_t __attribute__((ext_vector_type(2)));
-typedef float float4_t __attribute__((ext_vector_type(4)));
-
-constexpr int kTileThreads = 256;
-constexpr int kTileWaves = kTileThreads / 64;
-constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int D>
 struct Tile {
@@ -46,35 +34,6 @@ struct Tile {
   static constexpr int kSubs = kKeys / 16;
   static constexpr int kWords = D == 256 ? 2 : 1;    // 16 values' dwords a lane holds of a key
 };
-
-// Power of two that brings v (>= 0) into [2^14, 2^15), within float32's range,
-// and its inverse.
-__device__ __forceinline__ int lift_exponent(float v) { return max((int)(__float_as_uint(v) >> 23) & 255, 20); }
-__device__ __forceinline__ float lift(int ex) { return __uint_as_float((uint32_t)(268 - ex) << 23); }
-__device__ __forceinline__ float unlift(int ex) { return __uint_as_float((uint32_t)(ex - 14) << 23); }
-
-// u - 8 of the nibbles at bits 0 and 16 (4 and 20) of w.
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
-  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) | 0x64006400u);
-  return __builtin_bit_cast(uint32_t, v + half2_t{(_Float16)-1032.0f, (_Float16)-1032.0f});
-}
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
-  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x00F000F0u) | 0x64006400u);
-  const half2_t by = {(_Float16)0.0625f, (_Float16)0.0625f}, off = {(_Float16)-72.0f, (_Float16)-72.0f};
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, by, off));
-}
-
-// The 8 codes of a dword as halves, in the order (0, 4), (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ half8_t codes_of(uint32_t w) {
-  w ^= 0x88888888u;
-  u32x4 r;
-  r[0] = low_codes(w);
-  r[1] = high_codes(w);
-  w >>= 8;
-  r[2] = low_codes(w);
-  r[3] = high_codes(w);
-  return __builtin_bit_cast(half8_t, r);
-}
 
 __device__ __forceinline__ float max_over_j(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));
@@ -91,19 +50,6 @@ __device__ __forceinline__ float sum_groups(float v) {
   if constexpr (D >= 256) v += dpp_f<kDppRowRor4>(v);
   return v;
 }
-
-struct Call {
-  KvView kv;
-  coli_moe_kv_rows_t rows;
-  coli_moe_kv_attention_t a;
-  int group;       // query heads of a key head
-  int tiles;       // tiles of a sequence's key head that the grid has
-  int tile_waves;  // of them in one workgroup (1, 2 or 4)
-  int splits;      // of the keys
-  float *part_o;   // [row][split][D], row = token * q_heads + head
-  float2 *part_ml; // [row][split] maximum (of scores times log2 e) and sum
-  float2 *ml;      // [row], for the weights; NULL: not wanted
-};
 
 // The column of this lane: its group, and the query row it stands for.
 struct Column {
@@ -182,18 +128,6 @@ __device__ __forceinline__ float4_t scales4(uint2 v) {
                   __uint_as_float(v.y & 0xFFFF0000u)};
 }
 
-// Where 16 keys stand (they share a page): byte offsets are 64-bit and uniform.
-struct SubPlace {
-  int64_t ph;  // page * heads + head
-  int slot;
-  bool ok;
-};
-
-__device__ __forceinline__ SubPlace sub_place(const Call &c, const int32_t *table, int h, int key) {
-  const int page = row_page(c.kv, table, c.rows.table_width, key);
-  return {(int64_t)max(page, 0) * c.kv.p.kv_heads + h, key & (c.kv.p.page_size - 1), page >= 0};
-}
-
 // Keys of one step as they stand in memory.
 template <int D>
 struct KeyRegs {
@@ -232,19 +166,6 @@ __device__ __forceinline__ float4_t scores16(const KeyRegs<D> &r, int t, const Q
   return acc;
 }
 
-// Range of keys that the rows r0 .. r1 of a sequence's key head see.
-struct KeyRange {
-  int64_t lo, hi;
-};
-__device__ __forceinline__ KeyRange keys_of_rows(const Call &c, SeqSpan span, int64_t len, int r0, int r1) {
-  const int64_t p0 = len - span.n + r0 / c.group, p1 = len - span.n + r1 / c.group;
-  const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
-  KeyRange k;
-  k.hi = min(p1 + 1, cap);
-  k.lo = c.a.window ? max(p0 - c.a.window + 1, (int64_t)0) : 0;
-  return k;
-}
-
 // Zeros in the out rows of tokens that no sequence has.
 __device__ __forceinline__ void clear_outside(const Call &c, int D) {
   if (!c.a.clear || !c.rows.offsets) return;
@@ -277,7 +198,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attention_kernel(Call c, i
     const int split = (int)(rest % c.splits), h = (int)(rest / c.splits % H), s = (int)(rest / c.splits / H);
     const SeqSpan span = seq_span(c.rows, s);
     const int rows = span.n * c.group, r0 = tg * c.tile_waves * T::kRows;
-    if (r0 >= rows) continue;
+    if (r0 >= rows || rows > c.few_rows) continue;
     const int64_t len = c.rows.lengths[s];
     const int32_t *table = c.rows.table + s * c.rows.table_stride;
     const int tile = tg * c.tile_waves + wave % c.tile_waves;
@@ -447,8 +368,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attention_kernel(Call c, i
       const int token = span.first + row / c.group, head = h * c.group + row % c.group;
       const int64_t id = (int64_t)token * c.a.q_heads + head;
       if (c.splits > 1) {
-        c.part_o[(id * c.splits + split) * D + d] = o;
-        if (d == 0) c.part_ml[id * c.splits + split] = make_float2(mm, ll);
+        c.part_o[(id * c.part_splits + split) * D + d] = o;
+        if (d == 0) c.part_ml[id * c.part_splits + split] = make_float2(mm, ll);
       } else {
         store1(c.a.out, c.a.type, token * c.a.out_token + head * c.a.out_head + d, ll != 0.0f ? o / ll : 0.0f);
         if (d == 0 && c.ml) c.ml[id] = make_float2(mm, ll);
@@ -463,24 +384,22 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c)
   constexpr int kCols = D / 64;
   const int lane = threadIdx.x & 63;
   const int64_t waves = (int64_t)gridDim.x * kTileWaves, n = (int64_t)c.rows.tokens * c.a.q_heads;
-  int first = 0, last = c.rows.tokens;
-  if (c.rows.offsets) {
-    first = c.rows.offsets[0];
-    last = c.rows.offsets[c.rows.seqs];
-  }
   for (int64_t id = (int64_t)blockIdx.x * kTileWaves + uniform(threadIdx.x >> 6); id < n; id += waves) {
     const int token = (int)(id / c.a.q_heads), head = (int)(id % c.a.q_heads);
-    if (token < first || token >= last) continue;
-    const float2 *ml = c.part_ml + id * c.splits;
+    const int s = find_seq(c.rows, token);
+    if (s < 0) continue;
+    const int splits = seq_span(c.rows, s).n * c.group <= c.few_rows ? c.splits : c.prompt_splits;
+    if (splits == 1) continue;
+    const float2 *ml = c.part_ml + id * c.part_splits;
     float m = -INFINITY;
-    for (int k = 0; k < c.splits; ++k) m = fmaxf(m, ml[k].x);
+    for (int k = 0; k < splits; ++k) m = fmaxf(m, ml[k].x);
     const float base = m == -INFINITY ? 0.0f : m;
     float l = 0.0f, o[kCols] = {};
-    for (int k = 0; k < c.splits; ++k) {
+    for (int k = 0; k < splits; ++k) {
       const float fade = __builtin_amdgcn_exp2f(ml[k].x - base);
       l += ml[k].y * fade;
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) o[i] += c.part_o[(id * c.splits + k) * D + lane * kCols + i] * fade;
+      for (int i = 0; i < kCols; ++i) o[i] += c.part_o[(id * c.part_splits + k) * D + lane * kCols + i] * fade;
     }
     const int64_t at = token * c.a.out_token + head * c.a.out_head + lane * kCols;
 #pragma unroll
@@ -564,43 +483,50 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
   }
 }
 
-// How the keys are split, and where the workspace's parts are.
+// How the work is split, and where the workspace's parts are.
 struct Plan {
-  int rows_most;  // most query rows of a sequence's key head
-  int tiles, tile_waves, splits;
+  int tiles, tile_waves, few_rows, splits, prompt_splits;
+  bool prompts;
   size_t part_o, part_ml, ml, bytes;
 };
 
-constexpr int64_t kFill = 1024;             // workgroups that fill the chip (four a CU)
+constexpr int64_t kFill = 1024;             // workgroups of tiles that fill the chip (four a CU)
 constexpr int64_t kMaxParts = 1ll << 26;    // floats of partial results
+constexpr int kFewRows = 64;
 
 Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_moe_kv_attention_t &a) {
   Plan p;
   const int64_t group = a.q_heads / kv.kv_heads;
-  const int64_t most = r.offsets ? r.tokens : 1;
-  const int64_t rows = most * group;
   const int tile_rows = 16 / (kv.head_dim / kKvGroup);
-  p.rows_most = (int)rows;
-  const int tiles = (int)((rows + tile_rows - 1) / tile_rows);
+  const int64_t most = (r.offsets ? r.tokens : 1) * group;  // rows that a sequence's key head can have
+  // sequences of more rows take the prompts' kernel, if there can be any
+  p.prompts = r.offsets && most > kFewRows;
+  p.few_rows = p.prompts ? kFewRows : 1 << 30;
+  const int tiles = (int)((min(most, (int64_t)p.few_rows) + tile_rows - 1) / tile_rows);
   p.tile_waves = tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
   p.tiles = (tiles + p.tile_waves - 1) / p.tile_waves * p.tile_waves;
-  // every sequence's rows, to the tile, are at most this many workgroups
-  const int64_t groups = (r.tokens * group / (tile_rows * p.tile_waves) + r.seqs) * kv.kv_heads;
   const int64_t cap = (int64_t)r.table_width * kv.page_size;
-  int64_t splits = (kFill + groups - 1) / groups;
-  splits = min(splits, (cap + 255) / 256);
   const int64_t out = (int64_t)r.tokens * a.q_heads * kv.head_dim;
-  splits = min(splits, kMaxParts / max(out, (int64_t)1));
-  p.splits = (int)max(min(splits, (int64_t)128), (int64_t)1);
-  const int64_t rows_all = (int64_t)r.tokens * a.q_heads;
+  const int64_t parts = max(min(kMaxParts / max(out, (int64_t)1), (int64_t)128), (int64_t)1);
+  // workgroups without splits: every sequence's rows, to the tile, need at most this many
+  const int64_t groups = (min(r.tokens * group, (int64_t)r.seqs * p.few_rows) / (tile_rows * p.tile_waves) + r.seqs) *
+                         kv.kv_heads;
+  p.splits = (int)max(min(min((kFill + groups - 1) / groups, (cap + 255) / 256), parts), (int64_t)1);
+  p.prompt_splits = 1;
+  if (p.prompts) {
+    const int64_t blocks = (r.tokens * group / prompt_rows(kv.head_dim) + r.seqs) * kv.kv_heads;
+    p.prompt_splits = (int)max(min(min(512 / blocks, (cap + 511) / 512), parts), (int64_t)1);
+  }
+  const int64_t rows = (int64_t)r.tokens * a.q_heads;
+  const int splits = max(p.splits, p.prompt_splits);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   size_t at = 0;
   p.part_o = at;
-  if (p.splits > 1) at += up(rows_all * p.splits * kv.head_dim * sizeof(float));
+  if (splits > 1) at += up(rows * splits * kv.head_dim * sizeof(float));
   p.part_ml = at;
-  if (p.splits > 1) at += up(rows_all * p.splits * sizeof(float2));
+  if (splits > 1) at += up(rows * splits * sizeof(float2));
   p.ml = at;
-  if (a.weights_out) at += up(rows_all * sizeof(float2));
+  if (a.weights_out) at += up(rows * sizeof(float2));
   p.bytes = at > 0 ? at : 256;
   return p;
 }
@@ -612,7 +538,8 @@ hipError_t launch_all(const Call &c, hipStream_t s) {
   const int64_t work = (int64_t)c.rows.seqs * c.kv.p.kv_heads * c.splits * (c.tiles / c.tile_waves);
   const auto kernel = c.a.type == COLI_MOE_F16 ? kv_attention_kernel<D, true> : kv_attention_kernel<D, false>;
   hipError_t e = launch(kernel, dim3(grid_of(work)), dim3(kTileThreads), 0, s, c, work);
-  if (e == hipSuccess && c.splits > 1) {
+  if (e == hipSuccess && c.few_rows < 1 << 30) e = launch_attention_prompts(c, s);
+  if (e == hipSuccess && c.part_splits > 1) {
     const int64_t blocks = ((int64_t)c.rows.tokens * c.a.q_heads + kTileWaves - 1) / kTileWaves;
     e = launch(kv_attention_join_kernel<D>, dim3(grid_of(blocks)), dim3(kTileThreads), 0, s, c);
   }
@@ -637,8 +564,8 @@ hipError_t launch_kv_attention(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t
                                void *workspace, hipStream_t s) {
   const Plan p = plan_of(kv, r, a);
   char *ws = static_cast<char *>(workspace);
-  Call c{kv_view(kv), r, a, a.q_heads / kv.kv_heads, p.tiles, p.tile_waves, p.splits,
-         reinterpret_cast<float *>(ws + p.part_o), reinterpret_cast<float2 *>(ws + p.part_ml),
+  Call c{kv_view(kv), r, a, a.q_heads / kv.kv_heads, p.tiles, p.tile_waves, p.few_rows, p.splits, p.prompt_splits,
+         max(p.splits, p.prompt_splits), reinterpret_cast<float *>(ws + p.part_o), reinterpret_cast<float2 *>(ws + p.part_ml),
          a.weights_out ? reinterpret_cast<float2 *>(ws + p.ml) : nullptr};
   switch (kv.head_dim) {
     case 64: return launch_all<64>(c, s);

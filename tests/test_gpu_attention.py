@@ -192,3 +192,93 @@ def test_accumulates_in_place(dev):
     want = pool.weights.double() + 2 * w
     assert ((cache.weights.cpu().double() - want).abs() <= 2 * wtol + 4 * kv_ref.U * want)[w > 0].all()
     assert torch.equal(cache.weights.cpu()[w == 0], pool.weights[w == 0])
+
+
+# --- many query rows: prompts ---------------------------------------------
+
+@pytest.mark.parametrize("dim,page,heads,group,dtype", [
+    (64, 16, 2, 3, F16), (64, 64, 1, 16, BF16), (128, 64, 1, 8, BF16), (128, 16, 2, 5, F16), (256, 32, 1, 4, BF16),
+    (256, 16, 1, 7, F16)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_prompts(dev, dim, page, heads, group, dtype, window):
+    """Rows on both sides of the limits of a workgroup, beside a sequence of
+    one token and an empty one, on pasts that end inside a step."""
+    new = [70, 1, 0, 33, 130]
+    lengths = [70, 55, 9, 90, 259]
+    pool = Pool(lengths, heads, dim, page, seed=21).fill()
+    q = queries(sum(new), heads * group, dim, dtype, 22)
+    out, tol, w, wtol = kv_ref.attention(pool, q, new, window=window)
+    got, wo, _ = run(dev, pool, q, new, weights=True, window=window)
+    check(got, out, tol, dtype)
+    want = pool.weights.double() + w
+    assert ((wo.double() - want).abs() <= wtol + 2 * kv_ref.U * want)[w > 0].all()
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, F16), (256, BF16)])
+@pytest.mark.parametrize("far", [2.0 ** 30, 2.0 ** 60, 2.0 ** -30, 2.0 ** -50])
+def test_uneven_values_in_prompts(dev, dim, dtype, far):
+    """Values of one step many powers of two apart: where the large rows have
+    no weight the small ones still count in full."""
+    if dtype == F16 and far > 1:
+        far = 1 / far  # results stay in the type's range
+    pool = Pool([150], 1, dim, 16, seed=23)
+    g = torch.Generator().manual_seed(24)
+    toward = torch.randn(1, dim, generator=g)
+    for r in range(150):
+        big = far > 1 and r % 5 == 3
+        k = -8 * toward if big else torch.randn(1, dim, generator=g) + toward
+        pool.write(0, r, k, torch.randn(1, dim, generator=g) * (far if r % 5 == 3 else 1.0))
+    q = (torch.randn(75, 2, dim, generator=g) + 3 * toward).to(dtype)
+    out, tol, _, _ = kv_ref.attention(pool, q, [75])
+    got, _, _ = run(dev, pool, q, [75])
+    assert float(out.abs().max()) < 1e3  # the large rows have no weight
+    check(got, out, tol, dtype)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_nan_in_prompts(dev, dim):
+    """NaN keys and NaN values of one group reach exactly the queries that see
+    them, and of the values exactly the group's columns."""
+    new = 100
+    pool = Pool([140], 1, dim, 16, seed=25).fill()
+    one = torch.ones(1, dim)
+    bad = one.clone()
+    bad[0, dim - 3] = float("nan")
+    pool.write(0, 90, one, bad)
+    bad_key = one.clone()
+    bad_key[0, 0] = float("inf")
+    pool.write(0, 120, bad_key, one)
+    q = queries(new, 2, dim, BF16, 26)
+    got, _, _ = run(dev, pool, q, [new])
+    first = 140 - new
+    assert torch.isfinite(got[: 90 - first]).all()
+    assert torch.isfinite(got[90 - first: 120 - first, :, : dim - 64]).all()
+    assert got[90 - first: 120 - first, :, dim - 64:].isnan().all()
+    assert got[120 - first:].isnan().all()
+    windowed, _, _ = run(dev, pool, q, [new], window=10)
+    assert torch.isfinite(windowed[130 - first:]).all() and windowed[120 - first: 130 - first].isnan().all()
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+@pytest.mark.parametrize("tokens", [4, 90])
+def test_scales_and_missing_pages(dev, scale, tokens):
+    pool = Pool([300], 1, 128, 16, seed=27).fill()
+    for i in (0, 4, 5, 12):
+        pool.table[0, i] = -7
+    q = queries(tokens, 2, 128, BF16, 28)
+    out, tol, _, _ = kv_ref.attention(pool, q, [tokens], scale=scale)
+    got, _, _ = run(dev, pool, q, [tokens], scale=scale)
+    check(got, out, tol, BF16)
+
+
+def test_split_prompt(dev):
+    """Few rows over a long past: the keys are split over workgroups; and the
+    tokens of no sequence around it."""
+    pool = Pool([2300], 1, 64, 64, seed=29).fill()
+    q = queries(75, 2, 64, F16, 30)
+    out, tol, _, _ = kv_ref.attention(pool, q[3:73], [70])
+    cache = pool.to(dev, cm)
+    got = cache.attention(q.to(dev), pool.table.to(dev), torch.tensor([2300], dtype=torch.int32, device=dev),
+                          (offsets_of([70]) + 3).to(dev)).cpu()
+    check(got[3:73], out, tol, F16)
+    assert (got[:3] == 0).all() and (got[73:] == 0).all()
