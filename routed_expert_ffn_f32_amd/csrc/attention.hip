@@ -515,7 +515,7 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
   p.prompt_splits = 1;
   if (p.prompts) {
     const int64_t blocks = (r.tokens * group / prompt_rows(kv.head_dim) + r.seqs) * kv.kv_heads;
-    p.prompt_splits = (int)max(min(min(512 / blocks, (cap + 511) / 512), parts), (int64_t)1);
+    p.prompt_splits = (int)max(min(min(1536 / blocks, (cap + 511) / 512), parts), (int64_t)1);
   }
   const int64_t rows = (int64_t)r.tokens * a.q_heads;
   const int splits = max(p.splits, p.prompt_splits);

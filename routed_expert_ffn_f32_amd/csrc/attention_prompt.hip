@@ -30,7 +30,10 @@ typedef float float16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kBand = 26;    // powers of two of one pass over the values
 constexpr int kBands = 3;
-constexpr int kMayCross = 0x16;  // what the scheduler may move between groups of matrix instructions: vector, scalar, global
+template <int N>
+struct Num {
+  static constexpr int value = N;
+};
 constexpr float kSlack = 8;  // the maximum may be passed by 2^8 before sums are rescaled
 
 template <int D>
@@ -50,19 +53,30 @@ struct Prompt {
   // columns of a result side by side.
   static constexpr int kKeyRow = D + 8, kValRow = kKeys + 8;
   static constexpr int kOct = D / 8;
-  // One thread's unit of a step's expansion: 4 keys' values of 8 columns (half
-  // of the waves), or one key's 32 columns (D = 64: 16).
-  static constexpr int kPieces = D == 64 ? 4 : D / 32;
-  static constexpr int kStagers = kThreads / 2;
-  static constexpr int kUnits = kKeys * kPieces / kStagers;  // of a thread
-  static constexpr int kUnitKeys = kStagers / kPieces;       // keys from one unit to the next
-  static_assert(kUnits >= 1 && kUnitKeys * kUnits == kKeys && kUnitKeys % 16 == 0, "units cover a step");
+  // Half of the waves expand values, the others keys.  A lane's unit is 8
+  // columns of 4 keys' values, or 32 columns (D = 64: 16) of one key; a wave's
+  // lanes stay within 16 keys, which share a page.
+  static constexpr int kStageWaves = kWaves / 2;
+  static constexpr int kPieces = D == 64 ? 4 : D / 32;       // of a key's row
+  static constexpr int kWaveKeys = D == 256 ? 8 : 16;        // of a wave's unit
+  static constexpr int kUnitKeys = kStageWaves * kWaveKeys;  // from one unit to the next
+  static constexpr int kUnits = kKeys / kUnitKeys;           // of a lane
+  static_assert(kUnits >= 1 && kUnitKeys * kUnits == kKeys && kWaveKeys * kPieces == 64, "units cover a step");
 };
 
 __device__ __forceinline__ int wave_max(int v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v = max(v, __shfl_xor(v, d));
-  return uniform(v);
+  v = max(v, dpp_i<kDppQuadXor1>(v));
+  v = max(v, dpp_i<kDppQuadXor2>(v));
+  v = max(v, dpp_i<kDppRowRor4>(v));
+  v = max(v, dpp_i<kDppRowRor8>(v));
+  return max(max(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+             max(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+
+// The larger of a lane's and of the lane's 32 away.
+__device__ __forceinline__ float max_over_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // Exponents of the scales of a step: largest of the keys', largest and
@@ -70,6 +84,7 @@ __device__ __forceinline__ int wave_max(int v) {
 struct StepScales {
   int k, v, v_least;
   bool bad;
+  uint64_t there;  // keys that are on a page
 };
 
 // 2^-(exponent - 11): brings the largest scale to [2^11, 2^12), its values to
@@ -92,17 +107,23 @@ __device__ __forceinline__ uint32_t times(uint32_t codes, half2_t s) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, codes) * s);
 }
 
-// A unit of the next step as it stands in memory.
+// A unit of a step as it stands in memory, and values' codes with their scales.
 struct Staged {
   u32x4 code;
   uint2 scale;
+};
+struct ValueUnit {
+  uint32_t code[4];
+  half2_t scale[2];
 };
 
 template <int D, bool kTwice>
 __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(Call c, int64_t work) {
   using T = Prompt<D>;
-  __shared__ __align__(16) _Float16 lk[2][T::kKeys * T::kKeyRow];
+  // keys of the step, of the next (whose first scores are computed beside this one's last) and of the one after
+  __shared__ __align__(16) _Float16 lk[3][T::kKeys * T::kKeyRow];
   __shared__ __align__(16) _Float16 lv[2][D * T::kValRow];
+  __shared__ uint4 told[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), hf = lane >> 5, l32 = lane & 31;
   const int H = c.kv.p.kv_heads, ps = c.kv.p.page_size, S = c.rows.seqs;
 
@@ -129,8 +150,9 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
     const int64_t len = c.rows.lengths[s];
     const int32_t *table = c.rows.table + s * c.rows.table_stride;
     const KeyRange range = keys_of_rows(c, span, len, r0, r1);
-    const int64_t begin = range.lo & ~(int64_t)(T::kKeys - 1);
-    const int steps = range.hi > range.lo ? (int)((range.hi - begin + T::kKeys - 1) / T::kKeys) : 0;
+    // keys are numbers up to 2^30
+    const int first_key = (int)min(range.lo, (int64_t)1 << 30) & ~(T::kKeys - 1), end_key = (int)max(range.hi, (int64_t)0);
+    const int steps = range.hi > range.lo ? (end_key - first_key + T::kKeys - 1) / T::kKeys : 0;
     const int per = max((steps + c.prompt_splits - 1) / c.prompt_splits, 2);
     const int s0 = min(split * per, steps), s1 = min(s0 + per, steps);
 
@@ -144,9 +166,10 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
     const int q_lo = c.a.window ? (int)min(max(pos - c.a.window + 1, (int64_t)0), (int64_t)1 << 30) : 0;
     // and the wave's rows: keys that any and that all of them see
     const int w0 = min(r0 + wave * 32, rows - 1), w1 = min(r0 + wave * 32 + 31, rows - 1);
-    const bool any = r0 + wave * 32 < rows;
-    const int64_t p0 = len - span.n + w0 / c.group, p1 = len - span.n + w1 / c.group;
-    const int64_t any_lo = c.a.window ? p0 - c.a.window + 1 : 0, all_lo = c.a.window ? p1 - c.a.window + 1 : 0;
+    auto clamped = [](int64_t v) { return (int)min(max(v, (int64_t)-1), (int64_t)1 << 30); };
+    const int64_t pos0 = len - span.n + w0 / c.group, pos1 = len - span.n + w1 / c.group;
+    const int p0 = clamped(pos0);
+    const int all_lo = c.a.window ? clamped(pos1 - c.a.window + 1) : 0;
 
     half8_t q[T::kSteps];
     float q_scale;
@@ -191,322 +214,388 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
     float m = -INFINITY, sum = 0.0f;  // the maximum that the sums stand against; the sum of 2^7 times the weights
 
     // --- staging ---
-    const bool for_values = wave < T::kWaves / 2;
-    const int st = tid & (T::kStagers - 1);
-    // values: keys 4 quad .. + 3, columns 8 oct .. + 7; keys: key, columns 32 (D = 64: 16) piece ..
-    const int oct = st % T::kOct, quad = st / T::kOct;
-    const int piece = st % T::kPieces, key = st / T::kPieces;
-    const bool stages = !for_values || quad < T::kKeys / 4;
-    const int my_key = for_values ? 4 * quad : key;  // of the step, for the first unit
-    const int scale_key = lane % T::kKeys;
+    const bool for_values = wave < T::kStageWaves;
+    // values: keys 4 quad .. + 3 (of the wave's), columns 8 oct .. + 7 (D = 64 has fewer units than lanes);
+    // keys: columns 32 (D = 64: 16) piece .. of one key
+    const int oct = lane % T::kOct, quad = lane / T::kOct, piece = lane % T::kPieces;
+    const bool stages = !for_values || 4 * quad < T::kWaveKeys;
+    const int wave_key = wave % T::kStageWaves * T::kWaveKeys;        // of the step, for the first unit
+    const int lane_key = for_values ? 4 * quad % T::kWaveKeys : lane / T::kPieces;  // from there on
 
-    auto page_of = [&](int step, int k) {  // of key k of a step, -1 where none or none is seen
-      const int64_t at = begin + (int64_t)step * T::kKeys + k;
-      return step < s1 && at < range.hi ? row_page(c.kv, table, c.rows.table_width, at) : -1;
+    // Page of key k of a step: the table's entry as it stands, so that the load
+    // need not be waited for, and later -1 where there is none or none is seen.
+    const int last_page = c.rows.table_width - 1;
+    auto page_entry = [&](int step, int k) {
+      return table[min((first_key + step * T::kKeys + k) >> c.kv.shift, last_page)];
     };
-    // scales of a step, one key a lane
-    uint32_t sk[T::kGroups], sv[T::kGroups];
-    auto load_scales = [&](int step, int page) {
-      const int slot = ((int)begin + step * T::kKeys + scale_key) & (ps - 1);
-      const int64_t at = ((int64_t)max(page, 0) * H + h) * T::kGroups * ps + slot;
+    auto page_checked = [&](int step, int k, int entry) {
+      return step < s1 && first_key + step * T::kKeys + k < end_key && (unsigned)entry < (unsigned)c.kv.p.n_pages ? entry
+                                                                                                               : -1;
+    };
+    // The scales of a step: one wave looks at them, a key a lane, two steps ahead,
+    // and tells the others through LDS.
+    const int scale_key = lane % T::kKeys;
+    struct Scales {
+      uint16_t k[T::kGroups], v[T::kGroups];
+    };
+    auto load_scales = [&](int step, int page, Scales &to) {
+      const int slot = (first_key + step * T::kKeys + scale_key) & (ps - 1);
 #pragma unroll
       for (int g = 0; g < T::kGroups; ++g) {
-        sk[g] = c.kv.p.k_scales[at + g * ps];
-        sv[g] = c.kv.p.v_scales[at + g * ps];
-      }
-      const bool there = page >= 0;
-#pragma unroll
-      for (int g = 0; g < T::kGroups; ++g) {
-        sk[g] = there ? sk[g] : 0u;
-        sv[g] = there ? sv[g] : 0u;
+        const uint64_t at = scale_index<T::kGroups>(c.kv, max(page, 0), h, g, slot);
+        to.k[g] = c.kv.p.k_scales[at];
+        to.v[g] = c.kv.p.v_scales[at];
       }
     };
-    auto step_scales = [&]() {
-      int k = 0, v = 0, least = 254, bad = 0;
+    auto tell_scales = [&](int step, int page, const Scales &from) {
+      int k = 0, v = 0, least = 254;
+      bool bad = false;
 #pragma unroll
       for (int g = 0; g < T::kGroups; ++g) {
-        const int ek = (int)(sk[g] >> 7) & 255, ev = (int)(sv[g] >> 7) & 255;
-        bad |= ek == 255 || ev == 255;
+        const int bk = page < 0 ? 0 : from.k[g], bv = page < 0 ? 0 : from.v[g];
+        const int ek = bk >> 7 & 255, ev = bv >> 7 & 255;
+        bad = bad || ek == 255 || ev == 255;
         k = max(k, ek == 255 ? 0 : ek);
         v = max(v, ev == 255 ? 0 : ev);
-        least = min(least, (sv[g] & 0x7FFF) == 0 || ev == 255 ? 254 : ev);
+        least = min(least, (bv & 0x7FFF) == 0 || ev == 255 ? 254 : ev);
       }
+      const uint64_t there = __ballot(page >= 0);
+      const int any_bad = __any(bad) ? 1 << 24 : 0;
+      k = wave_max(k);
+      v = wave_max(v);
+      least = 254 - wave_max(254 - least);
+      if (lane == 0) told[(step - s0) & 3] = make_uint4(k | v << 8 | least << 16 | any_bad, 0, (uint32_t)there, (uint32_t)(there >> 32));
+    };
+    auto hear_scales = [&](int step) {
+      const uint4 t = told[(step - s0) & 3];
+      const int packed = uniform((int)t.x);
       StepScales r;
-      // three 8-bit maxima at a time
-      const int packed = wave_max(k | bad << 8);  // bad is the larger digit: the key maximum is taken again if set
-      r.bad = packed >> 8;
-      r.k = r.bad ? wave_max(k) : packed & 255;
-      r.v = wave_max(v);
-      r.v_least = 254 - wave_max(254 - least);
+      r.k = packed & 255;
+      r.v = packed >> 8 & 255;
+      r.v_least = packed >> 16 & 255;
+      r.bad = packed >> 24;
+      r.there = (uint32_t)uniform((int)t.z) | (uint64_t)(uint32_t)uniform((int)t.w) << 32;
       return r;
     };
+    // Codes and scales of a unit, by the same loads for keys and values: from a
+    // uniform address, a lane's own few bytes on.
+    const int lane_byte = lane_key * (D / 2) + (for_values ? 4 * oct : (D == 64 ? 8 : 16) * piece);
+    const int lane_scale = (for_values ? oct / 8 : piece * (D == 64 ? 16 : 32) / kKvGroup) * ps + (lane_key & ~3);
+    const uint8_t *codes = for_values ? c.kv.p.v_codes : c.kv.p.k_codes;
+    const uint16_t *scales = for_values ? c.kv.p.v_scales : c.kv.p.k_scales;
     auto load_codes = [&](int step, int page, int unit_key, Staged &g) {
-      const int slot = ((int)begin + step * T::kKeys + unit_key) & (ps - 1);
-      const int64_t ph = (int64_t)max(page, 0) * H + h;
-      if (for_values) {
-        if (!stages) return;
-        const uint8_t *base = c.kv.p.v_codes + (ph * ps + slot) * (D / 2) + 4 * oct;
+      const int slot = (first_key + step * T::kKeys + unit_key) & (ps - 1);
+      const uint8_t *base = codes + code_row(c.kv, max(page, 0), h, slot) * (D / 2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g.code[i] = *reinterpret_cast<const uint32_t *>(base + i * (D / 2));
-        g.scale = *reinterpret_cast<const uint2 *>(c.kv.p.v_scales +
-                                                   (ph * T::kGroups + 8 * oct / kKvGroup) * ps + slot);
-      } else {
-        const uint8_t *base = c.kv.p.k_codes + (ph * ps + slot) * (D / 2);
-        if constexpr (D == 64) {
-          const uint2 v = *reinterpret_cast<const uint2 *>(base + 8 * piece);
-          g.code = u32x4{v.x, v.y, 0, 0};
-        } else {
-          g.code = *reinterpret_cast<const u32x4 *>(base + 16 * piece);
-        }
-        const int group = piece * (D == 64 ? 16 : 32) / kKvGroup;
-        g.scale.x = c.kv.p.k_scales[(ph * T::kGroups + group) * ps + slot];
-      }
+      for (int i = 0; i < 4; ++i)  // D = 64: a key has two dwords
+        g.code[i] = *reinterpret_cast<const uint32_t *>(
+            base + (lane_byte + (for_values ? i * (D / 2) : (D == 64 ? i & 1 : i) * 4)));
+      // four keys from a multiple of four on
+      g.scale = *reinterpret_cast<const uint2 *>(scales + scale_index<T::kGroups>(c.kv, max(page, 0), h, 0, slot & ~3) +
+                                                 lane_scale);
     };
-    // keys of this thread's unit that take part: those before the range's end, on a page
-    auto expand_values = [&](int step, int page, int unit_key, const Staged &g, _Float16 *to, int ex, int limit) {
-      if (!stages) return;
-      const int64_t k0 = begin + (int64_t)step * T::kKeys + unit_key;
+    // Scales of a unit as halves: of its keys that are before the range's end and on
+    // a page, else 0.  Then its codes times them, in 8 pieces (values: a row of V'
+    // each; keys: 4, the even ones, a dword each).
+    auto value_unit = [&](int step, int page, int unit_key, const Staged &g, int ex, int limit) {
+      const int k0 = first_key + step * T::kKeys + unit_key + lane_key;
       const float up = scale_up(ex);
-      half2_t s[2];
+      ValueUnit r;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t two = i ? g.scale.y : g.scale.x;
-        const uint32_t a = page >= 0 && k0 + 2 * i < range.hi ? two & 0xFFFFu : 0u;
-        const uint32_t d = page >= 0 && k0 + 2 * i + 1 < range.hi ? two >> 16 : 0u;
-        s[i] = half2_t{val_scale(a, up, limit), val_scale(d, up, limit)};
+        const uint32_t a = page >= 0 && k0 + 2 * i < end_key ? two & 0xFFFFu : 0u;
+        const uint32_t d = page >= 0 && k0 + 2 * i + 1 < end_key ? two >> 16 : 0u;
+        r.scale[i] = half2_t{val_scale(a, up, limit), val_scale(d, up, limit)};
       }
-      uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = g.code[i] ^ 0x88888888u;
-      const int chunk = unit_key / 16 * 2 + (quad & 1), half = quad >> 1 & 1;
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const uint32_t sel = 0x0C040C00u + 0x00010001u * (i / 2);
-        const uint32_t t0 = __builtin_amdgcn_perm(w[1], w[0], sel), t1 = __builtin_amdgcn_perm(w[3], w[2], sel);
-        const uint2 lo = make_uint2(times(low_codes(t0), s[0]), times(low_codes(t1), s[1]));
-        const uint2 hi = make_uint2(times(high_codes(t0), s[0]), times(high_codes(t1), s[1]));
-        _Float16 *at = to + (i * T::kOct + oct) * T::kValRow + 8 * chunk + 4 * half;
-        *reinterpret_cast<uint2 *>(at) = lo;
-        *reinterpret_cast<uint2 *>(at + T::kOct * T::kValRow) = hi;
-      }
+      for (int i = 0; i < 4; ++i) r.code[i] = g.code[i] ^ 0x88888888u;
+      return r;
     };
-    auto expand_keys = [&](int step, int page, int unit_key, const Staged &g, _Float16 *to, int ex) {
-      const int64_t k0 = begin + (int64_t)step * T::kKeys + unit_key;
-      const _Float16 one = key_scale(page >= 0 && k0 < range.hi ? g.scale.x & 0xFFFFu : 0u, scale_up(ex));
-      const half2_t s = {one, one};
-#pragma unroll
-      for (int i = 0; i < (D == 64 ? 2 : 4); ++i) {
-        u32x4 v = __builtin_bit_cast(u32x4, codes_of(g.code[i]));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = times(v[e], s);
-        *reinterpret_cast<u32x4 *>(to + unit_key * T::kKeyRow + 8 * (piece * (D == 64 ? 2 : 4) + i)) = v;
-      }
+    auto expand_values = [&](const ValueUnit &r, int unit_key, _Float16 *to, int i) {
+      if (!stages) return;
+      const uint32_t sel = 0x0C040C00u + 0x00010001u * (i / 2);
+      const uint32_t t0 = __builtin_amdgcn_perm(r.code[1], r.code[0], sel);
+      const uint32_t t1 = __builtin_amdgcn_perm(r.code[3], r.code[2], sel);
+      // keys 0-3, 4-7, 8-11, 12-15 of 16 stand in the order 0-3, 8-11, 4-7, 12-15
+      const int at = (unit_key + lane_key) / 4, chunk = at / 4 * 2 + (at & 1), half = at >> 1 & 1;
+      *reinterpret_cast<uint2 *>(to + (i * T::kOct + oct) * T::kValRow + 8 * chunk + 4 * half) =
+          i & 1 ? make_uint2(times(high_codes(t0), r.scale[0]), times(high_codes(t1), r.scale[1]))
+                : make_uint2(times(low_codes(t0), r.scale[0]), times(low_codes(t1), r.scale[1]));
     };
-    // Operands are read four instructions ahead of the four that use them and no
-    // further: left alone, the compiler reads so many ahead that registers spill.
-    auto product = [&](const _Float16 *from, const half8_t (&p)[T::kKeys / 16], const half8_t (&p2)[T::kKeys / 16]) {
-      constexpr int kCount = T::kKeys / 16 * T::kParts;
-      half8_t a[2][4];
-      auto read = [&](int g) {
+    auto key_unit = [&](int step, int page, int unit_key, const Staged &g, int ex) {
+      const int k0 = first_key + step * T::kKeys + unit_key + lane_key;
+      const uint32_t two = k0 & 2 ? g.scale.y : g.scale.x, mine = k0 & 1 ? two >> 16 : two & 0xFFFFu;
+      const _Float16 one = key_scale(page >= 0 && k0 < end_key ? mine : 0u, scale_up(ex));
+      return half2_t{one, one};
+    };
+    auto expand_keys = [&](half2_t s, int unit_key, const Staged &g, _Float16 *to, int i) {
+      if (D == 64 && i > 1) return;
+      u32x4 v = __builtin_bit_cast(u32x4, codes_of(g.code[i]));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 4 * g + j, u = n / T::kParts, i = n % T::kParts;
-          if (n < kCount)
-            a[g & 1][j] = *reinterpret_cast<const half8_t *>(from + (32 * i + l32) * T::kValRow + 8 * (2 * u + hf));
-        }
+      for (int e = 0; e < 4; ++e) v[e] = times(v[e], s);
+      *reinterpret_cast<u32x4 *>(to + (unit_key + lane_key) * T::kKeyRow + 8 * (piece * (D == 64 ? 2 : 4) + i)) = v;
+    };
+    // The two products.  A matrix instruction is under way for 32 cycles after the
+    // 4 of its issue, so vector work is put between them: work(n) follows
+    // instruction n, and the scheduler is kept from moving what stands between two
+    // of them (left alone it gathers the vector work behind the last).  Operands
+    // are read kLead instructions ahead.
+    constexpr int kLead = 4;
+    auto product = [&](const _Float16 *from, int sub, const half8_t (&p)[2], const half8_t (&p2)[2], auto work) {
+      constexpr int kCount = 2 * T::kParts;
+      half8_t a[kLead];
+      auto read = [&](int n) {
+        const int u = 2 * sub + n / T::kParts, i = n % T::kParts;
+        return *reinterpret_cast<const half8_t *>(from + (32 * i + l32) * T::kValRow + 8 * (2 * u + hf));
       };
-      read(0);
 #pragma unroll
-      for (int g = 0; g < kCount / 4; ++g) {
-        read(g + 1);
-        __builtin_amdgcn_sched_barrier(kMayCross);
+      for (int n = 0; n < kLead; ++n) a[n] = read(n);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 4 * g + j, u = n / T::kParts, i = n % T::kParts;
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[g & 1][j], p[u], acc[i], 0, 0, 0);
-          if constexpr (kTwice) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[g & 1][j], p2[u], acc[i], 0, 0, 0);
-        }
-        __builtin_amdgcn_sched_barrier(kMayCross);
+      for (int n = 0; n < kCount; ++n) {
+        const int u = n / T::kParts, i = n % T::kParts;
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[n % kLead], p[u], acc[i], 0, 0, 0);
+        if constexpr (kTwice) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[n % kLead], p2[u], acc[i], 0, 0, 0);
+        if (n + kLead < kCount) a[n % kLead] = read(n + kLead);
+        work(n);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
-    auto scores = [&](const _Float16 *from, float16_t (&x)[T::kSubs]) {
-      constexpr int kCount = T::kSubs * T::kSteps;
-      half8_t a[2][4];
-      auto read = [&](int g) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 4 * g + j, i = n / T::kSubs, t = n % T::kSubs;
-          if (n < kCount)
-            a[g & 1][j] = *reinterpret_cast<const half8_t *>(from + (32 * t + l32) * T::kKeyRow + 8 * (2 * i + hf));
-        }
+    auto scores = [&](const _Float16 *from, int sub, float16_t &x, auto work) {
+      half8_t a[kLead];
+      auto read = [&](int n) {
+        return *reinterpret_cast<const half8_t *>(from + (32 * sub + l32) * T::kKeyRow + 8 * (2 * n + hf));
       };
-      read(0);
 #pragma unroll
-      for (int g = 0; g < kCount / 4; ++g) {
-        read(g + 1);
-        __builtin_amdgcn_sched_barrier(kMayCross);
+      for (int e = 0; e < 16; ++e) x[e] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 4 * g + j, i = n / T::kSubs, t = n % T::kSubs;
-          x[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[g & 1][j], q[i], x[t], 0, 0, 0);
-        }
-        __builtin_amdgcn_sched_barrier(kMayCross);
+      for (int n = 0; n < kLead; ++n) a[n] = read(n);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < T::kSteps; ++n) {
+        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[n % kLead], q[n], x, 0, 0, 0);
+        if (n + kLead < T::kSteps) a[n % kLead] = read(n + kLead);
+        work(n);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
 
-    // all units of this thread
+    // all units of this lane
     auto pages_of = [&](int step, int (&to)[T::kUnits]) {
 #pragma unroll
-      for (int u = 0; u < T::kUnits; ++u) to[u] = page_of(step, my_key + u * T::kUnitKeys);
+      for (int u = 0; u < T::kUnits; ++u) to[u] = page_entry(step, wave_key + lane_key + u * T::kUnitKeys);
+    };
+    auto check_pages = [&](int step, int (&pages)[T::kUnits]) {
+#pragma unroll
+      for (int u = 0; u < T::kUnits; ++u)
+        pages[u] = page_checked(step, wave_key + u * T::kUnitKeys, uniform(pages[u]));
     };
     auto load_units = [&](int step, const int (&pages)[T::kUnits], Staged (&to)[T::kUnits]) {
 #pragma unroll
-      for (int u = 0; u < T::kUnits; ++u) load_codes(step, pages[u], my_key + u * T::kUnitKeys, to[u]);
+      for (int u = 0; u < T::kUnits; ++u) load_codes(step, pages[u], wave_key + u * T::kUnitKeys, to[u]);
     };
-    auto expand_units = [&](int step, const int (&pages)[T::kUnits], const Staged (&from)[T::kUnits], int buf, int k_ex,
-                            int v_ex) {
+    auto expand_units = [&](int step, const int (&pages)[T::kUnits], const Staged (&from)[T::kUnits], _Float16 *values_to,
+                            _Float16 *keys_to, int k_ex, int v_ex, int limit) {
 #pragma unroll
       for (int u = 0; u < T::kUnits; ++u) {
-        const int unit_key = my_key + u * T::kUnitKeys;
-        if (for_values)
-          expand_values(step, pages[u], unit_key, from[u], lv[buf], v_ex, v_ex);
-        else
-          expand_keys(step, pages[u], unit_key, from[u], lk[buf], k_ex);
+        const int unit_key = wave_key + u * T::kUnitKeys;
+        if (for_values) {
+          const ValueUnit r = value_unit(step, pages[u], unit_key, from[u], v_ex, limit);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) expand_values(r, unit_key, values_to, i);
+        } else {
+          const half2_t scale = key_unit(step, pages[u], unit_key, from[u], k_ex);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) expand_keys(scale, unit_key, from[u], keys_to, i);
+        }
       }
     };
 
-    int unit = 12;  // exponent of the values' power of two that acc stands in
-    StepScales now;
-    uint64_t there = 0;  // keys of the step that are on a page
+    // Step t expands the values of t + 1 and the keys of t + 2.  Within it, 32 keys
+    // at a time: the scores of the next 32 beside the weights of these, then their
+    // product beside a share of the expansion.
+    const int ahead = for_values ? 1 : 2;
+    int unit = 12;      // exponent of the values' power of two that acc stands in
+    int now_unit = 12;  // and that the step's values are expanded to
+    int next_unit = 12;
+    int k_now = 0, k_next = 1, k_after = 2;  // whose keys stand where
+    StepScales now = {12, 12, 254, false, 0}, next = now, next2 = now;
     Staged g[T::kUnits];
-    int page[T::kUnits], now_page[T::kUnits], scale_page = page_of(s0, scale_key);
-    int now_unit = 12;
-    pages_of(s0, page);
+    int page[T::kUnits], page2[T::kUnits], now_page[T::kUnits], look_page = -1;
+    float16_t xa, xb;
     __syncthreads();  // of the item before, all is read
     if (s0 < s1) {
-      load_scales(s0, scale_page);
+      pages_of(s0, page);
+      check_pages(s0, page);
       load_units(s0, page, g);
-      there = __ballot(scale_page >= 0);
-      now = step_scales();
-      now_unit = scale_exponent(now.v);
-      unit = now_unit;
-      expand_units(s0, page, g, 0, scale_exponent(now.k), now_unit);
+      if (wave < 3) {
+        const int at = page_checked(s0 + wave, scale_key, page_entry(s0 + wave, scale_key));
+        Scales sc;
+        load_scales(s0 + wave, at, sc);
+        tell_scales(s0 + wave, at, sc);
+      }
+      __syncthreads();
+      now = hear_scales(s0);
+      next = hear_scales(s0 + 1);
+      unit = now_unit = scale_exponent(now.v);
+      expand_units(s0, page, g, lv[0], lk[0], scale_exponent(now.k), now_unit, now_unit);
 #pragma unroll
       for (int u = 0; u < T::kUnits; ++u) now_page[u] = page[u];
-      pages_of(s0 + 1, page);
-      scale_page = page_of(s0 + 1, scale_key);
-    }
-    __syncthreads();
-
-    for (int step = s0; step < s1; ++step) {
-      const int buf = (step - s0) & 1;
-      const bool more = step + 1 < s1;
-      int page2[T::kUnits], scale_page2 = -1;
-      if (more) {
-        load_scales(step + 1, scale_page);
-        load_units(step + 1, page, g);
-        pages_of(step + 2, page2);
-        scale_page2 = page_of(step + 2, scale_key);
+      if (!for_values) {
+        pages_of(s0 + 1, page);
+        check_pages(s0 + 1, page);
+        load_units(s0 + 1, page, g);
+        expand_units(s0 + 1, page, g, lv[1], lk[1], scale_exponent(next.k), 12, 12);
       }
-      const int key0 = (int)begin + step * T::kKeys;
-      const bool seen = any && key0 <= p1 && key0 + T::kKeys > any_lo;
-      half8_t p[T::kKeys / 16], p2[T::kKeys / 16];
-      if (seen) {
-        float16_t x[T::kSubs];
+      pages_of(s0 + ahead, page);
+      if ((s0 & (T::kWaves - 1)) == wave) look_page = page_entry(s0 + 3, scale_key);
+      __syncthreads();
+      scores(lk[0], 0, xa, [](int) {});
+    }
+    Scales look;
+    ValueUnit expanding;
+
+    auto begin_step = [&](int step) {
+      check_pages(step + ahead, page);
+      load_units(step + ahead, page, g);
+      pages_of(step + ahead + 1, page2);
+      // one wave in turn looks at the scales of step + 3, with the pages that it
+      // has asked for a step before
+      if ((step & (T::kWaves - 1)) == wave) {
+        look_page = page_checked(step + 3, scale_key, look_page);
+        load_scales(step + 3, look_page, look);
+      }
+      next2 = hear_scales(step + 2);
+      const int e1 = scale_exponent(next.v);
+      next_unit = e1 > now_unit || e1 < now_unit - kBand / 2 ? e1 : now_unit;
+    };
+    auto end_step = [&](int step) {
+      if ((step & (T::kWaves - 1)) == wave) tell_scales(step + 3, look_page, look);
+      if ((step + 1 & (T::kWaves - 1)) == wave) look_page = page_entry(step + 4, scale_key);
+      now = next;
+      next = next2;
+      now_unit = next_unit;
+      const int free_keys = k_now;
+      k_now = k_next;
+      k_next = k_after;
+      k_after = free_keys;
 #pragma unroll
-        for (int t = 0; t < T::kSubs; ++t) {
+      for (int u = 0; u < T::kUnits; ++u) {
+        now_page[u] = page[u];
+        page[u] = page2[u];
+      }
+      __syncthreads();
+    };
+    // keys 32 sub .. of a step, whose scores are x; y: those of the next 32
+    auto half_step = [&](int step, auto sub_of, float16_t &x, float16_t &y) {
+      constexpr int sub = decltype(sub_of)::value;
+      const int buf = (step - s0) & 1;
+      const int key0 = first_key + step * T::kKeys + 32 * sub;
+      const uint32_t there = (uint32_t)(now.there >> (32 * sub));
+      if (__builtin_expect(!(key0 + 31 <= p0 && key0 >= all_lo && there == ~0u), 0)) {
+        const uint32_t mine = there >> (4 * hf);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[t][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) {
+          const int at = 8 * (e / 4) + e % 4, k = key0 + at + 4 * hf;
+          x[e] = k <= q_hi && k >= q_lo && (mine >> at & 1) ? x[e] : -INFINITY;
         }
-        scores(lk[buf], x);
-        const bool whole = key0 + T::kKeys - 1 <= p0 && key0 >= all_lo && there == ~0ull;
-        if (!whole) {
-          const uint64_t mine = there >> (4 * hf);
+      }
+      const float f = q_scale * scale_unit(scale_exponent(now.k));
+      float top = x[0];
 #pragma unroll
-          for (int t = 0; t < T::kSubs; ++t)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int at = 32 * t + 8 * (e / 4) + e % 4, k = key0 + at + 4 * hf;
-              x[t][e] = k <= q_hi && k >= q_lo && (mine >> at & 1) ? x[t][e] : -INFINITY;
-            }
-        }
-        const float f = q_scale * scale_unit(scale_exponent(now.k));
-        float top = x[0][0];
-#pragma unroll
-        for (int t = 0; t < T::kSubs; ++t)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, x[t][e]);
-        top = fmaxf(top, __shfl_xor(top, 32)) * f;
-        if (__any(top > m + kSlack)) {
-          const float m1 = fmaxf(m, top);
-          const float fade = __builtin_amdgcn_exp2f(m - (m1 == -INFINITY ? 0.0f : m1));
-          m = m1;
-          sum *= fade;
-#pragma unroll
-          for (int i = 0; i < T::kParts; ++i) acc[i] *= fade;
-        }
-        const float base = (m == -INFINITY ? 0.0f : m) - 7.0f;
-#pragma unroll
-        for (int t = 0; t < T::kSubs; ++t)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][e], f, -base));
-            sum += v;
-            const _Float16 hi = (_Float16)v;
-            p[2 * t + e / 8][e % 8] = hi;
-            if constexpr (kTwice) p2[2 * t + e / 8][e % 8] = (_Float16)(v - (float)hi);
-          }
-        if (unit != now_unit) {
-#pragma unroll
-          for (int i = 0; i < T::kParts; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e], unit - now_unit);
-        }
-        product(lv[buf], p, p2);
-      } else if (unit != now_unit) {
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+      top = max_over_halves(top) * f;
+      if (__builtin_expect(__any(top > m + kSlack) || unit != now_unit, 0)) {
+        const float m1 = fmaxf(m, top);
+        const float fade = __builtin_amdgcn_exp2f(m - (m1 == -INFINITY ? 0.0f : m1));
+        m = m1;
+        sum *= fade;
 #pragma unroll
         for (int i = 0; i < T::kParts; ++i)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e], unit - now_unit);
+          for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e] * fade, unit - now_unit);
+        unit = now_unit;
       }
-      unit = now_unit;
-
-      // values far below the step's largest: passes of their own, in place of the step's values
-      if (now.v_least <= now_unit - kBand) {
-        for (int band = 1; band < kBands && now_unit >= band * kBand; ++band) {
-          const int ex = scale_exponent(now_unit - band * kBand);
+      const float base = (m == -INFINITY ? 0.0f : m) - 7.0f;
+      half8_t p[2], p2[2];
+      // weights: kEach exponentials after an instruction, and the sum and rounding of those before
+      constexpr int kEach = (16 + T::kSteps - 1) / T::kSteps;
+      float v[2][kEach];
+      auto settle = [&](int n) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const int at = n * kEach + j;
+          sum += v[n & 1][j];
+          const _Float16 hi = (_Float16)v[n & 1][j];
+          p[at / 8][at % 8] = hi;
+          if constexpr (kTwice) p2[at / 8][at % 8] = (_Float16)(v[n & 1][j] - (float)hi);
+        }
+      };
+      const bool last = sub + 1 == T::kSubs;
+      scores(lk[last ? k_next : k_now], last ? 0 : sub + 1, y, [&](int n) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const int at = n * kEach + j;
+          v[n & 1][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[at], f, -base));
+        }
+        if (n > 0) settle(n - 1);
+      });
+      settle(T::kSteps - 1);
+      // the expansion in this half's share of the 8 pieces of each unit
+      constexpr int kWork = 8 * T::kUnits / T::kSubs, kProduct = 2 * T::kParts;
+      auto pieces = [&](int n, auto expand) {
+        // piece j after instruction j kProduct / kWork
+#pragma unroll
+        for (int j = 0; j < kWork; ++j)
+          if (j * kProduct / kWork == n) expand(sub * kWork + j);
+      };
+      product(lv[buf], sub, p, p2, [&](int n) {
+        pieces(n, [&](int k) {
+          const int u = k / 8, unit_key = wave_key + u * T::kUnitKeys;
+          if (for_values) {
+            if (k % 8 == 0) expanding = value_unit(step + 1, page[u], unit_key, g[u], next_unit, next_unit);
+            expand_values(expanding, unit_key, lv[buf ^ 1], k % 8);
+          } else {
+            if (k % 8 == 0) expanding.scale[0] = key_unit(step + 2, page[u], unit_key, g[u], scale_exponent(next2.k));
+            if (k % 2 == 0) expand_keys(expanding.scale[0], unit_key, g[u], lk[k_after], k % 8 / 2);
+          }
+        });
+      });
+      // values far below the step's largest: passes of their own, in place of the step's values, which the last one
+      // puts back for the step's other half
+      if (__builtin_expect(now.v_least <= now_unit - kBand, 0)) {
+        const int bands = min(kBands, now_unit / kBand + 1);
+        for (int band = 1; band <= bands; ++band) {
+          const int limit = band < bands ? now_unit - band * kBand : now_unit, ex = scale_exponent(limit);
           __syncthreads();
           if (for_values) {
-#pragma unroll
-            for (int u = 0; u < T::kUnits; ++u) {
-              Staged again;
-              load_codes(step, now_page[u], my_key + u * T::kUnitKeys, again);
-              expand_values(step, now_page[u], my_key + u * T::kUnitKeys, again, lv[buf], ex, now_unit - band * kBand);
-            }
+            Staged again[T::kUnits];
+            load_units(step, now_page, again);
+            expand_units(step, now_page, again, lv[buf], lk[0], 12, ex, limit);
           }
           __syncthreads();
-          if (seen) {
+          if (band == bands) break;
 #pragma unroll
-            for (int i = 0; i < T::kParts; ++i)
+          for (int i = 0; i < T::kParts; ++i)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e], unit - ex);
-            product(lv[buf], p, p2);
+            for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e], unit - ex);
+          product(lv[buf], sub, p, p2, [](int) {});
 #pragma unroll
-            for (int i = 0; i < T::kParts; ++i)
+          for (int i = 0; i < T::kParts; ++i)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e], ex - unit);
-          }
+            for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e], ex - unit);
         }
       }
-      if (now.bad && seen) {
-        for (int k = key0; k < key0 + T::kKeys && k < range.hi; ++k) {
+      if (__builtin_expect(now.bad, 0)) {
+        for (int k = key0; k < key0 + 32 && k < end_key; ++k) {
           const int at_page = row_page(c.kv, table, c.rows.table_width, k);
           if (at_page < 0 || k > q_hi || k < q_lo) continue;
-          const int64_t at = ((int64_t)at_page * H + h) * T::kGroups * ps + (k & (ps - 1));
 #pragma unroll
           for (int gr = 0; gr < T::kGroups; ++gr) {
-            if ((c.kv.p.k_scales[at + gr * ps] & 0x7F80) == 0x7F80) sum = NAN;
-            if ((c.kv.p.v_scales[at + gr * ps] & 0x7F80) == 0x7F80)
+            const uint64_t at = scale_index<T::kGroups>(c.kv, at_page, h, gr, k & (ps - 1));
+            if ((c.kv.p.k_scales[at] & 0x7F80) == 0x7F80) sum = NAN;
+            if ((c.kv.p.v_scales[at] & 0x7F80) == 0x7F80)
 #pragma unroll
               for (int i = 0; i < T::kParts; ++i)
 #pragma unroll
@@ -515,23 +604,20 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
           }
         }
       }
-
-      if (more) {
-        const StepScales next = step_scales();
-        const int e = scale_exponent(next.v);
-        const int next_unit = e > now_unit || e < now_unit - kBand / 2 ? e : now_unit;
-        expand_units(step + 1, page, g, buf ^ 1, scale_exponent(next.k), next_unit);
-        now = next;
-        now_unit = next_unit;
-        there = __ballot(scale_page >= 0);
-#pragma unroll
-        for (int u = 0; u < T::kUnits; ++u) {
-          now_page[u] = page[u];
-          page[u] = page2[u];
-        }
-        scale_page = scale_page2;
+    };
+    for (int step = s0; step < s1; ++step) {
+      begin_step(step);
+      half_step(step, Num<0>{}, xa, xb);
+      if constexpr (T::kSubs == 2) {
+        half_step(step, Num<1>{}, xb, xa);
+        end_step(step);
+      } else {
+        end_step(step);
+        if (++step >= s1) break;
+        begin_step(step);
+        half_step(step, Num<0>{}, xb, xa);
+        end_step(step);
       }
-      __syncthreads();
     }
 
     sum += __shfl_xor(sum, 32);

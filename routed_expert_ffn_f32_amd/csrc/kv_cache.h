@@ -66,6 +66,18 @@ __device__ __forceinline__ int row_page(const KvView &kv, const int32_t *table, 
   return (unsigned)page < (unsigned)kv.p.n_pages ? page : -1;
 }
 
+// Index of a row of codes, and of the scale of its group g (kv.weights: that of
+// a row).  One 64-bit multiplication each: a page's rows of all heads are fewer
+// than 2^21 scales.
+__device__ __forceinline__ uint64_t code_row(const KvView &kv, int page, int h, int slot) {
+  return (uint64_t)(uint32_t)page * (uint32_t)(kv.p.kv_heads << kv.shift) + (uint32_t)((h << kv.shift) + slot);
+}
+template <int kGroups>
+__device__ __forceinline__ uint64_t scale_index(const KvView &kv, int page, int h, int g, int slot) {
+  return (uint64_t)(uint32_t)page * (uint32_t)((kv.p.kv_heads * kGroups) << kv.shift) +
+         (uint32_t)(((h * kGroups + g) << kv.shift) + slot);
+}
+
 hipError_t launch_rotary(const coli_moe_rotary_t &a, hipStream_t s);  // tokens >= 1
 hipError_t launch_kv_append(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_moe_kv_values_t &a,
                             hipStream_t s);  // tokens >= 1, as below
