@@ -62,18 +62,6 @@ struct Call {
   float2 *ml;      // [row], for the weights; NULL: not wanted
 };
 
-// Where 16 keys stand (they share a page): byte offsets are 64-bit and uniform.
-struct SubPlace {
-  int64_t ph;  // page * heads + head
-  int slot;
-  bool ok;
-};
-
-__device__ __forceinline__ SubPlace sub_place(const Call &c, const int32_t *table, int h, int key) {
-  const int page = row_page(c.kv, table, c.rows.table_width, key);
-  return {(int64_t)max(page, 0) * c.kv.p.kv_heads + h, key & (c.kv.p.page_size - 1), page >= 0};
-}
-
 // Range of keys that the rows r0 .. r1 of a sequence's key head see.
 struct KeyRange {
   int64_t lo, hi;

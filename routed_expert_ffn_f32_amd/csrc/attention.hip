@@ -27,27 +27,37 @@ namespace {
 template <int D>
 struct Tile {
   static constexpr int kGroups = D / kKvGroup;
-  static constexpr int kRows = 16 / kGroups;         // query rows of a tile
-  static constexpr int kSteps = D / 32;              // matrix instructions of a score
-  static constexpr int kParts = D / 16;              // of a value
-  static constexpr int kKeys = D == 256 ? 32 : 64;   // keys of one step of a wave
-  static constexpr int kSubs = kKeys / 16;
-  static constexpr int kWords = D == 256 ? 2 : 1;    // 16 values' dwords a lane holds of a key
+  static constexpr int kRows = 16 / kGroups;       // query rows of a tile
+  static constexpr int kSteps = D / 32;            // matrix instructions of 16 keys' scores
+  static constexpr int kParts = D / 16;            // of 32 keys' values
+  static constexpr int kWords = D == 256 ? 2 : 1;  // dwords of a key's values that a lane holds
 };
+constexpr int kStepKeys = 32;  // keys of one step of a wave
 
+// The larger of (sum over) a column's four lanes.
 __device__ __forceinline__ float max_over_j(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float sum_over_j(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
-// Sum over the groups of a row: every lane of the row's columns gets it.
+// Over the groups of a row: every lane of the row's columns gets it.
 template <int D>
 __device__ __forceinline__ float sum_groups(float v) {
   if constexpr (D >= 128) v += dpp_f<kDppRowRor8>(v);
   if constexpr (D >= 256) v += dpp_f<kDppRowRor4>(v);
+  return v;
+}
+template <int D>
+__device__ __forceinline__ float max_groups(float v) {
+  if constexpr (D >= 128) v = fmaxf(v, dpp_f<kDppRowRor8>(v));
+  if constexpr (D >= 256) v = fmaxf(v, dpp_f<kDppRowRor4>(v));
   return v;
 }
 
@@ -76,7 +86,9 @@ __device__ __forceinline__ Column column_of(const Call &c, SeqSpan span, int64_t
 }
 
 // The query operand of a column: exact in half precision after a power of two
-// per row (elements below 2^-28 of the row's largest are rounded).
+// per row (elements below 2^-28 of the row's largest are rounded).  The sign of
+// the call's scale goes with it and a scale of 0 makes it 0, so that what
+// multiplies a score is positive.
 template <int D>
 struct QueryOperand {
   half8_t b[Tile<D>::kSteps];
@@ -87,39 +99,38 @@ template <int D>
 __device__ __forceinline__ void load_query(const Call &c, const Column &q, QueryOperand<D> &f) {
   constexpr int kSteps = Tile<D>::kSteps;
   const int j = (threadIdx.x >> 4) & 3;
-  Raw8 raw[kSteps];
+  u32x4 raw[kSteps];
   float top = 0.0f;
-  const int64_t base = q.token * c.a.q_token + q.head * c.a.q_head;
+  const uint16_t *row = static_cast<const uint16_t *>(c.a.q) + (q.token * c.a.q_token + q.head * c.a.q_head);
 #pragma unroll
   for (int w = 0; w < kSteps; ++w) {
     // columns of dword w of this lane: D = 64 has two a lane, D = 256 two sets of four
     const int col = D == 64 ? 16 * j + 8 * w : D == 128 ? 32 * j + 8 * w : 128 * (w / 4) + 32 * j + 8 * (w % 4);
-    raw[w].lo = u32x4{0, 0, 0, 0};
-    if (q.live && col / kKvGroup == q.g) raw[w] = load_raw8(c.a.q, c.a.type, base + col);
+    raw[w] = u32x4{0, 0, 0, 0};
+    if (q.live && col / kKvGroup == q.g) raw[w] = load16(reinterpret_cast<const char *>(row + col));
   }
+  const int type = c.a.type;
 #pragma unroll
   for (int w = 0; w < kSteps; ++w) {
     float v[8];
-    unpack8(c.a.type, raw[w], v);
+    unpack8(type, Raw8{raw[w], raw[w]}, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
   }
-  top = max_over_j(top);
-  if constexpr (D >= 128) top = fmaxf(top, dpp_f<kDppRowRor8>(top));
-  if constexpr (D >= 256) top = fmaxf(top, dpp_f<kDppRowRor4>(top));
+  top = max_groups<D>(max_over_j(top));
   const int ex = lift_exponent(top);
-  const float up = lift(ex);
+  const float up = c.a.scale > 0.0f ? lift(ex) : c.a.scale < 0.0f ? -lift(ex) : 0.0f;
 #pragma unroll
   for (int w = 0; w < kSteps; ++w) {
     float v[8];
-    unpack8(c.a.type, raw[w], v);
+    unpack8(type, Raw8{raw[w], raw[w]}, v);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       f.b[w][2 * e] = (_Float16)(v[e] * up);
       f.b[w][2 * e + 1] = (_Float16)(v[e + 4] * up);
     }
   }
-  f.scale = c.a.scale * kLog2e * unlift(ex);
+  f.scale = c.a.scale != 0.0f ? fabsf(c.a.scale) * kLog2e * unlift(ex) : 1.0f;
 }
 
 // Four neighbouring scales of a column's group.
@@ -128,32 +139,86 @@ __device__ __forceinline__ float4_t scales4(uint2 v) {
                   __uint_as_float(v.y & 0xFFFF0000u)};
 }
 
-// Keys of one step as they stand in memory.
-template <int D>
-struct KeyRegs {
-  u32x4 k[Tile<D>::kSubs][D == 256 ? 2 : 1];
-  uint2 s[Tile<D>::kSubs];
+// Where a step's two 16 keys stand: uniform.  Pages of 16 rows: two places, else
+// one after the other.
+template <bool kSmallPages>
+struct Place {
+  int page[kSmallPages ? 2 : 1], slot;
+  bool ok[2];
 };
 
-template <int D>
-__device__ __forceinline__ void load_keys(const Call &c, const SubPlace &p, int t, int g, KeyRegs<D> &r) {
-  const int lane = threadIdx.x & 63, j = lane >> 4;
-  const int ps = c.kv.p.page_size;
-  const uint8_t *base = c.kv.p.k_codes + (p.ph * ps + p.slot) * (D / 2);
-  const int row = (lane & 15) * (D / 2);
-  if constexpr (D == 64) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(base + row + 8 * j);
-    r.k[t][0] = u32x4{v.x, v.y, 0, 0};
-  } else {
+template <bool kSmallPages>
+__device__ __forceinline__ Place<kSmallPages> place_of(const Call &c, const int32_t *table, int key0) {
+  Place<kSmallPages> p;
+  p.slot = kSmallPages ? 0 : key0 & (c.kv.p.page_size - 1);
 #pragma unroll
-    for (int w = 0; w < D / 128; ++w)
-      r.k[t][w] = *reinterpret_cast<const u32x4 *>(base + row + 64 * w + 16 * j);
+  for (int t = 0; t < (kSmallPages ? 2 : 1); ++t) {
+    const int i = (key0 >> c.kv.shift) + t;
+    const int entry = table[min(i, c.rows.table_width - 1)];
+    p.ok[t] = i < c.rows.table_width && (unsigned)entry < (unsigned)c.kv.p.n_pages;
+    p.page[t] = p.ok[t] ? entry : 0;
   }
-  const uint16_t *sc = c.kv.p.k_scales + (p.ph * Tile<D>::kGroups + g) * ps + p.slot + 4 * j;
-  r.s[t] = *reinterpret_cast<const uint2 *>(sc);
+  if constexpr (!kSmallPages) p.ok[1] = p.ok[0];
+  return p;
 }
 
-// Scores (times log2 e) of 16 keys: lane (column, j) gets keys 4 j .. 4 j + 3.
+// Keys and values of a step as they stand in memory.  Keys: lane (r, j) has
+// columns of key r of each 16 (see load_query) and the scales of its column's
+// group for keys 4 j ..  Values: lane (r, j) has, of keys 4 j .. 4 j + 3 of each
+// 16, the dword of columns 8 r .. 8 r + 7, and the same scales.
+template <int D>
+struct KeyRegs {
+  u32x4 k[2][D == 256 ? 2 : 1];
+  uint2 s[2];
+};
+template <int D>
+struct ValueRegs {
+  uint32_t v[2][4][Tile<D>::kWords];
+  uint2 s[2];
+};
+
+template <int D, bool kSmallPages>
+__device__ __forceinline__ void load_keys(const Call &c, const Place<kSmallPages> &p, int h, int g, KeyRegs<D> &r) {
+  const int lane = threadIdx.x & 63, j = lane >> 4;
+  const int row = (lane & 15) * (D / 2), scale = (g << c.kv.shift) + 4 * j;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int page = p.page[kSmallPages ? t : 0], slot = kSmallPages ? 0 : p.slot + 16 * t;
+    const uint8_t *base = c.kv.p.k_codes + code_row(c.kv, page, h, slot) * (D / 2);
+    if constexpr (D == 64) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(base + (row + 8 * j));
+      r.k[t][0] = u32x4{v.x, v.y, 0, 0};
+    } else {
+#pragma unroll
+      for (int w = 0; w < D / 128; ++w)
+        r.k[t][w] = *reinterpret_cast<const u32x4 *>(base + (row + 64 * w + 16 * j));
+    }
+    r.s[t] = *reinterpret_cast<const uint2 *>(
+        c.kv.p.k_scales + scale_index<Tile<D>::kGroups>(c.kv, page, h, 0, slot) + scale);
+  }
+}
+
+template <int D, bool kSmallPages>
+__device__ __forceinline__ void load_values(const Call &c, const Place<kSmallPages> &p, int h, int g, ValueRegs<D> &r) {
+  const int lane = threadIdx.x & 63, j = lane >> 4;
+  const int word = 4 * j * (D / 2) + (D == 64 ? (lane & 15) / 2 * 4 : (lane & 15) * 4);
+  const int scale = (g << c.kv.shift) + 4 * j;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int page = p.page[kSmallPages ? t : 0], slot = kSmallPages ? 0 : p.slot + 16 * t;
+    const uint8_t *base = c.kv.p.v_codes + code_row(c.kv, page, h, slot) * (D / 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = 0; w < Tile<D>::kWords; ++w)
+        r.v[t][i][w] = *reinterpret_cast<const uint32_t *>(base + (word + i * (D / 2) + 64 * w));
+    r.s[t] = *reinterpret_cast<const uint2 *>(
+        c.kv.p.v_scales + scale_index<Tile<D>::kGroups>(c.kv, page, h, 0, slot) + scale);
+  }
+}
+
+// Scores of 16 keys, to be multiplied by the operand's scale: lane (column, j)
+// gets keys 4 j .. 4 j + 3.
 template <int D>
 __device__ __forceinline__ float4_t scores16(const KeyRegs<D> &r, int t, const QueryOperand<D> &f) {
   float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -162,7 +227,7 @@ __device__ __forceinline__ float4_t scores16(const KeyRegs<D> &r, int t, const Q
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_of(r.k[t][w / 4][w % 4]), f.b[w], acc, 0, 0, 0);
   const float4_t sc = scales4(r.s[t]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = sum_groups<D>(acc[i] * sc[i]) * f.scale;
+  for (int i = 0; i < 4; ++i) acc[i] = sum_groups<D>(acc[i] * sc[i]);
   return acc;
 }
 
@@ -179,11 +244,19 @@ __device__ __forceinline__ void clear_outside(const Call &c, int D) {
   }
 }
 
+// Weights times scales are lifted to [2^6, 2^7) at a weight of 1 and may pass
+// it by the 2^8 that scores may pass the maximum by: 2^15 at most.
+constexpr float kSlack = 8.0f;
+__device__ __forceinline__ float weight_lift(int ex) { return __uint_as_float((uint32_t)(260 - ex) << 23); }
+__device__ __forceinline__ float weight_unlift(int ex) { return __uint_as_float((uint32_t)(ex - 6) << 23); }
+
 // One workgroup: `tile_waves` tiles of one sequence's key head over one split
 // of their keys; the waves of a tile take its steps of keys in turn and are
-// joined in LDS at the end.  kTwice: the weights as the sum of two halves.
-template <int D, bool kTwice>
-__global__ __launch_bounds__(kTileThreads, 2) void kv_attention_kernel(Call c, int64_t work) {
+// joined in LDS at the end.  The next step's keys are loaded when this one's
+// have been used, its values likewise, so a wave always has half a step under
+// way.  kTwice: the weights as the sum of two halves.
+template <int D, bool kTwice, bool kSmallPages>
+__global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void kv_attention_kernel(Call c, int64_t work) {
   using T = Tile<D>;
   constexpr int kOut = T::kRows * D;  // 1024
   __shared__ float so[kTileWaves][kOut];
@@ -205,140 +278,141 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attention_kernel(Call c, i
     const int kw = wave / c.tile_waves, kn = kTileWaves / c.tile_waves;
     const int r1 = min(r0 + c.tile_waves * T::kRows, rows) - 1;
     const KeyRange range = keys_of_rows(c, span, len, r0, r1);
-    const int64_t begin = range.lo & ~(int64_t)(T::kKeys - 1);
-    const int steps = range.hi > range.lo ? (int)((range.hi - begin + T::kKeys - 1) / T::kKeys) : 0;
+    // keys are numbers up to 2^30
+    const int begin = (int)min(range.lo, (int64_t)1 << 30) & ~(kStepKeys - 1), end = (int)max(range.hi, (int64_t)0);
+    const int steps = range.hi > range.lo ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
     const int per = max((steps + c.splits - 1) / c.splits, 4 * kn);  // a split has some work for each wave
     const int s0 = min(split * per, steps), s1 = min(s0 + per, steps);
 
     const Column q = column_of<D>(c, span, len, h, tile);
+    Place<kSmallPages> place, place_v;
+    KeyRegs<D> kr;
+    ValueRegs<D> vr;
+    int st = s0 + kw;
+    if (st < s1) {
+      place = place_of<kSmallPages>(c, table, begin + st * kStepKeys);
+      load_keys<D>(c, place, h, q.g, kr);
+      load_values<D>(c, place, h, q.g, vr);
+    }
     QueryOperand<D> f;
     load_query<D>(c, q, f);
     // rows of this wave's tile alone, for steps that all of them see whole
-    const int64_t pmin = len - span.n + min(tile * T::kRows, rows - 1) / c.group;
-    const int64_t pmax = len - span.n + min((tile + 1) * T::kRows, rows - 1) / c.group;
+    auto clamped = [](int64_t v) { return (int)min(max(v, (int64_t)-1), (int64_t)1 << 30); };
+    const int64_t first_pos = len - span.n + min(tile * T::kRows, rows - 1) / c.group;
+    const int64_t last_pos = len - span.n + min((tile + 1) * T::kRows - 1, rows - 1) / c.group;
+    const int all_hi = clamped(first_pos), all_lo = c.a.window ? clamped(last_pos - c.a.window + 1) : 0;
 
-    float m = -INFINITY, l = 0.0f, big = 0.0f;  // maximum, sum, largest weight times scale (against m)
-    int ex = lift_exponent(0.0f);               // of `big`: the weights are stored times lift(ex)
+    float m = -INFINITY, l = 0.0f;  // the maximum that the sums stand against; the sum
+    int ex = lift_exponent(0.0f);   // weights times scales are lifted by it
+    float big = 0.0f;               // the largest of them, lifted
     float4_t acc[T::kParts];
 #pragma unroll
     for (int i = 0; i < T::kParts; ++i) acc[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int st = s0 + kw; st < s1; st += kn) {
-      const int key0 = (int)begin + st * T::kKeys;
-      SubPlace place[T::kSubs];
-      bool all = true;
+    for (; st < s1; st += kn) {
+      const bool more = st + kn < s1;
+      place_v = place;
+      if (more) place = place_of<kSmallPages>(c, table, begin + (st + kn) * kStepKeys);
+      float4_t x[2], sv[2];
 #pragma unroll
-      for (int t = 0; t < T::kSubs; ++t) {
-        place[t] = sub_place(c, table, h, key0 + 16 * t);
-        all = all && place[t].ok;
-      }
-      KeyRegs<D> kr;
+      for (int t = 0; t < 2; ++t) x[t] = scores16<D>(kr, t, f);
+      if (more) load_keys<D>(c, place, h, q.g, kr);
 #pragma unroll
-      for (int t = 0; t < T::kSubs; ++t) load_keys<D>(c, place[t], t, q.g, kr);
-      // values: lane (r, j) holds, of keys 4 j .. 4 j + 3 of each 16, the dword of columns 8 r .. 8 r + 7
-      uint32_t vw[T::kSubs][4][T::kWords];
-      uint2 vs[T::kSubs];
+      for (int t = 0; t < 2; ++t) sv[t] = scales4(vr.s[t]);
+      const int key0 = begin + st * kStepKeys;
+      if (__builtin_expect(!(key0 + kStepKeys - 1 <= all_hi && key0 >= all_lo && place_v.ok[0] && place_v.ok[1]), 0)) {
 #pragma unroll
-      for (int t = 0; t < T::kSubs; ++t) {
-        const int ps = c.kv.p.page_size;
-        const uint8_t *base = c.kv.p.v_codes + (place[t].ph * ps + place[t].slot) * (D / 2);
-        const int word = D == 64 ? (lane & 15) / 2 * 4 : (lane & 15) * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int w = 0; w < T::kWords; ++w)
-            vw[t][i][w] = *reinterpret_cast<const uint32_t *>(base + (4 * j + i) * (D / 2) + word + 64 * w);
-        vs[t] = *reinterpret_cast<const uint2 *>(c.kv.p.v_scales + (place[t].ph * T::kGroups + q.g) * ps +
-                                                 place[t].slot + 4 * j);
-      }
-
-      float4_t p[T::kSubs], sv[T::kSubs];
-      float top = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < T::kSubs; ++t) {
-        p[t] = scores16<D>(kr, t, f);
-        sv[t] = scales4(vs[t]);
-      }
-      const bool whole = all && key0 + T::kKeys - 1 <= pmin && (!c.a.window || key0 > pmax - c.a.window) && key0 >= 0;
-      if (!whole) {
-#pragma unroll
-        for (int t = 0; t < T::kSubs; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = key0 + 16 * t + 4 * j + i;
-            const bool seen = place[t].ok && key <= q.hi && key >= q.lo;
-            p[t][i] = seen ? p[t][i] : -INFINITY;
+            const bool seen = place_v.ok[t] && key <= q.hi && key >= q.lo;
+            x[t][i] = seen ? x[t][i] : -INFINITY;
             sv[t][i] = seen ? sv[t][i] : 0.0f;
           }
       }
+      float top = x[0][0];
 #pragma unroll
-      for (int t = 0; t < T::kSubs; ++t)
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e / 4][e % 4]);
+      top *= f.scale;
+      float w[8], sum;
+      auto weigh = [&]() {
+        const float base = m == -INFINITY ? 0.0f : m, up = weight_lift(ex);
+        sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, p[t][i]);
-      const float m1 = fmaxf(m, max_over_j(top));
-      const float base = m1 == -INFINITY ? 0.0f : m1;
-      const float fade = __builtin_amdgcn_exp2f(m - base);
-      float sum = 0.0f, most = 0.0f;
-#pragma unroll
-      for (int t = 0; t < T::kSubs; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = __builtin_amdgcn_exp2f(p[t][i] - base);
-          sum += e;
-          p[t][i] = e * sv[t][i];
-          most = fmaxf(most, fabsf(p[t][i]));
+        for (int e = 0; e < 8; ++e) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e / 4][e % 4], f.scale, -base));
+          sum += p;
+          w[e] = p * sv[e / 4][e % 4] * up;
         }
-      m = m1;
-      l = l * fade + sum;
-      big = fmaxf(big * fade, max_over_j(most));
-      const int ex1 = lift_exponent(big);
-      const float turn = __builtin_amdgcn_ldexpf(fade, ex - ex1);
-      ex = ex1;
-      if (__any(turn != 1.0f)) {
+      };
+      weigh();
+      float most = big;
 #pragma unroll
-        for (int i = 0; i < T::kParts; ++i) acc[i] *= turn;
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(w[e]));
+      if (__builtin_expect(__any(top > m + kSlack || most > 0x1p15f), 0)) {
+        // a new maximum, and the lift by the largest weight times scale against it
+        const float m1 = fmaxf(m, max_over_j(top)), base = m1 == -INFINITY ? 0.0f : m1;
+        const float fade = __builtin_amdgcn_exp2f(m - base);
+        m = m1;
+        most = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          most = fmaxf(most, fabsf(__builtin_amdgcn_exp2f(__builtin_fmaf(x[e / 4][e % 4], f.scale, -base)) *
+                                   sv[e / 4][e % 4]));
+        most = fmaxf(max_over_j(most), max_over_j(big) * weight_unlift(ex) * fade);
+        const int ex1 = lift_exponent(most);
+        l *= fade;
+#pragma unroll
+        for (int i = 0; i < T::kParts; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e] * fade, ex - ex1);
+        ex = ex1;
+        most *= weight_lift(ex);
+        weigh();
       }
-      const float up = lift(ex);
+      big = most;
+      l += sum;
+
+      half8_t b, b2;
 #pragma unroll
-      for (int t = 0; t < T::kSubs; t += 2) {
-        half8_t b, b2;
+      for (int e = 0; e < 8; ++e) {
+        b[e] = (_Float16)w[e];
+        if constexpr (kTwice) b2[e] = (_Float16)(w[e] - (float)b[e]);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = p[t + i / 4][i % 4] * up;
-          b[i] = (_Float16)v;
-          if constexpr (kTwice) b2[i] = (_Float16)(v - (float)b[i]);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < T::kWords; ++k) vr.v[t][i][k] ^= 0x88888888u;
+      // D = 64: a lane's four columns are one half of its dword
+      const uint32_t half = D == 64 ? 0x00020002u * (lane & 1) : 0u;
+#pragma unroll
+      for (int i = 0; i < T::kParts; i += 2) {
+        const uint32_t sel = (0x0C040C00u + 0x00010001u * (i / 2 % 4)) + half;
+        u32x4 lo, hi;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t two =
+              __builtin_amdgcn_perm(vr.v[e / 2][2 * (e % 2) + 1][i / 8], vr.v[e / 2][2 * (e % 2)][i / 8], sel);
+          lo[e] = low_codes(two);
+          hi[e] = high_codes(two);
         }
-        uint32_t v[8][T::kWords];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int w = 0; w < T::kWords; ++w) v[i][w] = vw[t + i / 4][i % 4][w] ^ 0x88888888u;
-        // D = 64: a lane's four columns are one half of its dword
-        const uint32_t half = D == 64 ? 0x00020002u * (lane & 1) : 0u;
-#pragma unroll
-        for (int i = 0; i < T::kParts; i += 2) {
-          const uint32_t sel = (0x0C040C00u + 0x00010001u * (i / 2 % 4)) + half;
-          u32x4 lo, hi;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t two = __builtin_amdgcn_perm(v[2 * e + 1][i / 8], v[2 * e][i / 8], sel);
-            lo[e] = low_codes(two);
-            hi[e] = high_codes(two);
-          }
-          const half8_t a0 = __builtin_bit_cast(half8_t, lo), a1 = __builtin_bit_cast(half8_t, hi);
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, b, acc[i], 0, 0, 0);
-          acc[i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, b, acc[i + 1], 0, 0, 0);
-          if constexpr (kTwice) {
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, b2, acc[i], 0, 0, 0);
-            acc[i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, b2, acc[i + 1], 0, 0, 0);
-          }
+        const half8_t a0 = __builtin_bit_cast(half8_t, lo), a1 = __builtin_bit_cast(half8_t, hi);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, b, acc[i], 0, 0, 0);
+        acc[i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, b, acc[i + 1], 0, 0, 0);
+        if constexpr (kTwice) {
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, b2, acc[i], 0, 0, 0);
+          acc[i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, b2, acc[i + 1], 0, 0, 0);
         }
       }
+      if (more) load_values<D>(c, place, h, q.g, vr);
     }
 
     // this wave's sums, against its maximum: to LDS
     l = sum_over_j(l);
-    const float down = unlift(ex);
+    const float down = weight_unlift(ex);
     const int col = lane & 15, r = col % T::kRows;
     __syncthreads();  // of the item before, all is read
     if (j == 0 && q.g == 0) sml[wave][r] = make_float2(m, l);
@@ -359,11 +433,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attention_kernel(Call c, i
       const float base = mm == -INFINITY ? 0.0f : mm;
       float o = 0.0f, ll = 0.0f;
       for (int k = 0; k < kn; ++k) {
-        const int w = k * c.tile_waves + tw;
-        const float2 v = sml[w][rr];
+        const int wv = k * c.tile_waves + tw;
+        const float2 v = sml[wv][rr];
         const float fade = __builtin_amdgcn_exp2f(v.x - base);
         ll += v.y * fade;
-        o += so[w][rr * D + d] * fade;
+        o += so[wv][rr * D + d] * fade;
       }
       const int token = span.first + row / c.group, head = h * c.group + row % c.group;
       const int64_t id = (int64_t)token * c.a.q_heads + head;
@@ -378,28 +452,62 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_attention_kernel(Call c, i
   }
 }
 
-// Joins the splits of a row: one wave a row, D / 64 columns a lane.
+// Joins the splits of a row: one wave a row, D / 64 columns a lane.  Where only
+// sequences of few rows have splits, the rows are counted by sequence, else by
+// token.
 template <int D>
-__global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c) {
+__global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c, int few, int64_t work) {
   constexpr int kCols = D / 64;
   const int lane = threadIdx.x & 63;
-  const int64_t waves = (int64_t)gridDim.x * kTileWaves, n = (int64_t)c.rows.tokens * c.a.q_heads;
-  for (int64_t id = (int64_t)blockIdx.x * kTileWaves + uniform(threadIdx.x >> 6); id < n; id += waves) {
-    const int token = (int)(id / c.a.q_heads), head = (int)(id % c.a.q_heads);
-    const int s = find_seq(c.rows, token);
-    if (s < 0) continue;
-    const int splits = seq_span(c.rows, s).n * c.group <= c.few_rows ? c.splits : c.prompt_splits;
-    if (splits == 1) continue;
+  const int64_t waves = (int64_t)gridDim.x * kTileWaves;
+  for (int64_t item = (int64_t)blockIdx.x * kTileWaves + uniform(threadIdx.x >> 6); item < work; item += waves) {
+    int token, head, splits = c.splits;
+    if (few > 0) {
+      const int i = (int)(item % few), h = (int)(item / few % c.kv.p.kv_heads), s = (int)(item / few / c.kv.p.kv_heads);
+      const SeqSpan span = seq_span(c.rows, s);
+      const int rows = span.n * c.group;
+      if (i >= rows || rows > c.few_rows) continue;
+      token = span.first + i / c.group;
+      head = h * c.group + i % c.group;
+    } else {
+      token = (int)(item / c.a.q_heads);
+      head = (int)(item % c.a.q_heads);
+      const int s = find_seq(c.rows, token);
+      if (s < 0) continue;
+      if (seq_span(c.rows, s).n * c.group > c.few_rows) splits = c.prompt_splits;
+      if (splits == 1) continue;
+    }
+    const int64_t id = (int64_t)token * c.a.q_heads + head;
     const float2 *ml = c.part_ml + id * c.part_splits;
-    float m = -INFINITY;
-    for (int k = 0; k < splits; ++k) m = fmaxf(m, ml[k].x);
-    const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[kCols] = {};
-    for (int k = 0; k < splits; ++k) {
-      const float fade = __builtin_amdgcn_exp2f(ml[k].x - base);
-      l += ml[k].y * fade;
+    // a split a lane: at most 128
+    float2 mine[2];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) o[i] += c.part_o[(id * c.part_splits + k) * D + lane * kCols + i] * fade;
+    for (int k = 0; k < 2; ++k) mine[k] = lane + 64 * k < splits ? ml[lane + 64 * k] : make_float2(-INFINITY, 0.0f);
+    float m = fmaxf(mine[0].x, mine[1].x);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    const float base = m == -INFINITY ? 0.0f : m;
+    float fade[2], l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      fade[k] = __builtin_amdgcn_exp2f(mine[k].x - base);
+      l += mine[k].y * fade[k];
+    }
+    l = wave_sum(l);
+    float o[kCols] = {};
+    const float *from = c.part_o + id * c.part_splits * D + lane * kCols;
+    for (int k0 = 0; k0 < splits; k0 += 8) {
+      float v[8][kCols];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)  // the last one again past the end, times 0
+        __builtin_memcpy(v[k], from + (int64_t)min(k0 + k, splits - 1) * D, sizeof v[k]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float all = __shfl(k0 + k < 64 ? fade[0] : fade[1], (k0 + k) & 63);
+        const float by = k0 + k < splits ? all : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) o[i] += by != 0.0f ? v[k][i] * by : 0.0f;
+      }
     }
     const int64_t at = token * c.a.out_token + head * c.a.out_head + lane * kCols;
 #pragma unroll
@@ -408,76 +516,82 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c)
   }
 }
 
+template <int D>
+constexpr int kWeightSteps = D == 256 ? 1 : 2;  // steps of keys of a wave
+
 // weights_out = weights + sums of the softmax weights of each row of the
 // cache, from the scores again and each query's maximum and sum.  A wave
 // takes one step of keys of a sequence's key head and all tiles of queries
 // that see any of them, so that a place has one writer.
-template <int D>
+template <int D, bool kSmallPages>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int chunks, int64_t work) {
   using T = Tile<D>;
+  constexpr int kCount = kWeightSteps<D>, kChunk = kCount * kStepKeys;
   const int lane = threadIdx.x & 63, j = lane >> 4, H = c.kv.p.kv_heads;
   const int64_t waves = (int64_t)gridDim.x * kTileWaves;
   for (int64_t item = (int64_t)blockIdx.x * kTileWaves + uniform(threadIdx.x >> 6); item < work; item += waves) {
-    const int key0 = (int)(item % chunks) * T::kKeys;
+    const int key0 = (int)(item % chunks) * kChunk;
     const int h = (int)(item / chunks % H), s = (int)(item / chunks / H);
     const SeqSpan span = seq_span(c.rows, s);
     const int64_t len = c.rows.lengths[s], start = len - span.n;
     if (span.n == 0 || key0 >= len) continue;
-    // queries that see any of the step's keys
+    // queries that see any of these keys
     const int64_t i0 = max((int64_t)key0 - start, (int64_t)0);
-    const int64_t i1 = c.a.window ? min(key0 + T::kKeys - 1 + (int64_t)c.a.window - start, (int64_t)span.n)
+    const int64_t i1 = c.a.window ? min(key0 + kChunk - 1 + (int64_t)c.a.window - start, (int64_t)span.n)
                                   : (int64_t)span.n;
     if (i0 >= i1) continue;
     const int32_t *table = c.rows.table + s * c.rows.table_stride;
-    SubPlace place[T::kSubs];
-    KeyRegs<D> kr;
+    Place<kSmallPages> place[kCount];
+    KeyRegs<D> kr[kCount];
     const int g = (lane & 15) / T::kRows;
 #pragma unroll
-    for (int t = 0; t < T::kSubs; ++t) {
-      place[t] = sub_place(c, table, h, key0 + 16 * t);
-      load_keys<D>(c, place[t], t, g, kr);
+    for (int n = 0; n < kCount; ++n) {
+      place[n] = place_of<kSmallPages>(c, table, key0 + n * kStepKeys);
+      load_keys<D>(c, place[n], h, g, kr[n]);
     }
-    float4_t sum[T::kSubs];
+    float4_t sum[kCount][2];
 #pragma unroll
-    for (int t = 0; t < T::kSubs; ++t) sum[t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int n = 0; n < 2 * kCount; ++n) sum[n / 2][n % 2] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const int last = (int)((i1 * c.group - 1) / T::kRows);
     for (int tile = (int)(i0 * c.group / T::kRows); tile <= last; ++tile) {
       const Column q = column_of<D>(c, span, len, h, tile);
+      const float2 ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
       QueryOperand<D> f;
       load_query<D>(c, q, f);
-      const float2 ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
       const float share = ml.y != 0.0f ? 1.0f / ml.y : 0.0f;
 #pragma unroll
-      for (int t = 0; t < T::kSubs; ++t) {
-        const float4_t p = scores16<D>(kr, t, f);
+      for (int n = 0; n < 2 * kCount; ++n) {
+        const float4_t p = scores16<D>(kr[n / 2], n % 2, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int key = key0 + 16 * t + 4 * j + i;
-          const bool seen = q.live && q.g == 0 && place[t].ok && key <= q.hi && key >= q.lo;
-          sum[t][i] += seen ? __builtin_amdgcn_exp2f(p[i] - ml.x) * share : 0.0f;
+          const int key = key0 + 16 * n + 4 * j + i;
+          const bool seen = q.live && q.g == 0 && place[n / 2].ok[n % 2] && key <= q.hi && key >= q.lo;
+          sum[n / 2][n % 2][i] +=
+              seen ? __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], f.scale, -ml.x)) * share : 0.0f;
         }
       }
     }
-    // over the 16 columns: one lane of each j stores its four keys
+    // over the 16 columns: one lane of each j stores four keys
 #pragma unroll
-    for (int t = 0; t < T::kSubs; ++t) {
+    for (int n = 0; n < 2 * kCount; ++n) {
+      float4_t v = sum[n / 2][n % 2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float v = sum[t][i];
-        v += dpp_f<kDppQuadXor1>(v);
-        v += dpp_f<kDppQuadXor2>(v);
-        v += dpp_f<kDppRowRor4>(v);
-        v += dpp_f<kDppRowRor8>(v);
-        sum[t][i] = v;
+        v[i] += dpp_f<kDppQuadXor1>(v[i]);
+        v[i] += dpp_f<kDppQuadXor2>(v[i]);
+        v[i] += dpp_f<kDppRowRor4>(v[i]);
+        v[i] += dpp_f<kDppRowRor8>(v[i]);
       }
-      if ((lane & 15) != t || !place[t].ok) continue;
+      if ((lane & 15) != n || !place[n / 2].ok[n % 2]) continue;
+      const int page = place[n / 2].page[kSmallPages ? n % 2 : 0];
+      const int slot = (key0 + 16 * n + 4 * j) & (c.kv.p.page_size - 1);
+      const uint64_t at = code_row(c.kv, page, h, slot);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t key = key0 + 16 * t + 4 * j + i;
+        const int64_t key = key0 + 16 * n + 4 * j + i;
         // seen by the last query at least, and by the first one's window
         if (key >= len || (c.a.window && key <= start - c.a.window)) continue;
-        const int64_t at = place[t].ph * c.kv.p.page_size + place[t].slot + 4 * j + i;
-        c.a.weights_out[at] = c.kv.p.weights[at] + sum[t][i];
+        c.a.weights_out[at + i] = c.kv.p.weights[at + i] + v[i];
       }
     }
   }
@@ -515,7 +629,7 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
   p.prompt_splits = 1;
   if (p.prompts) {
     const int64_t blocks = (r.tokens * group / prompt_rows(kv.head_dim) + r.seqs) * kv.kv_heads;
-    p.prompt_splits = (int)max(min(min(1536 / blocks, (cap + 511) / 512), parts), (int64_t)1);
+    p.prompt_splits = (int)max(min(min(768 / blocks, (cap + 511) / 512), parts), (int64_t)1);
   }
   const int64_t rows = (int64_t)r.tokens * a.q_heads;
   const int splits = max(p.splits, p.prompt_splits);
@@ -533,24 +647,37 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
 
 unsigned grid_of(int64_t blocks) { return (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20); }
 
-template <int D>
+template <int D, bool kSmallPages>
 hipError_t launch_all(const Call &c, hipStream_t s) {
   const int64_t work = (int64_t)c.rows.seqs * c.kv.p.kv_heads * c.splits * (c.tiles / c.tile_waves);
-  const auto kernel = c.a.type == COLI_MOE_F16 ? kv_attention_kernel<D, true> : kv_attention_kernel<D, false>;
+  const auto kernel = c.a.type == COLI_MOE_F16 ? kv_attention_kernel<D, true, kSmallPages>
+                                               : kv_attention_kernel<D, false, kSmallPages>;
   hipError_t e = launch(kernel, dim3(grid_of(work)), dim3(kTileThreads), 0, s, c, work);
-  if (e == hipSuccess && c.few_rows < 1 << 30) e = launch_attention_prompts(c, s);
+  const bool prompts = c.few_rows < 1 << 30;
+  if (e == hipSuccess && prompts) e = launch_attention_prompts(c, s);
   if (e == hipSuccess && c.part_splits > 1) {
-    const int64_t blocks = ((int64_t)c.rows.tokens * c.a.q_heads + kTileWaves - 1) / kTileWaves;
-    e = launch(kv_attention_join_kernel<D>, dim3(grid_of(blocks)), dim3(kTileThreads), 0, s, c);
+    // rows of sequences of few rows alone, or of all tokens
+    const int64_t few = prompts ? min((int64_t)c.rows.tokens * c.group, (int64_t)c.few_rows)
+                                : (c.rows.offsets ? (int64_t)c.rows.tokens : 1) * c.group;
+    const int64_t by_seq = few * c.rows.seqs * c.kv.p.kv_heads, by_token = (int64_t)c.rows.tokens * c.a.q_heads;
+    const bool seqs = c.prompt_splits == 1 && by_seq <= by_token;
+    const int64_t rows = seqs ? by_seq : by_token;
+    e = launch(kv_attention_join_kernel<D>, dim3(grid_of((rows + kTileWaves - 1) / kTileWaves)), dim3(kTileThreads), 0, s,
+               c, seqs ? (int)few : 0, rows);
   }
   if (e == hipSuccess && c.a.weights_out) {
     const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
-    const int chunks = (int)((cap + Tile<D>::kKeys - 1) / Tile<D>::kKeys);
+    const int chunks = (int)((cap + kWeightSteps<D> * kStepKeys - 1) / (kWeightSteps<D> * kStepKeys));
     const int64_t items = (int64_t)c.rows.seqs * c.kv.p.kv_heads * chunks;
-    e = launch(kv_weights_kernel<D>, dim3(grid_of((items + kTileWaves - 1) / kTileWaves)), dim3(kTileThreads), 0, s, c,
-               chunks, items);
+    e = launch(kv_weights_kernel<D, kSmallPages>, dim3(grid_of((items + kTileWaves - 1) / kTileWaves)),
+               dim3(kTileThreads), 0, s, c, chunks, items);
   }
   return e;
+}
+
+template <int D>
+hipError_t launch_all(const Call &c, hipStream_t s) {
+  return c.kv.p.page_size < kStepKeys ? launch_all<D, true>(c, s) : launch_all<D, false>(c, s);
 }
 
 }  // namespace
