@@ -24,20 +24,21 @@ __device__ __forceinline__ int lift_exponent(float v) { return max((int)(__float
 __device__ __forceinline__ float lift(int ex) { return __uint_as_float((uint32_t)(268 - ex) << 23); }
 __device__ __forceinline__ float unlift(int ex) { return __uint_as_float((uint32_t)(ex - 14) << 23); }
 
-// u - 8 of the nibbles at bits 0 and 16 (4 and 20) of w.
+// The signed codes at bits 0 and 16 (4 and 20) of w: the exclusive or with 8
+// that makes u of a code and the exponent of 1024 are one constant, so the two
+// masks are one three-input instruction.
 __device__ __forceinline__ uint32_t low_codes(uint32_t w) {
-  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) | 0x64006400u);
+  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) ^ 0x64086408u);
   return __builtin_bit_cast(uint32_t, v + half2_t{(_Float16)-1032.0f, (_Float16)-1032.0f});
 }
 __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
-  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x00F000F0u) | 0x64006400u);
+  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x00F000F0u) ^ 0x64806480u);
   const half2_t by = {(_Float16)0.0625f, (_Float16)0.0625f}, off = {(_Float16)-72.0f, (_Float16)-72.0f};
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, by, off));
 }
 
 // The 8 codes of a dword as halves, in the order (0, 4), (1, 5), (2, 6), (3, 7).
 __device__ __forceinline__ half8_t codes_of(uint32_t w) {
-  w ^= 0x88888888u;
   u32x4 r;
   r[0] = low_codes(w);
   r[1] = high_codes(w);

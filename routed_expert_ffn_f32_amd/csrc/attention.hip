@@ -50,14 +50,14 @@ __device__ __forceinline__ float sum_over_j(float v) {
 // Over the groups of a row: every lane of the row's columns gets it.
 template <int D>
 __device__ __forceinline__ float sum_groups(float v) {
-  if constexpr (D >= 128) v += dpp_f<kDppRowRor8>(v);
-  if constexpr (D >= 256) v += dpp_f<kDppRowRor4>(v);
+  if constexpr (D >= 128) v += dpp_row_f<kDppRowRor8>(v);
+  if constexpr (D >= 256) v += dpp_row_f<kDppRowRor4>(v);
   return v;
 }
 template <int D>
 __device__ __forceinline__ float max_groups(float v) {
-  if constexpr (D >= 128) v = fmaxf(v, dpp_f<kDppRowRor8>(v));
-  if constexpr (D >= 256) v = fmaxf(v, dpp_f<kDppRowRor4>(v));
+  if constexpr (D >= 128) v = fmaxf(v, dpp_row_f<kDppRowRor8>(v));
+  if constexpr (D >= 256) v = fmaxf(v, dpp_row_f<kDppRowRor4>(v));
   return v;
 }
 
@@ -140,23 +140,39 @@ __device__ __forceinline__ float4_t scales4(uint2 v) {
 }
 
 // Where a step's two 16 keys stand: uniform.  Pages of 16 rows: two places, else
-// one after the other.
+// one after the other.  The table's entries are asked for a step before they
+// are needed, as they stand.
+template <bool kSmallPages>
+struct Entries {
+  int entry[kSmallPages ? 2 : 1];
+};
 template <bool kSmallPages>
 struct Place {
-  int page[kSmallPages ? 2 : 1], slot;
+  uint64_t row[kSmallPages ? 2 : 1];    // of codes
+  uint64_t scale[kSmallPages ? 2 : 1];  // first scale of group 0
   bool ok[2];
 };
 
 template <bool kSmallPages>
-__device__ __forceinline__ Place<kSmallPages> place_of(const Call &c, const int32_t *table, int key0) {
+__device__ __forceinline__ Entries<kSmallPages> entries_of(const Call &c, const int32_t *table, int key0) {
+  Entries<kSmallPages> e;
+#pragma unroll
+  for (int t = 0; t < (kSmallPages ? 2 : 1); ++t)
+    e.entry[t] = table[min((key0 >> c.kv.shift) + t, c.rows.table_width - 1)];
+  return e;
+}
+
+template <int D, bool kSmallPages>
+__device__ __forceinline__ Place<kSmallPages> place_of(const Call &c, const Entries<kSmallPages> &e, int h, int key0) {
   Place<kSmallPages> p;
-  p.slot = kSmallPages ? 0 : key0 & (c.kv.p.page_size - 1);
+  const int slot = kSmallPages ? 0 : key0 & (c.kv.p.page_size - 1);
 #pragma unroll
   for (int t = 0; t < (kSmallPages ? 2 : 1); ++t) {
-    const int i = (key0 >> c.kv.shift) + t;
-    const int entry = table[min(i, c.rows.table_width - 1)];
-    p.ok[t] = i < c.rows.table_width && (unsigned)entry < (unsigned)c.kv.p.n_pages;
-    p.page[t] = p.ok[t] ? entry : 0;
+    const int entry = uniform(e.entry[t]);
+    p.ok[t] = (key0 >> c.kv.shift) + t < c.rows.table_width && (unsigned)entry < (unsigned)c.kv.p.n_pages;
+    const int page = p.ok[t] ? entry : 0;
+    p.row[t] = code_row(c.kv, page, h, slot);
+    p.scale[t] = scale_index<Tile<D>::kGroups>(c.kv, page, h, 0, slot);
   }
   if constexpr (!kSmallPages) p.ok[1] = p.ok[0];
   return p;
@@ -178,42 +194,40 @@ struct ValueRegs {
 };
 
 template <int D, bool kSmallPages>
-__device__ __forceinline__ void load_keys(const Call &c, const Place<kSmallPages> &p, int h, int g, KeyRegs<D> &r) {
+__device__ __forceinline__ void load_keys(const Call &c, const Place<kSmallPages> &p, int g, KeyRegs<D> &r) {
   const int lane = threadIdx.x & 63, j = lane >> 4;
-  const int row = (lane & 15) * (D / 2), scale = (g << c.kv.shift) + 4 * j;
+  const uint32_t row = (lane & 15) * (D / 2) + (D == 64 ? 8 : 16) * j, scale = (g << c.kv.shift) + 4 * j;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int page = p.page[kSmallPages ? t : 0], slot = kSmallPages ? 0 : p.slot + 16 * t;
-    const uint8_t *base = c.kv.p.k_codes + code_row(c.kv, page, h, slot) * (D / 2);
+    const int n = kSmallPages ? t : 0, rows = kSmallPages ? 0 : 16 * t;
+    const uint8_t *base = c.kv.p.k_codes + p.row[n] * (D / 2);
     if constexpr (D == 64) {
-      const uint2 v = *reinterpret_cast<const uint2 *>(base + (row + 8 * j));
+      const uint2 v = *reinterpret_cast<const uint2 *>(base + row + rows * (D / 2));
       r.k[t][0] = u32x4{v.x, v.y, 0, 0};
     } else {
 #pragma unroll
       for (int w = 0; w < D / 128; ++w)
-        r.k[t][w] = *reinterpret_cast<const u32x4 *>(base + (row + 64 * w + 16 * j));
+        r.k[t][w] = *reinterpret_cast<const u32x4 *>(base + row + (rows * (D / 2) + 64 * w));
     }
-    r.s[t] = *reinterpret_cast<const uint2 *>(
-        c.kv.p.k_scales + scale_index<Tile<D>::kGroups>(c.kv, page, h, 0, slot) + scale);
+    r.s[t] = *reinterpret_cast<const uint2 *>(c.kv.p.k_scales + p.scale[n] + scale + rows);
   }
 }
 
 template <int D, bool kSmallPages>
-__device__ __forceinline__ void load_values(const Call &c, const Place<kSmallPages> &p, int h, int g, ValueRegs<D> &r) {
+__device__ __forceinline__ void load_values(const Call &c, const Place<kSmallPages> &p, int g, ValueRegs<D> &r) {
   const int lane = threadIdx.x & 63, j = lane >> 4;
-  const int word = 4 * j * (D / 2) + (D == 64 ? (lane & 15) / 2 * 4 : (lane & 15) * 4);
-  const int scale = (g << c.kv.shift) + 4 * j;
+  const uint32_t word = 4 * j * (D / 2) + (D == 64 ? (lane & 15) / 2 * 4 : (lane & 15) * 4);
+  const uint32_t scale = (g << c.kv.shift) + 4 * j;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int page = p.page[kSmallPages ? t : 0], slot = kSmallPages ? 0 : p.slot + 16 * t;
-    const uint8_t *base = c.kv.p.v_codes + code_row(c.kv, page, h, slot) * (D / 2);
+    const int n = kSmallPages ? t : 0, rows = kSmallPages ? 0 : 16 * t;
+    const uint8_t *base = c.kv.p.v_codes + p.row[n] * (D / 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int w = 0; w < Tile<D>::kWords; ++w)
-        r.v[t][i][w] = *reinterpret_cast<const uint32_t *>(base + (word + i * (D / 2) + 64 * w));
-    r.s[t] = *reinterpret_cast<const uint2 *>(
-        c.kv.p.v_scales + scale_index<Tile<D>::kGroups>(c.kv, page, h, 0, slot) + scale);
+        r.v[t][i][w] = *reinterpret_cast<const uint32_t *>(base + word + ((rows + i) * (D / 2) + 64 * w));
+    r.s[t] = *reinterpret_cast<const uint2 *>(c.kv.p.v_scales + p.scale[n] + scale + rows);
   }
 }
 
@@ -285,14 +299,19 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void
     const int s0 = min(split * per, steps), s1 = min(s0 + per, steps);
 
     const Column q = column_of<D>(c, span, len, h, tile);
-    Place<kSmallPages> place, place_v;
+    Entries<kSmallPages> entries;
+    Place<kSmallPages> place;
+    bool ok[2];  // the 16 keys of this step are there
     KeyRegs<D> kr;
     ValueRegs<D> vr;
     int st = s0 + kw;
     if (st < s1) {
-      place = place_of<kSmallPages>(c, table, begin + st * kStepKeys);
-      load_keys<D>(c, place, h, q.g, kr);
-      load_values<D>(c, place, h, q.g, vr);
+      const int key0 = begin + st * kStepKeys;
+      entries = entries_of<kSmallPages>(c, table, key0);
+      place = place_of<D>(c, entries, h, key0);
+      entries = entries_of<kSmallPages>(c, table, key0 + kn * kStepKeys);
+      load_keys<D>(c, place, q.g, kr);
+      load_values<D>(c, place, q.g, vr);
     }
     QueryOperand<D> f;
     load_query<D>(c, q, f);
@@ -311,22 +330,26 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void
 
     for (; st < s1; st += kn) {
       const bool more = st + kn < s1;
-      place_v = place;
-      if (more) place = place_of<kSmallPages>(c, table, begin + (st + kn) * kStepKeys);
+      const int key0 = begin + st * kStepKeys, next_key = key0 + kn * kStepKeys;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) ok[t] = place.ok[t];
+      if (more) {
+        place = place_of<D>(c, entries, h, next_key);
+        entries = entries_of<kSmallPages>(c, table, next_key + kn * kStepKeys);
+      }
       float4_t x[2], sv[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) x[t] = scores16<D>(kr, t, f);
-      if (more) load_keys<D>(c, place, h, q.g, kr);
+      if (more) load_keys<D>(c, place, q.g, kr);
 #pragma unroll
       for (int t = 0; t < 2; ++t) sv[t] = scales4(vr.s[t]);
-      const int key0 = begin + st * kStepKeys;
-      if (__builtin_expect(!(key0 + kStepKeys - 1 <= all_hi && key0 >= all_lo && place_v.ok[0] && place_v.ok[1]), 0)) {
+      if (__builtin_expect(!(key0 + kStepKeys - 1 <= all_hi && key0 >= all_lo && ok[0] && ok[1]), 0)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = key0 + 16 * t + 4 * j + i;
-            const bool seen = place_v.ok[t] && key <= q.hi && key >= q.lo;
+            const bool seen = ok[t] && key <= q.hi && key >= q.lo;
             x[t][i] = seen ? x[t][i] : -INFINITY;
             sv[t][i] = seen ? sv[t][i] : 0.0f;
           }
@@ -380,12 +403,6 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void
         b[e] = (_Float16)w[e];
         if constexpr (kTwice) b2[e] = (_Float16)(w[e] - (float)b[e]);
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int k = 0; k < T::kWords; ++k) vr.v[t][i][k] ^= 0x88888888u;
       // D = 64: a lane's four columns are one half of its dword
       const uint32_t half = D == 64 ? 0x00020002u * (lane & 1) : 0u;
 #pragma unroll
@@ -407,7 +424,7 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void
           acc[i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, b2, acc[i + 1], 0, 0, 0);
         }
       }
-      if (more) load_values<D>(c, place, h, q.g, vr);
+      if (more) load_values<D>(c, place, q.g, vr);
     }
 
     // this wave's sums, against its maximum: to LDS
@@ -546,8 +563,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
     const int g = (lane & 15) / T::kRows;
 #pragma unroll
     for (int n = 0; n < kCount; ++n) {
-      place[n] = place_of<kSmallPages>(c, table, key0 + n * kStepKeys);
-      load_keys<D>(c, place[n], h, g, kr[n]);
+      place[n] = place_of<D>(c, entries_of<kSmallPages>(c, table, key0 + n * kStepKeys), h, key0 + n * kStepKeys);
+      load_keys<D>(c, place[n], g, kr[n]);
     }
     float4_t sum[kCount][2];
 #pragma unroll
@@ -577,15 +594,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
       float4_t v = sum[n / 2][n % 2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] += dpp_f<kDppQuadXor1>(v[i]);
-        v[i] += dpp_f<kDppQuadXor2>(v[i]);
-        v[i] += dpp_f<kDppRowRor4>(v[i]);
-        v[i] += dpp_f<kDppRowRor8>(v[i]);
+        v[i] += dpp_row_f<kDppQuadXor1>(v[i]);
+        v[i] += dpp_row_f<kDppQuadXor2>(v[i]);
+        v[i] += dpp_row_f<kDppRowRor4>(v[i]);
+        v[i] += dpp_row_f<kDppRowRor8>(v[i]);
       }
       if ((lane & 15) != n || !place[n / 2].ok[n % 2]) continue;
-      const int page = place[n / 2].page[kSmallPages ? n % 2 : 0];
-      const int slot = (key0 + 16 * n + 4 * j) & (c.kv.p.page_size - 1);
-      const uint64_t at = code_row(c.kv, page, h, slot);
+      const uint64_t at = place[n / 2].row[kSmallPages ? n % 2 : 0] + (kSmallPages ? 0 : 16 * (n % 2)) + 4 * j;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t key = key0 + 16 * n + 4 * j + i;

@@ -309,7 +309,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
         r.scale[i] = half2_t{val_scale(a, up, limit), val_scale(d, up, limit)};
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r.code[i] = g.code[i] ^ 0x88888888u;
+      for (int i = 0; i < 4; ++i) r.code[i] = g.code[i];
       return r;
     };
     auto expand_values = [&](const ValueUnit &r, int unit_key, _Float16 *to, int i) {

@@ -26,6 +26,13 @@ __device__ __forceinline__ int dpp_i(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xF, false);
 }
 
+// The same within rows, where every lane has a source: without a value to fall
+// back on, the compiler folds the move into the instruction that uses it.
+template <int CTRL>
+__device__ __forceinline__ float dpp_row_f(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
 // Raw buffer loads: the descriptor covers [base, base + bytes); lanes pass a
 // 32-bit byte offset (VGPR) and the wave a uniform one (SGPR).  Reads past
 // `bytes` return zero instead of faulting.
