@@ -56,6 +56,7 @@ struct Call {
   int tiles;       // tiles of a sequence's key head that the grid has
   int tile_waves;  // of them in one workgroup (1, 2 or 4)
   int few_rows;    // a key head's query rows up to which a sequence takes the tiles of 16 columns
+  int waves;       // of a workgroup of tiles, 4 or 8
   int splits, prompt_splits;  // of the keys, by the tiles and by the prompts' kernel
   int part_splits;  // the larger
   float *part_o;   // [row][split][D], row = token * q_heads + head

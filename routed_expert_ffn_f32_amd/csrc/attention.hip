@@ -20,6 +20,7 @@
 // products by exponents that it does not normalise: next to a large product
 // everything below 2^-17 of it was lost.)
 #include "attention.h"
+#include "lds_dma.h"
 
 namespace coli {
 namespace {
@@ -31,6 +32,13 @@ struct Tile {
   static constexpr int kSteps = D / 32;            // matrix instructions of 16 keys' scores
   static constexpr int kParts = D / 16;            // of 32 keys' values
   static constexpr int kWords = D == 256 ? 2 : 1;  // dwords of a key's values that a lane holds
+  // A step in LDS: codes of 32 keys and of their values as in memory, then the
+  // scales, 64 bytes for each group of the keys and then of the values.
+  static constexpr int kCodes = 16 * D;            // bytes of the keys, and of the values
+  static constexpr int kScales = 2 * kCodes;       // where the scales start
+  static constexpr int kCopies = 2 * D / 64 + (D == 256 ? 2 : 1);  // instructions that fetch a step
+  static constexpr int kStep = kScales + (D == 256 ? 512 : 256);
+  static constexpr int kRing = D == 64 ? 4 : D == 128 ? 3 : 2;     // steps a wave has room for
 };
 constexpr int kStepKeys = 32;  // keys of one step of a wave
 
@@ -213,24 +221,6 @@ __device__ __forceinline__ void load_keys(const Call &c, const Place<kSmallPages
   }
 }
 
-template <int D, bool kSmallPages>
-__device__ __forceinline__ void load_values(const Call &c, const Place<kSmallPages> &p, int g, ValueRegs<D> &r) {
-  const int lane = threadIdx.x & 63, j = lane >> 4;
-  const uint32_t word = 4 * j * (D / 2) + (D == 64 ? (lane & 15) / 2 * 4 : (lane & 15) * 4);
-  const uint32_t scale = (g << c.kv.shift) + 4 * j;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int n = kSmallPages ? t : 0, rows = kSmallPages ? 0 : 16 * t;
-    const uint8_t *base = c.kv.p.v_codes + p.row[n] * (D / 2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int w = 0; w < Tile<D>::kWords; ++w)
-        r.v[t][i][w] = *reinterpret_cast<const uint32_t *>(base + word + ((rows + i) * (D / 2) + 64 * w));
-    r.s[t] = *reinterpret_cast<const uint2 *>(c.kv.p.v_scales + p.scale[n] + scale + rows);
-  }
-}
-
 // Scores of 16 keys, to be multiplied by the operand's scale: lane (column, j)
 // gets keys 4 j .. 4 j + 3.
 template <int D>
@@ -264,19 +254,92 @@ constexpr float kSlack = 8.0f;
 __device__ __forceinline__ float weight_lift(int ex) { return __uint_as_float((uint32_t)(260 - ex) << 23); }
 __device__ __forceinline__ float weight_unlift(int ex) { return __uint_as_float((uint32_t)(ex - 6) << 23); }
 
+// Copies a step's codes and scales into LDS.
+template <int D, bool kSmallPages>
+__device__ __forceinline__ void fetch_step(const Call &c, const Place<kSmallPages> &p, uint32_t lds) {
+  using T = Tile<D>;
+  const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint8_t *codes = kv ? c.kv.p.v_codes : c.kv.p.k_codes;
+    const uint32_t to = lds + kv * T::kCodes;
+    if constexpr (D == 64 && kSmallPages) {
+      const uint8_t *lo = codes + p.row[0] * (D / 2), *hi = codes + p.row[kSmallPages ? 1 : 0] * (D / 2);
+      dma16v(to, (lane < 32 ? lo : hi) + (lane & 31) * 16);
+    } else {
+#pragma unroll
+      for (int n = 0; n < D / 64; ++n) {  // 1024 bytes each: within 16 keys, but for D = 64
+        constexpr int kEach = D >= 128 ? D / 128 : 1;  // of 16 keys
+        const int t = kSmallPages ? n / kEach : 0, at = kSmallPages ? n % kEach : n;
+        dma16(to + n * 1024, codes + p.row[kSmallPages ? t : 0] * (D / 2) + at * 1024, lane * 16);
+      }
+    }
+  }
+  // 16 lanes a group, two scales each
+#pragma unroll
+  for (int n = 0; n < (D == 256 ? 2 : 1); ++n) {
+    const uint32_t seg = lane / 16, g = D == 64 ? 0 : D == 128 ? seg & 1 : seg;
+    const bool values = D == 64 ? seg & 1 : D == 128 ? seg >> 1 : n == 1;
+    const uint16_t *scales = values ? c.kv.p.v_scales : c.kv.p.k_scales;
+    const uint64_t first = kSmallPages && (lane & 8) ? p.scale[kSmallPages ? 1 : 0] : p.scale[0];
+    dma4v(lds + T::kScales + n * 256,
+          scales + first + (g << c.kv.shift) + (kSmallPages ? lane & 7 : lane & 15) * 2);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void read_keys(const char *step, int g, KeyRegs<D> &r) {
+  const int lane = threadIdx.x & 63, j = lane >> 4;
+  const char *row = step + (lane & 15) * (D / 2) + (D == 64 ? 8 : 16) * j;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    if constexpr (D == 64) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(row + 16 * t * (D / 2));
+      r.k[t][0] = u32x4{v.x, v.y, 0, 0};
+    } else {
+#pragma unroll
+      for (int w = 0; w < D / 128; ++w) r.k[t][w] = *reinterpret_cast<const u32x4 *>(row + 16 * t * (D / 2) + 64 * w);
+    }
+    r.s[t] = *reinterpret_cast<const uint2 *>(step + Tile<D>::kScales + 64 * g + 32 * t + 8 * j);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void read_values(const char *step, int g, ValueRegs<D> &r) {
+  using T = Tile<D>;
+  const int lane = threadIdx.x & 63, j = lane >> 4;
+  const char *word =
+      step + T::kCodes + 4 * j * (D / 2) + (D == 64 ? (lane & 15) / 2 * 4 : (lane & 15) * 4);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = 0; w < T::kWords; ++w)
+        r.v[t][i][w] = *reinterpret_cast<const uint32_t *>(word + (16 * t + i) * (D / 2) + 64 * w);
+    r.s[t] = *reinterpret_cast<const uint2 *>(step + T::kScales + 64 * (T::kGroups + g) + 32 * t + 8 * j);
+  }
+}
+
 // One workgroup: `tile_waves` tiles of one sequence's key head over one split
 // of their keys; the waves of a tile take its steps of keys in turn and are
-// joined in LDS at the end.  The next step's keys are loaded when this one's
-// have been used, its values likewise, so a wave always has half a step under
-// way.  kTwice: the weights as the sum of two halves.
-template <int D, bool kTwice, bool kSmallPages>
-__global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void kv_attention_kernel(Call c, int64_t work) {
+// joined in LDS at the end.  A wave copies its steps into a ring of its own in
+// LDS, up to kRing - 1 ahead.  kTwice: the weights as the sum of two halves.
+template <int D, bool kTwice, bool kSmallPages, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128 ? 3 : 4) void kv_attention_kernel(
+    Call c, int64_t work) {
   using T = Tile<D>;
   constexpr int kOut = T::kRows * D;  // 1024
-  __shared__ float so[kTileWaves][kOut];
-  __shared__ float2 sml[kTileWaves][T::kRows];
+  constexpr int kThreads = 64 * kWaves;
+  // the rings; at the end every wave's sums and results
+  __shared__ __align__(16) char shared[kWaves * T::kRing * T::kStep];
+  static_assert(T::kRing * T::kStep >= kOut * 4 + T::kRows * 8, "results fit where the ring was");
+  float *so = reinterpret_cast<float *>(shared);                                // [wave][row][column]
+  float2 *sml = reinterpret_cast<float2 *>(shared + kWaves * kOut * sizeof(float));  // [wave][row]
   const int tid = threadIdx.x, lane = tid & 63, j = lane >> 4, wave = uniform(tid >> 6);
   const int H = c.kv.p.kv_heads;
+  const char *ring = shared + wave * T::kRing * T::kStep;
+  const uint32_t ring_lds = uniform(lds_addr(ring));
   if (blockIdx.x == 0) clear_outside(c, D);
   for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
     const int tgroups = c.tiles / c.tile_waves;
@@ -289,29 +352,37 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void
     const int64_t len = c.rows.lengths[s];
     const int32_t *table = c.rows.table + s * c.rows.table_stride;
     const int tile = tg * c.tile_waves + wave % c.tile_waves;
-    const int kw = wave / c.tile_waves, kn = kTileWaves / c.tile_waves;
+    const int kw = wave / c.tile_waves, kn = kWaves / c.tile_waves;
     const int r1 = min(r0 + c.tile_waves * T::kRows, rows) - 1;
     const KeyRange range = keys_of_rows(c, span, len, r0, r1);
     // keys are numbers up to 2^30
     const int begin = (int)min(range.lo, (int64_t)1 << 30) & ~(kStepKeys - 1), end = (int)max(range.hi, (int64_t)0);
     const int steps = range.hi > range.lo ? (end - begin + kStepKeys - 1) / kStepKeys : 0;
-    const int per = max((steps + c.splits - 1) / c.splits, 4 * kn);  // a split has some work for each wave
+    const int per = max((steps + c.splits - 1) / c.splits, 2 * kn);  // a split has some work for each wave
     const int s0 = min(split * per, steps), s1 = min(s0 + per, steps);
+    const int mine = s1 - s0 > kw ? (s1 - s0 - kw + kn - 1) / kn : 0;  // steps of this wave
+    const int first_key = begin + (s0 + kw) * kStepKeys, key_step = kn * kStepKeys;
 
     const Column q = column_of<D>(c, span, len, h, tile);
+    __syncthreads();  // of the item before, all is read
+    // the table's entries of 64 steps at a time, a step a lane
     Entries<kSmallPages> entries;
-    Place<kSmallPages> place;
-    bool ok[2];  // the 16 keys of this step are there
-    KeyRegs<D> kr;
-    ValueRegs<D> vr;
-    int st = s0 + kw;
-    if (st < s1) {
-      const int key0 = begin + st * kStepKeys;
-      entries = entries_of<kSmallPages>(c, table, key0);
-      place = place_of<D>(c, entries, h, key0);
-      entries = entries_of<kSmallPages>(c, table, key0 + kn * kStepKeys);
-      load_keys<D>(c, place, q.g, kr);
-      load_values<D>(c, place, q.g, vr);
+    auto look_up = [&](int i) { entries = entries_of<kSmallPages>(c, table, first_key + min(i + lane, mine - 1) * key_step); };
+    uint32_t there = 0;  // bit 2 slot + t: the 16 keys are on a page
+    auto fetch = [&](int i, int slot) {
+      const int key0 = first_key + i * key_step;
+      Entries<kSmallPages> e;
+#pragma unroll
+      for (int t = 0; t < (kSmallPages ? 2 : 1); ++t) e.entry[t] = __builtin_amdgcn_readlane(entries.entry[t], i & 63);
+      const Place<kSmallPages> p = place_of<D>(c, e, h, key0);
+      there = (there & ~(3u << 2 * slot)) | (uint32_t)(p.ok[0] | p.ok[1] << 1) << 2 * slot;
+      fetch_step<D>(c, p, ring_lds + slot * T::kStep);
+    };
+    if (mine > 0) {
+      look_up(0);
+#pragma unroll
+      for (int i = 0; i < T::kRing - 1; ++i)
+        if (i < mine) fetch(i, i);
     }
     QueryOperand<D> f;
     load_query<D>(c, q, f);
@@ -328,19 +399,29 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void
 #pragma unroll
     for (int i = 0; i < T::kParts; ++i) acc[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (; st < s1; st += kn) {
-      const bool more = st + kn < s1;
-      const int key0 = begin + st * kStepKeys, next_key = key0 + kn * kStepKeys;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) ok[t] = place.ok[t];
-      if (more) {
-        place = place_of<D>(c, entries, h, next_key);
-        entries = entries_of<kSmallPages>(c, table, next_key + kn * kStepKeys);
+    int slot = 0;
+    for (int i = 0; i < mine; ++i) {
+      // this step has come when only the later ones' copies are under way
+      if (i + T::kRing - 1 <= mine)
+        dma_wait<(T::kRing - 2) * T::kCopies>();
+      else
+        dma_wait<0>();
+      const char *step = ring + slot * T::kStep;
+      KeyRegs<D> kr;
+      read_keys<D>(step, q.g, kr);
+      const int key0 = first_key + i * key_step;
+      const bool ok[2] = {(there >> 2 * slot & 1) != 0, (there >> 2 * slot & 2) != 0};
+      if (i + T::kRing - 1 < mine) {
+        // where the step before this one was
+        const int ahead = i + T::kRing - 1, at = slot == 0 ? T::kRing - 1 : slot - 1;
+        if ((ahead & 63) == 0) look_up(ahead);
+        fetch(ahead, at);
       }
       float4_t x[2], sv[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) x[t] = scores16<D>(kr, t, f);
-      if (more) load_keys<D>(c, place, q.g, kr);
+      ValueRegs<D> vr;
+      read_values<D>(step, q.g, vr);
 #pragma unroll
       for (int t = 0; t < 2; ++t) sv[t] = scales4(vr.s[t]);
       if (__builtin_expect(!(key0 + kStepKeys - 1 <= all_hi && key0 >= all_lo && ok[0] && ok[1]), 0)) {
@@ -424,37 +505,37 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void
           acc[i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, b2, acc[i + 1], 0, 0, 0);
         }
       }
-      if (more) load_values<D>(c, place, q.g, vr);
+      slot = slot + 1 == T::kRing ? 0 : slot + 1;
     }
 
     // this wave's sums, against its maximum: to LDS
     l = sum_over_j(l);
     const float down = weight_unlift(ex);
     const int col = lane & 15, r = col % T::kRows;
-    __syncthreads();  // of the item before, all is read
-    if (j == 0 && q.g == 0) sml[wave][r] = make_float2(m, l);
+    __syncthreads();  // all rings are read
+    if (j == 0 && q.g == 0) sml[wave * T::kRows + r] = make_float2(m, l);
 #pragma unroll
     for (int i = 0; i < T::kParts; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int d = D == 64 ? 16 * j + 4 * e + i : 128 * (i / 8) + 32 * j + 8 * e + i % 8;
-        if (d / kKvGroup == q.g) so[wave][r * D + d] = acc[i][e] * down;
+        if (d / kKvGroup == q.g) so[wave * kOut + r * D + d] = acc[i][e] * down;
       }
     __syncthreads();
-    for (int e = tid; e < c.tile_waves * kOut; e += kTileThreads) {
+    for (int e = tid; e < c.tile_waves * kOut; e += kThreads) {
       const int tw = e / kOut, rr = e % kOut / D, d = e % D;
       const int row = r0 + tw * T::kRows + rr;
       if (row >= rows) continue;
       float mm = -INFINITY;
-      for (int k = 0; k < kn; ++k) mm = fmaxf(mm, sml[k * c.tile_waves + tw][rr].x);
+      for (int k = 0; k < kn; ++k) mm = fmaxf(mm, sml[(k * c.tile_waves + tw) * T::kRows + rr].x);
       const float base = mm == -INFINITY ? 0.0f : mm;
       float o = 0.0f, ll = 0.0f;
       for (int k = 0; k < kn; ++k) {
         const int wv = k * c.tile_waves + tw;
-        const float2 v = sml[wv][rr];
+        const float2 v = sml[wv * T::kRows + rr];
         const float fade = __builtin_amdgcn_exp2f(v.x - base);
         ll += v.y * fade;
-        o += so[wv][rr * D + d] * fade;
+        o += so[wv * kOut + rr * D + d] * fade;
       }
       const int token = span.first + row / c.group, head = h * c.group + row % c.group;
       const int64_t id = (int64_t)token * c.a.q_heads + head;
@@ -469,15 +550,17 @@ __global__ __launch_bounds__(kTileThreads, D == 256 ? 2 : D == 128 ? 3 : 4) void
   }
 }
 
-// Joins the splits of a row: one wave a row, D / 64 columns a lane.  Where only
-// sequences of few rows have splits, the rows are counted by sequence, else by
-// token.
-template <int D>
+// Joins the splits of a row: kJoin waves a row (1 or 4, for few rows of many
+// splits), D / 64 columns a lane.  Where only sequences of few rows have
+// splits, the rows are counted by sequence, else by token.
+template <int D, int kJoin>
 __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c, int few, int64_t work) {
-  constexpr int kCols = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t waves = (int64_t)gridDim.x * kTileWaves;
-  for (int64_t item = (int64_t)blockIdx.x * kTileWaves + uniform(threadIdx.x >> 6); item < work; item += waves) {
+  constexpr int kCols = D / 64, kRowsEach = kTileWaves / kJoin;
+  __shared__ float sums[kJoin > 1 ? kTileWaves : 1][D];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int part = wave % kJoin;
+  const int64_t step = (int64_t)gridDim.x * kRowsEach;
+  for (int64_t item = (int64_t)blockIdx.x * kRowsEach + wave / kJoin; item < work; item += step) {
     int token, head, splits = c.splits;
     if (few > 0) {
       const int i = (int)(item % few), h = (int)(item / few % c.kv.p.kv_heads), s = (int)(item / few / c.kv.p.kv_heads);
@@ -500,6 +583,15 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c,
     float2 mine[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) mine[k] = lane + 64 * k < splits ? ml[lane + 64 * k] : make_float2(-INFINITY, 0.0f);
+    // this wave's splits, eight under way at a time; the last one again past the end, times 0
+    const int per = (splits + kJoin - 1) / kJoin, first = part * per, last = min(first + per, splits);
+    const float *from = c.part_o + id * c.part_splits * D + lane * kCols;
+    float v[8][kCols];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) __builtin_memcpy(v[k], from + (int64_t)min(k0 + k, splits - 1) * D, sizeof v[k]);
+    };
+    load(first);
     float m = fmaxf(mine[0].x, mine[1].x);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
@@ -512,19 +604,28 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c,
     }
     l = wave_sum(l);
     float o[kCols] = {};
-    const float *from = c.part_o + id * c.part_splits * D + lane * kCols;
-    for (int k0 = 0; k0 < splits; k0 += 8) {
-      float v[8][kCols];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)  // the last one again past the end, times 0
-        __builtin_memcpy(v[k], from + (int64_t)min(k0 + k, splits - 1) * D, sizeof v[k]);
+    for (int k0 = first; k0 < last; k0 += 8) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float all = __shfl(k0 + k < 64 ? fade[0] : fade[1], (k0 + k) & 63);
-        const float by = k0 + k < splits ? all : 0.0f;
+        const float by = k0 + k < last ? all : 0.0f;
 #pragma unroll
         for (int i = 0; i < kCols; ++i) o[i] += by != 0.0f ? v[k][i] * by : 0.0f;
       }
+      if (k0 + 8 < last) load(k0 + 8);
+    }
+    if constexpr (kJoin > 1) {  // one row a workgroup
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) sums[wave][lane * kCols + i] = o[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        o[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) o[i] += sums[k][lane * kCols + i];
+      }
+      __syncthreads();
+      if (part > 0) continue;
     }
     const int64_t at = token * c.a.out_token + head * c.a.out_head + lane * kCols;
 #pragma unroll
@@ -614,7 +715,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
 
 // How the work is split, and where the workspace's parts are.
 struct Plan {
-  int tiles, tile_waves, few_rows, splits, prompt_splits;
+  int tiles, tile_waves, few_rows, waves, splits, prompt_splits;
   bool prompts;
   size_t part_o, part_ml, ml, bytes;
 };
@@ -622,6 +723,7 @@ struct Plan {
 constexpr int64_t kFill = 1024;             // workgroups of tiles that fill the chip (four a CU)
 constexpr int64_t kMaxParts = 1ll << 26;    // floats of partial results
 constexpr int kFewRows = 64;
+constexpr int64_t kShortContext = 1024;
 
 Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_moe_kv_attention_t &a) {
   Plan p;
@@ -641,6 +743,12 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
   const int64_t groups = (min(r.tokens * group, (int64_t)r.seqs * p.few_rows) / (tile_rows * p.tile_waves) + r.seqs) *
                          kv.kv_heads;
   p.splits = (int)max(min(min((kFill + groups - 1) / groups, (cap + 255) / 256), parts), (int64_t)1);
+  // short contexts: one workgroup of more waves is sooner done than splits and their joining
+  p.waves = 4;
+  if (p.splits > 1 && cap <= kShortContext) {
+    p.waves = 8;
+    p.splits = 1;
+  }
   p.prompt_splits = 1;
   if (p.prompts) {
     const int64_t blocks = (r.tokens * group / prompt_rows(kv.head_dim) + r.seqs) * kv.kv_heads;
@@ -665,9 +773,12 @@ unsigned grid_of(int64_t blocks) { return (unsigned)(blocks < (1 << 20) ? blocks
 template <int D, bool kSmallPages>
 hipError_t launch_all(const Call &c, hipStream_t s) {
   const int64_t work = (int64_t)c.rows.seqs * c.kv.p.kv_heads * c.splits * (c.tiles / c.tile_waves);
-  const auto kernel = c.a.type == COLI_MOE_F16 ? kv_attention_kernel<D, true, kSmallPages>
-                                               : kv_attention_kernel<D, false, kSmallPages>;
-  hipError_t e = launch(kernel, dim3(grid_of(work)), dim3(kTileThreads), 0, s, c, work);
+  const bool twice = c.a.type == COLI_MOE_F16;
+  const auto kernel = c.waves == 8 ? twice ? kv_attention_kernel<D, true, kSmallPages, 8>
+                                           : kv_attention_kernel<D, false, kSmallPages, 8>
+                      : twice      ? kv_attention_kernel<D, true, kSmallPages, 4>
+                                   : kv_attention_kernel<D, false, kSmallPages, 4>;
+  hipError_t e = launch(kernel, dim3(grid_of(work)), dim3(64 * c.waves), 0, s, c, work);
   const bool prompts = c.few_rows < 1 << 30;
   if (e == hipSuccess && prompts) e = launch_attention_prompts(c, s);
   if (e == hipSuccess && c.part_splits > 1) {
@@ -677,8 +788,10 @@ hipError_t launch_all(const Call &c, hipStream_t s) {
     const int64_t by_seq = few * c.rows.seqs * c.kv.p.kv_heads, by_token = (int64_t)c.rows.tokens * c.a.q_heads;
     const bool seqs = c.prompt_splits == 1 && by_seq <= by_token;
     const int64_t rows = seqs ? by_seq : by_token;
-    e = launch(kv_attention_join_kernel<D>, dim3(grid_of((rows + kTileWaves - 1) / kTileWaves)), dim3(kTileThreads), 0, s,
-               c, seqs ? (int)few : 0, rows);
+    const bool wide = rows <= 1024 && c.part_splits >= 32;
+    e = launch(wide ? kv_attention_join_kernel<D, kTileWaves> : kv_attention_join_kernel<D, 1>,
+               dim3(grid_of(wide ? rows : (rows + kTileWaves - 1) / kTileWaves)), dim3(kTileThreads), 0, s, c,
+               seqs ? (int)few : 0, rows);
   }
   if (e == hipSuccess && c.a.weights_out) {
     const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
@@ -706,7 +819,7 @@ hipError_t launch_kv_attention(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t
                                void *workspace, hipStream_t s) {
   const Plan p = plan_of(kv, r, a);
   char *ws = static_cast<char *>(workspace);
-  Call c{kv_view(kv), r, a, a.q_heads / kv.kv_heads, p.tiles, p.tile_waves, p.few_rows, p.splits, p.prompt_splits,
+  Call c{kv_view(kv), r, a, a.q_heads / kv.kv_heads, p.tiles, p.tile_waves, p.few_rows, p.waves, p.splits, p.prompt_splits,
          max(p.splits, p.prompt_splits), reinterpret_cast<float *>(ws + p.part_o), reinterpret_cast<float2 *>(ws + p.part_ml),
          a.weights_out ? reinterpret_cast<float2 *>(ws + p.ml) : nullptr};
   switch (kv.head_dim) {

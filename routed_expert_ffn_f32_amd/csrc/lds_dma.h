@@ -26,6 +26,11 @@ __device__ __forceinline__ void dma16v(uint32_t lds, const void *addr) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(addr)
                : "memory", "m0");
 }
+// Four bytes a lane.
+__device__ __forceinline__ void dma4v(uint32_t lds, const void *addr) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(addr)
+               : "memory", "m0");
+}
 template <int N>
 __device__ __forceinline__ void dma_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
