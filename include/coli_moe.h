@@ -756,6 +756,7 @@ typedef struct {
 /* Keys and values [tokens][kv_heads][head_dim] of a call. */
 typedef struct {
   int32_t type;  /* F32, BF16 or F16 */
+  int32_t clear; /* read: 1 sets rows of tokens in no sequence to 0, 0 leaves them as they were; append: 0 */
   void *k;
   int64_t k_token, k_head;
   void *v;

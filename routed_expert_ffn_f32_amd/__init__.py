@@ -132,7 +132,7 @@ class coli_moe_kv_rows_t(ctypes.Structure):
 
 
 class coli_moe_kv_values_t(ctypes.Structure):
-    _fields_ = [("type", ctypes.c_int32), ("k", ctypes.c_void_p), ("k_token", ctypes.c_int64),
+    _fields_ = [("type", ctypes.c_int32), ("clear", ctypes.c_int32), ("k", ctypes.c_void_p), ("k_token", ctypes.c_int64),
                 ("k_head", ctypes.c_int64), ("v", ctypes.c_void_p), ("v_token", ctypes.c_int64),
                 ("v_head", ctypes.c_int64)]
 
@@ -1010,7 +1010,7 @@ class KVCache:
         rows = self._rows(k.shape[0], table, lengths, offsets)
         if rows.tokens and rows.seqs:
             _enqueue("coli_moe_kv_append", self.device, self._kv, rows,
-                     coli_moe_kv_values_t(code, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh))
+                     coli_moe_kv_values_t(code, 0, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh))
             torch._C._increment_version(self._written)
 
     def read(self, tokens: int, table, lengths, offsets=None, dtype=None):
@@ -1021,13 +1021,13 @@ class KVCache:
         dtype = torch.bfloat16 if dtype is None else dtype
         code = _dtype_code(dtype, "dtype")
         rows = self._rows(tokens, table, lengths, offsets)
-        new = self.k_codes.new_empty if offsets is None else self.k_codes.new_zeros
         shape = (tokens, self.heads, self.dim)
+        new = self.k_codes.new_empty if rows.seqs else self.k_codes.new_zeros
         k, v = new(shape, dtype=dtype), new(shape, dtype=dtype)
         if tokens and rows.seqs:
             t, h = self.heads * self.dim, self.dim
             _enqueue("coli_moe_kv_read", self.device, self._kv, rows,
-                     coli_moe_kv_values_t(code, k.data_ptr(), t, h, v.data_ptr(), t, h))
+                     coli_moe_kv_values_t(code, 1, k.data_ptr(), t, h, v.data_ptr(), t, h))
         return k, v
 
     def attention(self, q, table, lengths, offsets=None, scale: float | None = None, window: int = 0, out=None,
@@ -1072,6 +1072,8 @@ class KVCache:
         rows = self._rows(tokens, table, lengths, offsets)
         a = coli_moe_kv_attention_t(heads, code, window, not given, dim ** -0.5 if scale is None else scale,
                                     q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, wp)
+        if not given and not rows.seqs:
+            out.zero_()
         if tokens and rows.seqs:
             lib = _lib or load_library()
             nbytes = lib.coli_moe_kv_attention_workspace_bytes(self._kv, rows, a)

@@ -634,17 +634,51 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c,
   }
 }
 
-template <int D>
-constexpr int kWeightSteps = D == 256 ? 1 : 2;  // steps of keys of a wave
+// Steps of keys that a wave of the weights' kernel takes.
+template <int D, bool kOneTile>
+constexpr int kWeightSteps = kOneTile ? 8 : D == 256 ? 1 : 2;
 
-// weights_out = weights + sums of the softmax weights of each row of the
-// cache, from the scores again and each query's maximum and sum.  A wave
-// takes one step of keys of a sequence's key head and all tiles of queries
-// that see any of them, so that a place has one writer.
-template <int D, bool kSmallPages>
+// Softmax weights of 16 keys, summed over the columns of a tile.
+template <int D>
+__device__ __forceinline__ void add_weights(const KeyRegs<D> &kr, int t, bool there, int key, const Column &q,
+                                            const QueryOperand<D> &f, float2 ml, float share, float4_t &sum) {
+  const float4_t p = scores16<D>(kr, t, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool seen = q.live && q.g == 0 && there && key + i <= q.hi && key + i >= q.lo;
+    sum[i] += seen ? __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], f.scale, -ml.x)) * share : 0.0f;
+  }
+}
+
+// weights_out = weights + v, summed over the 16 columns, for four keys from
+// `key` on: by one lane of each j, those that a query sees.
+__device__ __forceinline__ void store_weights(const Call &c, float4_t v, uint64_t at, int key, int64_t len,
+                                              int64_t start, bool mine) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] += dpp_row_f<kDppQuadXor1>(v[i]);
+    v[i] += dpp_row_f<kDppQuadXor2>(v[i]);
+    v[i] += dpp_row_f<kDppRowRor4>(v[i]);
+    v[i] += dpp_row_f<kDppRowRor8>(v[i]);
+  }
+  if (!mine) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // seen by the last query at least, and by the first one's window
+    if (key + i >= len || (c.a.window && key + i <= start - c.a.window)) continue;
+    c.a.weights_out[at + i] = c.kv.p.weights[at + i] + v[i];
+  }
+}
+
+// The weights of the rows of the cache, from the scores again and each query's
+// maximum and sum.  A wave takes kCount steps of keys of a sequence's key head
+// and all tiles of queries that see any of them, so that a place has one writer.
+// kOneTile: no sequence has more, so the queries are loaded once and the next
+// step's keys while this one's are used.
+template <int D, bool kSmallPages, bool kOneTile>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int chunks, int64_t work) {
   using T = Tile<D>;
-  constexpr int kCount = kWeightSteps<D>, kChunk = kCount * kStepKeys;
+  constexpr int kCount = kWeightSteps<D, kOneTile>, kChunk = kCount * kStepKeys;
   const int lane = threadIdx.x & 63, j = lane >> 4, H = c.kv.p.kv_heads;
   const int64_t waves = (int64_t)gridDim.x * kTileWaves;
   for (int64_t item = (int64_t)blockIdx.x * kTileWaves + uniform(threadIdx.x >> 6); item < work; item += waves) {
@@ -659,55 +693,73 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
                                   : (int64_t)span.n;
     if (i0 >= i1) continue;
     const int32_t *table = c.rows.table + s * c.rows.table_stride;
-    Place<kSmallPages> place[kCount];
-    KeyRegs<D> kr[kCount];
     const int g = (lane & 15) / T::kRows;
-#pragma unroll
-    for (int n = 0; n < kCount; ++n) {
-      place[n] = place_of<D>(c, entries_of<kSmallPages>(c, table, key0 + n * kStepKeys), h, key0 + n * kStepKeys);
-      load_keys<D>(c, place[n], g, kr[n]);
-    }
-    float4_t sum[kCount][2];
-#pragma unroll
-    for (int n = 0; n < 2 * kCount; ++n) sum[n / 2][n % 2] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const int last = (int)((i1 * c.group - 1) / T::kRows);
-    for (int tile = (int)(i0 * c.group / T::kRows); tile <= last; ++tile) {
-      const Column q = column_of<D>(c, span, len, h, tile);
-      const float2 ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
-      QueryOperand<D> f;
+    auto operand = [&](int tile, Column &q, QueryOperand<D> &f, float2 &ml) {
+      q = column_of<D>(c, span, len, h, tile);
+      ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
       load_query<D>(c, q, f);
+    };
+    if constexpr (kOneTile) {
+      const int count = (int)min((len - key0 + kStepKeys - 1) / kStepKeys, (int64_t)kCount);
+      // entries of all steps, a step a lane
+      const Entries<kSmallPages> all = entries_of<kSmallPages>(c, table, key0 + min(lane, count - 1) * kStepKeys);
+      auto place = [&](int n) {
+        Entries<kSmallPages> e;
+#pragma unroll
+        for (int t = 0; t < (kSmallPages ? 2 : 1); ++t) e.entry[t] = __builtin_amdgcn_readlane(all.entry[t], n);
+        return place_of<D>(c, e, h, key0 + n * kStepKeys);
+      };
+      Place<kSmallPages> now = place(0), next = now;
+      KeyRegs<D> kr, ahead;
+      load_keys<D>(c, now, g, kr);
+      Column q;
+      QueryOperand<D> f;
+      float2 ml;
+      operand(0, q, f, ml);
       const float share = ml.y != 0.0f ? 1.0f / ml.y : 0.0f;
+      for (int n = 0; n < count; ++n) {
+        if (n + 1 < count) {
+          next = place(n + 1);
+          load_keys<D>(c, next, g, ahead);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int key = key0 + n * kStepKeys + 16 * t + 4 * j;
+          float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+          add_weights<D>(kr, t, now.ok[t], key, q, f, ml, share, sum);
+          const uint64_t at = now.row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
+          store_weights(c, sum, at, key, len, start, (lane & 15) == t && now.ok[t]);
+        }
+        now = next;
+        kr = ahead;
+      }
+    } else {
+      Place<kSmallPages> place[kCount];
+      KeyRegs<D> kr[kCount];
+      float4_t sum[kCount][2];
+#pragma unroll
+      for (int n = 0; n < kCount; ++n) {
+        place[n] = place_of<D>(c, entries_of<kSmallPages>(c, table, key0 + n * kStepKeys), h, key0 + n * kStepKeys);
+        load_keys<D>(c, place[n], g, kr[n]);
+        sum[n][0] = sum[n][1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      const int last = (int)((i1 * c.group - 1) / T::kRows);
+      for (int tile = (int)(i0 * c.group / T::kRows); tile <= last; ++tile) {
+        Column q;
+        QueryOperand<D> f;
+        float2 ml;
+        operand(tile, q, f, ml);
+        const float share = ml.y != 0.0f ? 1.0f / ml.y : 0.0f;
+#pragma unroll
+        for (int n = 0; n < 2 * kCount; ++n)
+          add_weights<D>(kr[n / 2], n % 2, place[n / 2].ok[n % 2], key0 + 16 * n + 4 * j, q, f, ml, share,
+                         sum[n / 2][n % 2]);
+      }
 #pragma unroll
       for (int n = 0; n < 2 * kCount; ++n) {
-        const float4_t p = scores16<D>(kr[n / 2], n % 2, f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = key0 + 16 * n + 4 * j + i;
-          const bool seen = q.live && q.g == 0 && place[n / 2].ok[n % 2] && key <= q.hi && key >= q.lo;
-          sum[n / 2][n % 2][i] +=
-              seen ? __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], f.scale, -ml.x)) * share : 0.0f;
-        }
-      }
-    }
-    // over the 16 columns: one lane of each j stores four keys
-#pragma unroll
-    for (int n = 0; n < 2 * kCount; ++n) {
-      float4_t v = sum[n / 2][n % 2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += dpp_row_f<kDppQuadXor1>(v[i]);
-        v[i] += dpp_row_f<kDppQuadXor2>(v[i]);
-        v[i] += dpp_row_f<kDppRowRor4>(v[i]);
-        v[i] += dpp_row_f<kDppRowRor8>(v[i]);
-      }
-      if ((lane & 15) != n || !place[n / 2].ok[n % 2]) continue;
-      const uint64_t at = place[n / 2].row[kSmallPages ? n % 2 : 0] + (kSmallPages ? 0 : 16 * (n % 2)) + 4 * j;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t key = key0 + 16 * n + 4 * j + i;
-        // seen by the last query at least, and by the first one's window
-        if (key >= len || (c.a.window && key <= start - c.a.window)) continue;
-        c.a.weights_out[at + i] = c.kv.p.weights[at + i] + v[i];
+        const uint64_t at = place[n / 2].row[kSmallPages ? n % 2 : 0] + (kSmallPages ? 0 : 16 * (n % 2)) + 4 * j;
+        store_weights(c, sum[n / 2][n % 2], at, key0 + 16 * n + 4 * j, len, start,
+                      (lane & 15) == n && place[n / 2].ok[n % 2]);
       }
     }
   }
@@ -725,6 +777,10 @@ constexpr int64_t kMaxParts = 1ll << 26;    // floats of partial results
 constexpr int kFewRows = 64;
 constexpr int64_t kShortContext = 1024;
 
+// On the host, where min and max of HIP's headers are those of int.
+int64_t least_of(int64_t a, int64_t b) { return a < b ? a : b; }
+int64_t most_of(int64_t a, int64_t b) { return a > b ? a : b; }
+
 Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_moe_kv_attention_t &a) {
   Plan p;
   const int64_t group = a.q_heads / kv.kv_heads;
@@ -733,16 +789,16 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
   // sequences of more rows take the prompts' kernel, if there can be any
   p.prompts = r.offsets && most > kFewRows;
   p.few_rows = p.prompts ? kFewRows : 1 << 30;
-  const int tiles = (int)((min(most, (int64_t)p.few_rows) + tile_rows - 1) / tile_rows);
+  const int tiles = (int)((least_of(most, p.few_rows) + tile_rows - 1) / tile_rows);
   p.tile_waves = tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
   p.tiles = (tiles + p.tile_waves - 1) / p.tile_waves * p.tile_waves;
   const int64_t cap = (int64_t)r.table_width * kv.page_size;
   const int64_t out = (int64_t)r.tokens * a.q_heads * kv.head_dim;
-  const int64_t parts = max(min(kMaxParts / max(out, (int64_t)1), (int64_t)128), (int64_t)1);
+  const int64_t parts = most_of(least_of(kMaxParts / most_of(out, 1), 128), 1);
   // workgroups without splits: every sequence's rows, to the tile, need at most this many
-  const int64_t groups = (min(r.tokens * group, (int64_t)r.seqs * p.few_rows) / (tile_rows * p.tile_waves) + r.seqs) *
+  const int64_t groups = (least_of(r.tokens * group, (int64_t)r.seqs * p.few_rows) / (tile_rows * p.tile_waves) + r.seqs) *
                          kv.kv_heads;
-  p.splits = (int)max(min(min((kFill + groups - 1) / groups, (cap + 255) / 256), parts), (int64_t)1);
+  p.splits = (int)most_of(least_of(least_of((kFill + groups - 1) / groups, (cap + 255) / 256), parts), 1);
   // short contexts: one workgroup of more waves is sooner done than splits and their joining
   p.waves = 4;
   if (p.splits > 1 && cap <= kShortContext) {
@@ -752,7 +808,7 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
   p.prompt_splits = 1;
   if (p.prompts) {
     const int64_t blocks = (r.tokens * group / prompt_rows(kv.head_dim) + r.seqs) * kv.kv_heads;
-    p.prompt_splits = (int)max(min(min(768 / blocks, (cap + 511) / 512), parts), (int64_t)1);
+    p.prompt_splits = (int)most_of(least_of(least_of(768 / blocks, (cap + 511) / 512), parts), 1);
   }
   const int64_t rows = (int64_t)r.tokens * a.q_heads;
   const int splits = max(p.splits, p.prompt_splits);
@@ -783,7 +839,7 @@ hipError_t launch_all(const Call &c, hipStream_t s) {
   if (e == hipSuccess && prompts) e = launch_attention_prompts(c, s);
   if (e == hipSuccess && c.part_splits > 1) {
     // rows of sequences of few rows alone, or of all tokens
-    const int64_t few = prompts ? min((int64_t)c.rows.tokens * c.group, (int64_t)c.few_rows)
+    const int64_t few = prompts ? least_of((int64_t)c.rows.tokens * c.group, c.few_rows)
                                 : (c.rows.offsets ? (int64_t)c.rows.tokens : 1) * c.group;
     const int64_t by_seq = few * c.rows.seqs * c.kv.p.kv_heads, by_token = (int64_t)c.rows.tokens * c.a.q_heads;
     const bool seqs = c.prompt_splits == 1 && by_seq <= by_token;
@@ -795,10 +851,12 @@ hipError_t launch_all(const Call &c, hipStream_t s) {
   }
   if (e == hipSuccess && c.a.weights_out) {
     const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
-    const int chunks = (int)((cap + kWeightSteps<D> * kStepKeys - 1) / (kWeightSteps<D> * kStepKeys));
+    const bool one = (c.rows.offsets ? (int64_t)c.rows.tokens : 1) * c.group <= Tile<D>::kRows;
+    const int keys = kStepKeys * (one ? kWeightSteps<D, true> : kWeightSteps<D, false>);
+    const int chunks = (int)((cap + keys - 1) / keys);
     const int64_t items = (int64_t)c.rows.seqs * c.kv.p.kv_heads * chunks;
-    e = launch(kv_weights_kernel<D, kSmallPages>, dim3(grid_of((items + kTileWaves - 1) / kTileWaves)),
-               dim3(kTileThreads), 0, s, c, chunks, items);
+    e = launch(one ? kv_weights_kernel<D, kSmallPages, true> : kv_weights_kernel<D, kSmallPages, false>,
+               dim3(grid_of((items + kTileWaves - 1) / kTileWaves)), dim3(kTileThreads), 0, s, c, chunks, items);
   }
   return e;
 }

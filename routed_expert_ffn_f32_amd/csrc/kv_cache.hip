@@ -11,109 +11,190 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// Code of x for the scale s (> 0, finite): x / s rounded to the nearest, ties
-// to even, held within [-7, 7].  x and s are 24- and 8-bit numbers, so the
-// quotient's rounding to float32 could only put it on a border from just
-// beside it; the remainder d = x - q s is exact and tells.
-__device__ __forceinline__ int code4(float x, float s) {
-  const float y = fminf(fmaxf(x / s, -8.0f), 8.0f);
-  float q = rintf(y);
+// Code of x for the scale s (> 0, finite; r near 1 / s): x / s rounded to the
+// nearest, ties to even, held within [-7, 7].  x r may round to the integer
+// beside the right one; d = x - q s is exact (s has 8 bits) and tells.
+__device__ __forceinline__ int code4(float x, float s, float r) {
+  float q = rintf(x * r);
   const float d = __builtin_fmaf(-q, s, x), h = 0.5f * s;
-  if (fabsf(q) < 8.0f) {
-    if (d > h || (d == h && ((int)q & 1)))
-      q += 1.0f;
-    else if (d < -h || (d == -h && ((int)q & 1)))
-      q -= 1.0f;
-  }
+  if (fabsf(d) > h || (fabsf(d) == h && ((int)q & 1))) q += __builtin_copysignf(1.0f, d);
   return (int)fminf(fmaxf(q, -7.0f), 7.0f);
 }
 
+// Where up to kGroup consecutive tokens from t0 on stand: lane i < kGroup gets
+// token t0 + i's page (-1: none) and slot, and whether a sequence has it.  The
+// first token's sequence is searched, the others' are counted from there, so
+// that the lookups of all are under way together.
+constexpr int kGroup = 8;
+struct Located {
+  int page, slot;
+  bool in_seq;
+};
+
+__device__ __forceinline__ Located locate(const KvView &kv, const coli_moe_kv_rows_t &r, int t0) {
+  const int lane = threadIdx.x & 63, t = min(t0 + min(lane, kGroup - 1), r.tokens - 1);
+  int s = t, first = t, last = t + 1, len = 0;  // the token's sequence, its bounds and length
+  if (!r.offsets) {
+    len = r.lengths[s];
+  } else if (r.seqs < 64) {
+    // every bound and length at once, a lane each
+    const int bound = r.offsets[min(lane, r.seqs)], lens = r.lengths[min(lane, r.seqs - 1)];
+    s = 0;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      const int k = __popcll(__ballot(lane < r.seqs && bound <= min(t0 + i, r.tokens - 1)));
+      if (lane == i) s = max(k - 1, 0);
+    }
+    first = __shfl(bound, s);
+    last = __shfl(bound, s + 1);
+    len = __shfl(lens, s);
+  } else {
+    // the last sequence that starts at or before t0, 0 for none
+    int lo = 0, n = r.seqs;
+    while (n > 1) {
+      const int step = (n + 63) / 64, i = lane * step;
+      const int k = __popcll(__ballot(i < n && r.offsets[lo + i] <= t0));
+      lo += max(k - 1, 0) * step;
+      n = k == 0 ? 1 : min(step, n - (k - 1) * step);
+    }
+    lo = uniform(lo);
+    const int bound = r.offsets[min(lo + 1 + lane, r.seqs)];
+    s = lo;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      // sequences that start at or before the token, among the next 64
+      const int k = __popcll(__ballot(lo + 1 + lane < r.seqs && bound <= min(t0 + i, r.tokens - 1)));
+      if (lane == i) s = lo + k;
+    }
+    // more than 64 sequences begin within the group (all but a few are empty): on from there
+    if (s == lo + 64)
+      while (s + 1 < r.seqs && r.offsets[s + 1] <= t) ++s;
+    first = r.offsets[s], last = r.offsets[s + 1], len = r.lengths[s];
+  }
+  Located l;
+  l.in_seq = t0 + lane < r.tokens && lane < kGroup && first <= t && t < last;
+  const int64_t row = (int64_t)len - (min(last, r.tokens) - t);
+  l.page = l.in_seq ? row_page(kv, r.table + s * r.table_stride, r.table_width, row) : -1;
+  l.slot = (int)row & (kv.p.page_size - 1);
+  return l;
+}
+
 // Eight columns a thread, eight threads a scale: a wave takes eight groups of
-// one token at a time, of its keys and then its values.
+// one token at a time, kUnder such pieces of its tokens under way together.
+template <int kType, int kUnder>
 __global__ __launch_bounds__(kRowThreads) void kv_append_kernel(KvView kv, coli_moe_kv_rows_t r,
                                                                 coli_moe_kv_values_t a, int parts) {
   const int lane = threadIdx.x & 63, D = kv.p.head_dim, ng = D / kKvGroup;
-  const int groups = 2 * kv.p.kv_heads * ng;
+  const int groups = 2 * kv.p.kv_heads * ng, steps = (groups + 7) / 8;
   const int64_t waves = (int64_t)gridDim.x * (kRowThreads / 64);
-  for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + uniform(threadIdx.x >> 6);
-       w < (int64_t)r.tokens * parts; w += waves) {
-    const int t = (int)(w / parts), part = (int)(w % parts);
-    const int s = find_seq(r, t);
-    if (s < 0) continue;
-    const int64_t row = token_row(r, s, t);
-    const int page = row_page(kv, r.table + s * r.table_stride, r.table_width, row);
-    if (page < 0) continue;
-    const int slot = (int)row & (kv.p.page_size - 1);
-    for (int g0 = part * 8; g0 < groups; g0 += parts * 8) {
-      const int gi = g0 + lane / 8;
-      const bool live = gi < groups;  // all lanes take part in the maximum
-      const bool is_v = gi >= groups / 2;
-      const int hg = is_v ? gi - groups / 2 : gi, h = hg / ng, g = hg % ng;
-      const int col = g * kKvGroup + (lane & 7) * 8;
-      float x[8];
-      if (live)
-        unpack8(a.type, is_v ? load_raw8(a.v, a.type, t * a.v_token + h * a.v_head + col)
-                             : load_raw8(a.k, a.type, t * a.k_token + h * a.k_head + col), x);
-      else
-        for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-      // as integers: Inf and NaN are above every finite value
-      uint32_t top = 0;
+  const int64_t work = (int64_t)((r.tokens + kGroup - 1) / kGroup) * parts;
+  for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + uniform(threadIdx.x >> 6); w < work; w += waves) {
+    const int t0 = (int)(w / parts) * kGroup, count = min(kGroup, r.tokens - t0);
+    Located at;
+    bool located = false;
+    for (int n0 = (int)(w % parts) * kUnder; n0 < count * steps; n0 += parts * kUnder) {
+      Raw8 raw[kUnder];
+      // which group a lane has of piece n0 + u: its token, and 0 .. groups - 1 of keys and values
+      auto group_of = [&](int u) { return (n0 + u) % steps * 8 + lane / 8; };
+      auto token_of = [&](int u) { return min((n0 + u) / steps, count - 1); };
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-      top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 4));
-      if (!live) continue;
-      // the quotient in float32 never falls on a bfloat16 border that the exact one is not on
-      const uint16_t sb = top >= 0x7F800000u ? 0x7FC0 : to_bf16(__uint_as_float(top) / 7.0f);
-      const float sc = from_bf16(sb);
-      uint32_t codes = 0;
-      if (sc > 0.0f) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) codes |= (uint32_t)(code4(x[j], sc) & 15) << (4 * j);
+      for (int u = 0; u < kUnder; ++u) {
+        const int gi = min(group_of(u), groups - 1), is_v = gi >= groups / 2, hg = gi - (is_v ? groups / 2 : 0);
+        const int64_t t = t0 + token_of(u);
+        const int h = hg / ng, col = hg % ng * kKvGroup + (lane & 7) * 8;
+        raw[u] = load_raw8(is_v ? a.v : a.k, kType,
+                           is_v ? t * a.v_token + h * a.v_head + col : t * a.k_token + h * a.k_head + col);
       }
-      const int64_t ph = (int64_t)page * kv.p.kv_heads + h;
-      uint8_t *cp = (is_v ? kv.p.v_codes : kv.p.k_codes) + (ph * kv.p.page_size + slot) * (D / 2) + col / 2;
-      *reinterpret_cast<uint32_t *>(cp) = codes;
-      if ((lane & 7) == 0) {
-        (is_v ? kv.p.v_scales : kv.p.k_scales)[(ph * ng + g) * kv.p.page_size + slot] = sb;
-        if (kv.p.weights && g == 0 && !is_v) kv.p.weights[ph * kv.p.page_size + slot] = 0.0f;
+      // looked up while the first values are on their way
+      if (!located) at = locate(kv, r, t0);
+      located = true;
+#pragma unroll
+      for (int u = 0; u < kUnder; ++u) {
+        const int token = token_of(u);
+        const int page = __builtin_amdgcn_readlane(at.page, token), slot = __builtin_amdgcn_readlane(at.slot, token);
+        float x[8];
+        unpack8(kType, raw[u], x);
+        // as integers: Inf and NaN are above every finite value
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+        top = max(top, (uint32_t)dpp_i<kDppQuadXor1>((int)top));
+        top = max(top, (uint32_t)dpp_i<kDppQuadXor2>((int)top));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 4));
+        const int gi = group_of(u);
+        if (gi >= groups || n0 + u >= count * steps || page < 0) continue;
+        const bool is_v = gi >= groups / 2;
+        const int hg = is_v ? gi - groups / 2 : gi, h = hg / ng, g = hg % ng, col = g * kKvGroup + (lane & 7) * 8;
+        // the quotient in float32 never falls on a bfloat16 border that the exact one is not on
+        const uint16_t sb = top >= 0x7F800000u ? 0x7FC0 : to_bf16(__uint_as_float(top) / 7.0f);
+        float sc = from_bf16(sb);
+        uint32_t codes = 0;
+        if (sc > 0.0f) {
+          // away from the scales whose reciprocal overflows
+          const float up = sc < 0x1p-100f ? 0x1p64f : 1.0f;
+          sc *= up;
+          const float rc = __builtin_amdgcn_rcpf(sc);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) codes |= (uint32_t)(code4(x[j] * up, sc, rc) & 15) << (4 * j);
+        }
+        const uint64_t row = code_row(kv, page, h, slot);
+        *reinterpret_cast<uint32_t *>((is_v ? kv.p.v_codes : kv.p.k_codes) + row * (D / 2) + col / 2) = codes;
+        if ((lane & 7) == 0) {
+          (is_v ? kv.p.v_scales : kv.p.k_scales)[(((int64_t)page * kv.p.kv_heads + h) * ng + g) * kv.p.page_size +
+                                                 slot] = sb;
+          if (kv.p.weights && g == 0 && !is_v) kv.p.weights[row] = 0.0f;
+        }
       }
     }
   }
 }
 
-// Eight columns a thread; a wave takes 512 columns of one token at a time.
+// Eight columns a thread; a wave takes 512 columns of one token at a time,
+// kUnder such pieces of its tokens under way together.
+template <int kType, int kUnder>
 __global__ __launch_bounds__(kRowThreads) void kv_read_kernel(KvView kv, coli_moe_kv_rows_t r, coli_moe_kv_values_t a,
                                                               int parts) {
   const int lane = threadIdx.x & 63, D = kv.p.head_dim, ng = D / kKvGroup;
-  const int units = 2 * kv.p.kv_heads * (D / 8);
+  const int units = 2 * kv.p.kv_heads * (D / 8), steps = (units + 63) / 64;
   const int64_t waves = (int64_t)gridDim.x * (kRowThreads / 64);
-  for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + uniform(threadIdx.x >> 6);
-       w < (int64_t)r.tokens * parts; w += waves) {
-    const int t = (int)(w / parts), part = (int)(w % parts);
-    const int s = find_seq(r, t);
-    if (s < 0) continue;
-    const int64_t row = token_row(r, s, t);
-    const int page = row_page(kv, r.table + s * r.table_stride, r.table_width, row);
-    const int slot = (int)row & (kv.p.page_size - 1);
-    for (int u = part * 64 + lane; u < units; u += parts * 64) {
-      const bool is_v = u >= units / 2;
-      const int hu = is_v ? u - units / 2 : u, h = hu / (D / 8), col = hu % (D / 8) * 8;
-      float x[8] = {};
-      if (page >= 0) {
-        const int64_t ph = (int64_t)page * kv.p.kv_heads + h;
-        const uint8_t *cp = (is_v ? kv.p.v_codes : kv.p.k_codes) + (ph * kv.p.page_size + slot) * (D / 2) + col / 2;
-        const int c = *reinterpret_cast<const int *>(cp);
-        const float sc = from_bf16(
-            (is_v ? kv.p.v_scales : kv.p.k_scales)[(ph * ng + col / kKvGroup) * kv.p.page_size + slot]);
+  const int64_t work = (int64_t)((r.tokens + kGroup - 1) / kGroup) * parts;
+  for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 64) + uniform(threadIdx.x >> 6); w < work; w += waves) {
+    const int t0 = (int)(w / parts) * kGroup, count = min(kGroup, r.tokens - t0);
+    const Located at = locate(kv, r, t0);
+    for (int n0 = (int)(w % parts) * kUnder; n0 < count * steps; n0 += parts * kUnder) {
+      int code[kUnder];
+      uint16_t scale[kUnder];
+      auto unit_of = [&](int u) { return (n0 + u) % steps * 64 + lane; };
+      auto token_of = [&](int u) { return min((n0 + u) / steps, count - 1); };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = (float)((c << (28 - 4 * j)) >> 28) * sc;
+      for (int u = 0; u < kUnder; ++u) {
+        const int token = token_of(u), page = max(__builtin_amdgcn_readlane(at.page, token), 0);
+        const int slot = __builtin_amdgcn_readlane(at.slot, token);
+        const int n = min(unit_of(u), units - 1), is_v = n >= units / 2, hu = n - (is_v ? units / 2 : 0);
+        const int h = hu / (D / 8), col = hu % (D / 8) * 8;
+        code[u] = *reinterpret_cast<const int *>((is_v ? kv.p.v_codes : kv.p.k_codes) +
+                                                 code_row(kv, page, h, slot) * (D / 2) + col / 2);
+        scale[u] = (is_v ? kv.p.v_scales : kv.p.k_scales)[(((int64_t)page * kv.p.kv_heads + h) * ng + col / kKvGroup) *
+                                                              kv.p.page_size + slot];
       }
-      if (is_v)
-        store8(a.v, a.type, t * a.v_token + h * a.v_head + col, x);
-      else
-        store8(a.k, a.type, t * a.k_token + h * a.k_head + col, x);
+#pragma unroll
+      for (int u = 0; u < kUnder; ++u) {
+        const int token = token_of(u), page = __builtin_amdgcn_readlane(at.page, token);
+        const bool in_seq = __builtin_amdgcn_readlane((int)at.in_seq, token);
+        const int n = unit_of(u);
+        if (n >= units || n0 + u >= count * steps || !(in_seq || a.clear)) continue;
+        const bool is_v = n >= units / 2;
+        const int hu = is_v ? n - units / 2 : n, h = hu / (D / 8), col = hu % (D / 8) * 8;
+        const float sc = page >= 0 ? from_bf16(scale[u]) : 0.0f;
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = page >= 0 ? (float)((code[u] << (28 - 4 * j)) >> 28) * sc : 0.0f;
+        const int64_t t = t0 + token;
+        if (is_v)
+          store8(a.v, kType, t * a.v_token + h * a.v_head + col, x);
+        else
+          store8(a.k, kType, t * a.k_token + h * a.k_head + col, x);
+      }
     }
   }
 }
@@ -123,6 +204,7 @@ __global__ __launch_bounds__(kRowThreads) void kv_read_kernel(KvView kv, coli_mo
 // ---------------------------------------------------------------------------
 
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectRows = 32768;  // rows whose keys LDS holds; those beyond are looked up each time
 
 // Weights in an order of unsigned integers: larger weights larger, NaN above
 // everything, -0 as 0.
@@ -135,40 +217,23 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
 __device__ __forceinline__ uint32_t row_key(const KvView &kv, const int32_t *table, int width, int h, int row) {
   const int page = row_page(kv, table, width, row);
   if (page < 0) return rank_key(0.0f);
-  return rank_key(kv.p.weights[(((int64_t)page * kv.p.kv_heads + h) << kv.shift) + (row & (kv.p.page_size - 1))]);
-}
-
-// Sum of v over the threads before this one, and over all (*total).
-__device__ __forceinline__ int block_scan(int v, int *lds, int *total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int x = v;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 63) lds[wave] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < kSelectThreads / 64; ++i) {
-    if (i < wave) before += lds[i];
-    all += lds[i];
-  }
-  __syncthreads();
-  *total = all;
-  return before + x - v;
+  return rank_key(kv.p.weights[code_row(kv, page, h, row & (kv.p.page_size - 1))]);
 }
 
 // The rows that one sequence's key head keeps: the c-th largest key of the
-// middle rows is found digit by digit (8 bits, largest first), then rows in
-// order are kept while they are first, recent, above it, or among the first
-// of those equal to it.
+// middle rows is found digit by digit (8 bits, largest first), then rows are
+// kept while they are first, recent, above it, or among the first of those
+// equal to it; each thread has rows side by side, so one sum over the
+// workgroup places them.  Bound by the latency of its steps: every wave adds up
+// a digit's counts for itself, so that a digit is one barrier.
 __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(KvView kv, coli_moe_kv_rows_t r,
                                                                    coli_moe_kv_evict_t a) {
-  __shared__ int hist[256];
-  __shared__ int scan[kSelectThreads / 64];
-  __shared__ int chosen[2];  // digit, rows still to take below it
-  const int H = kv.p.kv_heads, tid = threadIdx.x;
+  constexpr int kWaves = kSelectThreads / 64;
+  __shared__ uint32_t keys[kSelectRows];
+  __shared__ int hist[4][256];
+  __shared__ int2 sums[kWaves];
+  static_assert(4 * 256 == kSelectThreads, "a count a thread");
+  const int H = kv.p.kv_heads, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int64_t w = blockIdx.x; w < (int64_t)r.seqs * H; w += gridDim.x) {
     const int s = (int)(w / H), h = (int)(w % H);
     const int32_t *table = r.table + s * r.table_stride;
@@ -184,46 +249,84 @@ __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(KvView kv, co
     }
     const int lo = a.first, hi = len - a.recent;
     int need = keep - a.first - a.recent;  // of the middle rows, 0 .. hi - lo
-    uint32_t key = 0, known = 0;           // digits found so far, and their mask
-    if (need > 0) {
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
-        __syncthreads();
+    const bool any = need > 0;
+    uint32_t key = 0, known = 0;  // digits found so far, and their mask
+    __syncthreads();              // of the item before, all is read
+    auto key_of = [&](int row) {
+      return row - lo < kSelectRows ? keys[row - lo] : row_key(kv, table, r.table_width, h, row);
+    };
+    if (any) {
+      (&hist[0][0])[tid] = 0;
+      // four lookups under way together
+      const int held = min(hi - lo, kSelectRows);
+      for (int i0 = tid; i0 < held; i0 += 4 * kSelectThreads) {
+        uint32_t k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          k[u] = row_key(kv, table, r.table_width, h, lo + min(i0 + u * kSelectThreads, held - 1));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (i0 + u * kSelectThreads < held) keys[i0 + u * kSelectThreads] = k[u];
+      }
+      __syncthreads();
+      for (int n = 0; n < 4; ++n) {
+        const int shift = 24 - 8 * n;
         for (int row = lo + tid; row < hi; row += kSelectThreads) {
-          const uint32_t k = row_key(kv, table, r.table_width, h, row);
-          if ((k & known) == key) atomicAdd(&hist[(k >> shift) & 255], 1);
+          const uint32_t k = key_of(row);
+          if ((k & known) == key) atomicAdd(&hist[n][(k >> shift) & 255], 1);
         }
         __syncthreads();
-        // rows in digits above d, from the largest digit down
-        const int v = tid < 256 ? hist[255 - tid] : 0;
-        int total;
-        const int before = block_scan(v, scan, &total);
-        if (tid < 256 && before < need && before + v >= need) {
-          chosen[0] = 255 - tid;
-          chosen[1] = need - before;
+        // digits from the largest down, four a lane, and the rows in them and above
+        int count[4], upto = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) upto += count[i] = hist[n][255 - 4 * lane - i];
+        const int own = upto;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const int y = __shfl_up(upto, d);
+          if (lane >= d) upto += y;
         }
-        __syncthreads();
-        key |= (uint32_t)chosen[0] << shift;
+        const int at = __builtin_ctzll(__ballot(upto >= need) | 1ull << 63);
+        int digit = 255 - 4 * lane, rest = need - (upto - own);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (digit == 255 - 4 * lane - i && rest > count[i]) {
+            rest -= count[i];
+            --digit;
+          }
+        key |= (uint32_t)__builtin_amdgcn_readlane(digit, at) << shift;
         known |= 255u << shift;
-        need = chosen[1];
-        __syncthreads();
+        need = __builtin_amdgcn_readlane(rest, at);
       }
     }
-    // need: rows equal to `key` still to take, in order (0 when no middle row is kept)
-    const bool any = keep > a.first + a.recent;
-    int out = 0, equal = 0;
-    for (int base = 0; base < len; base += kSelectThreads) {
-      const int row = base + tid;
+    // need: rows equal to `key` still to take, in order
+    const int each = (len + kSelectThreads - 1) / kSelectThreads;
+    const int from = min(tid * each, len), to = min(from + each, len);
+    int same = 0, above = 0;
+    for (int row = from; row < to; ++row) {
       const bool middle = row >= lo && row < hi;
-      const uint32_t k = middle && any ? row_key(kv, table, r.table_width, h, row) : 0;
-      const int same = middle && any && k == key ? 1 : 0;
-      int sames, takes;
-      const int rank = equal + block_scan(same, scan, &sames);
-      const int take = row < len && (!middle || (any && (k > key || (same && rank < need)))) ? 1 : 0;
-      const int at = out + block_scan(take, scan, &takes);
-      if (take) kept[at] = row;
-      equal += sames;
-      out += takes;
+      const uint32_t k = middle && any ? key_of(row) : 0;
+      same += middle && any && k == key ? 1 : 0;
+      above += !middle || (any && k > key) ? 1 : 0;
+    }
+    // of the threads before this one
+    int rank = same, at = above;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int x = __shfl_up(rank, d), y = __shfl_up(at, d);
+      if (lane >= d) rank += x, at += y;
+    }
+    if (lane == 63) sums[wave] = make_int2(rank, at);
+    __syncthreads();
+    rank -= same, at -= above;
+    for (int i = 0; i < wave; ++i) rank += sums[i].x, at += sums[i].y;
+    at += min(rank, need);  // those equal that were taken
+    for (int row = from; row < to; ++row) {
+      const bool middle = row >= lo && row < hi;
+      const uint32_t k = middle && any ? key_of(row) : 0;
+      const bool equal = middle && any && k == key;
+      if (!middle || (any && k > key) || (equal && rank < need)) kept[at++] = row;
+      rank += equal ? 1 : 0;
     }
   }
 }
@@ -262,22 +365,52 @@ __global__ __launch_bounds__(kRowThreads) void kv_move_kernel(KvView kv, coli_mo
 
 unsigned grid_of(int64_t blocks) { return (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20); }
 
+// Waves of a token group's pieces: one piece each where that does not fill the
+// chip, else as many waves of four pieces as do, or one.
+struct Parts {
+  int under, parts;
+};
+Parts parts_of(int tokens, int steps) {
+  const int64_t groups = (tokens + kGroup - 1) / kGroup, fill = 8192 / groups;
+  const int pieces = (tokens < kGroup ? tokens : kGroup) * steps, fours = (pieces + 3) / 4;
+  if (pieces <= fill) return {1, pieces};
+  return {4, (int)(fill < 1 ? 1 : fours < fill ? fours : fill)};
+}
+
+using RowsKernel = void (*)(KvView, coli_moe_kv_rows_t, coli_moe_kv_values_t, int);
+
+template <int kUnder>
+RowsKernel append_of(int type) {
+  return type == COLI_MOE_F32    ? kv_append_kernel<COLI_MOE_F32, kUnder>
+         : type == COLI_MOE_BF16 ? kv_append_kernel<COLI_MOE_BF16, kUnder>
+                                 : kv_append_kernel<COLI_MOE_F16, kUnder>;
+}
+template <int kUnder>
+RowsKernel read_of(int type) {
+  return type == COLI_MOE_F32    ? kv_read_kernel<COLI_MOE_F32, kUnder>
+         : type == COLI_MOE_BF16 ? kv_read_kernel<COLI_MOE_BF16, kUnder>
+                                 : kv_read_kernel<COLI_MOE_F16, kUnder>;
+}
+
+hipError_t launch_rows(RowsKernel kernel, const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r,
+                       const coli_moe_kv_values_t &a, const Parts &p, hipStream_t s) {
+  const int64_t waves = (int64_t)((r.tokens + kGroup - 1) / kGroup) * p.parts;
+  return launch(kernel, dim3(grid_of((waves + kRowThreads / 64 - 1) / (kRowThreads / 64))), dim3(kRowThreads), 0, s,
+                kv_view(kv), r, a, p.parts);
+}
+
 }  // namespace
 
 hipError_t launch_kv_append(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_moe_kv_values_t &a,
                             hipStream_t s) {
-  const int groups = 2 * kv.kv_heads * (kv.head_dim / kKvGroup), steps = (groups + 7) / 8;
-  const int parts = r.tokens >= 2048 ? 1 : steps;  // few tokens: a wave per eight groups
-  const int64_t blocks = ((int64_t)r.tokens * parts + kRowThreads / 64 - 1) / (kRowThreads / 64);
-  return launch(kv_append_kernel, dim3(grid_of(blocks)), dim3(kRowThreads), 0, s, kv_view(kv), r, a, parts);
+  const Parts p = parts_of(r.tokens, (2 * kv.kv_heads * (kv.head_dim / kKvGroup) + 7) / 8);
+  return launch_rows(p.under == 1 ? append_of<1>(a.type) : append_of<4>(a.type), kv, r, a, p, s);
 }
 
 hipError_t launch_kv_read(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_moe_kv_values_t &a,
                           hipStream_t s) {
-  const int units = 2 * kv.kv_heads * (kv.head_dim / 8), steps = (units + 63) / 64;
-  const int parts = r.tokens >= 2048 ? 1 : steps;
-  const int64_t blocks = ((int64_t)r.tokens * parts + kRowThreads / 64 - 1) / (kRowThreads / 64);
-  return launch(kv_read_kernel, dim3(grid_of(blocks)), dim3(kRowThreads), 0, s, kv_view(kv), r, a, parts);
+  const Parts p = parts_of(r.tokens, (2 * kv.kv_heads * (kv.head_dim / 8) + 63) / 64);
+  return launch_rows(p.under == 1 ? read_of<1>(a.type) : read_of<4>(a.type), kv, r, a, p, s);
 }
 
 hipError_t launch_kv_evict(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_moe_kv_evict_t &a,

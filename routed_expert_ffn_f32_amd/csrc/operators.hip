@@ -197,7 +197,8 @@ int kv_values_check(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *r, const 
   if (code == COLI_MOE_OK) code = kv_rows_check(kv, r);
   if (code == COLI_MOE_OK) code = kv_tokens_check(r);
   if (code != COLI_MOE_OK) return code;
-  if (!a || !coli::float_type(a->type) || !kv_pointers_ok(kv) || !kv_row_pointers_ok(r)) return COLI_MOE_EARG;
+  if (!a || !coli::float_type(a->type) || a->clear < 0 || a->clear > (written ? 1 : 0)) return COLI_MOE_EARG;
+  if (!kv_pointers_ok(kv) || !kv_row_pointers_ok(r)) return COLI_MOE_EARG;
   if (r->tokens == 0) return COLI_MOE_OK;
   if (!heads_ok(a->k, a->type, r->tokens, a->k_token, kv->kv_heads, a->k_head, kv->head_dim, written) ||
       !heads_ok(a->v, a->type, r->tokens, a->v_token, kv->kv_heads, a->v_head, kv->head_dim, written))
