@@ -191,9 +191,9 @@ __global__ __launch_bounds__(kRowThreads) void kv_read_kernel(KvView kv, coli_mo
         for (int j = 0; j < 8; ++j) x[j] = page >= 0 ? (float)((code[u] << (28 - 4 * j)) >> 28) * sc : 0.0f;
         const int64_t t = t0 + token;
         if (is_v)
-          store8(a.v, kType, t * a.v_token + h * a.v_head + col, x);
+          store8<(kUnder > 1)>(a.v, kType, t * a.v_token + h * a.v_head + col, x);
         else
-          store8(a.k, kType, t * a.k_token + h * a.k_head + col, x);
+          store8<(kUnder > 1)>(a.k, kType, t * a.k_token + h * a.k_head + col, x);
       }
     }
   }
@@ -371,7 +371,7 @@ struct Parts {
   int under, parts;
 };
 Parts parts_of(int tokens, int steps) {
-  const int64_t groups = (tokens + kGroup - 1) / kGroup, fill = 8192 / groups;
+  const int64_t groups = (tokens + kGroup - 1) / kGroup, fill = 16384 / groups;
   const int pieces = (tokens < kGroup ? tokens : kGroup) * steps, fours = (pieces + 3) / 4;
   if (pieces <= fill) return {1, pieces};
   return {4, (int)(fill < 1 ? 1 : fours < fill ? fours : fill)};

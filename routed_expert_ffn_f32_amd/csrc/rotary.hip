@@ -29,6 +29,7 @@ struct RotaryShape {
   int units;                   // of all heads of a token
 };
 
+template <bool kPast>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_t a, RotaryShape sh, int split) {
   __shared__ float2 cs[kMaxPairs];
   const int half = a.part / 2;
@@ -49,7 +50,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_
       if (k >= sh.pair_units) {
         const int c = a.part + 8 * (k - sh.pair_units), n = a.dim - c;
         unpack8(a.type, load_raw8(a.x, a.type, x + c, n), v);
-        store8(a.out, a.type, o + c, n, v);
+        store8<kPast>(a.out, a.type, o + c, n, v);
       } else if (a.interleaved) {
         const int c = 8 * k, n = a.part - c;
         unpack8(a.type, load_raw8(a.x, a.type, x + c, n), v);
@@ -59,7 +60,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_
           y[j] = __builtin_fmaf(v[j], e.x, -(v[j + 1] * e.y));
           y[j + 1] = __builtin_fmaf(v[j], e.y, v[j + 1] * e.x);
         }
-        store8(a.out, a.type, o + c, n, y);
+        store8<kPast>(a.out, a.type, o + c, n, y);
       } else {
         const int c = 8 * k, n = half - c;
         float b[8], z[8];
@@ -72,8 +73,8 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_
           y[j] = __builtin_fmaf(v[j], e.x, -(b[j] * e.y));
           z[j] = __builtin_fmaf(v[j], e.y, b[j] * e.x);
         }
-        store8(a.out, a.type, o + c, n, y);
-        store8(a.out, a.type, o + half + c, n, z);
+        store8<kPast>(a.out, a.type, o + c, n, y);
+        store8<kPast>(a.out, a.type, o + half + c, n, z);
       }
     }
   }
@@ -92,7 +93,7 @@ hipError_t launch_rotary(const coli_moe_rotary_t &a, hipStream_t s) {
   const int blocks = (sh.units + kRotaryThreads - 1) / kRotaryThreads;
   const int split = a.tokens >= 1024 ? 1 : blocks < 8 ? blocks : 8;
   const int64_t work = (int64_t)a.tokens * split;
-  return launch(rotary_kernel, dim3((unsigned)(work < (1 << 20) ? work : 1 << 20)), dim3(kRotaryThreads), 0, s, a, sh,
+  return launch(split == 1 ? rotary_kernel<true> : rotary_kernel<false>, dim3((unsigned)(work < (1 << 20) ? work : 1 << 20)), dim3(kRotaryThreads), 0, s, a, sh,
                 split);
 }
 
