@@ -349,11 +349,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
     const SeqSpan span = seq_span(c.rows, s);
     const int rows = span.n * c.group, r0 = tg * c.tile_waves * T::kRows;
     if (r0 >= rows || rows > c.few_rows) continue;
+    // a sequence of fewer rows than the call has room for: its keys are dealt to more waves
+    const int tile_waves = rows <= T::kRows ? 1 : rows <= 2 * T::kRows ? min(c.tile_waves, 2) : c.tile_waves;
     const int64_t len = c.rows.lengths[s];
     const int32_t *table = c.rows.table + s * c.rows.table_stride;
-    const int tile = tg * c.tile_waves + wave % c.tile_waves;
-    const int kw = wave / c.tile_waves, kn = kWaves / c.tile_waves;
-    const int r1 = min(r0 + c.tile_waves * T::kRows, rows) - 1;
+    const int tile = tg * c.tile_waves + wave % tile_waves;
+    const int kw = wave / tile_waves, kn = kWaves / tile_waves;
+    const int r1 = min(r0 + tile_waves * T::kRows, rows) - 1;
     const KeyRange range = keys_of_rows(c, span, len, r0, r1);
     // keys are numbers up to 2^30
     const int begin = (int)min(range.lo, (int64_t)1 << 30) & ~(kStepKeys - 1), end = (int)max(range.hi, (int64_t)0);
@@ -522,16 +524,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
         if (d / kKvGroup == q.g) so[wave * kOut + r * D + d] = acc[i][e] * down;
       }
     __syncthreads();
-    for (int e = tid; e < c.tile_waves * kOut; e += kThreads) {
+    for (int e = tid; e < tile_waves * kOut; e += kThreads) {
       const int tw = e / kOut, rr = e % kOut / D, d = e % D;
       const int row = r0 + tw * T::kRows + rr;
       if (row >= rows) continue;
       float mm = -INFINITY;
-      for (int k = 0; k < kn; ++k) mm = fmaxf(mm, sml[(k * c.tile_waves + tw) * T::kRows + rr].x);
+      for (int k = 0; k < kn; ++k) mm = fmaxf(mm, sml[(k * tile_waves + tw) * T::kRows + rr].x);
       const float base = mm == -INFINITY ? 0.0f : mm;
       float o = 0.0f, ll = 0.0f;
       for (int k = 0; k < kn; ++k) {
-        const int wv = k * c.tile_waves + tw;
+        const int wv = k * tile_waves + tw;
         const float2 v = sml[wv * T::kRows + rr];
         const float fade = __builtin_amdgcn_exp2f(v.x - base);
         ll += v.y * fade;
@@ -650,24 +652,36 @@ __device__ __forceinline__ void add_weights(const KeyRegs<D> &kr, int t, bool th
   }
 }
 
-// weights_out = weights + v, summed over the 16 columns, for four keys from
-// `key` on: by one lane of each j, those that a query sees.
-__device__ __forceinline__ void store_weights(const Call &c, float4_t v, uint64_t at, int key, int64_t len,
-                                              int64_t start, bool mine) {
+// Sums of two steps' halves over the 16 columns: lane 16 j + t (t 0 or 1) gets
+// those of the four keys of its j of half t.
+__device__ __forceinline__ float4_t fold_weights(float4_t v0, float4_t v1) {
+  const bool odd = threadIdx.x & 1;
+  float4_t v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] += dpp_row_f<kDppQuadXor1>(v[i]);
+    // the even lanes gather half 0, the odd ones half 1
+    const float keep = odd ? v1[i] : v0[i], give = odd ? v0[i] : v1[i];
+    v[i] = keep + dpp_row_f<kDppQuadXor1>(give);
     v[i] += dpp_row_f<kDppQuadXor2>(v[i]);
     v[i] += dpp_row_f<kDppRowRor4>(v[i]);
     v[i] += dpp_row_f<kDppRowRor8>(v[i]);
   }
-  if (!mine) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // seen by the last query at least, and by the first one's window
-    if (key + i >= len || (c.a.window && key + i <= start - c.a.window)) continue;
-    c.a.weights_out[at + i] = c.kv.p.weights[at + i] + v[i];
+  return v;
+}
+
+// weights_out = was + v for four keys from `key` on, those that a query sees:
+// the last query at least, and the first one's window.
+__device__ __forceinline__ void store_weights(const Call &c, float4_t was, float4_t v, uint64_t at, int key,
+                                              int64_t len, int64_t start) {
+  const int64_t lo = c.a.window ? start - c.a.window : -1;
+  float *out = c.a.weights_out + at;
+  if (__builtin_expect(key + 3 < len && key > lo, 1)) {
+    *reinterpret_cast<float4_t *>(out) = was + v;
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (key + i < len && key + i > lo) out[i] = was[i] + v[i];
 }
 
 // The weights of the rows of the cache, from the scores again and each query's
@@ -709,29 +723,36 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
         for (int t = 0; t < (kSmallPages ? 2 : 1); ++t) e.entry[t] = __builtin_amdgcn_readlane(all.entry[t], n);
         return place_of<D>(c, e, h, key0 + n * kStepKeys);
       };
-      Place<kSmallPages> now = place(0), next = now;
-      KeyRegs<D> kr, ahead;
-      load_keys<D>(c, now, g, kr);
+      const int t = lane & 1;  // the half whose weights this lane would store
+      const bool mine = (lane & 15) < 2;
+      struct Ahead {
+        KeyRegs<D> kr;
+        float4_t was;
+        uint64_t at;
+        bool ok[2];
+      } now, next;
+      auto load = [&](int n, Ahead &x) {
+        const Place<kSmallPages> p = place(n);
+        load_keys<D>(c, p, g, x.kr);
+        x.at = p.row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
+        x.was = *reinterpret_cast<const float4_t *>(c.kv.p.weights + x.at);
+        x.ok[0] = p.ok[0], x.ok[1] = p.ok[1];
+      };
+      load(0, now);
       Column q;
       QueryOperand<D> f;
       float2 ml;
       operand(0, q, f, ml);
       const float share = ml.y != 0.0f ? 1.0f / ml.y : 0.0f;
       for (int n = 0; n < count; ++n) {
-        if (n + 1 < count) {
-          next = place(n + 1);
-          load_keys<D>(c, next, g, ahead);
-        }
+        if (n + 1 < count) load(n + 1, next);
+        const int key = key0 + n * kStepKeys + 4 * j;
+        float4_t sum[2] = {};
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int key = key0 + n * kStepKeys + 16 * t + 4 * j;
-          float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-          add_weights<D>(kr, t, now.ok[t], key, q, f, ml, share, sum);
-          const uint64_t at = now.row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
-          store_weights(c, sum, at, key, len, start, (lane & 15) == t && now.ok[t]);
-        }
+        for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, now.ok[u], key + 16 * u, q, f, ml, share, sum[u]);
+        const float4_t v = fold_weights(sum[0], sum[1]);
+        if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
         now = next;
-        kr = ahead;
       }
     } else {
       Place<kSmallPages> place[kCount];
@@ -756,10 +777,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
                          sum[n / 2][n % 2]);
       }
 #pragma unroll
-      for (int n = 0; n < 2 * kCount; ++n) {
-        const uint64_t at = place[n / 2].row[kSmallPages ? n % 2 : 0] + (kSmallPages ? 0 : 16 * (n % 2)) + 4 * j;
-        store_weights(c, sum[n / 2][n % 2], at, key0 + 16 * n + 4 * j, len, start,
-                      (lane & 15) == n && place[n / 2].ok[n % 2]);
+      for (int n = 0; n < kCount; ++n) {
+        const int t = lane & 1;
+        const uint64_t at = place[n].row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
+        const float4_t v = fold_weights(sum[n][0], sum[n][1]);
+        if ((lane & 15) < 2 && (t ? place[n].ok[1] : place[n].ok[0]))
+          store_weights(c, *reinterpret_cast<const float4_t *>(c.kv.p.weights + at), v, at,
+                        key0 + n * kStepKeys + 16 * t + 4 * j, len, start);
       }
     }
   }
@@ -775,7 +799,8 @@ struct Plan {
 constexpr int64_t kFill = 1024;             // workgroups of tiles that fill the chip (four a CU)
 constexpr int64_t kMaxParts = 1ll << 26;    // floats of partial results
 constexpr int kFewRows = 64;
-constexpr int64_t kShortContext = 1024;
+constexpr int64_t kCus = 256;
+constexpr int64_t kShortContext = 768, kShortOfMany = 4096;
 
 // On the host, where min and max of HIP's headers are those of int.
 int64_t least_of(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -792,16 +817,22 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
   const int tiles = (int)((least_of(most, p.few_rows) + tile_rows - 1) / tile_rows);
   p.tile_waves = tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
   p.tiles = (tiles + p.tile_waves - 1) / p.tile_waves * p.tile_waves;
-  const int64_t cap = (int64_t)r.table_width * kv.page_size;
+  // keys that a sequence's rows can see
+  const int64_t cap = least_of((int64_t)r.table_width * kv.page_size,
+                               a.window ? (int64_t)a.window + (r.offsets ? r.tokens : 1) : (int64_t)1 << 30);
   const int64_t out = (int64_t)r.tokens * a.q_heads * kv.head_dim;
   const int64_t parts = most_of(least_of(kMaxParts / most_of(out, 1), 128), 1);
   // workgroups without splits: every sequence's rows, to the tile, need at most this many
   const int64_t groups = (least_of(r.tokens * group, (int64_t)r.seqs * p.few_rows) / (tile_rows * p.tile_waves) + r.seqs) *
                          kv.kv_heads;
   p.splits = (int)most_of(least_of(least_of((kFill + groups - 1) / groups, (cap + 255) / 256), parts), 1);
-  // short contexts: one workgroup of more waves is sooner done than splits and their joining
+  // Short contexts: one workgroup of more waves is sooner done than splits and
+  // their joining (one sequence of 8 key heads, 64 of queries, 512 keys: 13.4
+  // against 14.7 us, 1024: 16.0 against 14.7), for longer where sequences alone
+  // give every CU one (32 sequences, 2000 keys: 23.5 against 27.9 us, 4000:
+  // 33.4 against 34.8).
   p.waves = 4;
-  if (p.splits > 1 && cap <= kShortContext) {
+  if (p.splits > 1 && cap <= ((int64_t)r.seqs * kv.kv_heads >= kCus ? kShortOfMany : kShortContext)) {
     p.waves = 8;
     p.splits = 1;
   }
