@@ -23,7 +23,7 @@ LIB = os.path.join(LIBDIR, "libcoli_moe.so")
 SOURCES = ["coli_moe.hip", "expert_cache.hip", "router.hip", "dispatch.hip", "expert_gemv.hip", "expert_batch.hip",
            "expert_mfma.hip", "probes.hip", "operators.hip", "rmsnorm.hip", "balance.hip",
            "linear.hip", "linear_rows.hip", "rotary.hip", "kv_cache.hip", "attention.hip",
-           "attention_prompt.hip"]
+           "attention_prompt.hip", "attention_weights.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -62,6 +62,8 @@ struct Call {
   float *part_o;   // [row][split][D], row = token * q_heads + head
   float2 *part_ml; // [row][split] maximum (of scores times log2 e) and sum
   float2 *ml;      // [row], for the weights; NULL: not wanted
+  char *q_halves;  // for the prompts' weights: [key head][token][head of the group][D] halves
+  float4 *q_info;  // and what each row's scores are multiplied by, its maximum, 1 / its sum
 };
 
 // Range of keys that the rows r0 .. r1 of a sequence's key head see.
@@ -81,5 +83,45 @@ __device__ __forceinline__ KeyRange keys_of_rows(const Call &c, SeqSpan span, in
 // the registers: the results of 32 rows alone fill half of 256.
 constexpr int prompt_rows(int dim) { return dim == 256 ? 128 : 256; }
 hipError_t launch_attention_prompts(const Call &c, hipStream_t s);
+hipError_t launch_prompt_weights(const Call &c, hipStream_t s);
+
+// Where a step's two 16 keys stand: uniform.  Pages of 16 rows: two places, else
+// one after the other.  The table's entries are asked for a step before they
+// are needed, as they stand.
+template <bool kSmallPages>
+struct Entries {
+  int entry[kSmallPages ? 2 : 1];
+};
+template <bool kSmallPages>
+struct Place {
+  uint64_t row[kSmallPages ? 2 : 1];    // of codes
+  uint64_t scale[kSmallPages ? 2 : 1];  // first scale of group 0
+  bool ok[2];
+};
+
+template <bool kSmallPages>
+__device__ __forceinline__ Entries<kSmallPages> entries_of(const Call &c, const int32_t *table, int key0) {
+  Entries<kSmallPages> e;
+#pragma unroll
+  for (int t = 0; t < (kSmallPages ? 2 : 1); ++t)
+    e.entry[t] = table[min((key0 >> c.kv.shift) + t, c.rows.table_width - 1)];
+  return e;
+}
+
+template <int D, bool kSmallPages>
+__device__ __forceinline__ Place<kSmallPages> place_of(const Call &c, const Entries<kSmallPages> &e, int h, int key0) {
+  Place<kSmallPages> p;
+  const int slot = kSmallPages ? 0 : key0 & (c.kv.p.page_size - 1);
+#pragma unroll
+  for (int t = 0; t < (kSmallPages ? 2 : 1); ++t) {
+    const int entry = uniform(e.entry[t]);
+    p.ok[t] = (key0 >> c.kv.shift) + t < c.rows.table_width && (unsigned)entry < (unsigned)c.kv.p.n_pages;
+    const int page = p.ok[t] ? entry : 0;
+    p.row[t] = code_row(c.kv, page, h, slot);
+    p.scale[t] = scale_index<D / kKvGroup>(c.kv, page, h, 0, slot);
+  }
+  if constexpr (!kSmallPages) p.ok[1] = p.ok[0];
+  return p;
+}
 
 }  // namespace coli

@@ -147,45 +147,6 @@ __device__ __forceinline__ float4_t scales4(uint2 v) {
                   __uint_as_float(v.y & 0xFFFF0000u)};
 }
 
-// Where a step's two 16 keys stand: uniform.  Pages of 16 rows: two places, else
-// one after the other.  The table's entries are asked for a step before they
-// are needed, as they stand.
-template <bool kSmallPages>
-struct Entries {
-  int entry[kSmallPages ? 2 : 1];
-};
-template <bool kSmallPages>
-struct Place {
-  uint64_t row[kSmallPages ? 2 : 1];    // of codes
-  uint64_t scale[kSmallPages ? 2 : 1];  // first scale of group 0
-  bool ok[2];
-};
-
-template <bool kSmallPages>
-__device__ __forceinline__ Entries<kSmallPages> entries_of(const Call &c, const int32_t *table, int key0) {
-  Entries<kSmallPages> e;
-#pragma unroll
-  for (int t = 0; t < (kSmallPages ? 2 : 1); ++t)
-    e.entry[t] = table[min((key0 >> c.kv.shift) + t, c.rows.table_width - 1)];
-  return e;
-}
-
-template <int D, bool kSmallPages>
-__device__ __forceinline__ Place<kSmallPages> place_of(const Call &c, const Entries<kSmallPages> &e, int h, int key0) {
-  Place<kSmallPages> p;
-  const int slot = kSmallPages ? 0 : key0 & (c.kv.p.page_size - 1);
-#pragma unroll
-  for (int t = 0; t < (kSmallPages ? 2 : 1); ++t) {
-    const int entry = uniform(e.entry[t]);
-    p.ok[t] = (key0 >> c.kv.shift) + t < c.rows.table_width && (unsigned)entry < (unsigned)c.kv.p.n_pages;
-    const int page = p.ok[t] ? entry : 0;
-    p.row[t] = code_row(c.kv, page, h, slot);
-    p.scale[t] = scale_index<Tile<D>::kGroups>(c.kv, page, h, 0, slot);
-  }
-  if constexpr (!kSmallPages) p.ok[1] = p.ok[0];
-  return p;
-}
-
 // Keys and values of a step as they stand in memory.  Keys: lane (r, j) has
 // columns of key r of each 16 (see load_query) and the scales of its column's
 // group for keys 4 j ..  Values: lane (r, j) has, of keys 4 j .. 4 j + 3 of each
@@ -700,7 +661,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
     const int h = (int)(item / chunks % H), s = (int)(item / chunks / H);
     const SeqSpan span = seq_span(c.rows, s);
     const int64_t len = c.rows.lengths[s], start = len - span.n;
-    if (span.n == 0 || key0 >= len) continue;
+    if (span.n == 0 || key0 >= len || span.n * c.group > c.few_rows) continue;
     // queries that see any of these keys
     const int64_t i0 = max((int64_t)key0 - start, (int64_t)0);
     const int64_t i1 = c.a.window ? min(key0 + kChunk - 1 + (int64_t)c.a.window - start, (int64_t)span.n)
@@ -793,7 +754,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
 struct Plan {
   int tiles, tile_waves, few_rows, waves, splits, prompt_splits;
   bool prompts;
-  size_t part_o, part_ml, ml, bytes;
+  size_t part_o, part_ml, ml, q_halves, q_info, bytes;
 };
 
 constexpr int64_t kFill = 1024;             // workgroups of tiles that fill the chip (four a CU)
@@ -851,6 +812,11 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
   if (splits > 1) at += up(rows * splits * sizeof(float2));
   p.ml = at;
   if (a.weights_out) at += up(rows * sizeof(float2));
+  // the prompts' weights: a tile may read up to 32 rows past the last
+  p.q_halves = at;
+  if (a.weights_out && p.prompts) at += up((rows + 32) * kv.head_dim * sizeof(_Float16));
+  p.q_info = at;
+  if (a.weights_out && p.prompts) at += up((rows + 32) * sizeof(float4));
   p.bytes = at > 0 ? at : 256;
   return p;
 }
@@ -888,6 +854,7 @@ hipError_t launch_all(const Call &c, hipStream_t s) {
     const int64_t items = (int64_t)c.rows.seqs * c.kv.p.kv_heads * chunks;
     e = launch(one ? kv_weights_kernel<D, kSmallPages, true> : kv_weights_kernel<D, kSmallPages, false>,
                dim3(grid_of((items + kTileWaves - 1) / kTileWaves)), dim3(kTileThreads), 0, s, c, chunks, items);
+    if (e == hipSuccess && prompts) e = launch_prompt_weights(c, s);
   }
   return e;
 }
@@ -910,7 +877,8 @@ hipError_t launch_kv_attention(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t
   char *ws = static_cast<char *>(workspace);
   Call c{kv_view(kv), r, a, a.q_heads / kv.kv_heads, p.tiles, p.tile_waves, p.few_rows, p.waves, p.splits, p.prompt_splits,
          max(p.splits, p.prompt_splits), reinterpret_cast<float *>(ws + p.part_o), reinterpret_cast<float2 *>(ws + p.part_ml),
-         a.weights_out ? reinterpret_cast<float2 *>(ws + p.ml) : nullptr};
+         a.weights_out ? reinterpret_cast<float2 *>(ws + p.ml) : nullptr, ws + p.q_halves,
+         reinterpret_cast<float4 *>(ws + p.q_info)};
   switch (kv.head_dim) {
     case 64: return launch_all<64>(c, s);
     case 128: return launch_all<128>(c, s);
