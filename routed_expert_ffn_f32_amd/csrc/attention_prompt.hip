@@ -14,8 +14,8 @@
 // the exponent lacks is made up by one power of two for the keys and one for
 // the values of each step.  Where the scales of a step's values are more than
 // 25 powers of two apart, the small ones follow in passes of their own, so a
-// value counts down to 2^-77 of the largest next to it.  Rows whose scale is
-// NaN (or Inf) stay out of the products, where 0 times NaN would reach rows
+// value counts down to 2^-77 of the largest next to it, or 2^-100 of the
+// largest before it.  Rows whose scale is NaN (or Inf) stay out of the products, where 0 times NaN would reach rows
 // that do not see them, and are put on those that do.
 //
 // Bound: 4 D flops of the matrix cores a score against about 9 vector
@@ -419,6 +419,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
     int unit = 12;      // exponent of the values' power of two that acc stands in
     int now_unit = 12;  // and that the step's values are expanded to
     int next_unit = 12;
+    int top_unit = 12;  // the largest so far
     int k_now = 0, k_next = 1, k_after = 2;  // whose keys stand where
     StepScales now = {12, 12, 254, false, 0}, next = now, next2 = now;
     Staged g[T::kUnits];
@@ -438,7 +439,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
       __syncthreads();
       now = hear_scales(s0);
       next = hear_scales(s0 + 1);
-      unit = now_unit = scale_exponent(now.v);
+      unit = now_unit = top_unit = scale_exponent(now.v);
       expand_units(s0, page, g, lv[0], lk[0], scale_exponent(now.k), now_unit, now_unit);
 #pragma unroll
       for (int u = 0; u < T::kUnits; ++u) now_page[u] = page[u];
@@ -467,8 +468,11 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
         load_scales(step + 3, look_page, look);
       }
       next2 = hear_scales(step + 2);
-      const int e1 = scale_exponent(next.v);
-      next_unit = e1 > now_unit || e1 < now_unit - kBand / 2 ? e1 : now_unit;
+      // A step of much smaller values has a smaller unit, but not one that sums of
+      // the largest so far would overflow in; one without values has none of its own.
+      const int e1 = next.v == 0 ? now_unit : scale_exponent(next.v);
+      next_unit = e1 > now_unit || e1 < now_unit - kBand / 2 ? max(e1, top_unit - kBand) : now_unit;
+      top_unit = max(top_unit, next_unit);
     };
     auto end_step = [&](int step) {
       if ((step & (T::kWaves - 1)) == wave) tell_scales(step + 3, look_page, look);
