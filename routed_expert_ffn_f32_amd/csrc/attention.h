@@ -18,6 +18,24 @@ constexpr int kTileThreads = 256;
 constexpr int kTileWaves = kTileThreads / 64;
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// A weight is exp2((u x - m) cs) with the power of two u and the maximum m of
+// u x.  One multiply-add, x (u cs) - m cs, has the rounding of m cs, common to
+// all keys of a row but not to its other maxima; so above this size of m cs the
+// difference is taken first.
+constexpr float kFar = 16.0f;
+
+// The maximum that a row's sums stand against may be passed by 2^kSlack before
+// they are brought to a new one.
+constexpr float kSlack = 8.0f;
+
+// 2^-kSlack of exp2((v - m) cs) for a score v computed once more: at most 1,
+// which the rounding of scores too large for float32 to tell apart could
+// otherwise pass by far.  share_again takes it back.  A NaN row's share is NaN.
+__device__ __forceinline__ float weight_again(float difference, float cs) {
+  return __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(__builtin_fmaf(difference, cs, -kSlack)), 0.0f, 1.0f);
+}
+__device__ __forceinline__ float share_again(float sum) { return sum != 0.0f ? 0x1p8f / sum : 0.0f; }
+
 // Power of two that brings v (>= 0) into [2^14, 2^15), within float32's range,
 // and its inverse.
 __device__ __forceinline__ int lift_exponent(float v) { return max((int)(__float_as_uint(v) >> 23) & 255, 20); }
@@ -52,6 +70,7 @@ struct Call {
   KvView kv;
   coli_moe_kv_rows_t rows;
   coli_moe_kv_attention_t a;
+  float cs;        // a score q . k times this is a power of two's exponent: |scale| log2 e (the sign goes with q)
   int group;       // query heads of a key head
   int tiles;       // tiles of a sequence's key head that the grid has
   int tile_waves;  // of them in one workgroup (1, 2 or 4)
@@ -60,10 +79,10 @@ struct Call {
   int splits, prompt_splits;  // of the keys, by the tiles and by the prompts' kernel
   int part_splits;  // the larger
   float *part_o;   // [row][split][D], row = token * q_heads + head
-  float2 *part_ml; // [row][split] maximum (of scores times log2 e) and sum
+  float2 *part_ml; // [row][split] maximum (of scores without cs) and sum
   float2 *ml;      // [row], for the weights; NULL: not wanted
   char *q_halves;  // for the prompts' weights: [key head][token][head of the group][D] halves
-  float4 *q_info;  // and what each row's scores are multiplied by, its maximum, 1 / its sum
+  float4 *q_info;  // and each row's power of two, its maximum, 1 / its sum
 };
 
 // Range of keys that the rows r0 .. r1 of a sequence's key head see.

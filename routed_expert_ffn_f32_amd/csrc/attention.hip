@@ -100,7 +100,7 @@ __device__ __forceinline__ Column column_of(const Call &c, SeqSpan span, int64_t
 template <int D>
 struct QueryOperand {
   half8_t b[Tile<D>::kSteps];
-  float scale;  // of a summed score, with log2 e
+  float unit;  // that takes the power of two back
 };
 
 template <int D>
@@ -138,7 +138,7 @@ __device__ __forceinline__ void load_query(const Call &c, const Column &q, Query
       f.b[w][2 * e + 1] = (_Float16)(v[e + 4] * up);
     }
   }
-  f.scale = c.a.scale != 0.0f ? fabsf(c.a.scale) * kLog2e * unlift(ex) : 1.0f;
+  f.unit = unlift(ex);
 }
 
 // Four neighbouring scales of a column's group.
@@ -210,8 +210,7 @@ __device__ __forceinline__ void clear_outside(const Call &c, int D) {
 }
 
 // Weights times scales are lifted to [2^6, 2^7) at a weight of 1 and may pass
-// it by the 2^8 that scores may pass the maximum by: 2^15 at most.
-constexpr float kSlack = 8.0f;
+// it by the 2^kSlack that scores may pass the maximum by: 2^15 at most.
 __device__ __forceinline__ float weight_lift(int ex) { return __uint_as_float((uint32_t)(260 - ex) << 23); }
 __device__ __forceinline__ float weight_unlift(int ex) { return __uint_as_float((uint32_t)(ex - 6) << 23); }
 
@@ -356,6 +355,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
     const int all_hi = clamped(first_pos), all_lo = c.a.window ? clamped(last_pos - c.a.window + 1) : 0;
 
     float m = -INFINITY, l = 0.0f;  // the maximum that the sums stand against; the sum
+    bool far = false;               // a column's maximum is above kFar
     int ex = lift_exponent(0.0f);   // weights times scales are lifted by it
     float big = 0.0f;               // the largest of them, lifted
     float4_t acc[T::kParts];
@@ -401,14 +401,23 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
       float top = x[0][0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e / 4][e % 4]);
-      top *= f.scale;
+      top *= f.unit;
       float w[8], sum;
       auto weigh = [&]() {
         const float base = m == -INFINITY ? 0.0f : m, up = weight_lift(ex);
+        float z[8];
+        if (__builtin_expect(far, 0)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = __builtin_fmaf(x[e / 4][e % 4], f.unit, -base) * c.cs;
+        } else {
+          const float by = fmaxf(f.unit * c.cs, 0x1p-126f), less = base * c.cs;  // -Inf times by is -Inf
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = __builtin_fmaf(x[e / 4][e % 4], by, -less);
+        }
         sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e / 4][e % 4], f.scale, -base));
+          const float p = __builtin_amdgcn_exp2f(z[e]);
           sum += p;
           w[e] = p * sv[e / 4][e % 4] * up;
         }
@@ -417,15 +426,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
       float most = big;
 #pragma unroll
       for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(w[e]));
-      if (__builtin_expect(__any(top > m + kSlack || most > 0x1p15f), 0)) {
+      if (__builtin_expect(__any((top - m) * c.cs > kSlack || most > 0x1p15f), 0)) {
         // a new maximum, and the lift by the largest weight times scale against it
         const float m1 = fmaxf(m, max_over_j(top)), base = m1 == -INFINITY ? 0.0f : m1;
-        const float fade = __builtin_amdgcn_exp2f(m - base);
+        const float fade = __builtin_amdgcn_exp2f((m - base) * c.cs);
         m = m1;
+        far = __any(fabsf(m) * c.cs > kFar && m != -INFINITY);
         most = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          most = fmaxf(most, fabsf(__builtin_amdgcn_exp2f(__builtin_fmaf(x[e / 4][e % 4], f.scale, -base)) *
+          most = fmaxf(most, fabsf(__builtin_amdgcn_exp2f(__builtin_fmaf(x[e / 4][e % 4], f.unit, -base) * c.cs) *
                                    sv[e / 4][e % 4]));
         most = fmaxf(max_over_j(most), max_over_j(big) * weight_unlift(ex) * fade);
         const int ex1 = lift_exponent(most);
@@ -496,7 +506,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
       for (int k = 0; k < kn; ++k) {
         const int wv = k * tile_waves + tw;
         const float2 v = sml[wv * T::kRows + rr];
-        const float fade = __builtin_amdgcn_exp2f(v.x - base);
+        const float fade = __builtin_amdgcn_exp2f((v.x - base) * c.cs);
         ll += v.y * fade;
         o += so[wv * kOut + rr * D + d] * fade;
       }
@@ -562,7 +572,7 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c,
     float fade[2], l = 0.0f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      fade[k] = __builtin_amdgcn_exp2f(mine[k].x - base);
+      fade[k] = __builtin_amdgcn_exp2f((mine[k].x - base) * c.cs);
       l += mine[k].y * fade[k];
     }
     l = wave_sum(l);
@@ -604,12 +614,13 @@ constexpr int kWeightSteps = kOneTile ? 8 : D == 256 ? 1 : 2;
 // Softmax weights of 16 keys, summed over the columns of a tile.
 template <int D>
 __device__ __forceinline__ void add_weights(const KeyRegs<D> &kr, int t, bool there, int key, const Column &q,
-                                            const QueryOperand<D> &f, float2 ml, float share, float4_t &sum) {
+                                            const QueryOperand<D> &f, float2 ml, float cs, float share,
+                                            float4_t &sum) {
   const float4_t p = scores16<D>(kr, t, f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const bool seen = q.live && q.g == 0 && there && key + i <= q.hi && key + i >= q.lo;
-    sum[i] += seen ? __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], f.scale, -ml.x)) * share : 0.0f;
+    sum[i] += seen ? weight_again(__builtin_fmaf(p[i], f.unit, -ml.x), cs) * share : 0.0f;
   }
 }
 
@@ -704,13 +715,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
       QueryOperand<D> f;
       float2 ml;
       operand(0, q, f, ml);
-      const float share = ml.y != 0.0f ? 1.0f / ml.y : 0.0f;
+      const float share = share_again(ml.y);
       for (int n = 0; n < count; ++n) {
         if (n + 1 < count) load(n + 1, next);
         const int key = key0 + n * kStepKeys + 4 * j;
         float4_t sum[2] = {};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, now.ok[u], key + 16 * u, q, f, ml, share, sum[u]);
+        for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, sum[u]);
         const float4_t v = fold_weights(sum[0], sum[1]);
         if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
         now = next;
@@ -731,10 +742,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
         QueryOperand<D> f;
         float2 ml;
         operand(tile, q, f, ml);
-        const float share = ml.y != 0.0f ? 1.0f / ml.y : 0.0f;
+        const float share = share_again(ml.y);
 #pragma unroll
         for (int n = 0; n < 2 * kCount; ++n)
-          add_weights<D>(kr[n / 2], n % 2, place[n / 2].ok[n % 2], key0 + 16 * n + 4 * j, q, f, ml, share,
+          add_weights<D>(kr[n / 2], n % 2, place[n / 2].ok[n % 2], key0 + 16 * n + 4 * j, q, f, ml, c.cs, share,
                          sum[n / 2][n % 2]);
       }
 #pragma unroll
@@ -875,7 +886,8 @@ hipError_t launch_kv_attention(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t
                                void *workspace, hipStream_t s) {
   const Plan p = plan_of(kv, r, a);
   char *ws = static_cast<char *>(workspace);
-  Call c{kv_view(kv), r, a, a.q_heads / kv.kv_heads, p.tiles, p.tile_waves, p.few_rows, p.waves, p.splits, p.prompt_splits,
+  const float cs = a.scale != 0.0f ? fminf(fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f), 0x1p127f) : 1.0f;
+  Call c{kv_view(kv), r, a, cs, a.q_heads / kv.kv_heads, p.tiles, p.tile_waves, p.few_rows, p.waves, p.splits, p.prompt_splits,
          max(p.splits, p.prompt_splits), reinterpret_cast<float *>(ws + p.part_o), reinterpret_cast<float2 *>(ws + p.part_ml),
          a.weights_out ? reinterpret_cast<float2 *>(ws + p.ml) : nullptr, ws + p.q_halves,
          reinterpret_cast<float4 *>(ws + p.q_info)};

@@ -12,7 +12,8 @@
 //
 // A code times its scale, 4 and 8 significant bits, is exact in a half; what
 // the exponent lacks is made up by one power of two for the keys and one for
-// the values of each step.  Where the scales of a step's values are more than
+// the values of each step.  A key whose scale is more than 25 powers of two
+// below another's of its step has its scores computed apart.  Where the scales of a step's values are more than
 // 25 powers of two apart, the small ones follow in passes of their own, so a
 // value counts down to 2^-77 of the largest next to it, or 2^-100 of the
 // largest before it.  Rows whose scale is NaN (or Inf) stay out of the products, where 0 times NaN would reach rows
@@ -34,7 +35,6 @@ template <int N>
 struct Num {
   static constexpr int value = N;
 };
-constexpr float kSlack = 8;  // the maximum may be passed by 2^8 before sums are rescaled
 
 template <int D>
 struct Prompt {
@@ -79,10 +79,11 @@ __device__ __forceinline__ float max_over_halves(float v) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// Exponents of the scales of a step: largest of the keys', largest and
-// smallest (of those not 0) of the values', and whether one is NaN or Inf.
+// Exponents of the scales of a step: largest of the keys' and the smallest that
+// is a key's largest, largest and smallest of the values' (none of 0), and
+// whether one is NaN or Inf.
 struct StepScales {
-  int k, v, v_least;
+  int k, v, v_least, k_least;
   bool bad;
   uint64_t there;  // keys that are on a page
 };
@@ -172,7 +173,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
     const int all_lo = c.a.window ? clamped(pos1 - c.a.window + 1) : 0;
 
     half8_t q[T::kSteps];
-    float q_scale;
+    float q_unit;
     {
       Raw8 raw[T::kSteps];
       const int64_t base = token * c.a.q_token + head * c.a.q_head;
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
           q[i][2 * e + 1] = (_Float16)(v[e + 4] * up);
         }
       }
-      q_scale = c.a.scale != 0.0f ? fabsf(c.a.scale) * kLog2e * unlift(ex) : 1.0f;
+      q_unit = unlift(ex);
     }
 
     float16_t acc[T::kParts];
@@ -212,6 +213,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
     float m = -INFINITY, sum = 0.0f;  // the maximum that the sums stand against; the sum of 2^7 times the weights
+    bool far = false;                 // a row's maximum is above kFar
 
     // --- staging ---
     const bool for_values = wave < T::kStageWaves;
@@ -249,22 +251,24 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
     };
     auto tell_scales = [&](int step, int page, const Scales &from) {
       int k = 0, v = 0, least = 254;
-      bool bad = false;
+      bool bad = false, some = false;
 #pragma unroll
       for (int g = 0; g < T::kGroups; ++g) {
         const int bk = page < 0 ? 0 : from.k[g], bv = page < 0 ? 0 : from.v[g];
         const int ek = bk >> 7 & 255, ev = bv >> 7 & 255;
         bad = bad || ek == 255 || ev == 255;
         k = max(k, ek == 255 ? 0 : ek);
+        some = some || (bk & 0x7FFF) != 0;
         v = max(v, ev == 255 ? 0 : ev);
         least = min(least, (bv & 0x7FFF) == 0 || ev == 255 ? 254 : ev);
       }
       const uint64_t there = __ballot(page >= 0);
       const int any_bad = __any(bad) ? 1 << 24 : 0;
+      const int k_least = 254 - wave_max(254 - (some ? k : 254));
       k = wave_max(k);
       v = wave_max(v);
       least = 254 - wave_max(254 - least);
-      if (lane == 0) told[(step - s0) & 3] = make_uint4(k | v << 8 | least << 16 | any_bad, 0, (uint32_t)there, (uint32_t)(there >> 32));
+      if (lane == 0) told[(step - s0) & 3] = make_uint4(k | v << 8 | least << 16 | any_bad, k_least, (uint32_t)there, (uint32_t)(there >> 32));
     };
     auto hear_scales = [&](int step) {
       const uint4 t = told[(step - s0) & 3];
@@ -274,6 +278,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
       r.v = packed >> 8 & 255;
       r.v_least = packed >> 16 & 255;
       r.bad = packed >> 24;
+      r.k_least = uniform((int)t.y);
       r.there = (uint32_t)uniform((int)t.z) | (uint64_t)(uint32_t)uniform((int)t.w) << 32;
       return r;
     };
@@ -421,7 +426,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
     int next_unit = 12;
     int top_unit = 12;  // the largest so far
     int k_now = 0, k_next = 1, k_after = 2;  // whose keys stand where
-    StepScales now = {12, 12, 254, false, 0}, next = now, next2 = now;
+    StepScales now = {12, 12, 254, 254, false, 0}, next = now, next2 = now;
     Staged g[T::kUnits];
     int page[T::kUnits], page2[T::kUnits], now_page[T::kUnits], look_page = -1;
     float16_t xa, xb;
@@ -497,6 +502,34 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
       const int buf = (step - s0) & 1;
       const int key0 = first_key + step * T::kKeys + 32 * sub;
       const uint32_t there = (uint32_t)(now.there >> (32 * sub));
+      const int k_ex = scale_exponent(now.k);
+      // keys far below the step's largest, which a row may not even see: their scores from the codes as they stand
+      if (__builtin_expect(now.k_least <= k_ex - kBand, 0)) {
+        for (int k = 0; k < 32; ++k) {
+          const int page = key0 + k < end_key ? row_page(c.kv, table, c.rows.table_width, key0 + k) : -1;
+          if (page < 0) continue;
+          const int slot = (key0 + k) & (ps - 1);
+          const uint32_t *code = reinterpret_cast<const uint32_t *>(c.kv.p.k_codes + code_row(c.kv, page, h, slot) * (D / 2));
+          const uint16_t *sc = c.kv.p.k_scales + scale_index<T::kGroups>(c.kv, page, h, 0, slot);
+          int own = 0;
+#pragma unroll
+          for (int gr = 0; gr < T::kGroups; ++gr) own = max(own, sc[gr * ps] >> 7 & 255);
+          if (own > k_ex - kBand) continue;  // in the product, or NaN
+          float total = 0.0f;
+#pragma unroll
+          for (int n = 0; n < T::kSteps; ++n) {
+            __builtin_amdgcn_sched_barrier(0);  // one after the other: registers are short
+            const half8_t v = codes_of(code[2 * n + hf]);
+            float part = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) part = __builtin_fmaf((float)v[e], (float)q[n][e], part);
+            total = __builtin_fmaf(part, from_bf16(sc[16 * n / kKvGroup * ps]) * scale_up(k_ex), total);
+          }
+          total += __shfl_xor(total, 32);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = k == 8 * (e / 4) + e % 4 + 4 * hf ? total : x[e];
+        }
+      }
       if (__builtin_expect(!(key0 + 31 <= p0 && key0 >= all_lo && there == ~0u), 0)) {
         const uint32_t mine = there >> (4 * hf);
 #pragma unroll
@@ -505,15 +538,17 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
           x[e] = k <= q_hi && k >= q_lo && (mine >> at & 1) ? x[e] : -INFINITY;
         }
       }
-      const float f = q_scale * scale_unit(scale_exponent(now.k));
+      // more than 0, so that masked scores stay what they are
+      const float f = fmaxf(q_unit * scale_unit(k_ex), 0x1p-126f);
       float top = x[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
       top = max_over_halves(top) * f;
-      if (__builtin_expect(__any(top > m + kSlack) || unit != now_unit, 0)) {
+      if (__builtin_expect(__any((top - m) * c.cs > kSlack) || unit != now_unit, 0)) {
         const float m1 = fmaxf(m, top);
-        const float fade = __builtin_amdgcn_exp2f(m - (m1 == -INFINITY ? 0.0f : m1));
+        const float fade = __builtin_amdgcn_exp2f((m - (m1 == -INFINITY ? 0.0f : m1)) * c.cs);
         m = m1;
+        far = __any(fabsf(m) * c.cs > kFar && m != -INFINITY);
         sum *= fade;
 #pragma unroll
         for (int i = 0; i < T::kParts; ++i)
@@ -521,7 +556,14 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
           for (int e = 0; e < 16; ++e) acc[i][e] = __builtin_amdgcn_ldexpf(acc[i][e] * fade, unit - now_unit);
         unit = now_unit;
       }
-      const float base = (m == -INFINITY ? 0.0f : m) - 7.0f;
+      const float base = m == -INFINITY ? 0.0f : m;
+      float by = fmaxf(f * c.cs, 0x1p-126f), plus = __builtin_fmaf(-base, c.cs, 7.0f);
+      if (__builtin_expect(far, 0)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = __builtin_fmaf(x[e], f, -base);
+        by = c.cs;
+        plus = 7.0f;
+      }
       half8_t p[2], p2[2];
       // weights: kEach exponentials after an instruction, and the sum and rounding of those before
       constexpr int kEach = (16 + T::kSteps - 1) / T::kSteps;
@@ -541,7 +583,7 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
           const int at = n * kEach + j;
-          v[n & 1][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[at], f, -base));
+          v[n & 1][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[at], by, plus));
         }
         if (n > 0) settle(n - 1);
       });

@@ -56,8 +56,7 @@ __global__ __launch_bounds__(256) void kv_weight_rows_kernel(Call c, int64_t row
     *reinterpret_cast<half8_t *>(c.q_halves + row * (2 * D) + (piece ^ (int)(in_head & 7)) * 16) = y;
     if (piece == 0) {
       const float2 ml = c.ml[id];
-      c.q_info[row] = make_float4(c.a.scale != 0.0f ? fabsf(c.a.scale) * kLog2e * unlift(ex) : 1.0f,
-                                  ml.x == -INFINITY ? 0.0f : ml.x, ml.y != 0.0f ? 1.0f / ml.y : 0.0f, 0.0f);
+      c.q_info[row] = make_float4(unlift(ex), ml.x == -INFINITY ? 0.0f : ml.x, share_again(ml.y), 0.0f);
     }
   }
 }
@@ -189,7 +188,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_weights_kernel(Call 
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int key = 32 * u + 8 * (i / 4) + i % 4;
-            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][i], fk[u][i] * f.x, -f.y)) * f.z;
+            const float w = weight_again(__builtin_fmaf(x[u][i], fk[u][i] * f.x, -f.y), c.cs) * f.z;
             sum[u][i] += key <= hi && key >= lo ? w : 0.0f;
           }
         continue;
@@ -198,7 +197,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_weights_kernel(Call 
       for (int u = 0; u < kTiles; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          sum[u][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(__builtin_fmaf(x[u][i], fk[u][i] * f.x, -f.y)), f.z,
+          sum[u][i] = __builtin_fmaf(weight_again(__builtin_fmaf(x[u][i], fk[u][i] * f.x, -f.y), c.cs), f.z,
                                      sum[u][i]);
     }
     // sums over the 32 columns; lane (r, hf) with r < 16 stores key r's register

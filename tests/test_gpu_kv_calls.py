@@ -267,6 +267,66 @@ def test_values_far_apart(dev, dim, far, tokens):
     assert ((got.double() - out).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("far", [2.0 ** 35, 2.0 ** 90])
+@pytest.mark.parametrize("tokens", [3, 60])
+def test_keys_far_apart(dev, dim, far, tokens):
+    """One new row's key is many powers of two above all others: those that do
+    not see it keep their results, and for those that do it is out of the
+    question, or all of it."""
+    pool, near = (Pool([150], 1, dim, 32, seed=37).fill() for _ in range(2))
+    g = torch.Generator().manual_seed(38)
+    toward, value = torch.randn(1, dim, generator=g), torch.randn(1, dim, generator=g)
+    row = 150 - tokens + 1
+    pool.write(0, row, -far * toward, value)
+    near.write(0, row, -12 * toward, value)
+    way = 1.0 - 2.0 * (torch.arange(tokens) % 3 == 2).float().view(-1, 1, 1)
+    q = (torch.randn(tokens, 2, dim, generator=g) + toward * way).bfloat16()
+    # 12 times is as good as far: either way its weight, or all others', is below 2^-36
+    z = q.double() @ near.rows(0, 150)[0][:, 0].t() * dim ** -0.5
+    far_z, rest = z[1:, :, row], torch.cat([z[1:, :, :row], z[1:, :, row + 1:]], -1)
+    assert ((far_z < rest.amin(-1) - 30) | (far_z > rest.amax(-1) + 30)).all() and (far_z > 0).any()
+    out, tol, _, _ = kv_ref.attention(near, q, [tokens])
+    got = pool.to(dev, cm).attention(q.to(dev), pool.table.to(dev), ints([150], dev), ints([0, tokens], dev)).cpu()
+    assert ((got.double() - out).abs() <= tol + 2.0 ** -30).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("tokens", [2, 50])
+@pytest.mark.parametrize("length", [130, 2600])
+def test_large_scores(dev, dim, tokens, length):
+    """Scores of 10^8, far beyond what float32 tells apart, and of zeros: one
+    key has all the weight, and queries of zeros weigh all keys alike, in
+    splits too."""
+    pool = Pool([length], 1, dim, 64, seed=41)
+    pool.weights.zero_()
+    g = torch.Generator().manual_seed(42)
+    signs = 2.0 * torch.randint(0, 2, (length, 1, dim), generator=g) - 1
+    for r in range(length):
+        pool.write(0, r, signs[r] * 8192, torch.randn(1, dim, generator=g))
+    q = torch.zeros(tokens, 3, dim)
+    at = length - tokens + torch.arange(tokens)
+    chosen = (at * 7919) % (length - tokens)
+    q[:, 0], q[:, 1] = signs[chosen, 0] * 30000, signs[chosen, 0] * -30000
+    q = q.half()
+    cache = pool.to(dev, cm)
+    sums = torch.zeros_like(cache.weights)
+    args = pool.table.to(dev), ints([length], dev), ints([0, tokens], dev)
+    got = cache.attention(q.to(dev), *args, weights_out=sums).cpu().double()
+    v = pool.rows(0, length)[1][:, 0]
+    assert (got[:, 0] - v[chosen]).abs().le(2.0 ** -11 * v[chosen].abs() + 2.0 ** -25).all()
+    assert torch.isfinite(got).all()
+    mean = v.cumsum(0)[at] / (at + 1).view(-1, 1)
+    size = v.abs().cumsum(0)[at] / (at + 1).view(-1, 1)
+    # a float32 sum, and weights of 22 bits
+    assert (got[:, 2] - mean).abs().le(2.0 ** -11 * mean.abs() + (length + 128) * U * 8 * size + 2.0 ** -25).all()
+    # Weights come from scores computed once more.  Neighbouring float32 numbers are 128 apart at 2^30, where these
+    # scores are, so a sum in another order may fall short of the maximum by 2^-100 of its weight, or pass it, where
+    # it counts 2^8 at most.  The queries of zeros have no such scores: each gives 1 in all.
+    total = sums.double().sum().item()
+    assert tokens * (1 - 2.0 ** -18) <= total <= 3 * 2 ** 8 * tokens
+
+
 @pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (256, 32)])
 def test_weights_of_prompts_in_wide_tables(dev, dim, page):
     """The tables have room for far more rows than the sequences have, so that
