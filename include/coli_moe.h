@@ -793,9 +793,14 @@ int coli_moe_kv_read(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, co
  * over the tokens of the call and the query heads of its key head, for every
  * row that a query sees; other places are left as they were.  weights_out may
  * be kv->weights.  (Rows that several sequences of the call see get the sum of
- * some of them.)  The scaled scores have to be within float32's range.  Out
- * rows of tokens in no sequence are left as they were (clear 0) or set to 0
- * (clear 1).  The same call gives the same bits.
+ * some of them.)  The scores q . k have to be within float32's range.  A scale
+ * of the cache that is NaN or Inf makes the results NaN of the queries that
+ * see its row: a key's whole, a value's in the columns of its group.  In
+ * sequences of more than 64 query rows (tokens times q_heads / kv_heads) values
+ * below 2^-77 of the largest of their 64 neighbouring rows, or below 2^-100 of
+ * the largest before them, may count as 0.  Out rows of tokens in no sequence
+ * are left as they were (clear 0) or set to 0 (clear 1).  The same call gives
+ * the same bits.
  */
 typedef struct {
   int32_t q_heads;  /* a multiple of kv_heads, at most 256 times as many */
@@ -829,7 +834,7 @@ int coli_moe_kv_attention(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *row
  * (pages of the same cache, none of them in the table: other places are only
  * read, so pages may be shared between sequences and the call repeated).
  * kept[s][h][i] is the row that went to row i (-1 behind the last), and
- * new_lengths[s] = min(lengths[s], keep).  Rows that do not exist have weight
+ * new_lengths[s] = min(lengths[s], keep), 0 at least.  Rows that do not exist have weight
  * 0 when they compete and leave their places in `into` as they were.
  * rows->tokens and rows->offsets are not looked at.
  */

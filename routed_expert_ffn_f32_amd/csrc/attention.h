@@ -81,7 +81,7 @@ struct Call {
   float *part_o;   // [row][split][D], row = token * q_heads + head
   float2 *part_ml; // [row][split] maximum (of scores without cs) and sum
   float2 *ml;      // [row], for the weights; NULL: not wanted
-  char *q_halves;  // for the prompts' weights: [key head][token][head of the group][D] halves
+  char *q_halves;  // for the weights of more rows than a tile: [key head][token][head of the group][D] halves
   float4 *q_info;  // and each row's power of two, its maximum, 1 / its sum
 };
 
@@ -102,7 +102,7 @@ __device__ __forceinline__ KeyRange keys_of_rows(const Call &c, SeqSpan span, in
 // the registers: the results of 32 rows alone fill half of 256.
 constexpr int prompt_rows(int dim) { return dim == 256 ? 128 : 256; }
 hipError_t launch_attention_prompts(const Call &c, hipStream_t s);
-hipError_t launch_prompt_weights(const Call &c, hipStream_t s);
+hipError_t launch_row_weights(const Call &c, hipStream_t s);
 
 // Where a step's two 16 keys stand: uniform.  Pages of 16 rows: two places, else
 // one after the other.  The table's entries are asked for a step before they

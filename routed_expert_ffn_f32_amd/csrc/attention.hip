@@ -607,10 +607,6 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c,
   }
 }
 
-// Steps of keys that a wave of the weights' kernel takes.
-template <int D, bool kOneTile>
-constexpr int kWeightSteps = kOneTile ? 8 : D == 256 ? 1 : 2;
-
 // Softmax weights of 16 keys, summed over the columns of a tile.
 template <int D>
 __device__ __forceinline__ void add_weights(const KeyRegs<D> &kr, int t, bool there, int key, const Column &q,
@@ -656,15 +652,18 @@ __device__ __forceinline__ void store_weights(const Call &c, float4_t was, float
     if (key + i < len && key + i > lo) out[i] = was[i] + v[i];
 }
 
-// The weights of the rows of the cache, from the scores again and each query's
-// maximum and sum.  A wave takes kCount steps of keys of a sequence's key head
-// and all tiles of queries that see any of them, so that a place has one writer.
-// kOneTile: no sequence has more, so the queries are loaded once and the next
-// step's keys while this one's are used.
-template <int D, bool kSmallPages, bool kOneTile>
+// The weights of the rows of the cache where no sequence's key head has more
+// rows than a tile, from the scores again and each query's maximum and sum.  A
+// wave takes kWeightSteps steps of a sequence's key head, so that a place has
+// one writer; the next step's keys and weights are on their way while this
+// one's are used.  Bound by bytes in long contexts, in short ones by the three
+// loads that follow each other: 16 sequences of up to 4096 rows, 8 key heads of
+// 128 columns, 15 us (36 MB of keys); one step at a time 26 us.
+constexpr int kWeightSteps = 8;
+
+template <int D, bool kSmallPages>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int chunks, int64_t work) {
-  using T = Tile<D>;
-  constexpr int kCount = kWeightSteps<D, kOneTile>, kChunk = kCount * kStepKeys;
+  constexpr int kChunk = kWeightSteps * kStepKeys;
   const int lane = threadIdx.x & 63, j = lane >> 4, H = c.kv.p.kv_heads;
   const int64_t waves = (int64_t)gridDim.x * kTileWaves;
   for (int64_t item = (int64_t)blockIdx.x * kTileWaves + uniform(threadIdx.x >> 6); item < work; item += waves) {
@@ -672,91 +671,49 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
     const int h = (int)(item / chunks % H), s = (int)(item / chunks / H);
     const SeqSpan span = seq_span(c.rows, s);
     const int64_t len = c.rows.lengths[s], start = len - span.n;
-    if (span.n == 0 || key0 >= len || span.n * c.group > c.few_rows) continue;
+    if (span.n == 0 || key0 >= len) continue;
     // queries that see any of these keys
     const int64_t i0 = max((int64_t)key0 - start, (int64_t)0);
     const int64_t i1 = c.a.window ? min(key0 + kChunk - 1 + (int64_t)c.a.window - start, (int64_t)span.n)
                                   : (int64_t)span.n;
     if (i0 >= i1) continue;
     const int32_t *table = c.rows.table + s * c.rows.table_stride;
-    const int g = (lane & 15) / T::kRows;
-    auto operand = [&](int tile, Column &q, QueryOperand<D> &f, float2 &ml) {
-      q = column_of<D>(c, span, len, h, tile);
-      ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
-      load_query<D>(c, q, f);
+    const int count = (int)min((len - key0 + kStepKeys - 1) / kStepKeys, (int64_t)kWeightSteps);
+    // entries of all steps, a step a lane
+    const Entries<kSmallPages> all = entries_of<kSmallPages>(c, table, key0 + min(lane, count - 1) * kStepKeys);
+    const int t = lane & 1;  // the half whose weights this lane would store
+    const bool mine = (lane & 15) < 2;
+    struct Ahead {
+      KeyRegs<D> kr;
+      float4_t was;
+      uint64_t at;
+      bool ok[2];
+    } now, next;
+    auto load = [&](int n, Ahead &x) {
+      Entries<kSmallPages> e;
+#pragma unroll
+      for (int u = 0; u < (kSmallPages ? 2 : 1); ++u) e.entry[u] = __builtin_amdgcn_readlane(all.entry[u], n);
+      const Place<kSmallPages> p = place_of<D>(c, e, h, key0 + n * kStepKeys);
+      load_keys<D>(c, p, (lane & 15) / Tile<D>::kRows, x.kr);
+      x.at = p.row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
+      x.was = *reinterpret_cast<const float4_t *>(c.kv.p.weights + x.at);
+      x.ok[0] = p.ok[0], x.ok[1] = p.ok[1];
     };
-    if constexpr (kOneTile) {
-      const int count = (int)min((len - key0 + kStepKeys - 1) / kStepKeys, (int64_t)kCount);
-      // entries of all steps, a step a lane
-      const Entries<kSmallPages> all = entries_of<kSmallPages>(c, table, key0 + min(lane, count - 1) * kStepKeys);
-      auto place = [&](int n) {
-        Entries<kSmallPages> e;
+    load(0, now);
+    const Column q = column_of<D>(c, span, len, h, 0);
+    const float2 ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
+    QueryOperand<D> f;
+    load_query<D>(c, q, f);
+    const float share = share_again(ml.y);
+    for (int n = 0; n < count; ++n) {
+      if (n + 1 < count) load(n + 1, next);
+      const int key = key0 + n * kStepKeys + 4 * j;
+      float4_t sum[2] = {};
 #pragma unroll
-        for (int t = 0; t < (kSmallPages ? 2 : 1); ++t) e.entry[t] = __builtin_amdgcn_readlane(all.entry[t], n);
-        return place_of<D>(c, e, h, key0 + n * kStepKeys);
-      };
-      const int t = lane & 1;  // the half whose weights this lane would store
-      const bool mine = (lane & 15) < 2;
-      struct Ahead {
-        KeyRegs<D> kr;
-        float4_t was;
-        uint64_t at;
-        bool ok[2];
-      } now, next;
-      auto load = [&](int n, Ahead &x) {
-        const Place<kSmallPages> p = place(n);
-        load_keys<D>(c, p, g, x.kr);
-        x.at = p.row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
-        x.was = *reinterpret_cast<const float4_t *>(c.kv.p.weights + x.at);
-        x.ok[0] = p.ok[0], x.ok[1] = p.ok[1];
-      };
-      load(0, now);
-      Column q;
-      QueryOperand<D> f;
-      float2 ml;
-      operand(0, q, f, ml);
-      const float share = share_again(ml.y);
-      for (int n = 0; n < count; ++n) {
-        if (n + 1 < count) load(n + 1, next);
-        const int key = key0 + n * kStepKeys + 4 * j;
-        float4_t sum[2] = {};
-#pragma unroll
-        for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, sum[u]);
-        const float4_t v = fold_weights(sum[0], sum[1]);
-        if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
-        now = next;
-      }
-    } else {
-      Place<kSmallPages> place[kCount];
-      KeyRegs<D> kr[kCount];
-      float4_t sum[kCount][2];
-#pragma unroll
-      for (int n = 0; n < kCount; ++n) {
-        place[n] = place_of<D>(c, entries_of<kSmallPages>(c, table, key0 + n * kStepKeys), h, key0 + n * kStepKeys);
-        load_keys<D>(c, place[n], g, kr[n]);
-        sum[n][0] = sum[n][1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      }
-      const int last = (int)((i1 * c.group - 1) / T::kRows);
-      for (int tile = (int)(i0 * c.group / T::kRows); tile <= last; ++tile) {
-        Column q;
-        QueryOperand<D> f;
-        float2 ml;
-        operand(tile, q, f, ml);
-        const float share = share_again(ml.y);
-#pragma unroll
-        for (int n = 0; n < 2 * kCount; ++n)
-          add_weights<D>(kr[n / 2], n % 2, place[n / 2].ok[n % 2], key0 + 16 * n + 4 * j, q, f, ml, c.cs, share,
-                         sum[n / 2][n % 2]);
-      }
-#pragma unroll
-      for (int n = 0; n < kCount; ++n) {
-        const int t = lane & 1;
-        const uint64_t at = place[n].row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
-        const float4_t v = fold_weights(sum[n][0], sum[n][1]);
-        if ((lane & 15) < 2 && (t ? place[n].ok[1] : place[n].ok[0]))
-          store_weights(c, *reinterpret_cast<const float4_t *>(c.kv.p.weights + at), v, at,
-                        key0 + n * kStepKeys + 16 * t + 4 * j, len, start);
-      }
+      for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, sum[u]);
+      const float4_t v = fold_weights(sum[0], sum[1]);
+      if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
+      now = next;
     }
   }
 }
@@ -777,6 +734,12 @@ constexpr int64_t kShortContext = 768, kShortOfMany = 4096;
 // On the host, where min and max of HIP's headers are those of int.
 int64_t least_of(int64_t a, int64_t b) { return a < b ? a : b; }
 int64_t most_of(int64_t a, int64_t b) { return a > b ? a : b; }
+
+// Whether the rows of a sequence's key head are one tile at most, for all that
+// the call's sizes tell.
+bool one_tile(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, int64_t group) {
+  return (r.offsets ? r.tokens : 1) * group <= 16 / (kv.head_dim / kKvGroup);
+}
 
 Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_moe_kv_attention_t &a) {
   Plan p;
@@ -823,11 +786,12 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
   if (splits > 1) at += up(rows * splits * sizeof(float2));
   p.ml = at;
   if (a.weights_out) at += up(rows * sizeof(float2));
-  // the prompts' weights: a tile may read up to 32 rows past the last
+  // queries for the weights: a tile may read up to 32 rows past the last
   p.q_halves = at;
-  if (a.weights_out && p.prompts) at += up((rows + 32) * kv.head_dim * sizeof(_Float16));
+  const bool halves = a.weights_out && !one_tile(kv, r, group);
+  if (halves) at += up((rows + 32) * kv.head_dim * sizeof(_Float16));
   p.q_info = at;
-  if (a.weights_out && p.prompts) at += up((rows + 32) * sizeof(float4));
+  if (halves) at += up((rows + 32) * sizeof(float4));
   p.bytes = at > 0 ? at : 256;
   return p;
 }
@@ -857,17 +821,13 @@ hipError_t launch_all(const Call &c, hipStream_t s) {
                dim3(grid_of(wide ? rows : (rows + kTileWaves - 1) / kTileWaves)), dim3(kTileThreads), 0, s, c,
                seqs ? (int)few : 0, rows);
   }
-  if (e == hipSuccess && c.a.weights_out) {
-    const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
-    const bool one = (c.rows.offsets ? (int64_t)c.rows.tokens : 1) * c.group <= Tile<D>::kRows;
-    const int keys = kStepKeys * (one ? kWeightSteps<D, true> : kWeightSteps<D, false>);
-    const int chunks = (int)((cap + keys - 1) / keys);
-    const int64_t items = (int64_t)c.rows.seqs * c.kv.p.kv_heads * chunks;
-    e = launch(one ? kv_weights_kernel<D, kSmallPages, true> : kv_weights_kernel<D, kSmallPages, false>,
-               dim3(grid_of((items + kTileWaves - 1) / kTileWaves)), dim3(kTileThreads), 0, s, c, chunks, items);
-    if (e == hipSuccess && prompts) e = launch_prompt_weights(c, s);
-  }
-  return e;
+  if (e != hipSuccess || !c.a.weights_out) return e;
+  if (!one_tile(c.kv.p, c.rows, c.group)) return launch_row_weights(c, s);
+  const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
+  const int chunks = (int)((cap + kWeightSteps * kStepKeys - 1) / (kWeightSteps * kStepKeys));
+  const int64_t items = (int64_t)c.rows.seqs * c.kv.p.kv_heads * chunks;
+  return launch(kv_weights_kernel<D, kSmallPages>, dim3(grid_of((items + kTileWaves - 1) / kTileWaves)),
+                dim3(kTileThreads), 0, s, c, chunks, items);
 }
 
 template <int D>

@@ -1,5 +1,5 @@
-// The attention weights of cached rows for sequences of many new tokens: for
-// every key the sum over the query rows of its key head of
+// The attention weights of cached rows where sequences have more rows of
+// queries than one tile of the attention's: for every key the sum over the query rows of its key head of
 //   exp2(scale q . k - m) / l
 // with the rows' maxima m and sums l that the attention has left.
 //
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(256) void kv_weight_rows_kernel(Call c, int64_t row
 
 // kTiles: of 32 keys a wave.
 template <int D, int kTiles, bool kSmallPages>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_weights_kernel(Call c, int64_t work) {
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_row_weights_kernel(Call c, int64_t work) {
   constexpr int kKeys = kWaves * 32 * kTiles;
   constexpr int kSteps = D / 16, kGroups = D / kKvGroup;
   constexpr int kTileBytes = kRowTile * D * 2, kInfoBytes = kRowTile * 16;
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_weights_kernel(Call 
     const SeqSpan span = seq_span(c.rows, s);
     const int64_t len = c.rows.lengths[s], start = len - span.n;
     const int rows = span.n * c.group;
-    if (rows <= c.few_rows || key0 >= len) continue;
+    if (rows == 0 || key0 >= len) continue;
     // queries that see any of these keys
     const int64_t i0 = max((int64_t)key0 - start, (int64_t)0);
     const int64_t i1 = c.a.window ? min(key0 + kKeys - 1 + (int64_t)c.a.window - start, (int64_t)span.n)
@@ -238,15 +238,15 @@ hipError_t launch_d(const Call &c, hipStream_t s) {
   const int64_t one_keys = kWaves * 32, one = (int64_t)c.rows.seqs * c.kv.p.kv_heads * ((cap + one_keys - 1) / one_keys);
   const bool small = c.kv.p.page_size == 16;
   if (work < 256)
-    return launch(small ? kv_prompt_weights_kernel<D, 1, true> : kv_prompt_weights_kernel<D, 1, false>,
+    return launch(small ? kv_row_weights_kernel<D, 1, true> : kv_row_weights_kernel<D, 1, false>,
                   dim3(grid_of(one)), dim3(64 * kWaves), 0, s, c, one);
-  return launch(small ? kv_prompt_weights_kernel<D, kMost, true> : kv_prompt_weights_kernel<D, kMost, false>,
+  return launch(small ? kv_row_weights_kernel<D, kMost, true> : kv_row_weights_kernel<D, kMost, false>,
                 dim3(grid_of(work)), dim3(64 * kWaves), 0, s, c, work);
 }
 
 }  // namespace
 
-hipError_t launch_prompt_weights(const Call &c, hipStream_t s) {
+hipError_t launch_row_weights(const Call &c, hipStream_t s) {
   switch (c.kv.p.head_dim) {
     case 64: return launch_d<64>(c, s);
     case 128: return launch_d<128>(c, s);
