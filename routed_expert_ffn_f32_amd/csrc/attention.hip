@@ -19,6 +19,18 @@
 // as subnormal halves, need no addition, but the matrix core aligns its
 // products by exponents that it does not normalise: next to a large product
 // everything below 2^-17 of it was lost.)
+//
+// A weight times its scale is rounded to the 11 bits of a half (results of 8
+// bits, bfloat16) or to two halves' 22 (results of 11, half precision).
+//
+// Bound by bytes where there are many keys, 136 of a key head of 128 columns
+// for one query: a decode batch of 64 sequences of up to 8192 rows, 8 key heads
+// for 64 queries, 327 MB, takes 87 us with its join (3.8 TB/s; a large copy
+// 5.1), one sequence of 131071 rows, 143 MB, 42 us.  What keeps it from the
+// copy's rate is the 350 vector instructions of a step of 32 keys (columns are
+// only 8 rows, so the expansion of codes has few to be shared by).  One sequence
+// of 517 rows takes 14 us: a launch, three loads that follow each other
+// (length, page, rows), five steps a wave and the join of eight waves.
 #include "attention.h"
 #include "lds_dma.h"
 
@@ -725,8 +737,14 @@ struct Plan {
   size_t part_o, part_ml, ml, q_halves, q_info, bytes;
 };
 
-constexpr int64_t kFill = 1024;             // workgroups of tiles that fill the chip (four a CU)
-constexpr int64_t kMaxParts = 1ll << 26;    // floats of partial results
+// Workgroups of tiles that fill the chip: four a CU.  (768: one long sequence 48
+// instead of 43 us.)
+constexpr int64_t kFill = 1024;
+constexpr int64_t kMaxParts = 1ll << 26;  // floats of partial results
+// Rows of a sequence's key head that the tiles take; more go to the prompts'
+// kernel, whose 256 rows share each expanded key.  (8 sequences of 6000 rows, 8
+// key heads of 8 query heads: 64 rows 57 us by the tiles, 72 rows 87 by the
+// other; tiles read the keys once for every 32 rows.)
 constexpr int kFewRows = 64;
 constexpr int64_t kCus = 256;
 constexpr int64_t kShortContext = 768, kShortOfMany = 4096;
@@ -771,6 +789,7 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
     p.waves = 8;
     p.splits = 1;
   }
+  // the prompts' kernel has at most two workgroups a CU and a join of its own, so three for every CU at most
   p.prompt_splits = 1;
   if (p.prompts) {
     const int64_t blocks = (r.tokens * group / prompt_rows(kv.head_dim) + r.seqs) * kv.kv_heads;

@@ -1,15 +1,19 @@
 // The attention weights of cached rows where sequences have more rows of
-// queries than one tile of the attention's: for every key the sum over the query rows of its key head of
-//   exp2(scale q . k - m) / l
+// queries than one tile of the attention's: for every key the sum over the
+// query rows of its key head of
+//   exp2((q . k - m) cs) / l
 // with the rows' maxima m and sums l that the attention has left.
 //
 // A product whose result is summed over the queries at once: each wave holds 64
 // keys (D = 256: 32) as the left operand for good, the query rows come by in
 // tiles of 32 through LDS, and the sums of a key stay in its registers, one for
-// each query column, until the end.  Bound by what follows the product (an
-// exponential and three operations an element), so queries are made halves once
-// by a kernel of their own and the tiles that all keys and rows of see whole
-// have no masks.
+// each query column, until the end.  A key has a power of two of its own, so
+// its codes times its scales are exact.  Bound by what follows the product (an
+// exponential and four operations an element, 32 cycles to the product's 16 at
+// D = 128), so queries are made halves once by a kernel of their own, and the
+// tiles that all rows see whole have no masks.  Two prompts of up to 1500 tokens
+// on up to 16384 rows, 64 query heads on 8 of 128 columns: 1.1 ms; by the tiles
+// of the attention, a tile's scores once more for each 64 keys, 6.2.
 #include "attention.h"
 #include "lds_dma.h"
 
