@@ -674,58 +674,62 @@ __device__ __forceinline__ void store_weights(const Call &c, float4_t was, float
 constexpr int kWeightSteps = 8;
 
 template <int D, bool kSmallPages>
-__global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int chunks, int64_t work) {
+__global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int parts, int64_t work) {
   constexpr int kChunk = kWeightSteps * kStepKeys;
   const int lane = threadIdx.x & 63, j = lane >> 4, H = c.kv.p.kv_heads;
   const int64_t waves = (int64_t)gridDim.x * kTileWaves;
   for (int64_t item = (int64_t)blockIdx.x * kTileWaves + uniform(threadIdx.x >> 6); item < work; item += waves) {
-    const int key0 = (int)(item % chunks) * kChunk;
-    const int h = (int)(item / chunks % H), s = (int)(item / chunks / H);
+    const int h = (int)(item / parts % H), s = (int)(item / parts / H);
     const SeqSpan span = seq_span(c.rows, s);
     const int64_t len = c.rows.lengths[s], start = len - span.n;
-    if (span.n == 0 || key0 >= len) continue;
-    // queries that see any of these keys
-    const int64_t i0 = max((int64_t)key0 - start, (int64_t)0);
-    const int64_t i1 = c.a.window ? min(key0 + kChunk - 1 + (int64_t)c.a.window - start, (int64_t)span.n)
-                                  : (int64_t)span.n;
-    if (i0 >= i1) continue;
-    const int32_t *table = c.rows.table + s * c.rows.table_stride;
-    const int count = (int)min((len - key0 + kStepKeys - 1) / kStepKeys, (int64_t)kWeightSteps);
-    // entries of all steps, a step a lane
-    const Entries<kSmallPages> all = entries_of<kSmallPages>(c, table, key0 + min(lane, count - 1) * kStepKeys);
-    const int t = lane & 1;  // the half whose weights this lane would store
-    const bool mine = (lane & 15) < 2;
-    struct Ahead {
-      KeyRegs<D> kr;
-      float4_t was;
-      uint64_t at;
-      bool ok[2];
-    } now, next;
-    auto load = [&](int n, Ahead &x) {
-      Entries<kSmallPages> e;
+    const int64_t end = min(len, (int64_t)c.rows.table_width << c.kv.shift);
+    if (span.n == 0) continue;
+    // a table may be far wider than its sequence: the parts go on to the sequence's end
+    for (int64_t key_at = item % parts * kChunk; key_at < end; key_at += (int64_t)parts * kChunk) {
+      const int key0 = (int)key_at;
+      // queries that see any of these keys
+      const int64_t i0 = max((int64_t)key0 - start, (int64_t)0);
+      const int64_t i1 = c.a.window ? min(key0 + kChunk - 1 + (int64_t)c.a.window - start, (int64_t)span.n)
+                                    : (int64_t)span.n;
+      if (i0 >= i1) continue;
+      const int32_t *table = c.rows.table + s * c.rows.table_stride;
+      const int count = (int)min((end - key0 + kStepKeys - 1) / kStepKeys, (int64_t)kWeightSteps);
+      // entries of all steps, a step a lane
+      const Entries<kSmallPages> all = entries_of<kSmallPages>(c, table, key0 + min(lane, count - 1) * kStepKeys);
+      const int t = lane & 1;  // the half whose weights this lane would store
+      const bool mine = (lane & 15) < 2;
+      struct Ahead {
+        KeyRegs<D> kr;
+        float4_t was;
+        uint64_t at;
+        bool ok[2];
+      } now, next;
+      auto load = [&](int n, Ahead &x) {
+        Entries<kSmallPages> e;
 #pragma unroll
-      for (int u = 0; u < (kSmallPages ? 2 : 1); ++u) e.entry[u] = __builtin_amdgcn_readlane(all.entry[u], n);
-      const Place<kSmallPages> p = place_of<D>(c, e, h, key0 + n * kStepKeys);
-      load_keys<D>(c, p, (lane & 15) / Tile<D>::kRows, x.kr);
-      x.at = p.row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
-      x.was = *reinterpret_cast<const float4_t *>(c.kv.p.weights + x.at);
-      x.ok[0] = p.ok[0], x.ok[1] = p.ok[1];
-    };
-    load(0, now);
-    const Column q = column_of<D>(c, span, len, h, 0);
-    const float2 ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
-    QueryOperand<D> f;
-    load_query<D>(c, q, f);
-    const float share = share_again(ml.y);
-    for (int n = 0; n < count; ++n) {
-      if (n + 1 < count) load(n + 1, next);
-      const int key = key0 + n * kStepKeys + 4 * j;
-      float4_t sum[2] = {};
+        for (int u = 0; u < (kSmallPages ? 2 : 1); ++u) e.entry[u] = __builtin_amdgcn_readlane(all.entry[u], n);
+        const Place<kSmallPages> p = place_of<D>(c, e, h, key0 + n * kStepKeys);
+        load_keys<D>(c, p, (lane & 15) / Tile<D>::kRows, x.kr);
+        x.at = p.row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
+        x.was = *reinterpret_cast<const float4_t *>(c.kv.p.weights + x.at);
+        x.ok[0] = p.ok[0], x.ok[1] = p.ok[1];
+      };
+      load(0, now);
+      const Column q = column_of<D>(c, span, len, h, 0);
+      const float2 ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
+      QueryOperand<D> f;
+      load_query<D>(c, q, f);
+      const float share = share_again(ml.y);
+      for (int n = 0; n < count; ++n) {
+        if (n + 1 < count) load(n + 1, next);
+        const int key = key0 + n * kStepKeys + 4 * j;
+        float4_t sum[2] = {};
 #pragma unroll
-      for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, sum[u]);
-      const float4_t v = fold_weights(sum[0], sum[1]);
-      if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
-      now = next;
+        for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, sum[u]);
+        const float4_t v = fold_weights(sum[0], sum[1]);
+        if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
+        now = next;
+      }
     }
   }
 }
@@ -843,10 +847,11 @@ hipError_t launch_all(const Call &c, hipStream_t s) {
   if (e != hipSuccess || !c.a.weights_out) return e;
   if (!one_tile(c.kv.p, c.rows, c.group)) return launch_row_weights(c, s);
   const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
-  const int chunks = (int)((cap + kWeightSteps * kStepKeys - 1) / (kWeightSteps * kStepKeys));
-  const int64_t items = (int64_t)c.rows.seqs * c.kv.p.kv_heads * chunks;
-  return launch(kv_weights_kernel<D, kSmallPages>, dim3(grid_of((items + kTileWaves - 1) / kTileWaves)),
-                dim3(kTileThreads), 0, s, c, chunks, items);
+  // four waves a SIMD, or what the table has room for
+  const int64_t heads = (int64_t)c.rows.seqs * c.kv.p.kv_heads, chunk = kWeightSteps * kStepKeys;
+  const int64_t parts = least_of((cap + chunk - 1) / chunk, (4096 + heads - 1) / heads);
+  return launch(kv_weights_kernel<D, kSmallPages>, dim3(grid_of((heads * parts + kTileWaves - 1) / kTileWaves)),
+                dim3(kTileThreads), 0, s, c, (int)parts, heads * parts);
 }
 
 template <int D>

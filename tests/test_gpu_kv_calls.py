@@ -349,6 +349,32 @@ def test_weights_of_prompts_in_wide_tables(dev, dim, page):
         assert ((sums == -1) | (sums.double() - want).abs().le(wtol + 2 * U * want))[~seen].all()
 
 
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (256, 32)])
+@pytest.mark.parametrize("seqs", [3, 700])
+def test_weights_of_single_tokens_in_wide_tables(dev, dim, page, seqs):
+    """As above, and more sequences than there are waves for parts of each."""
+    lengths = [(37 * i) % 90 if i != 1 else 700 for i in range(seqs)]
+    pool = Pool(lengths, 2, dim, page, seed=33, capacity=1 << 13)
+    pool.k_scales.nan_to_num_(0.01)
+    pool.v_scales.nan_to_num_(0.02)
+    q = torch.randn(seqs, 4, dim, generator=torch.Generator().manual_seed(2)).half()
+    few = [i for i in range(seqs) if i < 8 or i % 97 == 0]  # the oracle's
+    cache = pool.to(dev, cm)
+    sums = torch.full_like(cache.weights, -1.0)
+    got = cache.attention(q.to(dev), pool.table.to(dev), ints(lengths, dev), weights_out=sums).cpu()
+    for i in few:
+        one = Pool([lengths[i]], 2, dim, page, seed=1)
+        one.pages, one.table = pool.pages, pool.table[i: i + 1]
+        one.k_codes, one.v_codes, one.k_scales, one.v_scales = pool.k_codes, pool.v_codes, pool.k_scales, pool.v_scales
+        one.weights = pool.weights
+        out, tol, w, wtol = kv_ref.attention(one, q[i: i + 1], [1])
+        assert ((got[i: i + 1].double() - out).abs() <= tol).all()
+        want = pool.weights.double() + w
+        assert ((sums.cpu().double() - want).abs() <= wtol + 2 * U * want)[w > 0].all()
+    # nothing but the rows of sequences is touched
+    assert int((sums != -1).sum()) == 2 * sum(lengths)
+
+
 def test_long_eviction(dev):
     """More rows than LDS holds keys of, many of them alike."""
     L, keep, page = 40000, 11111, 256
