@@ -114,27 +114,13 @@ __device__ __forceinline__ void round8(int type, float (&v)[8]) {
     v[j] = type == COLI_MOE_BF16 ? from_bf16(to_bf16(v[j])) : (float)(_Float16)v[j];
 }
 
-// Elements i .. i + 7 = v, rounded to the type.  kPast: past the caches, for
-// results larger than they are.
-template <bool kPast = false>
-__device__ __forceinline__ void store16(char *p, const u32x4 &v) {
-  typedef u32x4 u32x4_any __attribute__((aligned(2)));
-  if constexpr (kPast)
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(p));
-  else
-    __builtin_memcpy(p, &v, 16);
-}
-
-template <bool kPast = false>
+// Elements i .. i + 7 = v, rounded to the type.
 __device__ __forceinline__ void store8(void *base, int type, int64_t i, const float (&v)[8]) {
   if (type == COLI_MOE_F32) {
-    u32x4 u[2];
-    __builtin_memcpy(u, v, 32);
-    store16<kPast>(static_cast<char *>(base) + i * 4, u[0]);
-    store16<kPast>(static_cast<char *>(base) + i * 4 + 16, u[1]);
+    __builtin_memcpy(static_cast<float *>(base) + i, v, 32);
     return;
   }
-  u32x4 u;
+  uint32_t u[4];
   if (type == COLI_MOE_BF16) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) u[j] = to_bf16(v[2 * j]) | ((uint32_t)to_bf16(v[2 * j + 1]) << 16);
@@ -142,19 +128,44 @@ __device__ __forceinline__ void store8(void *base, int type, int64_t i, const fl
 #pragma unroll
     for (int j = 0; j < 4; ++j) u[j] = to_f16(v[2 * j]) | ((uint32_t)to_f16(v[2 * j + 1]) << 16);
   }
-  store16<kPast>(static_cast<char *>(base) + i * 2, u);
+  __builtin_memcpy(static_cast<uint16_t *>(base) + i, u, 16);
 }
 
 // The same, those below n.
-template <bool kPast = false>
 __device__ __forceinline__ void store8(void *base, int type, int64_t i, int n, const float (&v)[8]) {
   if (n >= 8) {
-    store8<kPast>(base, type, i, v);
+    store8(base, type, i, v);
     return;
   }
 #pragma unroll
   for (int j = 0; j < 7; ++j)
     if (j < n) store1(base, type, i + j, v[j]);
+}
+
+// The same, past the caches, for results larger than they are.
+__device__ __forceinline__ void store16_past(char *p, const u32x4 &v) {
+  typedef u32x4 u32x4_any __attribute__((aligned(2)));
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(p));
+}
+__device__ __forceinline__ void store8_past(void *base, int type, int64_t i, int n, const float (&v)[8]) {
+  if (n < 8) {
+    store8(base, type, i, n, v);
+    return;
+  }
+  u32x4 u[2];
+  if (type == COLI_MOE_F32) {
+    __builtin_memcpy(u, v, 32);
+    store16_past(static_cast<char *>(base) + i * 4, u[0]);
+    store16_past(static_cast<char *>(base) + i * 4 + 16, u[1]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = type == COLI_MOE_BF16 ? to_bf16(v[2 * j]) : to_f16(v[2 * j]);
+    const uint32_t hi = type == COLI_MOE_BF16 ? to_bf16(v[2 * j + 1]) : to_f16(v[2 * j + 1]);
+    u[0][j] = lo | hi << 16;
+  }
+  store16_past(static_cast<char *>(base) + i * 2, u[0]);
 }
 
 }  // namespace coli

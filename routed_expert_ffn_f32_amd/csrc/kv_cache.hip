@@ -199,10 +199,12 @@ __global__ __launch_bounds__(kRowThreads) void kv_read_kernel(KvView kv, coli_mo
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = page >= 0 ? (float)((code[u] << (28 - 4 * j)) >> 28) * sc : 0.0f;
         const int64_t t = t0 + token;
-        if (is_v)
-          store8<(kUnder > 1)>(a.v, kType, t * a.v_token + h * a.v_head + col, x);
+        void *out = is_v ? a.v : a.k;
+        const int64_t to = is_v ? t * a.v_token + h * a.v_head + col : t * a.k_token + h * a.k_head + col;
+        if constexpr (kUnder > 1)
+          store8_past(out, kType, to, 8, x);
         else
-          store8<(kUnder > 1)>(a.k, kType, t * a.k_token + h * a.k_head + col, x);
+          store8(out, kType, to, x);
       }
     }
   }

@@ -36,6 +36,12 @@ template <bool kPast>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_t a, RotaryShape sh, int split) {
   __shared__ float2 cs[kMaxPairs];
   const int half = a.part / 2;
+  auto store = [&](int64_t i, int n, const float (&v)[8]) {
+    if constexpr (kPast)
+      store8_past(a.out, a.type, i, n, v);
+    else
+      store8(a.out, a.type, i, n, v);
+  };
   // split: consecutive workgroups that share a token's units
   for (int64_t w = blockIdx.x; w < (int64_t)a.tokens * split; w += gridDim.x) {
     const int64_t t = w / split;
@@ -53,7 +59,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_
       if (k >= sh.pair_units) {
         const int c = a.part + 8 * (k - sh.pair_units), n = a.dim - c;
         unpack8(a.type, load_raw8(a.x, a.type, x + c, n), v);
-        store8<kPast>(a.out, a.type, o + c, n, v);
+        store(o + c, n, v);
       } else if (a.interleaved) {
         const int c = 8 * k, n = a.part - c;
         unpack8(a.type, load_raw8(a.x, a.type, x + c, n), v);
@@ -63,7 +69,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_
           y[j] = __builtin_fmaf(v[j], e.x, -(v[j + 1] * e.y));
           y[j + 1] = __builtin_fmaf(v[j], e.y, v[j + 1] * e.x);
         }
-        store8<kPast>(a.out, a.type, o + c, n, y);
+        store(o + c, n, y);
       } else {
         const int c = 8 * k, n = half - c;
         float b[8], z[8];
@@ -76,8 +82,8 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_
           y[j] = __builtin_fmaf(v[j], e.x, -(b[j] * e.y));
           z[j] = __builtin_fmaf(v[j], e.y, b[j] * e.x);
         }
-        store8<kPast>(a.out, a.type, o + c, n, y);
-        store8<kPast>(a.out, a.type, o + half + c, n, z);
+        store(o + c, n, y);
+        store(o + half + c, n, z);
       }
     }
   }
