@@ -375,6 +375,39 @@ def test_weights_of_single_tokens_in_wide_tables(dev, dim, page, seqs):
     assert int((sums != -1).sum()) == 2 * sum(lengths)
 
 
+@pytest.mark.parametrize("capacity", [64, 1 << 14])
+def test_many_sequences(dev, capacity):
+    """300 sequences of which a few have new tokens, so that hundreds begin
+    at the same token; tokens before the first and behind the last."""
+    new, lengths, dim = [0] * 300, [13 * i % 50 + 6 for i in range(300)], 64
+    for i, n in ((0, 2), (1, 1), (95, 3), (96, 1), (200, 6), (299, 2)):
+        new[i] = n
+    pool = Pool(lengths, 1, dim, 16, seed=51, capacity=capacity).fill()
+    T = sum(new) + 4
+    g = torch.Generator().manual_seed(52)
+    k, v, q = (torch.randn(T, 1, dim, generator=g).bfloat16() for _ in range(3))
+    q = torch.cat([q, -q, q * 2], 1)
+    cache = pool.to(dev, cm)
+    args = pool.table.to(dev), ints(lengths, dev), (offsets_of(new) + 1).to(dev)
+    cache.append(k.to(dev), v.to(dev), *args)
+    want, t = torch.zeros(2, T, 1, dim), 1
+    for s, n in enumerate(new):
+        for i in range(n):
+            pool.write(s, lengths[s] - n + i, k[t].float(), v[t].float())
+            for x, into in ((k, want[0]), (v, want[1])):
+                codes, scale = kv_ref.quantise(x[t].float())
+                into[t] = (codes * scale.double().repeat_interleave(64, -1)).float()
+            t += 1
+    for name in ("k_codes", "v_codes"):
+        assert torch.equal(getattr(cache, name).cpu(), getattr(pool, name))
+    for a, b in zip(cache.read(T, *args, dtype=torch.float32), want):
+        assert torch.equal(a.cpu(), b)
+    out, tol, _, _ = kv_ref.attention(pool, q[1: 1 + sum(new)], new)
+    got = cache.attention(q.to(dev), *args).cpu()
+    assert ((got[1: 1 + sum(new)].double() - out).abs() <= tol).all()
+    assert (got[0] == 0).all() and (got[1 + sum(new):] == 0).all()
+
+
 def test_long_eviction(dev):
     """More rows than LDS holds keys of, many of them alike."""
     L, keep, page = 40000, 11111, 256
