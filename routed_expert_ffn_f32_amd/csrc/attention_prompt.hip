@@ -133,6 +133,11 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), hf = lane >> 5, l32 = lane & 31;
   const int H = c.kv.p.kv_heads, ps = c.kv.p.page_size, S = c.rows.seqs;
 
+  // a call that may have prompts but has none is over here (8 sequences of 8 tokens: 13.6 us without)
+  if (S <= 64) {
+    const SeqSpan mine = seq_span(c.rows, min(lane, S - 1));
+    if (!__any(mine.n * c.group > c.few_rows)) return;
+  }
   for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
     const int h = (int)(item % H), split = (int)(item / H % c.prompt_splits);
     // the last tiles of a sequence see the most keys: they come first
