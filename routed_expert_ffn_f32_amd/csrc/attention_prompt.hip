@@ -278,7 +278,9 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
       k = wave_max(k);
       v = wave_max(v);
       least = 254 - wave_max(254 - least);
-      if (lane == 0) told[(step - s0) & 3] = make_uint4(k | v << 8 | least << 16 | any_bad, k_least, (uint32_t)there, (uint32_t)(there >> 32));
+      if (lane == 0)
+        told[(step - s0) & 3] = make_uint4(k | v << 8 | least << 16 | any_bad, k_least, (uint32_t)there,
+                                           (uint32_t)(there >> 32));
     };
     auto hear_scales = [&](int step) {
       const uint4 t = told[(step - s0) & 3];
@@ -519,7 +521,8 @@ __global__ __launch_bounds__(Prompt<D>::kThreads, D == 256 ? 1 : 2) void kv_prom
           const int page = key0 + k < end_key ? row_page(c.kv, table, c.rows.table_width, key0 + k) : -1;
           if (page < 0) continue;
           const int slot = (key0 + k) & (ps - 1);
-          const uint32_t *code = reinterpret_cast<const uint32_t *>(c.kv.p.k_codes + code_row(c.kv, page, h, slot) * (D / 2));
+          const uint32_t *code =
+              reinterpret_cast<const uint32_t *>(c.kv.p.k_codes + code_row(c.kv, page, h, slot) * (D / 2));
           const uint16_t *sc = c.kv.p.k_scales + scale_index<T::kGroups>(c.kv, page, h, 0, slot);
           int own = 0;
 #pragma unroll

@@ -102,8 +102,8 @@ hipError_t launch_rotary(const coli_moe_rotary_t &a, hipStream_t s) {
   const int blocks = (sh.units + kRotaryThreads - 1) / kRotaryThreads;
   const int split = a.tokens >= 1024 ? 1 : blocks < 8 ? blocks : 8;
   const int64_t work = (int64_t)a.tokens * split;
-  return launch(split == 1 ? rotary_kernel<true> : rotary_kernel<false>, dim3((unsigned)(work < (1 << 20) ? work : 1 << 20)), dim3(kRotaryThreads), 0, s, a, sh,
-                split);
+  return launch(split == 1 ? rotary_kernel<true> : rotary_kernel<false>,
+                dim3((unsigned)(work < (1 << 20) ? work : 1 << 20)), dim3(kRotaryThreads), 0, s, a, sh, split);
 }
 
 }  // namespace coli

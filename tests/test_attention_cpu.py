@@ -82,7 +82,9 @@ def test_append_and_read_refusals(entry):
     for bad in BAD_ROWS + BAD_TOKENS + BAD_ROW_POINTERS:
         assert call(r=rows(**bad)) == -4, bad
     two = rows(tokens=2)
-    for bad in (dict(type=3), dict(type=-1), dict(clear=2 if entry.endswith("read") else 1), dict(clear=-1), dict(k=None), dict(k=A + 1), dict(v=None), dict(v=B + 1), dict(k_token=-1),
+    for bad in (dict(type=3), dict(type=-1), dict(clear=-1),
+                dict(clear=2 if entry.endswith("read") else 1), dict(k=None), dict(k=A + 1), dict(v=None),
+                dict(v=B + 1), dict(k_token=-1),
                 dict(k_head=-1), dict(v_token=1 << 41)):
         assert call(r=two, v=values(**bad)) == -4, bad
     if entry == "coli_moe_kv_read":

@@ -12,7 +12,7 @@ import routed_expert_ffn_f32_amd as cm
 import synth
 from tests import kv_ref
 from tests.gpu_util import DeviceLayer
-from tests.kv_ref import Pool, U, offsets_of
+from tests.kv_ref import Pool, U, offsets_of, unpack
 
 pytestmark = pytest.mark.gpu
 BF16, I32 = torch.bfloat16, torch.int32
@@ -64,7 +64,8 @@ def test_block(dev):
         a, b = before[:, : hq + heads].cpu().double().split(dim // 2, -1)
         want = torch.cat([a * c - b * s, a * s + b * c], -1)
         # angles reduced in 64 bits, then a handful of float32 roundings and the type's
-        assert ((qk.cpu().double() - want).abs() <= 2.0 ** -8 * want.abs() + 16 * U * (a.abs() + b.abs()).repeat(1, 1, 2)).all()
+        size = (a.abs() + b.abs()).repeat(1, 1, 2)
+        assert ((qk.cpu().double() - want).abs() <= 2.0 ** -8 * want.abs() + 16 * U * size).all()
         assert torch.equal(qkv[:, hq + heads:], before[:, hq + heads:])
         cache.append(qkv[:, hq: hq + heads], qkv[:, hq + heads:], table, lengths, off)
         host = qkv.cpu().float()
@@ -78,7 +79,8 @@ def test_block(dev):
         ref = o.flatten(1).cpu().double() @ wo.double().t()
         mass = o.flatten(1).cpu().double().abs() @ wo.double().abs().t()
         total = ref + x.cpu().double()
-        assert ((z.cpu().double() - total).abs() <= 2.0 ** -8 * total.abs() + (hq * dim + 2) * U * (mass + total.abs())).all()
+        size = mass + total.abs()
+        assert ((z.cpu().double() - total).abs() <= 2.0 ** -8 * total.abs() + (hq * dim + 2) * U * size).all()
         got, want = layer.moe.forward_normed(z), layer.moe.forward(cm.rms_norm(z.float()))
         assert torch.isfinite(got).all() and (got != 0).any() and got.shape == want.shape == (n, H)
     layer.close()
@@ -289,6 +291,29 @@ def test_keys_far_apart(dev, dim, far, tokens):
     out, tol, _, _ = kv_ref.attention(near, q, [tokens])
     got = pool.to(dev, cm).attention(q.to(dev), pool.table.to(dev), ints([150], dev), ints([0, tokens], dev)).cpu()
     assert ((got.double() - out).abs() <= tol + 2.0 ** -30).all()
+
+
+@pytest.mark.parametrize("dim,page", [(64, 32), (128, 16), (256, 64)])
+@pytest.mark.parametrize("tokens", [1, 3, 45])
+def test_codes_and_scales_of_a_users_own(dev, dim, page, tokens):
+    """Codes of -8 and scales below 0, which append never makes, through the
+    attention, its weights and reads."""
+    pool = Pool([190], 2, dim, page, seed=61)
+    g = torch.Generator().manual_seed(62)
+    for scales in (pool.k_scales, pool.v_scales):
+        scales.copy_(torch.randn(scales.shape, generator=g) / 3)
+    assert (unpack(pool.k_codes) == -8).any() and (pool.k_scales < 0).any()
+    q = torch.randn(tokens, 4, dim, generator=g).half()
+    out, tol, w, wtol = kv_ref.attention(pool, q, [tokens])
+    cache = pool.to(dev, cm)
+    args = pool.table.to(dev), ints([190], dev), ints([0, tokens], dev)
+    got = cache.attention(q.to(dev), *args, accumulate=True).cpu()
+    assert ((got.double() - out).abs() <= tol).all()
+    want = pool.weights.double() + w
+    assert ((cache.weights.cpu().double() - want).abs() <= wtol + 2 * U * want)[w > 0].all()
+    k, v, _, _, _ = pool.rows(0, 190)
+    for a, b in zip(cache.read(tokens, *args, dtype=torch.float32), (k, v)):
+        assert torch.equal(a.cpu().double(), b[190 - tokens:])
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
