@@ -859,7 +859,9 @@ def rotary_frequencies(part: int, base: float = 10000.0, scaling: str = "none", 
     base    base * factor^(part / (part - 2)), which leaves the fastest pair as it is and divides the slowest by
             factor;
     parts   pairs that turn more than beta_fast times in the original context as they are, those that turn less than
-            beta_slow times / factor, a linear blend by pair index between; scale 0.1 ln(factor) + 1.
+            beta_slow times / factor, a linear blend by pair index between (its ends, rounded outwards, are held
+            within 0 and part - 1: in a long original context no pair need be a whole factor slower); scale
+            0.1 ln(factor) + 1.
 
     The scale (1 but for parts) is rotary's."""
     import math
@@ -881,7 +883,7 @@ def rotary_frequencies(part: int, base: float = 10000.0, scaling: str = "none", 
         if not beta_fast > beta_slow > 0:
             raise ValueError(f"beta_fast > beta_slow > 0, got {beta_fast} and {beta_slow}")
         pair = lambda turns: part * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
-        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), part // 2 - 1)
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), part - 1)
         slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         freq = freq * (1 - slow) + freq / factor * slow
         scale = 0.1 * math.log(factor) + 1
