@@ -194,9 +194,13 @@ __device__ __forceinline__ void load_keys(const Call &c, const Place<kSmallPages
   }
 }
 
+// An infinite scale counts as NaN: its products are Inf or 0, which a maximum
+// or a weight of 0 would hide.
+__device__ __forceinline__ float finite_or_nan(float v) { return fabsf(v) == INFINITY ? NAN : v; }
+
 // Scores of 16 keys, to be multiplied by the operand's scale: lane (column, j)
-// gets keys 4 j .. 4 j + 3.
-template <int D>
+// gets keys 4 j .. 4 j + 3.  kOdd: some scales of the keys may be infinite.
+template <int D, bool kOdd = false>
 __device__ __forceinline__ float4_t scores16(const KeyRegs<D> &r, int t, const QueryOperand<D> &f) {
   float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -204,7 +208,7 @@ __device__ __forceinline__ float4_t scores16(const KeyRegs<D> &r, int t, const Q
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_of(r.k[t][w / 4][w % 4]), f.b[w], acc, 0, 0, 0);
   const float4_t sc = scales4(r.s[t]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = sum_groups<D>(acc[i] * sc[i]);
+  for (int i = 0; i < 4; ++i) acc[i] = sum_groups<D>(acc[i] * (kOdd ? finite_or_nan(sc[i]) : sc[i]));
   return acc;
 }
 
@@ -274,6 +278,18 @@ __device__ __forceinline__ void read_keys(const char *step, int g, KeyRegs<D> &r
     }
     r.s[t] = *reinterpret_cast<const uint2 *>(step + Tile<D>::kScales + 64 * g + 32 * t + 8 * j);
   }
+}
+
+// Whether one of a step's scales, of the keys or of the values, is NaN or Inf:
+// a lane looks at two (D = 256: four).
+constexpr uint32_t kNoNumber = 0x00800080u;  // that takes an exponent of all ones, twice, past the sign's bit
+template <int D>
+__device__ __forceinline__ bool scales_odd(const char *step) {
+  const char *at = step + Tile<D>::kScales + (threadIdx.x & 63) * (D == 256 ? 8 : 4);
+  uint32_t v = *reinterpret_cast<const uint32_t *>(at);
+  v = (v & 0x7FFF7FFFu) + kNoNumber;
+  if constexpr (D == 256) v |= (*reinterpret_cast<const uint32_t *>(at + 4) & 0x7FFF7FFFu) + kNoNumber;
+  return __any((v & 0x80008000u) != 0);
 }
 
 template <int D>
@@ -393,13 +409,20 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
         fetch(ahead, at);
       }
       float4_t x[2], sv[2];
+      const bool odd = scales_odd<D>(step);
 #pragma unroll
       for (int t = 0; t < 2; ++t) x[t] = scores16<D>(kr, t, f);
       ValueRegs<D> vr;
       read_values<D>(step, q.g, vr);
 #pragma unroll
       for (int t = 0; t < 2; ++t) sv[t] = scales4(vr.s[t]);
-      if (__builtin_expect(!(key0 + kStepKeys - 1 <= all_hi && key0 >= all_lo && ok[0] && ok[1]), 0)) {
+      if (__builtin_expect(!(key0 + kStepKeys - 1 <= all_hi && key0 >= all_lo && ok[0] && ok[1]) || odd, 0)) {
+        if (odd) {
+          KeyRegs<D> again;
+          read_keys<D>(step, q.g, again);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) x[t] = scores16<D, true>(again, t, f);
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -407,7 +430,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
             const int key = key0 + 16 * t + 4 * j + i;
             const bool seen = ok[t] && key <= q.hi && key >= q.lo;
             x[t][i] = seen ? x[t][i] : -INFINITY;
-            sv[t][i] = seen ? sv[t][i] : 0.0f;
+            sv[t][i] = seen ? finite_or_nan(sv[t][i]) : 0.0f;
           }
       }
       float top = x[0][0];

@@ -1,0 +1,88 @@
+"""The 4-bit cache at the ends of its numbers and of its rows: scales that are
+no numbers or next to the largest, in every kernel of the attention."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import routed_expert_ffn_f32_amd as cm
+from tests import kv_ref
+from tests.kv_ref import Pool, U, offsets_of, pack
+
+pytestmark = pytest.mark.gpu
+BF16, F16, I32 = torch.bfloat16, torch.float16, torch.int32
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def ints(values, dev):
+    return torch.tensor(values, dtype=I32, device=dev)
+
+
+# tokens of 3 query heads on one key head: rows of one tile, of several tiles, of a prompt; one workgroup, and splits
+ROWS = pytest.mark.parametrize("tokens,length", [(1, 150), (9, 150), (22, 150), (1, 900), (9, 900)])
+
+
+@pytest.mark.parametrize("dim,page", [(64, 32), (128, 16), (128, 64), (256, 64)])
+@ROWS
+@pytest.mark.parametrize("bad", [INF, -INF, float("nan")])
+def test_key_scales_that_are_no_numbers(dev, dim, page, tokens, length, bad):
+    """A row whose key has such a scale makes every query that sees it NaN,
+    whatever the sign of its product; the others keep their results."""
+    pool = Pool([length], 1, dim, page, seed=1).fill()
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(tokens, 3, dim, generator=g).bfloat16()
+    row = length - tokens + tokens // 2  # queries from the middle on see it
+    p = pool.place(0, row)
+    out, tol, w, wtol = kv_ref.attention(pool, q, [tokens])
+    group = dim // 64 - 1
+    pool.k_scales[p[0], 0, group, p[1]] = bad
+    codes = torch.randint(1, 8, (dim,), generator=g)
+    # the group's product is above 0, below 0 and 0 for three of the heads
+    codes[dim - 64:] *= torch.where(q[tokens // 2, 1, dim - 64:] > 0, -1, 1)
+    pool.k_codes[p[0], 0, p[1]] = pack(codes)
+    q[:, 2, dim - 64:] = 0
+    for dtype in (BF16, F16):
+        cache = pool.to(dev, cm)
+        got = cache.attention(q.to(dtype).to(dev), pool.table.to(dev), ints([length], dev),
+                              offsets_of([tokens]).to(dev), accumulate=True).cpu().double()
+        see = tokens // 2
+        assert got[see:].isnan().all()
+        keep = [0, 1]  # head 2's queries are other ones now
+        assert ((got[:see, keep] - out[:see, keep]).abs() <= tol[:see, keep] + 2.0 ** -8 * out[:see, keep].abs()).all()
+        sums = cache.weights.cpu()
+        for r in (0, row):
+            at = pool.place(0, r)
+            assert sums[at[0], 0, at[1]].isnan()
+
+
+@pytest.mark.parametrize("dim,page", [(64, 32), (128, 16), (128, 64), (256, 64)])
+@ROWS
+@pytest.mark.parametrize("bad", [INF, -INF, float("nan")])
+def test_value_scales_that_are_no_numbers(dev, dim, page, tokens, length, bad):
+    """A value with such a scale makes the columns of its group NaN in the
+    queries that see it, also where its codes are not 0; nothing else."""
+    pool = Pool([length], 1, dim, page, seed=3).fill()
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn(tokens, 3, dim, generator=g).bfloat16()
+    row = length - tokens + tokens // 2
+    p = pool.place(0, row)
+    pool.v_codes[p[0], 0, p[1]] = pack(torch.arange(dim) % 15 - 7)
+    out, tol, w, wtol = kv_ref.attention(pool, q, [tokens])
+    pool.v_scales[p[0], 0, dim // 64 - 1, p[1]] = bad
+    for dtype in (BF16, F16):
+        cache = pool.to(dev, cm)
+        got = cache.attention(q.to(dtype).to(dev), pool.table.to(dev), ints([length], dev),
+                              offsets_of([tokens]).to(dev), accumulate=True).cpu().double()
+        see, cut = tokens // 2, dim - 64
+        assert got[see:, :, cut:].isnan().all()
+        for a, b, t in ((got[:see], out[:see], tol[:see]), (got[see:, :, :cut], out[see:, :, :cut], tol[see:, :, :cut])):
+            assert ((a - b).abs() <= t).all()
+        # weights are the keys' matter
+        want = pool.weights.double() + w
+        assert ((cache.weights.cpu().double() - want).abs() <= wtol + 2 * U * want)[w > 0].all()
