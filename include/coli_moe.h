@@ -793,9 +793,10 @@ int coli_moe_kv_read(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, co
  * over the tokens of the call and the query heads of its key head, for every
  * row that a query sees; other places are left as they were.  weights_out may
  * be kv->weights.  (Rows that several sequences of the call see get the sum of
- * some of them.)  The scores q . k have to be within float32's range.  A scale
- * of the cache that is NaN or Inf makes the results NaN of the queries that
- * see its row: a key's whole, a value's in the columns of its group.  In
+ * some of them.)  The scores q . k, and the sums of the sizes of their products,
+ * have to be within float32's range.  A scale of the cache that is NaN or Inf
+ * makes the results NaN of the queries that see its row: a key's whole, a
+ * value's in the columns of its group.  In
  * sequences of more than 64 query rows (tokens times q_heads / kv_heads) values
  * below 2^-77 of the largest of their 64 neighbouring rows, or below 2^-100 of
  * the largest before them, may count as 0.  Out rows of tokens in no sequence

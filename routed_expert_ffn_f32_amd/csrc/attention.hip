@@ -198,8 +198,18 @@ __device__ __forceinline__ void load_keys(const Call &c, const Place<kSmallPages
 // or a weight of 0 would hide.
 __device__ __forceinline__ float finite_or_nan(float v) { return fabsf(v) == INFINITY ? NAN : v; }
 
-// Scores of 16 keys, to be multiplied by the operand's scale: lane (column, j)
-// gets keys 4 j .. 4 j + 3.  kOdd: some scales of the keys may be infinite.
+// A query's lifted products with codes are up to 2^27, so scales from 2^100 on
+// may take them past float32's range although the scores are within it.  Such a
+// step's scales are multiplied by this first and its scores by the inverse
+// afterwards; queries so large that the inverse would pass the range itself
+// have scores within it only with scales that need no care.
+constexpr float kDown = 0x1p-27f;
+__device__ __forceinline__ float scores_down(float unit) { return unit < 0x1p100f ? kDown : 1.0f; }
+__device__ __forceinline__ float odd_unit(float unit) { return unit < 0x1p100f ? unit * (1 / kDown) : unit; }
+
+// Scores of 16 keys, to be multiplied by the operand's unit: lane (column, j)
+// gets keys 4 j .. 4 j + 3.  kOdd: some scales of the keys may be infinite or
+// above 2^100, and what the scores are to be multiplied by is odd_unit.
 template <int D, bool kOdd = false>
 __device__ __forceinline__ float4_t scores16(const KeyRegs<D> &r, int t, const QueryOperand<D> &f) {
   float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -208,7 +218,8 @@ __device__ __forceinline__ float4_t scores16(const KeyRegs<D> &r, int t, const Q
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_of(r.k[t][w / 4][w % 4]), f.b[w], acc, 0, 0, 0);
   const float4_t sc = scales4(r.s[t]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = sum_groups<D>(acc[i] * (kOdd ? finite_or_nan(sc[i]) : sc[i]));
+  for (int i = 0; i < 4; ++i)
+    acc[i] = sum_groups<D>(acc[i] * (kOdd ? finite_or_nan(sc[i]) * scores_down(f.unit) : sc[i]));
   return acc;
 }
 
@@ -280,15 +291,21 @@ __device__ __forceinline__ void read_keys(const char *step, int g, KeyRegs<D> &r
   }
 }
 
-// Whether one of a step's scales, of the keys or of the values, is NaN or Inf:
-// a lane looks at two (D = 256: four).
-constexpr uint32_t kNoNumber = 0x00800080u;  // that takes an exponent of all ones, twice, past the sign's bit
+// Of two scales: the sign's bits are those that are NaN, Inf or from 2^100 on.
+__device__ __forceinline__ uint32_t odd_bits(uint32_t two) { return (two & 0x7FFF7FFFu) + 0x0E800E80u; }
+// Whether one of a step's scales is, of the keys or of the values: a lane looks
+// at two (D = 256: four).
 template <int D>
 __device__ __forceinline__ bool scales_odd(const char *step) {
   const char *at = step + Tile<D>::kScales + (threadIdx.x & 63) * (D == 256 ? 8 : 4);
-  uint32_t v = *reinterpret_cast<const uint32_t *>(at);
-  v = (v & 0x7FFF7FFFu) + kNoNumber;
-  if constexpr (D == 256) v |= (*reinterpret_cast<const uint32_t *>(at + 4) & 0x7FFF7FFFu) + kNoNumber;
+  uint32_t v = odd_bits(*reinterpret_cast<const uint32_t *>(at));
+  if constexpr (D == 256) v |= odd_bits(*reinterpret_cast<const uint32_t *>(at + 4));
+  return __any((v & 0x80008000u) != 0);
+}
+// The same of a step's keys in registers.
+template <int D>
+__device__ __forceinline__ bool keys_odd(const KeyRegs<D> &r) {
+  const uint32_t v = odd_bits(r.s[0].x) | odd_bits(r.s[0].y) | odd_bits(r.s[1].x) | odd_bits(r.s[1].y);
   return __any((v & 0x80008000u) != 0);
 }
 
@@ -410,6 +427,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
       }
       float4_t x[2], sv[2];
       const bool odd = scales_odd<D>(step);
+      float unit = f.unit;
 #pragma unroll
       for (int t = 0; t < 2; ++t) x[t] = scores16<D>(kr, t, f);
       ValueRegs<D> vr;
@@ -422,6 +440,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
           read_keys<D>(step, q.g, again);
 #pragma unroll
           for (int t = 0; t < 2; ++t) x[t] = scores16<D, true>(again, t, f);
+          unit = odd_unit(f.unit);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -436,16 +455,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
       float top = x[0][0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e / 4][e % 4]);
-      top *= f.unit;
+      top *= unit;
       float w[8], sum;
       auto weigh = [&]() {
         const float base = m == -INFINITY ? 0.0f : m, up = weight_lift(ex);
         float z[8];
         if (__builtin_expect(far, 0)) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = __builtin_fmaf(x[e / 4][e % 4], f.unit, -base) * c.cs;
+          for (int e = 0; e < 8; ++e) z[e] = __builtin_fmaf(x[e / 4][e % 4], unit, -base) * c.cs;
         } else {
-          const float by = fmaxf(f.unit * c.cs, 0x1p-126f), less = base * c.cs;  // -Inf times by is -Inf
+          const float by = fmaxf(unit * c.cs, 0x1p-126f), less = base * c.cs;  // -Inf times by is -Inf
 #pragma unroll
           for (int e = 0; e < 8; ++e) z[e] = __builtin_fmaf(x[e / 4][e % 4], by, -less);
         }
@@ -470,7 +489,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
         most = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          most = fmaxf(most, fabsf(__builtin_amdgcn_exp2f(__builtin_fmaf(x[e / 4][e % 4], f.unit, -base) * c.cs) *
+          most = fmaxf(most, fabsf(__builtin_amdgcn_exp2f(__builtin_fmaf(x[e / 4][e % 4], unit, -base) * c.cs) *
                                    sv[e / 4][e % 4]));
         most = fmaxf(max_over_j(most), max_over_j(big) * weight_unlift(ex) * fade);
         const int ex1 = lift_exponent(most);
@@ -644,14 +663,19 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c,
 
 // Softmax weights of 16 keys, summed over the columns of a tile.
 template <int D>
-__device__ __forceinline__ void add_weights(const KeyRegs<D> &kr, int t, bool there, int key, const Column &q,
+__device__ __forceinline__ void add_weights(const KeyRegs<D> &kr, int t, bool odd, bool there, int key, const Column &q,
                                             const QueryOperand<D> &f, float2 ml, float cs, float share,
                                             float4_t &sum) {
-  const float4_t p = scores16<D>(kr, t, f);
+  float4_t p = scores16<D>(kr, t, f);
+  float unit = f.unit;
+  if (__builtin_expect(odd, 0)) {
+    p = scores16<D, true>(kr, t, f);
+    unit = odd_unit(f.unit);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const bool seen = q.live && q.g == 0 && there && key + i <= q.hi && key + i >= q.lo;
-    sum[i] += seen ? weight_again(__builtin_fmaf(p[i], f.unit, -ml.x), cs) * share : 0.0f;
+    sum[i] += seen ? weight_again(__builtin_fmaf(p[i], unit, -ml.x), cs) * share : 0.0f;
   }
 }
 
@@ -747,8 +771,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
         if (n + 1 < count) load(n + 1, next);
         const int key = key0 + n * kStepKeys + 4 * j;
         float4_t sum[2] = {};
+        const bool odd = keys_odd<D>(now.kr);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, sum[u]);
+        for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, odd, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, sum[u]);
         const float4_t v = fold_weights(sum[0], sum[1]);
         if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
         now = next;

@@ -86,3 +86,52 @@ def test_value_scales_that_are_no_numbers(dev, dim, page, tokens, length, bad):
         # weights are the keys' matter
         want = pool.weights.double() + w
         assert ((cache.weights.cpu().double() - want).abs() <= wtol + 2 * U * want)[w > 0].all()
+
+
+@pytest.mark.parametrize("dim,page", [(64, 32), (128, 16), (128, 64), (256, 64)])
+@ROWS
+@pytest.mark.parametrize("power", [95, 105, 120])
+def test_key_scales_next_to_the_largest(dev, dim, page, tokens, length, power):
+    """Keys of 2^power and queries as small: scores of ordinary size, from
+    products that are within float32's range whatever the order."""
+    pool = Pool([length], 1, dim, page, seed=5).fill()
+    g = torch.Generator().manual_seed(6)
+    pool.k_scales *= 2.0 ** power
+    q = (torch.randn(tokens, 3, dim, generator=g) * 2.0 ** -power).bfloat16()
+    q[:, 1] *= 2.0 ** 4  # scores far apart
+    out, tol, w, wtol = kv_ref.attention(pool, q, [tokens])
+    cache = pool.to(dev, cm)
+    got = cache.attention(q.to(dev), pool.table.to(dev), ints([length], dev), offsets_of([tokens]).to(dev),
+                          accumulate=True).cpu().double()
+    assert ((got - out).abs() <= tol).all()
+    want = pool.weights.double() + w
+    assert ((cache.weights.cpu().double() - want).abs() <= wtol + 2 * U * want)[w > 0].all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("tokens", [1, 9, 22])
+@pytest.mark.parametrize("power", [110, 124])
+def test_one_large_key_among_small_ones(dev, dim, tokens, power):
+    """A key of 2^power that takes all of a query's weight, or none, beside keys
+    of ordinary size whose scores are next to nothing then; queries of another
+    size that see the ordinary ones alone."""
+    pool = Pool([150], 1, dim, 64, seed=7).fill()
+    g = torch.Generator().manual_seed(8)
+    toward = torch.sign(torch.randn(1, dim, generator=g))
+    row, see = 150 - tokens + tokens // 2, tokens // 2
+    q = torch.randn(tokens, 3, dim, generator=g).bfloat16()
+    q[see:, 0] = (toward * 2.0 ** -20).bfloat16()
+    q[see:, 1] = (toward * -(2.0 ** -20)).bfloat16()
+    q[see:, 2] = (toward * 2.0 ** (1 - power)).bfloat16()
+    # all scores of heads 0 and 1 are below 2^-10 where the row is of zeros, so the weights are alike: without the row,
+    # or with it in full, what they are off by is at most a hundredth more
+    pool.write(0, row, 0 * toward, torch.randn(1, dim, generator=g))
+    _, small, _, _ = kv_ref.attention(pool, q, [tokens])
+    v = pool.rows(0, 150)[1][row, 0]
+    pool.write(0, row, toward * 2.0 ** power, v.float()[None])
+    assert torch.equal(pool.rows(0, 150)[1][row, 0], v)
+    out, tol, _, _ = kv_ref.attention(pool, q, [tokens])
+    tol[see:, 1] = 1.01 * small[see:, 1]
+    tol[see:, 0] = 2.0 ** -8 * v.abs()
+    got = pool.to(dev, cm).attention(q.to(dev), pool.table.to(dev), ints([150], dev), offsets_of([tokens]).to(dev)).cpu()
+    assert ((got.double() - out).abs() <= tol).all()
