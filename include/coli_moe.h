@@ -791,8 +791,10 @@ int coli_moe_kv_read(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, co
  * zeros.  With weights_out (which needs kv->weights), also
  *   weights_out[r] = kv->weights[r] + sum of the softmax weights of row r
  * over the tokens of the call and the query heads of its key head, for every
- * row that a query sees; other places are left as they were.  weights_out may
- * be kv->weights.  (Rows that several sequences of the call see get the sum of
+ * row that a query sees; other places are left as they were.  A weight comes from
+ * its score computed once more: it is at most 1, but where float32 tells a row's
+ * scores apart by steps far above 1 (2^30: 128) a query's need not sum to 1.
+ * weights_out may be kv->weights.  (Rows that several sequences of the call see get the sum of
  * some of them.)  The scores q . k, and the sums of the sizes of their products,
  * have to be within float32's range.  A scale of the cache that is NaN or Inf
  * makes the results NaN of the queries that see its row: a key's whole, a

@@ -27,12 +27,14 @@ constexpr float kFar = 16.0f;
 // they are brought to a new one.
 constexpr float kSlack = 8.0f;
 
-// 2^-kSlack of exp2((v - m) cs) for a score v computed once more: at most 1,
-// which the rounding of scores too large for float32 to tell apart could
-// otherwise pass by far.  share_again takes it back.  A NaN row's share is NaN.
-__device__ __forceinline__ float weight_again(float difference, float cs) {
-  return __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(__builtin_fmaf(difference, cs, -kSlack)), 0.0f, 1.0f);
+// A weight exp2((v - m) cs) / sum from a score v computed once more.  Scores too
+// large for float32 to tell apart may pass m by far then, so 2^-kSlack of the
+// exponential is held within 2^-kSlack of the row's sum: a weight is at most 1.
+// share_again takes both back.  A NaN row's share is NaN.
+__device__ __forceinline__ float weight_again(float difference, float cs, float limit) {
+  return __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(__builtin_fmaf(difference, cs, -kSlack)), 0.0f, limit);
 }
+__device__ __forceinline__ float limit_again(float sum) { return sum * 0x1p-8f; }
 __device__ __forceinline__ float share_again(float sum) { return sum != 0.0f ? 0x1p8f / sum : 0.0f; }
 
 // Power of two that brings v (>= 0) into [2^14, 2^15), within float32's range,
@@ -81,7 +83,7 @@ struct Call {
   float2 *part_ml; // [row][split] maximum (of scores without cs) and sum
   float2 *ml;      // [row], for the weights; NULL: not wanted
   char *q_halves;  // for the weights of more rows than a tile: [key head][token][head of the group][D] halves
-  float4 *q_info;  // and each row's power of two, its maximum, 1 / its sum
+  float4 *q_info;  // and each row's power of two, its maximum, share_again and limit_again
 };
 
 // Range of keys that the rows r0 .. r1 of a sequence's key head see.

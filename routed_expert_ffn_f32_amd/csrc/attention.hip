@@ -665,7 +665,7 @@ __global__ __launch_bounds__(kTileThreads) void kv_attention_join_kernel(Call c,
 template <int D>
 __device__ __forceinline__ void add_weights(const KeyRegs<D> &kr, int t, bool odd, bool there, int key, const Column &q,
                                             const QueryOperand<D> &f, float2 ml, float cs, float share,
-                                            float4_t &sum) {
+                                            float limit, float4_t &sum) {
   float4_t p = scores16<D>(kr, t, f);
   float unit = f.unit;
   if (__builtin_expect(odd, 0)) {
@@ -675,7 +675,7 @@ __device__ __forceinline__ void add_weights(const KeyRegs<D> &kr, int t, bool od
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const bool seen = q.live && q.g == 0 && there && key + i <= q.hi && key + i >= q.lo;
-    sum[i] += seen ? weight_again(__builtin_fmaf(p[i], unit, -ml.x), cs) * share : 0.0f;
+    sum[i] += seen ? weight_again(__builtin_fmaf(p[i], unit, -ml.x), cs, limit) * share : 0.0f;
   }
 }
 
@@ -766,14 +766,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
       const float2 ml = q.live ? c.ml[(int64_t)q.token * c.a.q_heads + q.head] : make_float2(0.0f, 0.0f);
       QueryOperand<D> f;
       load_query<D>(c, q, f);
-      const float share = share_again(ml.y);
+      const float share = share_again(ml.y), limit = limit_again(ml.y);
       for (int n = 0; n < count; ++n) {
         if (n + 1 < count) load(n + 1, next);
         const int key = key0 + n * kStepKeys + 4 * j;
         float4_t sum[2] = {};
         const bool odd = keys_odd<D>(now.kr);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) add_weights<D>(now.kr, u, odd, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, sum[u]);
+        for (int u = 0; u < 2; ++u)
+          add_weights<D>(now.kr, u, odd, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, limit, sum[u]);
         const float4_t v = fold_weights(sum[0], sum[1]);
         if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
         now = next;

@@ -60,7 +60,8 @@ __global__ __launch_bounds__(256) void kv_weight_rows_kernel(Call c, int64_t row
     *reinterpret_cast<half8_t *>(c.q_halves + row * (2 * D) + (piece ^ (int)(in_head & 7)) * 16) = y;
     if (piece == 0) {
       const float2 ml = c.ml[id];
-      c.q_info[row] = make_float4(unlift(ex), ml.x == -INFINITY ? 0.0f : ml.x, share_again(ml.y), 0.0f);
+      c.q_info[row] = make_float4(unlift(ex), ml.x == -INFINITY ? 0.0f : ml.x, share_again(ml.y),
+                                  limit_again(ml.y));
     }
   }
 }
@@ -196,7 +197,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_row_weights_kernel(Call c, 
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int key = 32 * u + 8 * (i / 4) + i % 4;
-              const float w = weight_again(__builtin_fmaf(x[u][i], fk[u][i] * f.x, -f.y), c.cs) * f.z;
+              const float w = weight_again(__builtin_fmaf(x[u][i], fk[u][i] * f.x, -f.y), c.cs, f.w) * f.z;
               sum[u][i] += key <= hi && key >= lo ? w : 0.0f;
             }
           continue;
@@ -205,7 +206,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_row_weights_kernel(Call c, 
         for (int u = 0; u < kTiles; ++u)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            sum[u][i] = __builtin_fmaf(weight_again(__builtin_fmaf(x[u][i], fk[u][i] * f.x, -f.y), c.cs), f.z,
+            sum[u][i] = __builtin_fmaf(weight_again(__builtin_fmaf(x[u][i], fk[u][i] * f.x, -f.y), c.cs, f.w), f.z,
                                        sum[u][i]);
       }
       // sums over the 32 columns; lane (r, hf) with r < 16 stores key r's register

@@ -135,3 +135,37 @@ def test_one_large_key_among_small_ones(dev, dim, tokens, power):
     tol[see:, 0] = 2.0 ** -8 * v.abs()
     got = pool.to(dev, cm).attention(q.to(dev), pool.table.to(dev), ints([150], dev), offsets_of([tokens]).to(dev)).cpu()
     assert ((got.double() - out).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("tokens", [2, 50, 120])
+@pytest.mark.parametrize("length", [130, 900])
+def test_a_weight_is_at_most_one(dev, dim, tokens, length):
+    """Scores of 2^30, where neighbouring float32 numbers are 128 apart, so that
+    a score computed once more may pass its row's maximum by far: still no query
+    adds more than 1 to a key."""
+    g = torch.Generator().manual_seed(dim + tokens + length)
+    pool = Pool([length], 1, dim, 64, seed=9)
+    pool.weights.zero_()
+    keys = torch.randn(length, 1, dim, generator=g) * 8192
+    for r in range(length):
+        pool.write(0, r, keys[r], torch.randn(1, dim, generator=g))
+    at = length - tokens + torch.arange(tokens)
+    chosen = (at * 7919) % (length - tokens)
+    q = torch.zeros(tokens, 2, dim)
+    q[:, 0] = keys[chosen, 0] * 4  # of its own key by far the largest score
+    q = q.bfloat16()
+    cache = pool.to(dev, cm)
+    cache.attention(q.to(dev), pool.table.to(dev), ints([length], dev), ints([0, tokens], dev), accumulate=True)
+    # head 1 is of zeros: all it sees alike
+    most = torch.zeros(length, dtype=torch.float64)
+    z = (q[:, 0].double() @ pool.rows(0, length)[0][:, 0].t()) * dim ** -0.5
+    for i in range(tokens):
+        seen = z[i, : at[i] + 1]
+        top = seen.argmax()
+        assert seen.topk(2).values.diff() < -1e7  # all others' weights are 0
+        most[top] += 1
+        most[: at[i] + 1] += 1 / (int(at[i]) + 1)
+    sums = cache.weights.cpu().double()
+    got = torch.stack([sums[p[0], 0, p[1]] for p in (pool.place(0, r) for r in range(length))])
+    assert (got <= most * (1 + (2 * tokens + 256) * U)).all()
