@@ -832,13 +832,15 @@ int coli_moe_kv_attention(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *row
  * Eviction: of every sequence and key head with more than `keep` rows, the
  * first `first` rows, the last `recent` and, of those between, the ones with
  * the largest kv->weights (ties: the lower row; NaN above everything) are
- * kept, `keep` in all, and all rows of shorter sequences.  In their order
- * they are copied, weights included, to rows 0 .. of the pages of `into`
+ * kept, `keep` in all, and all rows of shorter sequences.  Rows that do not
+ * exist are no rows here: they are neither counted nor kept.  In their order
+ * the rows are copied, weights included, to rows 0 .. of the pages of `into`
  * (pages of the same cache, none of them in the table: other places are only
  * read, so pages may be shared between sequences and the call repeated).
  * kept[s][h][i] is the row that went to row i (-1 behind the last), and
- * new_lengths[s] = min(lengths[s], keep), 0 at least.  Rows that do not exist have weight
- * 0 when they compete and leave their places in `into` as they were.
+ * new_lengths[s] the number of rows kept: an attention over `into` with these
+ * lengths sees rows of the sequence alone.  (A row whose place in `into` does
+ * not exist is dropped.)
  * rows->tokens and rows->offsets are not looked at.
  */
 typedef struct {

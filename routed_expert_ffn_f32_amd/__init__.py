@@ -1091,9 +1091,9 @@ class KVCache:
         first `first`, the last `recent` and the heaviest between them (the
         cache's weights; ties: the lower row), `keep` in all, and copies them
         in their order, with their weights, to rows 0 .. of the pages `into`
-        int32 [S, width] (none of them in the table).  Returns (kept int32 [S,
-        kv heads, keep], the row each came from or -1; new lengths int32
-        [S])."""
+        int32 [S, width] (none of them in the table).  Rows whose page is not
+        there are neither counted nor kept.  Returns (kept int32 [S, kv heads,
+        keep], the row each came from or -1; new lengths int32 [S])."""
         import torch
         dev = self.device
         if self.weights is None:

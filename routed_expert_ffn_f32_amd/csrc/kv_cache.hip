@@ -225,46 +225,87 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// A row that does not exist is below every weight.
 __device__ __forceinline__ uint32_t row_key(const KvView &kv, const int32_t *table, int width, int h, int row) {
   const int page = row_page(kv, table, width, row);
-  if (page < 0) return rank_key(0.0f);
+  if (page < 0) return 0;
   return rank_key(kv.p.weights[code_row(kv, page, h, row & (kv.p.page_size - 1))]);
+}
+
+// The row that `rank` rows that exist stand before, of the sequence's first len;
+// called by whole waves.
+__device__ int row_of_rank(const KvView &kv, const int32_t *table, int width, int len, int rank) {
+  const int lane = threadIdx.x & 63, pages = (len + kv.p.page_size - 1) >> kv.shift;
+  int left = rank >> kv.shift;  // pages that exist, before the row's
+  for (int i0 = 0; i0 < pages; i0 += 64) {
+    const int i = i0 + lane;
+    const bool there = i < pages && row_page(kv, table, width, (int64_t)i << kv.shift) >= 0;
+    const uint64_t mask = __ballot(there);
+    const int n = __popcll(mask);
+    if (left < n) {
+      const uint64_t it = __ballot(there && __popcll(mask & ((1ull << lane) - 1)) == left);
+      return min(((i0 + __builtin_ctzll(it)) << kv.shift) + (rank & (kv.p.page_size - 1)), len);
+    }
+    left -= n;
+  }
+  return len;
 }
 
 // The rows that one sequence's key head keeps: the c-th largest key of the
 // middle rows is found digit by digit (8 bits, largest first), then rows are
 // kept while they are first, recent, above it, or among the first of those
 // equal to it; each thread has rows side by side, so one sum over the
-// workgroup places them.  Bound by the latency of its steps: every wave adds up
-// a digit's counts for itself, so that a digit is one barrier.  600 rows 8 us,
-// 16 sequences of up to 8192 rows, 8 heads, 19 us.  (Counting a wave's equal
-// digits together before LDS is asked: 35.)
+// workgroup places them.  Rows that do not exist are none of these: the first
+// and the recent are counted among those that do.  Bound by the latency of its
+// steps: every wave adds up a digit's counts for itself, so that a digit is one
+// barrier.  600 rows 8 us, 16 sequences of up to 8192 rows, 8 heads, 19 us.
+// (Counting a wave's equal digits together before LDS is asked: 35.)
 __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(KvView kv, coli_moe_kv_rows_t r,
                                                                    coli_moe_kv_evict_t a) {
   constexpr int kWaves = kSelectThreads / 64;
   __shared__ uint32_t keys[kSelectRows];
   __shared__ int hist[4][256];
   __shared__ int2 sums[kWaves];
+  __shared__ int lost[2][kWaves];
   static_assert(4 * 256 == kSelectThreads, "a count a thread");
   const int H = kv.p.kv_heads, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int turn = 0;
   for (int64_t w = blockIdx.x; w < (int64_t)r.seqs * H; w += gridDim.x) {
     const int s = (int)(w / H), h = (int)(w % H);
     const int32_t *table = r.table + s * r.table_stride;
     // lengths may be anything; at most 2^30 rows stand in a table
     const int len = min(max(r.lengths[s], 0), r.table_width << kv.shift);
-    const int keep = min(a.keep, len);
+    // rows among them that do not exist
+    int gone = 0;
+    for (int i = tid << kv.shift; i < len; i += kSelectThreads << kv.shift)
+      if (row_page(kv, table, r.table_width, i) < 0) gone += min(kv.p.page_size, len - i);
+    if (__any(gone > 0))
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) gone += __shfl_xor(gone, d);
+    if (lane == 0) lost[turn][wave] = gone;
+    __syncthreads();  // and of the item before, all is read
+    gone = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) gone += lost[turn][i];
+    turn ^= 1;
+    const int have = len - gone;
+    const int keep = min(a.keep, have);
     int32_t *kept = a.kept + w * a.keep;
     if (h == 0 && tid == 0) a.new_lengths[s] = keep;
     for (int i = keep + tid; i < a.keep; i += kSelectThreads) kept[i] = -1;
-    if (len <= a.keep) {
+    if (len <= a.keep && gone == 0) {
       for (int i = tid; i < keep; i += kSelectThreads) kept[i] = i;
       continue;
     }
-    const int lo = a.first, hi = len - a.recent;
-    int need = keep - a.first - a.recent;  // of the middle rows, 0 .. hi - lo
+    // the middle: rows lo .. hi - 1
+    int lo = a.first, hi = len - a.recent;
+    if (__builtin_expect(gone > 0, 0)) {
+      lo = have > a.keep ? row_of_rank(kv, table, r.table_width, len, a.first) : len;
+      hi = have > a.keep ? row_of_rank(kv, table, r.table_width, len, have - a.recent) : len;
+    }
+    int need = have > a.keep ? keep - a.first - a.recent : 0;  // of the middle rows that exist, fewer than there are
     const bool any = need > 0;
     uint32_t key = 0, known = 0;  // digits found so far, and their mask
-    __syncthreads();              // of the item before, all is read
     auto key_of = [&](int row) {
       return row - lo < kSelectRows ? keys[row - lo] : row_key(kv, table, r.table_width, h, row);
     };
@@ -315,12 +356,15 @@ __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(KvView kv, co
     // need: rows equal to `key` still to take, in order
     const int each = (len + kSelectThreads - 1) / kSelectThreads;
     const int from = min(tid * each, len), to = min(from + each, len);
+    auto outside = [&](int row) {  // the first and the recent ones
+      return (row < lo || row >= hi) && (gone == 0 || row_page(kv, table, r.table_width, row) >= 0);
+    };
     int same = 0, above = 0;
     for (int row = from; row < to; ++row) {
       const bool middle = row >= lo && row < hi;
       const uint32_t k = middle && any ? key_of(row) : 0;
       same += middle && any && k == key ? 1 : 0;
-      above += !middle || (any && k > key) ? 1 : 0;
+      above += outside(row) || (any && k > key) ? 1 : 0;
     }
     // of the threads before this one
     int rank = same, at = above;
@@ -338,7 +382,7 @@ __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(KvView kv, co
       const bool middle = row >= lo && row < hi;
       const uint32_t k = middle && any ? key_of(row) : 0;
       const bool equal = middle && any && k == key;
-      if (!middle || (any && k > key) || (equal && rank < need)) kept[at++] = row;
+      if (outside(row) || (any && k > key) || (equal && rank < need)) kept[at++] = row;
       rank += equal ? 1 : 0;
     }
   }
