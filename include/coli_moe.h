@@ -791,19 +791,20 @@ int coli_moe_kv_read(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, co
  * zeros.  With weights_out (which needs kv->weights), also
  *   weights_out[r] = kv->weights[r] + sum of the softmax weights of row r
  * over the tokens of the call and the query heads of its key head, for every
- * row that a query sees; other places are left as they were.  A weight comes from
- * its score computed once more: it is at most 1, but where float32 tells a row's
- * scores apart by steps far above 1 (2^30: 128) a query's need not sum to 1.
- * weights_out may be kv->weights.  (Rows that several sequences of the call see get the sum of
- * some of them.)  The scores q . k, and the sums of the sizes of their products,
- * have to be within float32's range.  A scale of the cache that is NaN or Inf
- * makes the results NaN of the queries that see its row: a key's whole, a
- * value's in the columns of its group.  In
- * sequences of more than 64 query rows (tokens times q_heads / kv_heads) values
- * below 2^-77 of the largest of their 64 neighbouring rows, or below 2^-100 of
- * the largest before them, may count as 0.  Out rows of tokens in no sequence
- * are left as they were (clear 0) or set to 0 (clear 1).  The same call gives
- * the same bits.
+ * row that a query sees; other places are left as they were.  A weight comes
+ * from its score computed once more: it is at most 1, but where float32's
+ * neighbours are far apart (at scores of 2^30: 128) a query's need not sum to 1.
+ * weights_out may be kv->weights.  Rows that several sequences of the call see
+ * (pages of a common prefix) get the sum over all of them, added in no fixed
+ * order, so that its last bits may differ from call to call.  The scores q . k,
+ * and the sums of the sizes of their products, have to be within float32's
+ * range.  A scale of the cache that is NaN or Inf makes the results NaN of the
+ * queries that see its row: a key's whole, a value's in the columns of its
+ * group.  In sequences of more than 64 query rows (tokens times q_heads /
+ * kv_heads) values below 2^-77 of the largest of their 64 neighbouring rows, or
+ * below 2^-100 of the largest before them, may count as 0.  Out rows of tokens
+ * in no sequence are left as they were (clear 0) or set to 0 (clear 1).  But for
+ * the weights of rows of several sequences the same call gives the same bits.
  */
 typedef struct {
   int32_t q_heads;  /* a multiple of kv_heads, at most 256 times as many */

@@ -1040,7 +1040,8 @@ class KVCache:
         one.  scale: default 1 / sqrt(dim).  accumulate adds each row's softmax
         weights, over the tokens and the heads that share its key head, to the
         cache's weights, or, with weights_out (a tensor like them), stores the
-        sums there.  A token that sees no row gives zeros; tokens in no
+        sums there; rows that several sequences see get the sum over all of
+        them, in no fixed order.  A token that sees no row gives zeros; tokens in no
         sequence are left as they were in `out` (a fresh result holds zeros).
         Forward only: no gradient goes through it.  coli_moe_kv_attention in
         include/coli_moe.h gives the formulas."""

@@ -37,6 +37,10 @@ __device__ __forceinline__ float weight_again(float difference, float cs, float 
 __device__ __forceinline__ float limit_again(float sum) { return sum * 0x1p-8f; }
 __device__ __forceinline__ float share_again(float sum) { return sum != 0.0f ? 0x1p8f / sum : 0.0f; }
 
+// Adds to a place of weights_out, which several sequences may share: each adds
+// its own sum, once, in no order.
+__device__ __forceinline__ void add_weight(float *to, float v) { unsafeAtomicAdd(to, v); }
+
 // Power of two that brings v (>= 0) into [2^14, 2^15), within float32's range,
 // and its inverse.
 __device__ __forceinline__ int lift_exponent(float v) { return max((int)(__float_as_uint(v) >> 23) & 255, 20); }
@@ -84,6 +88,8 @@ struct Call {
   float2 *ml;      // [row], for the weights; NULL: not wanted
   char *q_halves;  // for the weights of more rows than a tile: [key head][token][head of the group][D] halves
   float4 *q_info;  // and each row's power of two, its maximum, share_again and limit_again
+  int blocks;      // workgroups of the tiles' kernel that take tiles; those after them copy weights
+  int copy_parts;  // of a sequence's key head, whose weights go to weights_out before the sums do; 0: they are there
 };
 
 // Range of keys that the rows r0 .. r1 of a sequence's key head see.

@@ -236,6 +236,35 @@ __device__ __forceinline__ void clear_outside(const Call &c, int D) {
   }
 }
 
+// weights_out = weights for the rows that a query sees, where the sums are not
+// added to the cache's own weights: part `item` of the sequences' key heads.  A
+// place may belong to several sequences, so this is done before any sum is
+// added, by workgroups of the attention's own launch (a launch of its own: 4 us
+// more).
+__device__ __forceinline__ void copy_weights(const Call &c, int64_t item) {
+  const int H = c.kv.p.kv_heads, parts = c.copy_parts;
+  const int h = (int)(item / parts % H), s = (int)(item / parts / H);
+  const SeqSpan span = seq_span(c.rows, s);
+  if (span.n == 0) return;
+  const int64_t len = c.rows.lengths[s], lo = c.a.window ? max(len - span.n - c.a.window + 1, (int64_t)0) : 0;
+  const int64_t end = min(len, (int64_t)c.rows.table_width << c.kv.shift);
+  const int32_t *table = c.rows.table + s * c.rows.table_stride;
+  const int64_t step = (int64_t)parts * (4 * blockDim.x);  // four rows a thread, within a page
+  for (int64_t key = (item % parts * blockDim.x + threadIdx.x) * 4; key < end; key += step) {
+    const int page = row_page(c.kv, table, c.rows.table_width, key);
+    if (page < 0 || key + 4 <= lo) continue;
+    const uint64_t at = code_row(c.kv, page, h, (int)key & (c.kv.p.page_size - 1));
+    const float4_t w = *reinterpret_cast<const float4_t *>(c.kv.p.weights + at);
+    if (key >= lo && key + 4 <= len) {
+      *reinterpret_cast<float4_t *>(c.a.weights_out + at) = w;
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (key + i >= lo && key + i < len) c.a.weights_out[at + i] = w[i];
+  }
+}
+
 // Weights times scales are lifted to [2^6, 2^7) at a weight of 1 and may pass
 // it by the 2^kSlack that scores may pass the maximum by: 2^15 at most.
 __device__ __forceinline__ float weight_lift(int ex) { return __uint_as_float((uint32_t)(260 - ex) << 23); }
@@ -343,10 +372,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || kWaves == 8 ? 2 : D == 128
   float2 *sml = reinterpret_cast<float2 *>(shared + kWaves * kOut * sizeof(float));  // [wave][row]
   const int tid = threadIdx.x, lane = tid & 63, j = lane >> 4, wave = uniform(tid >> 6);
   const int H = c.kv.p.kv_heads;
+  if (blockIdx.x >= (unsigned)c.blocks) {
+    const int64_t copies = (int64_t)c.rows.seqs * H * c.copy_parts;
+    for (int64_t item = blockIdx.x - c.blocks; item < copies; item += gridDim.x - c.blocks) copy_weights(c, item);
+    return;
+  }
   const char *ring = shared + wave * T::kRing * T::kStep;
   const uint32_t ring_lds = uniform(lds_addr(ring));
   if (blockIdx.x == 0) clear_outside(c, D);
-  for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
+  for (int64_t item = blockIdx.x; item < work; item += c.blocks) {
     const int tgroups = c.tiles / c.tile_waves;
     const int tg = (int)(item % tgroups);
     const int64_t rest = item / tgroups;
@@ -696,26 +730,20 @@ __device__ __forceinline__ float4_t fold_weights(float4_t v0, float4_t v1) {
   return v;
 }
 
-// weights_out = was + v for four keys from `key` on, those that a query sees:
-// the last query at least, and the first one's window.
-__device__ __forceinline__ void store_weights(const Call &c, float4_t was, float4_t v, uint64_t at, int key,
-                                              int64_t len, int64_t start) {
+// weights_out += v for four keys from `key` on, those that a query sees: the
+// last query at least, and the first one's window.
+__device__ __forceinline__ void store_weights(const Call &c, float4_t v, uint64_t at, int key, int64_t len,
+                                              int64_t start) {
   const int64_t lo = c.a.window ? start - c.a.window : -1;
-  float *out = c.a.weights_out + at;
-  if (__builtin_expect(key + 3 < len && key > lo, 1)) {
-    *reinterpret_cast<float4_t *>(out) = was + v;
-    return;
-  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (key + i < len && key + i > lo) out[i] = was[i] + v[i];
+    if (key + i < len && key + i > lo) add_weight(c.a.weights_out + at + i, v[i]);
 }
 
 // The weights of the rows of the cache where no sequence's key head has more
 // rows than a tile, from the scores again and each query's maximum and sum.  A
-// wave takes kWeightSteps steps of a sequence's key head, so that a place has
-// one writer; the next step's keys and weights are on their way while this
-// one's are used.  Bound by bytes in long contexts, in short ones by the three
+// wave takes kWeightSteps steps of a sequence's key head and adds each key's sum
+// once; the next step's keys are on their way while this one's are used.  Bound by bytes in long contexts, in short ones by the three
 // loads that follow each other: 16 sequences of up to 4096 rows, 8 key heads of
 // 128 columns, 15 us (36 MB of keys); one step at a time 26 us.
 constexpr int kWeightSteps = 8;
@@ -747,7 +775,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
       const bool mine = (lane & 15) < 2;
       struct Ahead {
         KeyRegs<D> kr;
-        float4_t was;
         uint64_t at;
         bool ok[2];
       } now, next;
@@ -758,7 +785,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
         const Place<kSmallPages> p = place_of<D>(c, e, h, key0 + n * kStepKeys);
         load_keys<D>(c, p, (lane & 15) / Tile<D>::kRows, x.kr);
         x.at = p.row[kSmallPages ? t : 0] + (kSmallPages ? 0 : 16 * t) + 4 * j;
-        x.was = *reinterpret_cast<const float4_t *>(c.kv.p.weights + x.at);
         x.ok[0] = p.ok[0], x.ok[1] = p.ok[1];
       };
       load(0, now);
@@ -776,7 +802,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_weights_kernel(Call c, int
         for (int u = 0; u < 2; ++u)
           add_weights<D>(now.kr, u, odd, now.ok[u], key + 16 * u, q, f, ml, c.cs, share, limit, sum[u]);
         const float4_t v = fold_weights(sum[0], sum[1]);
-        if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, now.was, v, now.at, key + 16 * t, len, start);
+        if (mine && (t ? now.ok[1] : now.ok[0])) store_weights(c, v, now.at, key + 16 * t, len, start);
         now = next;
       }
     }
@@ -871,14 +897,16 @@ Plan plan_of(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t &r, const coli_mo
 unsigned grid_of(int64_t blocks) { return (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20); }
 
 template <int D, bool kSmallPages>
-hipError_t launch_all(const Call &c, hipStream_t s) {
+hipError_t launch_all(Call &c, hipStream_t s) {
   const int64_t work = (int64_t)c.rows.seqs * c.kv.p.kv_heads * c.splits * (c.tiles / c.tile_waves);
   const bool twice = c.a.type == COLI_MOE_F16;
   const auto kernel = c.waves == 8 ? twice ? kv_attention_kernel<D, true, kSmallPages, 8>
                                            : kv_attention_kernel<D, false, kSmallPages, 8>
                       : twice      ? kv_attention_kernel<D, true, kSmallPages, 4>
                                    : kv_attention_kernel<D, false, kSmallPages, 4>;
-  hipError_t e = launch(kernel, dim3(grid_of(work)), dim3(64 * c.waves), 0, s, c, work);
+  c.blocks = (int)grid_of(work);
+  const int64_t copies = (int64_t)c.rows.seqs * c.kv.p.kv_heads * c.copy_parts;
+  hipError_t e = launch(kernel, dim3(c.blocks + grid_of(copies)), dim3(64 * c.waves), 0, s, c, work);
   const bool prompts = c.few_rows < 1 << 30;
   if (e == hipSuccess && prompts) e = launch_attention_prompts(c, s);
   if (e == hipSuccess && c.part_splits > 1) {
@@ -894,17 +922,17 @@ hipError_t launch_all(const Call &c, hipStream_t s) {
                seqs ? (int)few : 0, rows);
   }
   if (e != hipSuccess || !c.a.weights_out) return e;
+  const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift, heads = (int64_t)c.rows.seqs * c.kv.p.kv_heads;
   if (!one_tile(c.kv.p, c.rows, c.group)) return launch_row_weights(c, s);
-  const int64_t cap = (int64_t)c.rows.table_width << c.kv.shift;
   // four waves a SIMD, or what the table has room for
-  const int64_t heads = (int64_t)c.rows.seqs * c.kv.p.kv_heads, chunk = kWeightSteps * kStepKeys;
+  const int64_t chunk = kWeightSteps * kStepKeys;
   const int64_t parts = least_of((cap + chunk - 1) / chunk, (4096 + heads - 1) / heads);
   return launch(kv_weights_kernel<D, kSmallPages>, dim3(grid_of((heads * parts + kTileWaves - 1) / kTileWaves)),
                 dim3(kTileThreads), 0, s, c, (int)parts, heads * parts);
 }
 
 template <int D>
-hipError_t launch_all(const Call &c, hipStream_t s) {
+hipError_t launch_all(Call &c, hipStream_t s) {
   return c.kv.p.page_size < kStepKeys ? launch_all<D, true>(c, s) : launch_all<D, false>(c, s);
 }
 
@@ -923,7 +951,12 @@ hipError_t launch_kv_attention(const coli_moe_kv_t &kv, const coli_moe_kv_rows_t
   Call c{kv_view(kv), r, a, cs, a.q_heads / kv.kv_heads, p.tiles, p.tile_waves, p.few_rows, p.waves, p.splits, p.prompt_splits,
          max(p.splits, p.prompt_splits), reinterpret_cast<float *>(ws + p.part_o), reinterpret_cast<float2 *>(ws + p.part_ml),
          a.weights_out ? reinterpret_cast<float2 *>(ws + p.ml) : nullptr, ws + p.q_halves,
-         reinterpret_cast<float4 *>(ws + p.q_info)};
+         reinterpret_cast<float4 *>(ws + p.q_info), 0, 0};
+  if (a.weights_out && a.weights_out != kv.weights) {
+    // as many parts of a sequence's key head as its table has room for, up to four workgroups a CU
+    const int64_t heads = (int64_t)r.seqs * kv.kv_heads, chunk = 4 * 64 * p.waves;
+    c.copy_parts = (int)least_of(((int64_t)r.table_width * kv.page_size + chunk - 1) / chunk, (kFill + heads - 1) / heads);
+  }
   switch (kv.head_dim) {
     case 64: return launch_all<64>(c, s);
     case 128: return launch_all<128>(c, s);

@@ -227,7 +227,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_row_weights_kernel(Call c, 
         }
         const int key = keys0 + 32 * u + r;
         if (hf == 0 && ok[u] && key < len && (!c.a.window || key > start - c.a.window))
-          c.a.weights_out[at[u]] = c.kv.p.weights[at[u]] + v;
+          add_weight(c.a.weights_out + at[u], v);
       }
     }
   }
