@@ -673,7 +673,11 @@ int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream);
  * above: no handle, arguments in structs, device pointers, work on `stream`
  * alone, nothing allocated or copied, so every call may be captured.
  * Tensors of heads are [tokens][heads][dim] with strides in elements between
- * tokens and between heads; the elements of a head are contiguous.
+ * tokens and between heads; the elements of a head are contiguous.  Results
+ * that have elements in common with what the call reads, or with each other,
+ * are refused (-4), as far as not allowed below.  Views of one buffer that lie
+ * between each other's heads or tokens may be given if their strides are equal
+ * (an input's may be 0); with other strides their ranges have to be apart.
  * ---------------------------------------------------------------------------
  */
 

@@ -163,6 +163,61 @@ bool heads_ok(const void *p, int type, int64_t tokens, int64_t token, int64_t he
   return tokens <= 1 || heads <= 1 || token >= (heads - 1) * head + dim || head >= (tokens - 1) * token + dim;
 }
 
+// Whether [a, a + n) and [b, b + m) bytes have any in common.
+bool ranges_meet(const void *a, size_t n, const void *b, size_t m) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y ? y - x < n : x - y < m;
+}
+
+// A [tokens][heads] array of heads, heads_ok, and one that is written.
+struct Heads {
+  const void *p;
+  int64_t token, head;
+};
+
+// Whether an element of `in` is one of `out`.  Both may be views of one buffer
+// whose elements lie between each other's: exact where the strides are equal
+// (or in's 0), else any two that reach into each other's range count.
+bool heads_meet(Heads in, Heads out, int type, int64_t tokens, int64_t heads, int64_t dim) {
+  const int64_t size = (int64_t)coli::type_bytes(type);
+  auto bytes = [&](const Heads &a) {  // strides are up to kMaxStride: within 2^68
+    const __int128 n = ((tokens > 1 ? (__int128)(tokens - 1) * a.token : 0) +
+                        (heads > 1 ? (__int128)(heads - 1) * a.head : 0) + dim) * size;
+    return n > INT64_MAX ? (size_t)INT64_MAX : (size_t)n;
+  };
+  if (!ranges_meet(in.p, bytes(in), out.p, bytes(out))) return false;
+  // by the larger of out's strides, then the smaller: how many of each side, and out's stride
+  struct Level {
+    int64_t in, out, step;
+  };
+  auto level = [](int64_t n, int64_t in, int64_t step) {
+    return Level{n == 1 || in == 0 ? 1 : n, n, n == 1 ? 0 : step};
+  };
+  if ((tokens > 1 && in.token && in.token != out.token) || (heads > 1 && in.head && in.head != out.head)) return true;
+  Level outer = level(tokens, in.token, out.token), inner = level(heads, in.head, out.head);
+  if (inner.step > outer.step) {
+    const Level t = outer;
+    outer = inner;
+    inner = t;
+  }
+  // differences out - in in elements: delta + i outer.step + j inner.step, where out's own heads do not overlap, so
+  // that only the i and then the j that bring it next to 0 on either side need a look
+  const int64_t delta = ((intptr_t)out.p - (intptr_t)in.p) / size;
+  auto near = [](int64_t d, const Level &l, int k) {
+    if (l.step == 0) return (int64_t)0;
+    const int64_t q = -d / l.step - (-d % l.step < 0 ? 1 : 0) + k;
+    return q > l.out - 1 ? l.out - 1 : q < 1 - l.in ? 1 - l.in : q;
+  };
+  for (int k = 0; k < 2; ++k) {
+    const int64_t r = delta + near(delta, outer, k) * outer.step;
+    for (int n = 0; n < 2; ++n) {
+      const int64_t d = r + near(r, inner, n) * inner.step;
+      if (d > -dim && d < dim) return true;
+    }
+  }
+  return false;
+}
+
 int kv_check(const coli_moe_kv_t *kv) {
   if (!kv || kv->n_pages < 1 || kv->kv_heads < 1 || kv->kv_heads > 1024) return COLI_MOE_EARG;
   if (kv->page_size < 16 || kv->page_size > 256 || (kv->page_size & (kv->page_size - 1))) return COLI_MOE_EARG;
@@ -203,7 +258,10 @@ int kv_values_check(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *r, const 
   if (!heads_ok(a->k, a->type, r->tokens, a->k_token, kv->kv_heads, a->k_head, kv->head_dim, written) ||
       !heads_ok(a->v, a->type, r->tokens, a->v_token, kv->kv_heads, a->v_head, kv->head_dim, written))
     return COLI_MOE_EARG;
-  return written && a->k == a->v ? COLI_MOE_EARG : COLI_MOE_OK;
+  return written && heads_meet({a->k, a->k_token, a->k_head}, {a->v, a->v_token, a->v_head}, a->type, r->tokens,
+                               kv->kv_heads, kv->head_dim)
+             ? COLI_MOE_EARG
+             : COLI_MOE_OK;
 }
 
 bool finite(float v) { return v >= -0x1.fffffep+127f && v <= 0x1.fffffep+127f; }
@@ -235,7 +293,10 @@ int coli_moe_rotary(const coli_moe_rotary_t *a, void *stream) {
       !heads_ok(a->out, a->type, a->tokens, a->out_token, a->heads, a->out_head, a->dim, true))
     return COLI_MOE_EARG;
   if (!aligned_to(a->positions, a->wide ? 8 : 4) || (a->part > 0 && !aligned_to(a->freq, 4))) return COLI_MOE_EARG;
-  if (a->out == a->x && ((a->tokens > 1 && a->out_token != a->x_token) || (a->heads > 1 && a->out_head != a->x_head)))
+  const bool in_place = a->out == a->x && (a->tokens == 1 || a->out_token == a->x_token) &&
+                        (a->heads == 1 || a->out_head == a->x_head);
+  if (!in_place && heads_meet({a->x, a->x_token, a->x_head}, {a->out, a->out_token, a->out_head}, a->type, a->tokens,
+                              a->heads, a->dim))
     return COLI_MOE_EARG;
   return launched(launch_rotary(*a, static_cast<hipStream_t>(stream)));
 }
@@ -265,10 +326,15 @@ int coli_moe_kv_attention(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *row
   if (code != COLI_MOE_OK) return code;
   if (!kv_pointers_ok(kv) || !kv_row_pointers_ok(rows)) return COLI_MOE_EARG;
   if (a->weights_out && (!kv->weights || !aligned_to(a->weights_out, 16))) return COLI_MOE_EARG;
+  const size_t bytes = (size_t)kv->n_pages * kv->kv_heads * kv->page_size * sizeof(float);  // of the weights
+  if (a->weights_out && a->weights_out != kv->weights && ranges_meet(a->weights_out, bytes, kv->weights, bytes))
+    return COLI_MOE_EARG;
   if (rows->tokens == 0) return COLI_MOE_OK;
   if (!heads_ok(a->q, a->type, rows->tokens, a->q_token, a->q_heads, a->q_head, kv->head_dim, false) ||
       !heads_ok(a->out, a->type, rows->tokens, a->out_token, a->q_heads, a->out_head, kv->head_dim, true) ||
-      a->out == a->q || !aligned_to(workspace, 16))
+      heads_meet({a->q, a->q_token, a->q_head}, {a->out, a->out_token, a->out_head}, a->type, rows->tokens, a->q_heads,
+                 kv->head_dim) ||
+      !aligned_to(workspace, 16))
     return COLI_MOE_EARG;
   if (workspace_bytes < coli::kv_attention_workspace_bytes(*kv, *rows, *a)) return COLI_MOE_ECAPACITY;
   return launched(coli::launch_kv_attention(*kv, *rows, *a, workspace, static_cast<hipStream_t>(stream)));
@@ -285,7 +351,10 @@ int coli_moe_kv_evict(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, c
   if (!kv_pointers_ok(kv) || !kv->weights || !kv_row_pointers_ok(rows)) return COLI_MOE_EARG;
   if (!aligned_to(a->into, 4) || !aligned_to(a->kept, 4) || !aligned_to(a->new_lengths, 4)) return COLI_MOE_EARG;
   if (rows->seqs > 1 && (a->into_stride < 0 || a->into_stride > kMaxStride)) return COLI_MOE_EARG;
-  if (a->into == rows->table || a->new_lengths == rows->lengths) return COLI_MOE_EARG;
+  const size_t lengths = (size_t)rows->seqs * 4, kept = lengths * kv->kv_heads * a->keep;
+  if (a->into == rows->table || ranges_meet(a->new_lengths, lengths, rows->lengths, lengths) ||
+      ranges_meet(a->kept, kept, rows->lengths, lengths) || ranges_meet(a->kept, kept, a->new_lengths, lengths))
+    return COLI_MOE_EARG;
   return launched(coli::launch_kv_evict(*kv, *rows, *a, static_cast<hipStream_t>(stream)));
 }
 
