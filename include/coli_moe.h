@@ -688,9 +688,10 @@ int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream);
  *   out0 = scale (x0 cos a - x1 sin a),  out1 = scale (x0 sin a + x1 cos a);
  * elements from `part` on are copied.  The inverse with the same scale is the
  * transposed map, so it takes a gradient with respect to out to the one with
- * respect to x.  The angle is a float64 product reduced in float64, so far
- * positions lose nothing; the turn itself is float32, rounded once to the
- * type.  `out` may be x itself with equal strides, else no overlap.
+ * respect to x.  The angle, positions[t] * freq[i] for positions below 2^53, is
+ * reduced to a turn with an error below 2^-50 of one, so far positions lose
+ * nothing; the turn itself is float32, rounded once to the type.  `out` may be
+ * x itself with equal strides, else no overlap.
  */
 typedef struct {
   int32_t tokens;       /* 0..2^26; 0 checks the arguments and enqueues nothing */
@@ -700,7 +701,7 @@ typedef struct {
   int32_t type;         /* of x and out: F32, BF16 or F16 */
   int32_t interleaved;  /* 0: pairs (i, i + part / 2), 1: pairs (2 i, 2 i + 1) */
   int32_t inverse;      /* 0 or 1 */
-  int32_t wide;         /* positions are int64 (exact below 2^53 / freq's 24 bits), 0: int32 */
+  int32_t wide;         /* positions are int64 (exact below 2^53), 0: int32 */
   float scale;          /* finite */
   const void *x;
   int64_t x_token, x_head;

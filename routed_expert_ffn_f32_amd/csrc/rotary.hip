@@ -17,13 +17,19 @@ namespace {
 constexpr int kRotaryThreads = 256;
 constexpr int kMaxPairs = 2048;  // part / 2 at most
 
-// cos and sin of p * f: the product is exact in float64 for positions below
-// 2^29 and is reduced to turns there, so what float32 sees is an angle in
-// [-1/2, 1/2] half-turns with an error far below its own rounding.
+// cos and sin of p * f.  The product is a float64 with the rest that it was
+// rounded by, and 1 / (2 pi) has two parts, so that for |p| < 2^53 the turns are
+// off by less than 2^-50 when they are reduced to [-1/2, 1/2]; what float32 sees
+// is an angle in [-1, 1] half turns with its own rounding.  (One product by one
+// part was off by 2^-27 turns at positions of 2^28, by all of one at 2^53.)
 __device__ __forceinline__ float2 turn(double p, float f, float scale, bool inverse) {
-  const double turns = p * (double)f * 0.15915494309189535;  // 1 / (2 pi)
+  constexpr double kInv = 0x1.45f306dc9c883p-3, kInvRest = -0x1.6b01ec5417056p-57;
+  const double angle = p * (double)f, rest = __builtin_fma(p, (double)f, -angle), turns = angle * kInv;
+  double part = __builtin_fma(angle, kInvRest, __builtin_fma(rest, kInv, __builtin_fma(angle, kInv, -turns)));
+  part += turns - rint(turns);
+  part -= rint(part);
   float c, s;
-  sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+  sincospif(2.0f * (float)part, &s, &c);
   return make_float2(scale * c, inverse ? -scale * s : scale * s);
 }
 
@@ -32,8 +38,9 @@ struct RotaryShape {
   int units;                   // of all heads of a token
 };
 
+// Eight waves a SIMD: more than 96 scalar registers cost the prompt above 1.4 us.
 template <bool kPast>
-__global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(coli_moe_rotary_t a, RotaryShape sh, int split) {
+__global__ __launch_bounds__(kRotaryThreads, 8) void rotary_kernel(coli_moe_rotary_t a, RotaryShape sh, int split) {
   __shared__ float2 cs[kMaxPairs];
   const int half = a.part / 2;
   auto store = [&](int64_t i, int n, const float (&v)[8]) {
