@@ -676,8 +676,9 @@ int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream);
  * tokens and between heads; the elements of a head are contiguous.  Results
  * that have elements in common with what the call reads, or with each other,
  * are refused (-4), as far as not allowed below.  Views of one buffer that lie
- * between each other's heads or tokens may be given if their strides are equal
- * (an input's may be 0); with other strides their ranges have to be apart.
+ * between each other's heads or tokens may be given if their steps from token to
+ * token (or from head to head, where those are longer) are equal or an input's
+ * are 0; otherwise their ranges have to be apart.
  * ---------------------------------------------------------------------------
  */
 

@@ -176,8 +176,10 @@ struct Heads {
 };
 
 // Whether an element of `in` is one of `out`.  Both may be views of one buffer
-// whose elements lie between each other's: exact where the strides are equal
-// (or in's 0), else any two that reach into each other's range count.
+// whose elements lie between each other's: exact where in's heads are within a
+// token as out's are (or its tokens within a head) and the steps from token to
+// token are equal (or in's 0), else any two that reach into each other's range
+// count.
 bool heads_meet(Heads in, Heads out, int type, int64_t tokens, int64_t heads, int64_t dim) {
   const int64_t size = (int64_t)coli::type_bytes(type);
   auto bytes = [&](const Heads &a) {  // strides are up to kMaxStride: within 2^68
@@ -186,33 +188,42 @@ bool heads_meet(Heads in, Heads out, int type, int64_t tokens, int64_t heads, in
     return n > INT64_MAX ? (size_t)INT64_MAX : (size_t)n;
   };
   if (!ranges_meet(in.p, bytes(in), out.p, bytes(out))) return false;
-  // by the larger of out's strides, then the smaller: how many of each side, and out's stride
+  // how many steps each side takes, and how long they are; steps of 0 are none
   struct Level {
-    int64_t in, out, step;
+    int64_t in, in_step, out, out_step;
   };
-  auto level = [](int64_t n, int64_t in, int64_t step) {
-    return Level{n == 1 || in == 0 ? 1 : n, n, n == 1 ? 0 : step};
-  };
-  if ((tokens > 1 && in.token && in.token != out.token) || (heads > 1 && in.head && in.head != out.head)) return true;
+  auto level = [](int64_t n, int64_t a, int64_t b) { return Level{n == 1 || a == 0 ? 1 : n, a, n, n == 1 ? 0 : b}; };
   Level outer = level(tokens, in.token, out.token), inner = level(heads, in.head, out.head);
-  if (inner.step > outer.step) {
+  if (tokens > 1 && (heads == 1 || out.token < out.head)) {
     const Level t = outer;
     outer = inner;
     inner = t;
   }
-  // differences out - in in elements: delta + i outer.step + j inner.step, where out's own heads do not overlap, so
-  // that only the i and then the j that bring it next to 0 on either side need a look
-  const int64_t delta = ((intptr_t)out.p - (intptr_t)in.p) / size;
-  auto near = [](int64_t d, const Level &l, int k) {
-    if (l.step == 0) return (int64_t)0;
-    const int64_t q = -d / l.step - (-d % l.step < 0 ? 1 : 0) + k;
-    return q > l.out - 1 ? l.out - 1 : q < 1 - l.in ? 1 - l.in : q;
+  if (outer.out > 1 && ((outer.in > 1 && outer.in_step != outer.out_step) ||
+                        (__int128)(inner.in - 1) * inner.in_step + dim > outer.out_step))
+    return true;
+  // the number of steps, of those there are, that brings d to 0 or next below (k 0), or above (1)
+  auto near = [](int64_t d, int64_t step, int64_t least, int64_t most, int k) {
+    if (step == 0) return (int64_t)0;
+    const int64_t q = -d / step - (-d % step < 0 ? 1 : 0) + k;
+    return q > most ? most : q < least ? least : q;
   };
+  // out - in in elements
+  const int64_t delta = ((intptr_t)out.p - (intptr_t)in.p) / size;
+  const bool alike = inner.in == 1 || inner.in_step == inner.out_step;
   for (int k = 0; k < 2; ++k) {
-    const int64_t r = delta + near(delta, outer, k) * outer.step;
+    const int64_t r = delta + near(delta, outer.out_step, 1 - outer.in, outer.out - 1, k) * outer.out_step;
     for (int n = 0; n < 2; ++n) {
-      const int64_t d = r + near(r, inner, n) * inner.step;
-      if (d > -dim && d < dim) return true;
+      if (alike) {
+        const int64_t d = r + near(r, inner.out_step, 1 - inner.in, inner.out - 1, n) * inner.out_step;
+        if (d > -dim && d < dim) return true;
+        continue;
+      }
+      for (int64_t j = 0; j < inner.out; ++j) {
+        const int64_t at = r + j * inner.out_step;  // and in's step next to it
+        const int64_t d = at + near(at, inner.in_step, 1 - inner.in, 0, n) * inner.in_step;
+        if (d > -dim && d < dim) return true;
+      }
     }
   }
   return false;

@@ -19,7 +19,8 @@ def dev():
     return torch.device("cuda:0")
 
 
-@pytest.mark.parametrize("layout", ["parts of a token", "heads in turn", "tokens in turn", "halves of heads", "heads first"])
+@pytest.mark.parametrize("layout", ["parts of a token", "heads in turn", "tokens in turn", "halves of heads", "heads first",
+                                    "wider steps from head to head"])
 def test_results_between_the_inputs(dev, layout):
     T, H, D = 7, 4, 64
     g = torch.Generator().manual_seed(1)
@@ -35,6 +36,9 @@ def test_results_between_the_inputs(dev, layout):
     elif layout == "halves of heads":
         buf = torch.randn(T, H, 2 * D, generator=g).to(BF16).to(dev)
         x, out = buf[..., D:], buf[..., :D]
+    elif layout == "wider steps from head to head":
+        buf = torch.randn(T, 4 * H * D, generator=g).to(BF16).to(dev)
+        x, out = buf[:, : 3 * H * D].view(T, H, 3 * D)[..., :D], buf[:, 3 * H * D:].view(T, H, D)
     else:
         buf = torch.randn(H, 2 * T, D, generator=g).to(BF16).to(dev)
         x, out = buf[:, :T].transpose(0, 1), buf[:, T:].transpose(0, 1)

@@ -28,6 +28,8 @@ def test_rotary(out):
     dict(x_token=0, out=A + 2 * 64, out_token=128),     # one token for all, inside of the result
     dict(x_token=0, x_head=0, out=A - 2 * (3 * 128 + 1), out_token=128),
     dict(x_token=128, x_head=0, out=A + 2 * 127, out_token=128),
+    dict(x_token=1024, x_head=192, out=A + 2 * (64 + 65), out_token=1024, out_head=64),  # heads of other steps
+    dict(x_token=1024, x_head=64, out=A + 2 * 127, out_token=1024, out_head=192),
 ])
 def test_rotary_in_fused_buffers(out):
     assert rotary_rc(**{**dict(tokens=5, x=A, x_head=64, out_head=64), **out}) == BAD
