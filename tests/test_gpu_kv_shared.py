@@ -94,3 +94,27 @@ def test_as_many_sequences_as_there_may_be(dev, out):
     assert ((got[:, :, 0] <= S) & (got[:, :, 0] >= S - 2.0 ** -6)).all()
     want = torch.full((1, H, 16), -1.0) if out else torch.arange(16.0).expand(1, H, 16)
     assert torch.equal(got[:, :, 1:], want[:, :, 1:])
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [20, 1, 3]])
+def test_captured_sums_of_their_own(dev, new):
+    """Sums in a tensor of their own, replayed while the cache's weights change
+    between: each replay starts from the weights as they are."""
+    pool = Pool([90, 70, 40], 2, 64, 16, seed=5).fill()
+    q = torch.randn(sum(new), 4, 64, generator=torch.Generator().manual_seed(6)).bfloat16().to(dev)
+    off = None if max(new) == 1 else offsets_of(new).to(dev)
+    args = pool.table.to(dev), torch.tensor(pool.lengths, dtype=I32, device=dev), off
+    cache = pool.to(dev, cm)
+    sums, want = torch.full_like(cache.weights, -1.0), torch.full_like(cache.weights, -1.0)
+    cache.attention(q, *args, weights_out=sums)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = cache.attention(q, *args, weights_out=sums)
+    for turn in range(4):
+        sums.fill_(-1.0)
+        graph.replay()
+        out = cache.attention(q, *args, weights_out=want)
+        if turn % 2:
+            torch.cuda.synchronize()
+        assert torch.equal(got, out) and torch.equal(sums, want), turn
+        cache.weights.mul_(1.5)
