@@ -826,8 +826,9 @@ typedef struct {
 } coli_moe_kv_attention_t;
 
 /* Bytes of DEVICE workspace of the call, 0 for sizes out of range (pointers
- * are not looked at, but for weights_out being NULL or not).  It holds
- * nothing between calls; calls whose work may overlap need one each. */
+ * are not looked at, but for weights_out and rows->offsets being NULL or not: both
+ * as in the call).  It holds nothing between calls; calls whose work may overlap
+ * need one each. */
 size_t coli_moe_kv_attention_workspace_bytes(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows,
                                              const coli_moe_kv_attention_t *a);
 /* Errors: -4 NULL or misaligned pointer (workspace: 16 bytes), unsupported

@@ -25,12 +25,13 @@
 //
 // Bound by bytes where there are many keys, 136 of a key head of 128 columns
 // for one query: a decode batch of 64 sequences of up to 8192 rows, 8 key heads
-// for 64 queries, 327 MB, takes 87 us with its join (3.8 TB/s; a large copy
-// 5.1), one sequence of 131071 rows, 143 MB, 42 us.  What keeps it from the
-// copy's rate is the 350 vector instructions of a step of 32 keys (columns are
-// only 8 rows, so the expansion of codes has few to be shared by).  One sequence
-// of 517 rows takes 14 us: a launch, three loads that follow each other
-// (length, page, rows), five steps a wave and the join of eight waves.
+// for 64 queries, 327 MB, takes 91 us (3.6 TB/s; a large copy 5.1) with a
+// workgroup for each sequence's key head and no join, one sequence of 131071
+// rows, 143 MB, 42 us, 5 of them the join.  What keeps it from the copy's rate is
+// the 350 vector instructions of a step of 32 keys (columns are only 8 rows, so
+// the expansion of codes has few to be shared by).  One sequence of 517 rows
+// takes 14 us: a launch, three loads that follow each other (length, page, rows),
+// three steps a wave and the join of eight waves.
 #include "attention.h"
 #include "lds_dma.h"
 
@@ -743,9 +744,11 @@ __device__ __forceinline__ void store_weights(const Call &c, float4_t v, uint64_
 // The weights of the rows of the cache where no sequence's key head has more
 // rows than a tile, from the scores again and each query's maximum and sum.  A
 // wave takes kWeightSteps steps of a sequence's key head and adds each key's sum
-// once; the next step's keys are on their way while this one's are used.  Bound by bytes in long contexts, in short ones by the three
-// loads that follow each other: 16 sequences of up to 4096 rows, 8 key heads of
-// 128 columns, 15 us (36 MB of keys); one step at a time 26 us.
+// once; the next step's keys are on their way while this one's are used.  Bound
+// by bytes in long contexts, in short ones by the three loads that follow each
+// other: 16 sequences of up to 4096 rows, 8 key heads of 128 columns, 17 us (36 MB
+// of keys); one step at a time 26 us.  (A store in place of the addition is 15.5,
+// but sequences that share a page would lose sums.)
 constexpr int kWeightSteps = 8;
 
 template <int D, bool kSmallPages>

@@ -13,20 +13,24 @@
 // A code times its scale, 4 and 8 significant bits, is exact in a half; what
 // the exponent lacks is made up by one power of two for the keys and one for
 // the values of each step.  A key whose scale is more than 25 powers of two
-// below another's of its step has its scores computed apart.  Where the scales of a step's values are more than
-// 25 powers of two apart, the small ones follow in passes of their own, so a
-// value counts down to 2^-77 of the largest next to it, or 2^-100 of the
-// largest before it.  Rows whose scale is NaN (or Inf) stay out of the products, where 0 times NaN would reach rows
-// that do not see them, and are put on those that do.
+// below another's of its step has its scores computed apart.  Where the scales of
+// a step's values are more than 25 powers of two apart, the small ones follow in
+// passes of their own, so a value counts down to 2^-77 of the largest next to it,
+// or 2^-100 of the largest before it.  Rows whose scale is NaN (or Inf) stay out
+// of the products, where 0 times NaN would reach rows that do not see them, and
+// are put on those that do.
 //
-// Bound by the vector units: a wave's step of 64 keys has 64 matrix
-// instructions of 32 cycles and about 350 vector ones of 4, of which 32
-// exponentials take 16, beside 190 scalar.  Two prompts of up to 1500 tokens on
-// up to 16384 rows, 64 query heads on 8 of 128 columns: 1.55 ms, 625 TFLOP/s (a
-// large product of the library's: 1.17 PFLOP/s); with all work in its order,
-// before the scores of the next 32 keys went beside the weights of these, 1.85;
-// by the tiles of a few rows 5.5.  D = 64 runs at 370, D = 256, whose results
-// and queries leave one workgroup of four waves a CU its registers, at 280.
+// Bound by the sum of two units' work, of which too little runs at once: the
+// vector units are busy for 51 % of the time and the matrix cores for 33 (a
+// wave's step of 64 keys has 64 matrix instructions of 32 cycles and about 350
+// vector ones of 4, of which 32 exponentials take 16, beside 190 scalar; one
+// barrier a step keeps the waves of a SIMD in the same phase).  Two prompts of up
+// to 1500 tokens on up to 16384 rows, 64 query heads on 8 of 128 columns: 1.55 ms,
+// 625 TFLOP/s (a large product of the library's: 1.17 PFLOP/s); with all work in
+// its order, before the scores of the next 32 keys went beside the weights of
+// these, 1.85; by the tiles of a few rows 5.5.  D = 64 runs at 370, D = 256, whose
+// results and queries leave one workgroup of four waves a CU its registers, at
+// 280.
 #include "attention.h"
 
 namespace coli {

@@ -142,7 +142,7 @@ __device__ __forceinline__ void store8(void *base, int type, int64_t i, int n, c
     if (j < n) store1(base, type, i + j, v[j]);
 }
 
-// The same, past the caches, for results larger than they are.
+// The same, past the caches: for results of many tokens.
 __device__ __forceinline__ void store16_past(char *p, const u32x4 &v) {
   typedef u32x4 u32x4_any __attribute__((aligned(2)));
   __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(p));

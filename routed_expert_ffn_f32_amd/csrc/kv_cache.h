@@ -51,13 +51,6 @@ __device__ __forceinline__ int find_seq(const coli_moe_kv_rows_t &r, int t) {
   return r.offsets[lo] <= t && t < r.offsets[lo + 1] ? lo : -1;
 }
 
-// Row (in its sequence) of token t of sequence s; 64 bits, since lengths may
-// be anything.
-__device__ __forceinline__ int64_t token_row(const coli_moe_kv_rows_t &r, int s, int t) {
-  const int last = r.offsets ? min(r.offsets[s + 1], r.tokens) : s + 1;
-  return (int64_t)r.lengths[s] - (last - t);
-}
-
 // Page of rows row .. of sequence s, -1 where none is.
 __device__ __forceinline__ int row_page(const KvView &kv, const int32_t *table, int width, int64_t row) {
   const int64_t i = row >> kv.shift;

@@ -2,14 +2,17 @@
 // eviction by accumulated attention weight.  The attention over it is in
 // attention.hip.
 //
-// Append and read are bound by bytes where there are many tokens, and by the
-// loads that follow each other (sequence, length, page, rows) where there are
-// few; so eight tokens' places are looked up together, and there are as many
-// waves as one round of them can be.  4889 tokens, 4 heads of 256 halves: 16 us
-// to append (25 MB), 12 to read as float32 (45 MB); 64 tokens, 8 heads of 128:
-// 5 and 4 us.  61575 rows of 8 heads of 128 read as halves, 319 MB: 87 us (3.7
-// TB/s); reads of many tokens are stored past the caches (with them, an
-// eviction and this read take 166 us back to back instead of 147).
+// Few tokens are bound by the loads that follow each other (sequence, length,
+// page, rows), so eight tokens' places are looked up together, and there are as
+// many waves as one round of them can be: 64 tokens, 8 heads of 128: 5 us to
+// append, 4 to read.  Many tokens: read is bound by bytes, append by its
+// instructions.  4889 tokens, 4 heads of 256 halves: 16 us to append (25 MB, 5 us
+// at a copy's rate; a wave's eight groups of 64 columns are 330 vector
+// instructions, 10.6 us of issue in all), 12 to read as float32 (45 MB).  61575
+// rows of 8 heads of 128 read as halves, 319 MB: 87 us (3.7 TB/s); reads of many
+// tokens are stored past the caches (with them, an eviction and this read take 166
+// us back to back instead of 147; what a kernel that reads the result next makes
+// of it was not measured).
 #include "element_types.h"
 #include "internal.h"
 #include "kv_cache.h"

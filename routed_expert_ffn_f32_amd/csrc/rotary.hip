@@ -5,8 +5,9 @@
 // by all heads of a token, so a workgroup takes whole tokens, computes their
 // cosines and sines into LDS once and turns every head with them.  4096 tokens
 // of 56 heads of 128 halves, 64 of them turned: 24 us for 117 MB (4.9 TB/s; a
-// large copy 5.1).  Results of many tokens are stored past the caches: with
-// them, 37 us back to back.  One token of 72 heads: 3 us, a launch.
+// large copy 5.1).  Results of 1024 tokens and more are stored past the caches:
+// with them, 37 us back to back (what a kernel that reads the result next makes
+// of it was not measured).  One token of 72 heads: 3 us, a launch.
 #include "element_types.h"
 #include "internal.h"
 #include "kv_cache.h"
