@@ -674,11 +674,12 @@ int coli_moe_last_logits(const coli_moe_t *m, float *logits, void *stream);
  * alone, nothing allocated or copied, so every call may be captured.
  * Tensors of heads are [tokens][heads][dim] with strides in elements between
  * tokens and between heads; the elements of a head are contiguous.  Results
- * that have elements in common with what the call reads, or with each other,
- * are refused (-4), as far as not allowed below.  Views of one buffer that lie
- * between each other's heads or tokens may be given if their steps from token to
- * token (or from head to head, where those are longer) are equal or an input's
- * are 0; otherwise their ranges have to be apart.
+ * (of heads, weights_out, kept, new_lengths) that have elements in common with
+ * the inputs of their kind (heads, weights, lengths) or with each other are
+ * refused (-4), as far as not allowed below.  Heads in one buffer that lie between
+ * each other's may be given if their steps from token to token (or from head to
+ * head, where those are longer) are equal or an input's are 0; otherwise their
+ * ranges have to be apart.
  * ---------------------------------------------------------------------------
  */
 
@@ -800,9 +801,10 @@ int coli_moe_kv_read(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, co
  * row that a query sees; other places are left as they were.  A weight comes
  * from its score computed once more: it is at most 1, but where float32's
  * neighbours are far apart (at scores of 2^30: 128) a query's need not sum to 1.
- * weights_out may be kv->weights.  Rows that several sequences of the call see
- * (pages of a common prefix) get the sum over all of them, added in no fixed
- * order, so that its last bits may differ from call to call.  The scores q . k,
+ * weights_out may be kv->weights; it is the device's own memory (the sums are
+ * added by its atomics).  Rows that several sequences of the call see (pages of a
+ * common prefix) get the sum over all of them, added in no fixed order, so that
+ * its last bits may differ from call to call.  The scores q . k,
  * and the sums of the sizes of their products, have to be within float32's
  * range.  A scale of the cache that is NaN or Inf makes the results NaN of the
  * queries that see its row: a key's whole, a value's in the columns of its

@@ -177,9 +177,9 @@ struct Heads {
 
 // Whether an element of `in` is one of `out`.  Both may be views of one buffer
 // whose elements lie between each other's: exact where in's heads are within a
-// token as out's are (or its tokens within a head) and the steps from token to
-// token are equal (or in's 0), else any two that reach into each other's range
-// count.
+// token as out's are (or its tokens within a head), the steps from token to token
+// are equal (or in's 0) and those from head to head too, or the heads at most
+// 4096; else any two that reach into each other's range count.
 bool heads_meet(Heads in, Heads out, int type, int64_t tokens, int64_t heads, int64_t dim) {
   const int64_t size = (int64_t)coli::type_bytes(type);
   auto bytes = [&](const Heads &a) {  // strides are up to kMaxStride: within 2^68
@@ -211,6 +211,7 @@ bool heads_meet(Heads in, Heads out, int type, int64_t tokens, int64_t heads, in
   // out - in in elements
   const int64_t delta = ((intptr_t)out.p - (intptr_t)in.p) / size;
   const bool alike = inner.in == 1 || inner.in_step == inner.out_step;
+  if (!alike && inner.out > 4096) return true;  // more than is worth a look
   for (int k = 0; k < 2; ++k) {
     const int64_t r = delta + near(delta, outer.out_step, 1 - outer.in, outer.out - 1, k) * outer.out_step;
     for (int n = 0; n < 2; ++n) {

@@ -62,3 +62,11 @@ def test_evict():
     for a in (dict(new_lengths=B + 4), dict(new_lengths=B - 4), dict(kept=B - 2 * 2 * 8 * 4 + 4), dict(kept=B + 4),
               dict(kept=A + (5 << 20), new_lengths=A + (5 << 20) + 2 * 2 * 8 * 4 - 4)):
         assert call(**a) == BAD, a
+
+
+def test_sizes_at_their_limits():
+    """The longest steps and the most tokens are looked at without overflow."""
+    far = dict(tokens=1 << 26, heads=4096, x_token=1 << 40, x_head=1 << 40, out=A + 2, out_token=1 << 40, out_head=64)
+    assert rotary_rc(**far) == BAD
+    assert rotary_rc(**{**far, "heads": 1, "out_token": (1 << 40) - 64}) == BAD
+    assert rotary_rc(**{**far, "heads": 1, "x_token": 0}) == BAD
