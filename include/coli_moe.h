@@ -810,9 +810,14 @@ int coli_moe_kv_read(const coli_moe_kv_t *kv, const coli_moe_kv_rows_t *rows, co
  * queries that see its row: a key's whole, a value's in the columns of its
  * group.  In sequences of more than 64 query rows (tokens times q_heads /
  * kv_heads) values below 2^-77 of the largest of their 64 neighbouring rows, or
- * below 2^-100 of the largest before them, may count as 0.  Out rows of tokens
- * in no sequence are left as they were (clear 0) or set to 0 (clear 1).  But for
- * the weights of rows of several sequences the same call gives the same bits.
+ * below 2^-100 of the largest before them, may count as 0; so may, in their keys,
+ * groups of 64 columns whose scale is below 2^-25 of the largest of these 64 rows
+ * (2^-24 of its row's for the weights of more rows than a tile's 1024 /
+ * head_dim) while another of their row is not.  Elements of a query below 2^-28
+ * of its largest (or of 2^-107, if that is more) are rounded to steps of 2^-38 of
+ * it.  Out rows of tokens in no sequence are left as they were (clear 0) or set
+ * to 0 (clear 1).  But for the weights of rows of several sequences the same call
+ * gives the same bits.
  */
 typedef struct {
   int32_t q_heads;  /* a multiple of kv_heads, at most 256 times as many */
